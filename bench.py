@@ -47,7 +47,8 @@ CSRC = os.path.join("stochastic_sparse_kv_gb300", "csrc")
 KERNEL_SOURCES = [os.path.join(CSRC, f) for f in ("santa_common.cuh", "santa_sample.cuh", "santa_tcgen05.cuh", "santa_score.cuh",
                                                    "santa_gather.cuh", "santa_dense.cuh", "santa_cluster.cuh",
                                                    "santa_kernels.h", "santa_kernels_d128.cu", "santa_kernels_d64.cu",
-                                                   "santa_api.cu")]
+                                                   "santa_api.cu", "santa_host.h", "santa_kv4.cuh",
+                                                   "santa_window.cuh", "santa_window_api.cu")]
 # The sampled path is two launches chained by programmatic dependent launch (the value
 # stage's launch and prologue overlap the score grid's end), so one santa_decode call is
 # timed as the unit.

@@ -92,6 +92,7 @@ extern "C" {
 /* Device error bits (santa_device_status). */
 #define SANTA_DEV_BAD_SEQLEN 1      /* some seq_lens[b] outside [0, n_max]; treated as 0 */
 #define SANTA_DEV_TIMEOUT 2         /* a bounded wait on a shared-memory barrier gave up */
+#define SANTA_DEV_BAD_POSITION 4    /* a row's pos / counts outside the cache; the row is skipped */
 
 /* Problem shape.  scale = 0 selects 1/sqrt(d) rounded to fp32. */
 typedef struct {
@@ -112,9 +113,10 @@ typedef struct {
 int santa_workspace_size(const santa_shape *shape, int32_t S, int32_t mode, size_t *bytes);
 
 /*
- * santa_workspace_init -- zero the workspace's control block (counters and the device
- * error word) on `stream`.  Call once after allocating a workspace; every completed
- * santa_decode leaves the counters at zero again.  Call it again after an error.
+ * santa_workspace_init -- zero the workspace's control block (its first 64 KiB: counters and
+ * the device error word) on `stream`.  Call once after allocating a workspace; every
+ * completed call leaves the counters at zero again, so one workspace serves calls of any
+ * kind, shape and mode, one after another.  Call it again after an error.
  */
 int santa_workspace_init(void *workspace, size_t workspace_bytes, void *stream);
 
@@ -239,6 +241,94 @@ int santa_device_status(void *workspace, int32_t *code, void *stream);
 int santa_decode_static(const santa_shape *shape, const void *q, const void *k_cache,
                         const void *v_cache, const int32_t *seq_lens, int32_t S, int32_t mode,
                         uint64_t seed, float *out, int32_t *idx_out, void *stream);
+
+/* ------------------------------------------------------------------ the 4-bit KV cache
+ *
+ * A cache whose rows take d/2 bytes of codes and d/16 bytes of scales (72 bytes at d = 128,
+ * against 256 in bf16).  A row is d/16 groups of 16 consecutive values; a group x holds
+ *   scale  one byte, an unsigned float with 5 exponent bits (bias 15) and 3 mantissa bits:
+ *          the such number nearest max|x| / 6, ties to even, at most 10240 (0xE2).  As bits
+ *          it is bits 7-14 of the fp16 of the same value.  0xFF (a NaN) where the group
+ *          holds a NaN or an infinity: the whole group then reads back as NaN.
+ *   codes  4 bits each: sign (bit 3) and index into {0, .5, 1, 1.5, 2, 3, 4, 6} (bits 0-2),
+ *          the value nearest x / scale, ties to the even index, saturating at 6.  Byte i of
+ *          a row holds values 2i (low half) and 2i + 1 (high half).
+ * A code stands for sign * value * scale, which bf16 holds exactly.  Largest magnitude held:
+ * 61440; smallest: 2^-18.
+ */
+typedef struct {
+    void *k, *k_scale;   /* device uint8 [B, H_kv, n_max, d/2] and [B, H_kv, n_max, d/16] */
+    void *v, *v_scale;   /* the same for V.  All contiguous, 16-byte aligned; n_max must be a
+                          * multiple of 16 (SANTA_ERR_UNSUPPORTED otherwise) */
+} santa_kv4;
+
+/* bf16 K and V rows [B, T, H_kv, d] in device memory, 16-byte aligned.  Strides in elements
+ * for (batch, token, head): multiples of 8, not negative; a row's d values are contiguous.
+ * A stride whose dimension has size 1 is not read. */
+typedef struct {
+    void *k, *v;
+    int64_t k_stride[3], v_stride[3];
+} santa_rows;
+
+/*
+ * santa_kv4_append -- quantise new K and V rows into a 4-bit cache.
+ *
+ *  shape     B, H_kv, d and n_max of the cache (H_q and scale as for a decode call)
+ *  rows      the new rows (read only); any slice of a projection's output will do
+ *  T         tokens per batch row in `rows`; 0 does nothing
+ *  pos       device int32 [B]: cache row of each batch row's first new token (its sequence
+ *            length before the call)
+ *  counts    device int32 [B] or NULL: how many of the T tokens are live (padded prompts).
+ *            Row t < counts[b] goes to cache row pos[b] + t; nothing else is written
+ *  workspace any workspace of this library, or NULL: only its device error word is used.
+ *            A batch row with pos < 0, counts outside [0, T] or pos + counts > n_max is
+ *            skipped and sets SANTA_DEV_BAD_POSITION there
+ * B * H_kv * T * d / 16 must be below 2^31.  The caller advances its sequence lengths.
+ */
+int santa_kv4_append(const santa_shape *shape, const santa_kv4 *cache, const santa_rows *rows, int32_t T,
+                     const int32_t *pos, const int32_t *counts, void *workspace, void *stream);
+
+/*
+ * santa_kv4_read -- rows of a 4-bit cache back as bf16 (exact: every held value is a bf16).
+ * Arguments as for santa_kv4_append, with `rows` written instead: cache row pos[b] + t goes
+ * to row (b, t) for t < counts[b], and the other rows stay as they were.  No two rows may
+ * share memory: in order of size, each stride must step over all that the smaller ones span
+ * (SANTA_ERR_INVALID_ARG otherwise).  For example, with the strides of a bf16 cache
+ * [B, H_kv, n, d] it fills the cache that santa_decode samples.
+ */
+int santa_kv4_read(const santa_shape *shape, const santa_kv4 *cache, const santa_rows *rows, int32_t T,
+                   const int32_t *pos, const int32_t *counts, void *workspace, void *stream);
+
+/* ------------------------------------------------------------------ windowed exact attention
+ *
+ * One decode step of exact softmax attention over the visible keys of each sequence, the
+ * decoding token being the last of its n_b = seq_lens[b] keys:
+ *   window = 0   every key j < n_b
+ *   window > 0   the last `window` keys (j >= n_b - window) and the first `sinks` ones
+ * Keys that are not visible are not read into the result, whatever they hold (NaN too).
+ */
+
+/*
+ * santa_window_workspace_size -- bytes of workspace santa_decode_window and santa_decode_kv4
+ * need for this shape (the same for both).  Pure host computation.
+ */
+int santa_window_workspace_size(const santa_shape *shape, size_t *bytes);
+
+/*
+ * santa_decode_window -- over a bf16 cache.  q, k_cache, v_cache, seq_lens, out, workspace and
+ * stream as for santa_decode; window >= 0; sinks >= 0 (ignored when window = 0); flags 0 or
+ * SANTA_OUT_BF16.  n_b = 0 gives zeros.
+ */
+int santa_decode_window(const santa_shape *shape, const void *q, const void *k_cache, const void *v_cache,
+                        const int32_t *seq_lens, int32_t window, int32_t sinks, int32_t flags, float *out,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * santa_decode_kv4 -- over a 4-bit cache: exact attention on the values that the cache holds.
+ */
+int santa_decode_kv4(const santa_shape *shape, const void *q, const santa_kv4 *cache, const int32_t *seq_lens,
+                     int32_t window, int32_t sinks, int32_t flags, float *out, void *workspace,
+                     size_t workspace_bytes, void *stream);
 
 /*
  * santa_timeline_buffer -- for reading where a call's time goes: in a library built with

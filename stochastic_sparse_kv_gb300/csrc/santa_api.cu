@@ -10,6 +10,7 @@
 #include "santa_cluster.cuh"
 #include "santa_dense.cuh"
 #include "santa_gather.cuh"
+#include "santa_host.h"
 #include "santa_kernels.h"
 #include "santa_score.cuh"
 
@@ -149,6 +150,8 @@ struct FnCache {
 FnCache g_fn[256];
 int g_nfn = 0;
 
+}  // namespace
+
 int device_info(int *dev, int *sms, int *optin)
 {
     if (cudaGetDevice(dev) != cudaSuccess) return SANTA_ERR_CUDA;
@@ -198,8 +201,6 @@ int prepare_fn(const void *fn, int dev, int smem, int threads, int *occ)
     return *occ > 0 ? SANTA_OK : SANTA_ERR_UNSUPPORTED;
 }
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 int check_shape(const santa_shape *sh)
 {
     if (!sh) return SANTA_ERR_INVALID_ARG;
@@ -215,6 +216,14 @@ int check_shape(const santa_shape *sh)
     if ((long long)sh->B * sh->H_kv * sh->n_max >= (1ll << 31)) return SANTA_ERR_UNSUPPORTED;
     return SANTA_OK;
 }
+
+uint64_t wait_limit_ns()
+{
+    const unsigned long long v = g_wait_limit_ns.load(std::memory_order_relaxed);
+    return v ? v : 2000000000ull;
+}
+
+namespace {
 
 int check_mode_S(int32_t mode_flags, int32_t S)
 {
@@ -240,11 +249,17 @@ int check_decode_args(const santa_shape *shape, const void *q, const void *k_cac
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
         !aligned(seq_lens, 4) || (idx_out && !aligned(idx_out, 4)))
         return SANTA_ERR_MISALIGNED;
-    const WsLayout wl = ws_layout(shape->B, shape->H_q, shape->H_kv, shape->d, shape->n_max,
-                                  (mode_flags & 0xff) == SANTA_DENSE);
-    if (wl.ctrl + sizeof(int) * (CTRL_GROUPS + (size_t)shape->B * shape->H_kv) > 65536) return SANTA_ERR_UNSUPPORTED;
-    return SANTA_OK;
+    return check_groups(shape);
 }
+
+}  // namespace
+
+int check_groups(const santa_shape *sh)
+{
+    return (size_t)sh->B * sh->H_kv <= CTRL_MAX_GROUPS ? SANTA_OK : SANTA_ERR_UNSUPPORTED;
+}
+
+namespace {
 
 // cuTensorMapEncodeTiled from the driver, found once through the runtime (no link
 // against libcuda).
@@ -267,6 +282,8 @@ EncodeTiledFn encode_tiled()
     return fn;
 }
 
+}  // namespace
+
 // Row-major bf16 matrix [rows][D] as a 2-D tensor map with boxes of 64 columns (128
 // bytes, the 128-byte swizzle's width) by box_rows rows.
 int make_map_bf16(CUtensorMap *map, const void *base, int D, long long rows, int box_rows)
@@ -282,6 +299,8 @@ int make_map_bf16(CUtensorMap *map, const void *base, int D, long long rows, int
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? SANTA_OK : SANTA_ERR_CUDA;
 }
+
+namespace {
 
 // The single-pass cluster kernel, when it applies: one cluster of C CTAs per (b, KV head),
 // the largest C (at most 16) such that the B * H_kv clusters fit the GPU at once, each CTA
@@ -381,9 +400,9 @@ const char *santa_status_string(int status)
     case SANTA_ERR_MISALIGNED: return "pointer not aligned (16 bytes for tensors, 256 for the workspace)";
     case SANTA_ERR_WORKSPACE: return "workspace missing or too small";
     case SANTA_ERR_UNSUPPORTED: return "outside the supported limits (d in {64,128}, G in {1,2,4,8}, B <= 1024, "
-                                      "n_max <= 524288, S <= 4096, shared memory)";
+                                      "n_max <= 524288, a multiple of 16 for a 4-bit cache, S <= 4096, shared memory)";
     case SANTA_ERR_CUDA: return "CUDA runtime error";
-    case SANTA_ERR_DEVICE: return "device reported an error (bad seq_lens or a barrier timeout)";
+    case SANTA_ERR_DEVICE: return "device reported an error (bad seq_lens or positions, or a barrier timeout)";
     case SANTA_ERR_SCRATCH: return "the problem needs more scratch than the static buffer of santa_decode_static holds";
     default: return "unknown status";
     }
@@ -405,10 +424,7 @@ int santa_workspace_init(void *workspace, size_t workspace_bytes, void *stream)
     if (!aligned(workspace, 256)) return SANTA_ERR_MISALIGNED;
     const size_t n = workspace_bytes < 256 ? workspace_bytes : 256;
     if (n < sizeof(int) * 4) return SANTA_ERR_WORKSPACE;
-    // The control block is CTRL_GROUPS words plus one counter per group; the caller's
-    // workspace may be shared across shapes, so clear every counter word it can hold
-    // up to the first data region (a conservative 64 KiB bound).
-    size_t ctrl = workspace_bytes < (size_t)65536 ? workspace_bytes : (size_t)65536;
+    size_t ctrl = workspace_bytes < CTRL_BYTES ? workspace_bytes : CTRL_BYTES;
     ctrl = ctrl / 4 * 4;
     if (cudaMemsetAsync(workspace, 0, ctrl, (cudaStream_t)stream) != cudaSuccess) return SANTA_ERR_CUDA;
     return SANTA_OK;
@@ -485,8 +501,7 @@ int santa_decode(const santa_shape *shape, const void *q, const void *k_cache, c
     p.k2_hi = (float)k2;
     p.k2_lo = (float)(k2 - (double)p.k2_hi);
     p.tau2 = (float)(3.0 * 1.4426950408889634);  // re-score keys within e^-3 of the maximum
-    const unsigned long long wlim = g_wait_limit_ns.load(std::memory_order_relaxed);
-    p.wait_ns = wlim ? wlim : 2000000000ull;
+    p.wait_ns = wait_limit_ns();
     p.tl = g_timeline.load(std::memory_order_relaxed);
     p.tl_rows = p.tl ? g_timeline_rows.load(std::memory_order_relaxed) : 0;
 

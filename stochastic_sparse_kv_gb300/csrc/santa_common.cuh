@@ -24,10 +24,15 @@ constexpr int NMAX_LIMIT = 524288;   // longest KV cache (keys)
 constexpr int BMAX = 1024;           // batch rows per call
 constexpr int SMAX = 4096;           // samples per (b, h)
 
-// Control block (int32 words at the start of the workspace).
+// Control block: int32 words at the start of the workspace, the same CTRL_BYTES for every
+// call, so that one workspace serves calls of any kind and shape in any order.  Words from
+// CTRL_GROUPS on are the arrival counters of the (batch row, KV head) groups.
+constexpr size_t CTRL_BYTES = 65536;
+constexpr size_t CTRL_MAX_GROUPS = CTRL_BYTES / sizeof(int) - 64;
 enum : int { CTRL_ERR = 0, CTRL_WORK = 1, CTRL_EXIT = 2, CTRL_GROUPS = 64 };
 constexpr int DEV_BAD_SEQLEN = 1;
 constexpr int DEV_TIMEOUT = 2;
+constexpr int DEV_BAD_POSITION = 4;
 // Limit of the end-of-kernel drains (MMAs still running, TMA fills not yet consumed):
 // never the caller's shorter limit, so that an aborted CTA frees TMEM and exits only
 // after its asynchronous work has completed.
@@ -52,7 +57,7 @@ __host__ __device__ inline WsLayout ws_layout(int B, int H_q, int H_kv, int d, i
     const size_t BH = (size_t)B * H_q;
     size_t off = 0;
     L.ctrl = off;
-    off = align_up(off + sizeof(int) * (CTRL_GROUPS + (size_t)B * H_kv), 256);
+    off += CTRL_BYTES;
     L.qt = off;  // Bernoulli qK^T: the ternary query draws, bf16 [B*H_q][d]
     off = align_up(off + BH * (size_t)d * sizeof(uint16_t), 256);
     if (!dense) {

@@ -1,0 +1,186 @@
+// santa_window_api.cu -- the entry points of the 4-bit KV cache and of windowed decode
+// attention (declared in include/santa.h): argument checks and launches.
+#include <cmath>
+#include <utility>
+
+#include "../../include/santa.h"
+#include "santa_host.h"
+#include "santa_window.cuh"
+
+using namespace santa;
+
+namespace {
+
+int check_cache(const santa_shape *sh, const santa_kv4 *c)
+{
+    const int rc = check_shape(sh);
+    if (rc) return rc;
+    if (!c || !c->k || !c->k_scale || !c->v || !c->v_scale) return SANTA_ERR_INVALID_ARG;
+    if (sh->n_max % KV_GROUP != 0) return SANTA_ERR_UNSUPPORTED;
+    if (!aligned(c->k, 16) || !aligned(c->k_scale, 16) || !aligned(c->v, 16) || !aligned(c->v_scale, 16))
+        return SANTA_ERR_MISALIGNED;
+    return SANTA_OK;
+}
+
+// The checks and the launch shared by append and read.  `distinct`: the rows are written, so
+// no two may share memory.
+int move_rows(const santa_shape *sh, const santa_kv4 *c, const santa_rows *r, int32_t T, const int32_t *pos,
+              const int32_t *counts, void *workspace, void *stream, bool distinct)
+{
+    const int rc = check_cache(sh, c);
+    if (rc) return rc;
+    if (!r || !r->k || !r->v || !pos || T < 0) return SANTA_ERR_INVALID_ARG;
+    if (!aligned(r->k, 16) || !aligned(r->v, 16) || !aligned(pos, 4) || (counts && !aligned(counts, 4)) ||
+        (workspace && !aligned(workspace, 256)))
+        return SANTA_ERR_MISALIGNED;
+    const long long groups = (long long)sh->B * sh->H_kv * (sh->d / KV_GROUP);
+    if (T > 0 && groups > ((1ll << 31) - 1) / T) return SANTA_ERR_UNSUPPORTED;
+    const long long dims[3] = {sh->B, T, sh->H_kv};
+    for (int w = 0; w < 2; ++w) {
+        const int64_t *st = w ? r->v_stride : r->k_stride;
+        int order[3] = {0, 1, 2};
+        for (int i = 0; i < 3; ++i) {
+            if (dims[i] <= 1) continue;  // this stride is never used
+            if (st[i] < 0 || st[i] > (1ll << 40)) return SANTA_ERR_INVALID_ARG;
+            if (st[i] % 8 != 0) return SANTA_ERR_MISALIGNED;
+        }
+        if (!distinct) continue;
+        // from the innermost dimension out, each step clears everything inside it
+        for (int i = 1; i < 3; ++i)
+            for (int j = i; j > 0 && st[order[j]] < st[order[j - 1]]; --j) std::swap(order[j], order[j - 1]);
+        long long extent = sh->d;
+        for (int i = 0; i < 3; ++i) {
+            const int x = order[i];
+            if (dims[x] <= 1) continue;
+            if (st[x] < extent) return SANTA_ERR_INVALID_ARG;
+            extent += st[x] * (dims[x] - 1);
+        }
+    }
+    if (T == 0) return SANTA_OK;
+    Kv4Move m{};
+    m.code[0] = static_cast<uint8_t *>(c->k);
+    m.code[1] = static_cast<uint8_t *>(c->v);
+    m.scale[0] = static_cast<uint8_t *>(c->k_scale);
+    m.scale[1] = static_cast<uint8_t *>(c->v_scale);
+    m.row[0] = static_cast<uint16_t *>(r->k);
+    m.row[1] = static_cast<uint16_t *>(r->v);
+    for (int w = 0; w < 2; ++w) {
+        const int64_t *s = w ? r->v_stride : r->k_stride;
+        m.sb[w] = s[0];
+        m.st[w] = s[1];
+        m.sh[w] = s[2];
+    }
+    m.pos = pos;
+    m.counts = counts;
+    m.ctrl = static_cast<int32_t *>(workspace);
+    m.B = sh->B;
+    m.H_kv = sh->H_kv;
+    m.D = sh->d;
+    m.n_max = sh->n_max;
+    m.T = T;
+    const dim3 grid((unsigned)((groups * T + KV_NT - 1) / KV_NT), 2);
+    if (distinct)
+        santa_kv4_read_kernel<<<grid, KV_NT, 0, (cudaStream_t)stream>>>(m);
+    else
+        santa_kv4_append_kernel<<<grid, KV_NT, 0, (cudaStream_t)stream>>>(m);
+    return cudaGetLastError() == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
+}
+
+int check_window(const santa_shape *sh, const void *q, const int32_t *seq_lens, int32_t window, int32_t sinks,
+                 int32_t flags, const float *out, const void *workspace, size_t workspace_bytes)
+{
+    if (!q || !seq_lens || !out || window < 0 || sinks < 0 || (flags & ~SANTA_OUT_BF16)) return SANTA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(seq_lens, 4)) return SANTA_ERR_MISALIGNED;
+    size_t need = 0;
+    const int rc = santa_window_workspace_size(sh, &need);
+    if (rc) return rc;
+    if (!workspace || workspace_bytes < need) return SANTA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SANTA_ERR_MISALIGNED;
+    return SANTA_OK;
+}
+
+template <bool KV4>
+int launch_window(const santa_shape *sh, WinParams &p, int32_t flags, void *workspace, void *stream)
+{
+    p.ctrl = static_cast<int32_t *>(workspace);
+    p.B = sh->B;
+    p.H_q = sh->H_q;
+    p.H_kv = sh->H_kv;
+    p.n_max = sh->n_max;
+    p.G = sh->H_q / sh->H_kv;
+    p.out_bf16 = (flags & SANTA_OUT_BF16) ? 1 : 0;
+    const float scale = sh->scale != 0.f ? sh->scale : (float)(1.0 / std::sqrt((double)sh->d));
+    p.k2 = (float)((double)scale * 1.4426950408889634);
+    const void *fn = sh->d == 128 ? (const void *)santa_window_kernel<128, KV4> : (const void *)santa_window_kernel<64, KV4>;
+    void *args[] = {&p};
+    if (cudaLaunchKernel(fn, dim3((unsigned)(sh->B * sh->H_q)), dim3(WN_NT), args, 0, (cudaStream_t)stream) != cudaSuccess)
+        return SANTA_ERR_CUDA;
+    return SANTA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int santa_kv4_append(const santa_shape *shape, const santa_kv4 *cache, const santa_rows *rows, int32_t T,
+                     const int32_t *pos, const int32_t *counts, void *workspace, void *stream)
+{
+    return move_rows(shape, cache, rows, T, pos, counts, workspace, stream, false);
+}
+
+int santa_kv4_read(const santa_shape *shape, const santa_kv4 *cache, const santa_rows *rows, int32_t T,
+                   const int32_t *pos, const int32_t *counts, void *workspace, void *stream)
+{
+    return move_rows(shape, cache, rows, T, pos, counts, workspace, stream, true);
+}
+
+int santa_window_workspace_size(const santa_shape *shape, size_t *bytes)
+{
+    int rc = check_shape(shape);
+    if (rc || (rc = check_groups(shape))) return rc;
+    if (!bytes) return SANTA_ERR_INVALID_ARG;
+    *bytes = CTRL_BYTES;
+    return SANTA_OK;
+}
+
+int santa_decode_window(const santa_shape *shape, const void *q, const void *k_cache, const void *v_cache,
+                        const int32_t *seq_lens, int32_t window, int32_t sinks, int32_t flags, float *out,
+                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc = check_shape(shape);
+    if (rc) return rc;
+    if (!k_cache || !v_cache) return SANTA_ERR_INVALID_ARG;
+    if ((rc = check_window(shape, q, seq_lens, window, sinks, flags, out, workspace, workspace_bytes))) return rc;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return SANTA_ERR_MISALIGNED;
+    WinParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint8_t *>(k_cache);
+    p.v = static_cast<const uint8_t *>(v_cache);
+    p.seq_lens = seq_lens;
+    p.window = window;
+    p.sinks = sinks;
+    p.out = out;
+    return launch_window<false>(shape, p, flags, workspace, stream);
+}
+
+int santa_decode_kv4(const santa_shape *shape, const void *q, const santa_kv4 *cache, const int32_t *seq_lens,
+                     int32_t window, int32_t sinks, int32_t flags, float *out, void *workspace,
+                     size_t workspace_bytes, void *stream)
+{
+    int rc = check_cache(shape, cache);
+    if (rc) return rc;
+    if ((rc = check_window(shape, q, seq_lens, window, sinks, flags, out, workspace, workspace_bytes))) return rc;
+    WinParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint8_t *>(cache->k);
+    p.v = static_cast<const uint8_t *>(cache->v);
+    p.ks = static_cast<const uint8_t *>(cache->k_scale);
+    p.vs = static_cast<const uint8_t *>(cache->v_scale);
+    p.seq_lens = seq_lens;
+    p.window = window;
+    p.sinks = sinks;
+    p.out = out;
+    return launch_window<true>(shape, p, flags, workspace, stream);
+}
+
+}  // extern "C"

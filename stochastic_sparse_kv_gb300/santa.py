@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -22,12 +23,14 @@ GROUP_DEDUP = 0x100  # or-ed into a sampling mode: V rows loaded once per KV-hea
 OUT_BF16 = 0x200     # or-ed into any mode: out is bf16 (the fp32 result rounded once)
 BERNOULLI_QK = 0x400  # or-ed into any mode: score with each head's ternary query draw
 TWO_PASS = 0x800      # or-ed into a sampling mode: never the single-pass cluster kernel
-DEV_BAD_SEQLEN, DEV_TIMEOUT = 1, 2
+DEV_BAD_SEQLEN, DEV_TIMEOUT, DEV_BAD_POSITION = 1, 2, 4
 
 # every symbol include/santa.h declares
 EXPORTS = ("santa_workspace_size", "santa_workspace_init", "santa_decode", "santa_sample_points",
            "santa_device_status", "santa_status_string", "santa_version", "santa_decode_static",
-           "santa_set_wait_limit", "santa_ternary_query", "santa_call_info", "santa_timeline_buffer")
+           "santa_set_wait_limit", "santa_ternary_query", "santa_call_info", "santa_timeline_buffer",
+           "santa_kv4_append", "santa_kv4_read", "santa_decode_kv4", "santa_decode_window",
+           "santa_window_workspace_size")
 ERR_DEVICE = -6
 ERR_SCRATCH = -7
 STATIC_SCRATCH_BYTES = 16 << 20
@@ -42,6 +45,15 @@ class SantaError(RuntimeError):
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("n_max", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _Kv4(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3)]
 
 
 _lock = threading.Lock()
@@ -87,6 +99,16 @@ def load(path: str | None = None):
         lib.santa_timeline_buffer.restype = ctypes.c_int
         lib.santa_set_wait_limit.argtypes = [u64]
         lib.santa_set_wait_limit.restype = ctypes.c_int
+        shp, kvp, rwp = ctypes.POINTER(Shape), ctypes.POINTER(_Kv4), ctypes.POINTER(_Rows)
+        for f in (lib.santa_kv4_append, lib.santa_kv4_read):
+            f.argtypes = [shp, kvp, rwp, i32, vp, vp, vp, vp]
+            f.restype = ctypes.c_int
+        lib.santa_decode_kv4.argtypes = [shp, vp, kvp, vp, i32, i32, i32, vp, vp, sz, vp]
+        lib.santa_decode_kv4.restype = ctypes.c_int
+        lib.santa_decode_window.argtypes = [shp, vp, vp, vp, vp, i32, i32, i32, vp, vp, sz, vp]
+        lib.santa_decode_window.restype = ctypes.c_int
+        lib.santa_window_workspace_size.argtypes = [shp, ctypes.POINTER(sz)]
+        lib.santa_window_workspace_size.restype = ctypes.c_int
         lib.santa_version.argtypes = []
         lib.santa_version.restype = ctypes.c_int
         _lib, _lib_path = lib, os.path.realpath(p)
@@ -271,3 +293,166 @@ def device_status(workspace: torch.Tensor | None, stream=None) -> int:
     if rc not in (OK, ERR_DEVICE):
         _check(rc, "santa_device_status")
     return int(code.value)
+
+
+# ------------------------------------------------------------------ 4-bit KV cache, windowed attention
+
+class KV4Cache(NamedTuple):
+    """A 4-bit KV cache: uint8 codes [B, H_kv, n_max, d/2] and scales [B, H_kv, n_max, d/16]
+    for K and V, contiguous on one CUDA device (the format is described in santa.h)."""
+    k: torch.Tensor
+    k_scale: torch.Tensor
+    v: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def new_kv4_cache(B: int, H_kv: int, n_max: int, d: int, device="cuda") -> KV4Cache:
+    """An empty cache (all values zero) of capacity n_max rounded up to a multiple of 16."""
+    n = -(-int(n_max) // 16) * 16
+    return KV4Cache(*(torch.zeros(B, H_kv, n, w, dtype=torch.uint8, device=device) for w in (d // 2, d // 16) * 2))
+
+
+def _cuda_bf16(t: torch.Tensor, name: str):
+    if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor")
+
+
+def _int_vector(t: torch.Tensor, name: str, B: int, dev):
+    if t.dtype != torch.int32 or t.device != dev or t.shape != (B,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on the inputs' device")
+
+
+def _kv4_dims(cache: KV4Cache):
+    """(B, H_kv, n_max, d, device) of a checked cache."""
+    k, ks, v, vs = cache
+    shape, dev = k.shape, k.device
+    if len(shape) != 4 or not k.is_cuda:
+        raise ValueError("a 4-bit cache holds CUDA tensors of four dimensions")
+    B, H_kv, n_max, half = shape
+    if v.shape != shape or ks.shape != vs.shape or ks.shape != (B, H_kv, n_max, half // 8):
+        raise ValueError("4-bit cache shapes disagree: codes [B, H_kv, n_max, d/2], scales [B, H_kv, n_max, d/16]")
+    for t in cache:
+        if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+            raise ValueError("a 4-bit cache holds contiguous uint8 tensors on one CUDA device")
+    return B, H_kv, n_max, half * 2, dev
+
+
+class _on_device:
+    """The library launches on the current device: make it the tensors' own for the call."""
+    __slots__ = ("dev", "ctx")
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __enter__(self):
+        self.ctx = None
+        if self.dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.dev)
+            self.ctx.__enter__()
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def _stream_on(stream, dev) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+
+
+def _call_workspace(nbytes: int, dev, stream) -> torch.Tensor:
+    """The workspace of a call that was given none: one per device and stream, or, inside a
+    stream capture, one of the graph's own (two graphs that share one could not be replayed
+    at the same time, and its clearing has to be part of the graph)."""
+    if torch.cuda.is_current_stream_capturing():
+        return new_workspace(nbytes, dev, stream)
+    return _cached_workspace(nbytes, dev, stream if stream is not None else torch.cuda.current_stream(dev))
+
+
+def _move_rows(fn, what: str, cache, k, v, pos, counts, workspace, stream):
+    B, H_kv, n_max, d, dev = _kv4_dims(cache)
+    for t, name in ((k, "K rows"), (v, "V rows")):
+        if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a bf16 tensor [B, T, H_kv, d] on the cache's device, contiguous in d")
+        if t.shape != (B, k.shape[1], H_kv, d):
+            raise ValueError(f"{name} [B, T, H_kv, d] and the cache's shape disagree")
+    _int_vector(pos, "pos", B, dev)
+    if counts is not None:
+        _int_vector(counts, "counts", B, dev)
+    rows = _Rows(k.data_ptr(), v.data_ptr(), k.stride()[:3], v.stride()[:3])
+    with _on_device(dev):
+        rc = fn(ctypes.byref(make_shape(B, H_kv, H_kv, d, n_max)), ctypes.byref(_Kv4(*(t.data_ptr() for t in cache))),
+                ctypes.byref(rows), k.shape[1], pos.data_ptr(), counts.data_ptr() if counts is not None else None,
+                workspace.data_ptr() if workspace is not None else None, _stream_on(stream, dev))
+    _check(rc, what)
+
+
+def kv4_append(cache: KV4Cache, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor,
+               counts: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise new rows [B, T, H_kv, d] (bf16, any strides that are multiples of 8) into the
+    cache at rows pos[b] .. pos[b] + T - 1, or only the first counts[b] of them (int32 [B]).
+    Batch rows that would leave the cache are skipped; give a `workspace` to have that
+    reported by device_status (DEV_BAD_POSITION)."""
+    if k_new.dim() == 4 and k_new.shape[1] == 0:
+        return
+    _move_rows(load().santa_kv4_append, "santa_kv4_append", cache, k_new, v_new, pos, counts, workspace, stream)
+
+
+def kv4_read(cache: KV4Cache, pos: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
+             counts: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Rows pos[b] + t of the cache into k_out, v_out [B, T, H_kv, d] (bf16, strided as for
+    kv4_append) for t < counts[b] (default T); other rows stay as they were.  Exact.  For a
+    bf16 cache [B, H_kv, n, d] pass its transpose(1, 2).  Returns (k_out, v_out)."""
+    if k_out.dim() != 4 or k_out.shape[1] != 0:
+        _move_rows(load().santa_kv4_read, "santa_kv4_read", cache, k_out, v_out, pos, counts, workspace, stream)
+    return k_out, v_out
+
+
+def _window_call(q, dims, kv_args, fn, what, seq_lens, window, sinks, scale, out, out_dtype, workspace, stream):
+    B, H_kv, n_max, d, dev = dims
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.device != dev:
+        raise ValueError("q [B, H_q, d] and the cache's shape or device disagree")
+    _int_vector(seq_lens, "seq_lens", B, dev)
+    shape = make_shape(B, q.shape[1], H_kv, d, n_max, scale)
+    n = ctypes.c_size_t(0)
+    lib = load()
+    _check(lib.santa_window_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "santa_window_workspace_size")
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        if stream is not None:
+            out.record_stream(stream)
+    if out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or out.shape != q.shape or \
+            out.device != dev:
+        raise ValueError("out must be a contiguous fp32 or bf16 [B, H_q, d] tensor on q's device")
+    with _on_device(dev):
+        ws = workspace if workspace is not None else _call_workspace(n.value, dev, stream)
+        rc = getattr(lib, fn)(ctypes.byref(shape), q.data_ptr(), *kv_args, seq_lens.data_ptr(), int(window), int(sinks),
+                              OUT_BF16 if out.dtype == torch.bfloat16 else 0, out.data_ptr(), ws.data_ptr(), ws.numel(),
+                              _stream_on(stream, dev))
+    _check(rc, what)
+    return out
+
+
+def decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_lens: torch.Tensor, window: int,
+                  sinks: int = 0, scale: float = 0.0, out: torch.Tensor | None = None,
+                  out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None, stream=None):
+    """One step of exact attention over the last `window` keys of each sequence and its first
+    `sinks` (window = 0: every key).  q [B, H_q, d], k/v [B, H_kv, n_max, d] bf16, seq_lens
+    [B] int32, all on one CUDA device.  Returns out [B, H_q, d], fp32 or bf16."""
+    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        _cuda_bf16(t, name)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.device != k_cache.device:
+        raise ValueError("k_cache and v_cache [B, H_kv, n_max, d] disagree")
+    return _window_call(q, (*k_cache.shape, k_cache.device), (k_cache.data_ptr(), v_cache.data_ptr()),
+                        "santa_decode_window", "santa_decode_window", seq_lens, window, sinks, scale, out, out_dtype,
+                        workspace, stream)
+
+
+def decode_kv4(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor, window: int = 0, sinks: int = 0,
+               scale: float = 0.0, out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+               workspace: torch.Tensor | None = None, stream=None):
+    """One step of exact attention over a 4-bit cache: every key, or with window > 0 the last
+    `window` keys and the first `sinks`.  Arguments and result as for decode_window."""
+    _cuda_bf16(q, "q")
+    dims = _kv4_dims(cache)
+    return _window_call(q, dims, (ctypes.byref(_Kv4(*(t.data_ptr() for t in cache))),), "santa_decode_kv4",
+                        "santa_decode_kv4", seq_lens, window, sinks, scale, out, out_dtype, workspace, stream)
