@@ -5,115 +5,775 @@
 //   visible(j):  j < n  and  (window == 0  or  j >= n - window  or  j < sinks)
 //
 // The decoding token is the sequence's last key.  A sequence without keys gives zeros.
+//
+// One launch.  The work is the list of all tiles of TK keys that hold a visible key, over
+// all (batch row, KV head) groups; every CTA takes one contiguous share of the list and
+// every warp of it a contiguous share of that, so any mix of lengths and windows is spread
+// evenly without a queue.  A warp streams its tiles through a ring of its own in shared
+// memory (bulk copies issued by one lane, one mbarrier a stage, no barrier between warps)
+// and keeps the group's running sums in registers:
+//
+//  * scores: mma.sync m16n8k16, A = 16 keys, B = the group's query heads as the 8 columns.
+//    The product is 8 columns wide at most, and the 4-bit cache has to pass through
+//    registers to become fp16 anyway: a tcgen05 tile (M = 128 from shared memory or TMEM)
+//    would add a store and a load of every converted value to save the MMA issue slots,
+//    16 of about 250 per 16 keys.
+//  * p = 2^(k2 s + c), with c set so that the largest p so far lies in (2^3, 2^15]: c moves
+//    only when a score exceeds the one that set it by more than 2^6, so most tiles rescale
+//    nothing, and a piece's sums are scaled by exactly 2^c.
+//  * output: A = V^T (16 of the d dimensions by 16 keys), B = p.  movmatrix turns the score
+//    accumulators into that operand in registers.
+//
+// Precision.  The result is fp32, and the tensor cores round operands to 11 (fp16) or 8
+// (bf16) bits and truncate their sums, so: 4-bit values are exact in fp16, q is bf16 times a
+// power of two, products are exact; p is split into two fp16 or three bf16 terms (22 or 24
+// bits; groups of at most 4 heads put the first two terms side by side in the 8 columns);
+// at most two MMA steps are chained before the partial sum is added in fp32 with rounding.
+//
+// Groups that one warp holds whole are finished by it.  Pieces of others meet in shared
+// memory (their CTA joins them) and, where a group spans CTAs, in the workspace: the last
+// CTA to arrive (a counter per group, left at zero) joins the pieces in the order of the
+// list, so results do not depend on timing.
 #pragma once
 
 #include "santa_kv4.cuh"
+#include "santa_sample.cuh"
+#include "santa_tcgen05.cuh"
 
 namespace santa {
 
+constexpr int WN_WARPS = 8;
+constexpr int WN_NT = WN_WARPS * 32;
+constexpr int WN_MAX_CTAS = 512;          // partial slots in the workspace
+constexpr float WN_TOP = 9.f;             // log2 of p where a new maximum puts it
+constexpr float WN_SLACK = 6.f;           // and how far above that later ones may be
+
+__host__ __device__ constexpr int win_tile(int D, bool kv4) { return kv4 || D == 64 ? 32 : 16; }
+__host__ __device__ constexpr int win_stage(int D, bool kv4)
+{
+    return kv4 ? win_tile(D, true) * (D + D / 8) : win_tile(D, false) * D * 4;
+}
+// A piece of a group's sums: fp32 o[G][D], c[8], l[8].
+__host__ __device__ constexpr int win_piece(int G, int D) { return G * D + 16; }
+
 struct WinParams {
     const uint16_t *q;            // bf16 [B][H_q][D]
-    const uint8_t *k, *v;         // bf16 rows, or 4-bit codes
+    const uint8_t *k, *v;         // 4-bit codes (a bf16 cache is read through tensor maps)
     const uint8_t *ks, *vs;       // scales of a 4-bit cache
     const int32_t *seq_lens;
     float *out;
     int32_t *ctrl;
+    float *first;                 // [WN_MAX_CTAS][WN_WARPS] pieces: a warp's first, unfinished group
+    float *part;                  // [WN_MAX_CTAS][2] pieces: a CTA's first and last unfinished groups
     int B, H_q, H_kv, n_max, G;
     int window, sinks;
     int out_bf16;
-    float k2;                     // scale * log2(e)
+    int nstages;
+    float k2_hi, k2_lo;           // |scale| * log2(e) as an unevaluated sum
+    float qsign;                  // the sign of scale
+    uint64_t wait_ns;  // limit of a stage's wait
 };
 
-constexpr int WN_NT = 256;
+struct WinSmem {
+    int ring, bar, seg, flag, wt, nb, prefix, total;
+};
 
-template <int D, bool KV4>
-__device__ __forceinline__ void load_row(const uint8_t *rows, const uint8_t *scales, size_t row, int lane, float (&x)[D / 32])
+__host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B, int ns)
 {
-    constexpr int E = D / 32;
-    if (KV4) {
-        const float s = __half2float(ue5m3_half(scales[row * (D / KV_GROUP) + lane * E / KV_GROUP]));
-        const uint8_t *c = rows + row * (D / 2) + lane * E / 2;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            uint32_t h[4];
-            e2m1_unpack8(c[i], h);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[0]));
-            x[2 * i] = f.x * s;
-            x[2 * i + 1] = f.y * s;
+    WinSmem s{};
+    int off = 0;
+    s.ring = off; off += WN_WARPS * ns * win_stage(D, kv4);
+    s.bar = off; off += WN_WARPS * ns * 8;
+    s.seg = off; off += 2 * WN_WARPS * 4;        // group index of each warp's two pieces, or -1
+    s.flag = off; off += 16;
+    s.nb = off; off += (int)align_up((size_t)B * 4, 16);
+    s.prefix = off; off += (int)align_up((size_t)(B + 1) * 4, 16);
+    s.total = off + 1024;
+    return s;
+}
+
+// ------------------------------------------------------------------ tensor-core pieces
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8x8 matrix of 16-bit elements held one row of two per lane.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack_f16(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+
+// Untiled bulk copy, global to this CTA's shared memory (16-byte aligned, multiple of 16).
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// ------------------------------------------------------------------ the list of tiles
+
+// A sequence of n keys: tiles [0, ns) cover the sinks, then tiles tw.. up to the last key.
+struct WinTiles {
+    int w0, ns, tw, cnt;
+};
+
+template <int TK>
+__device__ __forceinline__ WinTiles win_tiles(int n, int window, int sinks)
+{
+    WinTiles t;
+    t.w0 = window > 0 ? max(0, n - window) : 0;
+    t.tw = t.w0 / TK;
+    t.ns = min((min(sinks, t.w0) + TK - 1) / TK, t.tw);
+    t.cnt = n > 0 ? t.ns + (n + TK - 1) / TK - t.tw : 0;
+    return t;
+}
+
+// A group of the list: batch row, KV head, its tiles and the list index of the first.
+template <int TK>
+struct WinGroup {
+    int b, g, n, start;
+    WinTiles t;
+
+    __device__ void seek(int tile, const int *prefix, const int *nb, const WinParams &p)
+    {
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= tile) lo = mid; else hi = mid - 1;
         }
-    } else {
-        const uint32_t *r = reinterpret_cast<const uint32_t *>(rows + row * (D * 2)) + lane * E / 2;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            x[2 * i] = bf16lo_to_f32(r[i]);
-            x[2 * i + 1] = bf16hi_to_f32(r[i]);
+        b = lo;
+        n = nb[lo];
+        t = win_tiles<TK>(n, p.window, p.sinks);
+        g = (tile - prefix[lo]) / t.cnt;
+        start = prefix[lo] + g * t.cnt;
+    }
+    __device__ int end() const { return start + t.cnt; }
+    __device__ int index(const WinParams &p) const { return b * p.H_kv + g; }
+    __device__ int key0(int tile) const
+    {
+        const int i = tile - start;
+        return (i < t.ns ? i : t.tw + i - t.ns) * TK;
+    }
+    // the group that holds the tile after this one's last (there is one)
+    __device__ void next(const int *nb, const WinParams &p)
+    {
+        start += t.cnt;
+        if (++g == p.H_kv) {
+            g = 0;
+            do n = nb[++b]; while (n == 0);
+            t = win_tiles<TK>(n, p.window, p.sinks);
         }
+    }
+};
+
+// First tile of share i of n shares of a list of T tiles, and the share that holds a tile.
+__device__ __forceinline__ int win_share(int i, int n, int T) { return (int)((long long)i * T / n); }
+__device__ __forceinline__ int win_owner(int tile, int n, int T) { return (int)((((long long)tile + 1) * n - 1) / T); }
+
+__device__ __forceinline__ void win_store(const WinParams &p, size_t i, float v)
+{
+    if (p.out_bf16)
+        reinterpret_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(v);
+    else
+        p.out[i] = v;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+// WIDE: groups of 5 to 8 heads (a column each); else up to 4 heads, columns 4-7 repeat 0-3.
+template <int D, bool KV4, bool WIDE>
+__device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMap *tm_k, const CUtensorMap *tm_v)
+{
+    constexpr int TK = win_tile(D, KV4), SUB = TK / 16, STAGE = win_stage(D, KV4);
+    constexpr int MT = D / 16;   // 16-row pieces of the output, and MMA steps of a score
+    constexpr int NP = KV4 ? 2 : 3;                     // terms of p
+    constexpr int NB = WIDE ? NP : (KV4 ? 1 : 2);       // MMAs they take
+    constexpr unsigned FULL = 0xffffffffu;
+    const float NEG_INF = __int_as_float(0xff800000);
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const int NS = p.nstages;
+    const WinSmem lay = win_smem(D, KV4, p.B, NS);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    uint8_t *ring = smem + lay.ring + warp * NS * STAGE;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + lay.bar) + warp * NS;
+    int *seg = reinterpret_cast<int *>(smem + lay.seg);
+    int *flag = reinterpret_cast<int *>(smem + lay.flag);
+    int *nb = reinterpret_cast<int *>(smem + lay.nb);
+    int *prefix = reinterpret_cast<int *>(smem + lay.prefix);
+    const int PIECE = win_piece(p.G, D);
+
+    // ---- setup: checked lengths and the list's prefix, barriers
+    if (warp == 0) {
+        int run = 0;
+        bool bad = false;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int n = b < p.B ? p.seq_lens[b] : 0;
+            if (n < 0 || n > p.n_max) {
+                bad = true;
+                n = 0;
+            }
+            const int cnt = p.H_kv * win_tiles<TK>(n, p.window, p.sinks).cnt;
+            int x = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(FULL, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b < p.B) {
+                nb[b] = n;
+                prefix[b] = run + x - cnt;
+            }
+            run += __shfl_sync(FULL, x, 31);
+        }
+        if (lane == 0) prefix[p.B] = run;
+        if (bad && blockIdx.x == 0) set_dev_error(p.ctrl, DEV_BAD_SEQLEN);
+    }
+    if (lane == 0) {
+        for (int s = 0; s < NS; ++s) mbar_init(&bar[s], 1);
+        mbar_fence_init();
+        seg[2 * warp] = seg[2 * warp + 1] = -1;
+    }
+    __syncthreads();
+
+    const int T = prefix[p.B];
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)  // sequences without keys
+        if (nb[b] == 0)
+            for (int i = tid; i < p.H_q * D; i += WN_NT) win_store(p, (size_t)b * p.H_q * D + i, 0.f);
+    const int NC = min((int)gridDim.x, (T + WN_WARPS - 1) / WN_WARPS);  // CTAs with a share
+    if ((int)blockIdx.x >= NC) return;
+    const int t0 = win_share(blockIdx.x, NC, T), t1 = win_share(blockIdx.x + 1, NC, T);
+    const int ta = t0 + win_share(warp, WN_WARPS, t1 - t0), tb = t0 + win_share(warp + 1, WN_WARPS, t1 - t0);
+
+    if (ta < tb) {
+        const uint64_t policy = l2_policy_evict_first();
+        // ---- the copies: `ig` is the group of the next tile to fetch
+        WinGroup<TK> ig;
+        ig.seek(ta, prefix, nb, p);
+        WinGroup<TK> cg = ig;
+        int it = ta, is = 0, cs = 0;
+        uint32_t cphase = 0;
+        auto fetch = [&]() {
+            if (it == ig.end()) ig.next(nb, p);
+            if (lane == 0) {
+                uint8_t *st = ring + is * STAGE;
+                const int k0 = ig.key0(it);
+                if (KV4) {
+                    const int rows = min(TK, p.n_max - k0);  // 16 or 32: n_max is a multiple of 16
+                    const size_t row = (size_t)ig.index(p) * p.n_max + k0;
+                    mbar_arrive_tx(&bar[is], (uint32_t)(rows * (D + D / 8)));
+                    bulk_load(st, p.k + row * (D / 2), rows * (D / 2), &bar[is], policy);
+                    bulk_load(st + TK * D, p.ks + row * (D / 16), rows * (D / 16), &bar[is], policy);
+                    bulk_load(st + TK * (D / 2), p.v + row * (D / 2), rows * (D / 2), &bar[is], policy);
+                    bulk_load(st + TK * (D + D / 16), p.vs + row * (D / 16), rows * (D / 16), &bar[is], policy);
+                } else {
+                    // whole boxes: rows past the group's last key are other keys or zeros, never used
+                    const int row = ig.index(p) * p.n_max + k0;
+                    mbar_arrive_tx(&bar[is], (uint32_t)STAGE);
+#pragma unroll
+                    for (int hf = 0; hf < D / 64; ++hf) {
+                        tma_load_2d(st + hf * TK * 128, tm_k, hf * 64, row, &bar[is], policy);
+                        tma_load_2d(st + TK * D * 2 + hf * TK * 128, tm_v, hf * 64, row, &bar[is], policy);
+                    }
+                }
+            }
+            ++it;
+            is = is + 1 == NS ? 0 : is + 1;
+        };
+        for (int i = 0; i < NS && it < tb; ++i) fetch();
+
+        // ---- the sums
+        uint32_t qf[MT][2];                  // B operand of the scores: head column r
+        float o[MT][4];                      // columns 2c, 2c+1 of output rows r, r+8 of each piece
+        float l0 = 0.f, l1 = 0.f, c0 = 0.f, c1 = 0.f, thr0 = NEG_INF, thr1 = NEG_INF;
+        float ka0 = p.k2_hi, ka1 = p.k2_hi, kb0 = p.k2_lo, kb1 = p.k2_lo;
+        bool dead = false;
+        for (int t = ta; t < tb; ++t) {
+            if (t == ta || t == cg.start) {
+                // a group begins: its queries (zero in columns without a head), empty sums
+                const int h = WIDE ? r : (r & 3);
+                const uint16_t *qh = p.q + ((size_t)cg.b * p.H_q + cg.g * p.G + h) * D;
+                const bool live = h < p.G;
+                if (KV4) {
+                    // lane c holds dimensions D/4 c .. of head r: step t takes 4 of them; scaled
+                    // by the power of two that puts the head's largest near 2^14
+                    float x[MT * 4];
+                    float big = 0.f;
+#pragma unroll
+                    for (int i = 0; i < MT / 2; ++i) {
+                        const uint4 w = live ? reinterpret_cast<const uint4 *>(qh + (D / 4) * c)[i] : make_uint4(0, 0, 0, 0);
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            x[8 * i + 2 * j] = bf16lo_to_f32(u[j]);
+                            x[8 * i + 2 * j + 1] = bf16hi_to_f32(u[j]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT * 4; ++i) big = fmaxf(big, fabsf(x[i]));
+                    big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
+                    big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
+                    const int e = max(-100, min(127, (int)(__float_as_uint(big) >> 23) - 127)) - 14;
+                    const float up = p.qsign * exp2i(-e);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        qf[i][0] = pack_f16(x[4 * i] * up, x[4 * i + 1] * up);
+                        qf[i][1] = pack_f16(x[4 * i + 2] * up, x[4 * i + 3] * up);
+                    }
+                    const int h0 = WIDE ? 2 * c : (2 * c) & 3;  // heads of this lane's columns
+                    const float d0 = exp2i(__shfl_sync(FULL, e, h0 * 4)), d1 = exp2i(__shfl_sync(FULL, e, h0 * 4 + 4));
+                    ka0 = p.k2_hi * d0;
+                    kb0 = p.k2_lo * d0;
+                    ka1 = p.k2_hi * d1;
+                    kb1 = p.k2_lo * d1;
+                } else {
+                    // lane c holds dimensions 16 c .. of each 64: step (half, u, w) takes 4 of them
+                    const uint32_t flip = p.qsign < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+                    for (int i = 0; i < MT / 2; ++i) {
+                        const uint4 w = live ? reinterpret_cast<const uint4 *>(qh + (i / 2) * 64 + 16 * c)[i & 1] : make_uint4(0, 0, 0, 0);
+                        qf[2 * i][0] = w.x ^ flip;
+                        qf[2 * i][1] = w.y ^ flip;
+                        qf[2 * i + 1][0] = w.z ^ flip;
+                        qf[2 * i + 1][1] = w.w ^ flip;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+                l0 = l1 = c0 = c1 = 0.f;
+                thr0 = thr1 = NEG_INF;
+            }
+            if (!dead && !__all_sync(FULL, mbar_wait_bounded(&bar[cs], cphase, p.wait_ns))) {
+                // no more copies, no more sums (the pieces still meet): those in flight end first
+                dead = true;
+                if (lane == 0) set_dev_error(p.ctrl, DEV_TIMEOUT);
+                int s2 = cs;
+                uint32_t ph = cphase;
+                for (int x = t; x < it; ++x) {
+                    mbar_wait_bounded(&bar[s2], ph, DRAIN_NS);
+                    s2 = s2 + 1 == NS ? 0 : s2 + 1;
+                    if (s2 == 0) ph ^= 1u;
+                }
+            }
+            if (!dead) {
+                const uint8_t *st = ring + cs * STAGE;
+                const int k0 = cg.key0(t);
+                // every key of the tile visible: no masks
+                const bool whole = (k0 >= cg.t.w0 || k0 + TK <= p.sinks) && k0 + TK <= cg.n;
+                auto seen = [&](int j) { return j < cg.n && (j >= cg.t.w0 || j < p.sinks); };
+
+                // ---- scores of keys r, r+8 of each 16, columns 2c, 2c+1
+                float s[SUB][4];
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    float acc[MT / 2][4];
+#pragma unroll
+                    for (int i = 0; i < MT / 2; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+                    if (KV4) {
+                        uint32_t a[2][MT][2];  // rows r, r+8: per step two fp16 pairs
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int kr = 16 * u + r + 8 * y;
+                            uint32_t w[D / 32];
+                            uint32_t sc[2];
+                            if (D == 128) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(st + kr * 64 + c * 16);
+                                w[0] = x.x, w[1] = x.y, w[D / 32 - 2] = x.z, w[D / 32 - 1] = x.w;
+                                const uint32_t b2 = *reinterpret_cast<const uint16_t *>(st + TK * D + kr * 8 + 2 * c);
+                                sc[0] = __byte_perm(b2, 0, 0x4040) << 7;
+                                sc[1] = __byte_perm(b2, 0, 0x4141) << 7;
+                            } else {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(st + kr * 32 + c * 8);
+                                w[0] = x.x, w[1] = x.y;
+                                sc[0] = sc[1] = (uint32_t)st[TK * D + kr * 4 + c] * 0x00800080u;
+                            }
+#pragma unroll
+                            for (int j = 0; j < D / 32; ++j) {
+                                uint32_t h[4];
+                                e2m1_unpack8(w[j], h);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) a[y][2 * j + i / 2][i & 1] = h2mul(h[i], sc[j / 2]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+                            mma_f16(acc[i / 2], a[0][i][0], a[1][i][0], a[0][i][1], a[1][i][1], qf[i][0], qf[i][1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < MT / 2; ++i) {  // piece i & 1 of the lane's 16 dimensions of half i / 2
+                            const uint8_t *kt = st + (i / 2) * TK * 128;
+                            const int pc = 2 * c + (i & 1), kr = 16 * u + r;
+                            const uint4 x = *reinterpret_cast<const uint4 *>(kt + kr * 128 + ((pc ^ r) << 4));
+                            const uint4 y = *reinterpret_cast<const uint4 *>(kt + (kr + 8) * 128 + ((pc ^ r) << 4));
+                            mma_bf16(acc[i], x.x, y.x, x.y, y.y, qf[2 * i][0], qf[2 * i][1]);
+                            mma_bf16(acc[i], x.z, y.z, x.w, y.w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x[MT / 2];
+#pragma unroll
+                        for (int i = 0; i < MT / 2; ++i) x[i] = acc[i][e];
+                        s[u][e] = MT == 8 ? (x[0] + x[1]) + (x[MT / 2 - 2] + x[MT / 2 - 1]) : x[0] + x[1];
+                    }
+                    if (!whole) {
+                        const int ja = k0 + 16 * u + r, jb = ja + 8;
+                        if (!seen(ja)) s[u][0] = s[u][1] = NEG_INF;
+                        if (!seen(jb)) s[u][2] = s[u][3] = NEG_INF;
+                    }
+                }
+
+                // ---- a new maximum, when it is far above the one that set c
+                float x0 = NEG_INF, x1 = NEG_INF;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    x0 = fmaxf(x0, fmaxf(s[u][0], s[u][2]));
+                    x1 = fmaxf(x1, fmaxf(s[u][1], s[u][3]));
+                }
+                if (__any_sync(FULL, x0 > thr0 || x1 > thr1)) {
+#pragma unroll
+                    for (int m = 4; m <= 16; m <<= 1) {
+                        x0 = fmaxf(x0, __shfl_xor_sync(FULL, x0, m));
+                        x1 = fmaxf(x1, __shfl_xor_sync(FULL, x1, m));
+                    }
+                    float f0 = 1.f, f1 = 1.f;
+                    if (x0 > thr0) {
+                        const float cn = fmaf(-x0, ka0, WN_TOP);
+                        f0 = ex2(fminf(cn - c0, 0.f));  // (of empty sums c is not yet set)
+                        c0 = cn;
+                        thr0 = x0 + WN_SLACK / ka0;
+                    }
+                    if (x1 > thr1) {
+                        const float cn = fmaf(-x1, ka1, WN_TOP);
+                        f1 = ex2(fminf(cn - c1, 0.f));
+                        c1 = cn;
+                        thr1 = x1 + WN_SLACK / ka1;
+                    }
+                    l0 *= f0;
+                    l1 *= f1;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        o[i][0] *= f0;
+                        o[i][1] *= f1;
+                        o[i][2] *= f0;
+                        o[i][3] *= f1;
+                    }
+                }
+
+                // ---- p, its sum, and its terms as the B operand of V^T p
+                uint32_t pb[SUB][NB][2];
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float a = ex2(fmaf(s[u][2 * y], kb0, fmaf(s[u][2 * y], ka0, c0)));
+                        float b = ex2(fmaf(s[u][2 * y + 1], kb1, fmaf(s[u][2 * y + 1], ka1, c1)));
+                        if (!whole && !seen(k0 + 16 * u + r + 8 * y)) a = b = 0.f;
+                        l0 += a;
+                        l1 += b;
+                        uint32_t term[NP];
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) {
+                            if (KV4) {
+                                term[i] = pack_f16(a, b);
+                                const float2 f = unpack_f16(term[i]);
+                                a -= f.x;
+                                b -= f.y;
+                            } else {
+                                term[i] = pack_bf16(a, b);
+                                a -= bf16lo_to_f32(term[i]);
+                                b -= bf16hi_to_f32(term[i]);
+                            }
+                        }
+                        if (WIDE) {
+#pragma unroll
+                            for (int i = 0; i < NP; ++i) pb[u][i % NB][y] = movmatrix(term[i]);
+                        } else {
+                            pb[u][0][y] = movmatrix(c < 2 ? term[0] : term[1]);
+                            if (!KV4) pb[u][NB - 1][y] = movmatrix(c < 2 ? term[NP - 1] : 0u);
+                        }
+                    }
+
+                // ---- o += V^T p, the tile's keys in one chain per piece
+                if (KV4) {
+                    const uint8_t *vt = st + TK * (D / 2), *vsc = st + TK * (D + D / 16);
+                    constexpr int RB = D / 2, W = D / 64;  // bytes of a row; words of a lane's D/8 dimensions
+                    uint32_t vw[SUB][4][W], sp[SUB][2];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        uint32_t sb[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int kk = 16 * u + 2 * c + (i & 1) + 8 * (i >> 1);
+                            if (W == 2) {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(vt + kk * RB + r * 8);
+                                vw[u][i][0] = x.x, vw[u][i][W - 1] = x.y;
+                            } else {
+                                vw[u][i][0] = *reinterpret_cast<const uint32_t *>(vt + kk * RB + r * 4);
+                            }
+                            sb[i] = vsc[kk * (D / 16) + (D == 128 ? r : r >> 1)];
+                            if (!whole && !seen(k0 + kk)) sb[i] = 0;  // what is not seen may be a NaN
+                        }
+                        sp[u][0] = (sb[0] | (sb[1] << 16)) << 7;
+                        sp[u][1] = (sb[2] | (sb[3] << 16)) << 7;
+                    }
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        float acc[4][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            uint32_t a[2][2][4];  // key pair, even or odd dimension, byte
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t x0w = vw[u][2 * y][w], x1w = vw[u][2 * y + 1][w];
+                                e2m1_unpack8((x0w & 0x0f0f0f0fu) | ((x1w << 4) & 0xf0f0f0f0u), a[y][0]);
+                                e2m1_unpack8(((x0w >> 4) & 0x0f0f0f0fu) | (x1w & 0xf0f0f0f0u), a[y][1]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    a[y][0][i] = h2mul(a[y][0][i], sp[u][y]);
+                                    a[y][1][i] = h2mul(a[y][1][i], sp[u][y]);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int n = 0; n < NB; ++n)
+                                    mma_f16(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[4 * w + i][e] += acc[i][e];
+                    }
+                } else {
+                    const uint32_t vt = smem_u32(st + TK * D * 2);
+                    uint32_t mk[SUB][2];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int j = k0 + 16 * u + 2 * c + 8 * y;
+                            mk[u][y] = whole ? 0xffffffffu : (seen(j) ? 0xffffu : 0u) | (seen(j + 1) ? 0xffff0000u : 0u);
+                        }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            // matrices: keys 0-7 and 8-15 by dimensions 0-7 and 8-15 of piece i
+                            const int kk = 16 * u + (lane & 7) + ((lane >> 4) << 3);
+                            const int pc = 2 * (i & 3) + ((lane >> 3) & 1);
+                            uint32_t a[4];
+                            ldmatrix_x4_trans(a, vt + (uint32_t)((i / 4) * TK * 128 + kk * 128 + ((pc ^ (kk & 7)) << 4)));
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+                                mma_bf16(acc, a[0] & mk[u][0], a[1] & mk[u][0], a[2] & mk[u][1], a[3] & mk[u][1], pb[u][n][0], pb[u][n][1]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][e] += acc[e];
+                    }
+                }
+            }
+            __syncwarp();
+            cs = cs + 1 == NS ? 0 : cs + 1;
+            if (cs == 0) cphase ^= 1u;
+            if (!dead && it < tb) fetch();
+            if (t + 1 != cg.end() && t + 1 != tb) continue;
+
+            // ---- the group's last tile here: its result, or a piece of it
+            // sums that no score has set c for are empty (or NaN): they weigh nothing
+            if (thr0 == NEG_INF) c0 = -NEG_INF;
+            if (thr1 == NEG_INF) c1 = -NEG_INF;
+#pragma unroll
+            for (int m = 4; m <= 16; m <<= 1) {
+                l0 += __shfl_xor_sync(FULL, l0, m);
+                l1 += __shfl_xor_sync(FULL, l1, m);
+            }
+            const bool all = ta <= cg.start && cg.end() <= tb;
+            const int slot = t + 1 == tb ? 1 : 0;  // the warp's last group, else its first
+            float *piece = slot ? reinterpret_cast<float *>(ring)
+                                : p.first + (size_t)(blockIdx.x * WN_WARPS + warp) * PIECE;
+            const size_t orow = (size_t)cg.b * p.H_q + cg.g * p.G;
+            // heads of the lane's values: x of column 2c (and y of 2c+1 in wide groups)
+            const int hx = WIDE ? 2 * c : 2 * (c & 1) + (c >> 1);
+            const float lx = WIDE || c < 2 ? l0 : l1, cx = WIDE || c < 2 ? c0 : c1;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int dim = KV4 ? (D / 8) * r + 2 * i + y : 16 * i + 8 * y + r;
+                    float x = o[i][2 * y], z = o[i][2 * y + 1];
+                    if (!WIDE) {  // columns j and j + 4 hold terms of the same head: lanes c, c ^ 2
+                        const float got = __shfl_xor_sync(FULL, c < 2 ? z : x, 2);
+                        x = (c < 2 ? x : z) + got;
+                    }
+                    if (hx < p.G) {
+                        if (all) win_store(p, (orow + hx) * D + dim, x / lx);
+                        else piece[hx * D + dim] = x;
+                    }
+                    if (WIDE && hx + 1 < p.G) {
+                        if (all) win_store(p, (orow + hx + 1) * D + dim, z / l1);
+                        else piece[(hx + 1) * D + dim] = z;
+                    }
+                }
+            if (!all) {
+                if (r == 0 && hx < p.G) {
+                    piece[p.G * D + hx] = cx;
+                    piece[p.G * D + 8 + hx] = lx;
+                    if (WIDE && hx + 1 < p.G) {
+                        piece[p.G * D + hx + 1] = c1;
+                        piece[p.G * D + 8 + hx + 1] = l1;
+                    }
+                }
+                if (lane == 0) seg[2 * warp + slot] = cg.index(p);
+            }
+            if (t + 1 < tb) cg.next(nb, p);
+        }
+    }
+    __syncthreads();  // (also makes the pieces in the workspace visible to the CTA)
+
+    // ---- join the CTA's pieces group by group, in the order of the list
+    auto piece_of = [&](int i) -> const float * {
+        return (i & 1) ? reinterpret_cast<const float *>(smem + lay.ring + (i >> 1) * NS * STAGE)
+                       : p.first + (size_t)(blockIdx.x * WN_WARPS + (i >> 1)) * PIECE;
+    };
+    for (int i = 0; i < 2 * WN_WARPS;) {
+        const int gi = seg[i];
+        if (gi < 0) {
+            ++i;
+            continue;
+        }
+        int e = i + 1;  // pieces of group gi lie in [i, e)
+        for (int x = i + 1; x < 2 * WN_WARPS; ++x)
+            if (seg[x] == gi) e = x + 1;
+        const int b = gi / p.H_kv, g = gi % p.H_kv;
+        const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
+        const int start = prefix[b] + g * cnt;
+        const bool all = t0 <= start && start + cnt <= t1;
+        float *part = p.part + (size_t)(2 * blockIdx.x + (t0 >= start ? 0 : 1)) * PIECE;
+        const size_t orow = (size_t)b * p.H_q + g * p.G;
+        for (int x = tid; x < p.G * D; x += WN_NT) {
+            const int h = x / D;
+            float C = __int_as_float(0x7f800000);
+            for (int j = i; j < e; ++j)
+                if (seg[j] == gi) C = fminf(C, piece_of(j)[p.G * D + h]);
+            float O = 0.f, L = 0.f;
+            for (int j = i; j < e; ++j)
+                if (seg[j] == gi) {
+                    const float *pc = piece_of(j);
+                    const float f = ex2(C - pc[p.G * D + h]);
+                    O = fmaf(f, pc[x], O);
+                    L = fmaf(f, pc[p.G * D + 8 + h], L);
+                }
+            if (all) {
+                win_store(p, orow * D + x, O / L);
+            } else {
+                part[x] = O;
+                if (x % D == 0) {
+                    part[p.G * D + h] = C;
+                    part[p.G * D + 8 + h] = L;
+                }
+            }
+        }
+        if (!all) {
+            const int ca = win_owner(start, NC, T), cb = win_owner(start + cnt - 1, NC, T);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int old = atomicAdd(p.ctrl + CTRL_GROUPS + gi, 1);
+                *flag = old == cb - ca;
+                if (old == cb - ca) p.ctrl[CTRL_GROUPS + gi] = 0;
+            }
+            __syncthreads();
+            if (*flag) {
+                __threadfence();
+                auto part_of = [&](int cta) {
+                    return p.part + (size_t)(2 * cta + (win_share(cta, NC, T) >= start ? 0 : 1)) * PIECE;
+                };
+                for (int x = tid; x < p.G * D; x += WN_NT) {
+                    const int h = x / D;
+                    float C = __int_as_float(0x7f800000);
+                    for (int j = ca; j <= cb; ++j) C = fminf(C, __ldcg(part_of(j) + p.G * D + h));
+                    float O = 0.f, L = 0.f;
+                    for (int j = ca; j <= cb; ++j) {
+                        const float *pc = part_of(j);
+                        const float f = ex2(C - __ldcg(pc + p.G * D + h));
+                        O = fmaf(f, __ldcg(pc + x), O);
+                        L = fmaf(f, __ldcg(pc + p.G * D + 8 + h), L);
+                    }
+                    win_store(p, orow * D + x, O / L);
+                }
+            }
+            __syncthreads();
+        }
+        i = e;
     }
 }
 
-// One CTA per (batch row, query head); its warps take alternate visible keys and join their
-// (maximum, sum, output) through shared memory.
-template <int D, bool KV4>
-__global__ void __launch_bounds__(WN_NT) santa_window_kernel(const WinParams p)
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(WN_NT, 2) santa_window_kv4_kernel(const WinParams p)
 {
-    constexpr int E = D / 32, NW = WN_NT / 32;
-    __shared__ float sm[NW], sl[NW], so[NW][D];
-    const int b = blockIdx.x / p.H_q, h = blockIdx.x % p.H_q, g = h / p.G;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int n = p.seq_lens[b];
-    if (n < 0 || n > p.n_max) {
-        if (threadIdx.x == 0 && h == 0) set_dev_error(p.ctrl, DEV_BAD_SEQLEN);
-        n = 0;
-    }
-    const int w0 = p.window > 0 ? max(0, n - p.window) : 0;
-    const int se = min(p.sinks, w0);
-    const int nv = se + n - w0;
-    float q[E], o[E] = {};
-    const uint16_t *qh = p.q + ((size_t)b * p.H_q + h) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = __uint_as_float((uint32_t)qh[e] << 16);
-    float m = __int_as_float(0xff800000), l = 0.f;
-    for (int i = warp; i < nv; i += NW) {
-        const size_t row = ((size_t)b * p.H_kv + g) * p.n_max + (size_t)(i < se ? i : w0 + i - se);
-        float k[E], v[E];
-        load_row<D, KV4>(p.k, p.ks, row, lane, k);
-        load_row<D, KV4>(p.v, p.vs, row, lane, v);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.k2;
-        const float mn = fmaxf(m, s);
-        const float f = m == mn ? 1.f : exp2f(m - mn), w = exp2f(s - mn);
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e] * f);
-        m = mn;
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float M = sm[0];
-        for (int w = 1; w < NW; ++w) M = fmaxf(M, sm[w]);
-        float L = 0.f, O = 0.f;
-        for (int w = 0; w < NW; ++w) {
-            const float f = sm[w] == M ? 1.f : exp2f(sm[w] - M);
-            L = fmaf(f, sl[w], L);
-            O = fmaf(f, so[w][threadIdx.x], O);
-        }
-        const float r = nv > 0 ? O / L : 0.f;
-        const size_t i = ((size_t)b * p.H_q + h) * D + threadIdx.x;
-        if (p.out_bf16)
-            reinterpret_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(r);
-        else
-            p.out[i] = r;
-    }
+    window_body<D, true, WIDE>(p, nullptr, nullptr);
+}
+
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(WN_NT, 1)
+    santa_window_bf16_kernel(const WinParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v)
+{
+    window_body<D, false, WIDE>(p, &tm_k, &tm_v);
 }
 
 }  // namespace santa

@@ -1,5 +1,6 @@
 // santa_window_api.cu -- the entry points of the 4-bit KV cache and of windowed decode
 // attention (declared in include/santa.h): argument checks and launches.
+#include <algorithm>
 #include <cmath>
 #include <utility>
 
@@ -99,21 +100,75 @@ int check_window(const santa_shape *sh, const void *q, const int32_t *seq_lens, 
     return SANTA_OK;
 }
 
-template <bool KV4>
-int launch_window(const santa_shape *sh, WinParams &p, int32_t flags, void *workspace, void *stream)
+// CTAs that can hold a share of the shape's tiles: the workspace has pieces for as many.
+long long window_ctas(const santa_shape *sh)
 {
-    p.ctrl = static_cast<int32_t *>(workspace);
+    const long long tiles = (long long)sh->B * sh->H_kv * ((sh->n_max + 15) / 16);
+    return std::min<long long>(WN_MAX_CTAS, (tiles + WN_WARPS - 1) / WN_WARPS);
+}
+
+const void *window_kernel(int D, bool kv4, bool wide)
+{
+    switch ((D == 128) * 4 + kv4 * 2 + wide) {
+    case 0: return (const void *)santa_window_bf16_kernel<64, false>;
+    case 1: return (const void *)santa_window_bf16_kernel<64, true>;
+    case 2: return (const void *)santa_window_kv4_kernel<64, false>;
+    case 3: return (const void *)santa_window_kv4_kernel<64, true>;
+    case 4: return (const void *)santa_window_bf16_kernel<128, false>;
+    case 5: return (const void *)santa_window_bf16_kernel<128, true>;
+    case 6: return (const void *)santa_window_kv4_kernel<128, false>;
+    default: return (const void *)santa_window_kv4_kernel<128, true>;
+    }
+}
+
+// bf16: k and v are the caches.  4-bit: p.k, p.ks, p.v and p.vs are set.
+int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void *v, int32_t flags, void *workspace,
+                  void *stream)
+{
+    const bool kv4 = k == nullptr;
+    const int D = sh->d, G = sh->H_q / sh->H_kv;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const long long cap = window_ctas(sh);
+    p.ctrl = reinterpret_cast<int32_t *>(ws);
+    p.first = reinterpret_cast<float *>(ws + CTRL_BYTES);
+    p.part = p.first + (size_t)cap * WN_WARPS * win_piece(G, D);
     p.B = sh->B;
     p.H_q = sh->H_q;
     p.H_kv = sh->H_kv;
     p.n_max = sh->n_max;
-    p.G = sh->H_q / sh->H_kv;
+    p.G = G;
     p.out_bf16 = (flags & SANTA_OUT_BF16) ? 1 : 0;
-    const float scale = sh->scale != 0.f ? sh->scale : (float)(1.0 / std::sqrt((double)sh->d));
-    p.k2 = (float)((double)scale * 1.4426950408889634);
-    const void *fn = sh->d == 128 ? (const void *)santa_window_kernel<128, KV4> : (const void *)santa_window_kernel<64, KV4>;
-    void *args[] = {&p};
-    if (cudaLaunchKernel(fn, dim3((unsigned)(sh->B * sh->H_q)), dim3(WN_NT), args, 0, (cudaStream_t)stream) != cudaSuccess)
+    const float scale = sh->scale != 0.f ? sh->scale : (float)(1.0 / std::sqrt((double)D));
+    const double k2 = std::fabs((double)scale) * 1.4426950408889634;
+    p.k2_hi = (float)k2;
+    p.k2_lo = (float)(k2 - (double)p.k2_hi);
+    p.qsign = scale < 0.f ? -1.f : 1.f;
+    p.wait_ns = wait_limit_ns();
+
+    int dev, sms, optin, rc;
+    if ((rc = device_info(&dev, &sms, &optin))) return rc;
+    // 4-bit: two CTAs to an SM (their registers and rings share it); bf16: one with the whole ring
+    const int room = kv4 ? (optin + 1024) / 2 - 1024 : optin;
+    p.nstages = 8;
+    while (p.nstages > 2 && win_smem(D, kv4, sh->B, p.nstages).total > room) --p.nstages;
+    const int smem = win_smem(D, kv4, sh->B, p.nstages).total;
+    if (smem > optin) return SANTA_ERR_UNSUPPORTED;
+    const void *fn = window_kernel(D, kv4, G > 4);
+    int occ = 0;
+    if ((rc = prepare_fn(fn, dev, smem, WN_NT, &occ))) return rc;
+    const int tile = win_tile(D, kv4);
+    const int most = p.window > 0 ? (int)std::min<long long>(sh->n_max, (long long)p.window + p.sinks) : sh->n_max;
+    // a group's visible keys touch at most two tiles more than they would fill
+    const long long tiles = (long long)sh->B * sh->H_kv * ((most + tile - 1) / tile + 2);
+    const long long grid = std::min(std::min<long long>(cap, (long long)sms * occ), (tiles + WN_WARPS - 1) / WN_WARPS);
+    CUtensorMap tm_k, tm_v;
+    if (!kv4) {
+        const long long rows = (long long)sh->B * sh->H_kv * sh->n_max;
+        if ((rc = make_map_bf16(&tm_k, k, D, rows, tile))) return rc;
+        if ((rc = make_map_bf16(&tm_v, v, D, rows, tile))) return rc;
+    }
+    void *args[] = {&p, &tm_k, &tm_v};
+    if (cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(WN_NT), args, (size_t)smem, (cudaStream_t)stream) != cudaSuccess)
         return SANTA_ERR_CUDA;
     return SANTA_OK;
 }
@@ -139,7 +194,8 @@ int santa_window_workspace_size(const santa_shape *shape, size_t *bytes)
     int rc = check_shape(shape);
     if (rc || (rc = check_groups(shape))) return rc;
     if (!bytes) return SANTA_ERR_INVALID_ARG;
-    *bytes = CTRL_BYTES;
+    const size_t piece = (size_t)win_piece(shape->H_q / shape->H_kv, shape->d) * sizeof(float);
+    *bytes = align_up(CTRL_BYTES + (size_t)window_ctas(shape) * (WN_WARPS + 2) * piece, 256);
     return SANTA_OK;
 }
 
@@ -154,13 +210,11 @@ int santa_decode_window(const santa_shape *shape, const void *q, const void *k_c
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return SANTA_ERR_MISALIGNED;
     WinParams p{};
     p.q = static_cast<const uint16_t *>(q);
-    p.k = static_cast<const uint8_t *>(k_cache);
-    p.v = static_cast<const uint8_t *>(v_cache);
     p.seq_lens = seq_lens;
     p.window = window;
     p.sinks = sinks;
     p.out = out;
-    return launch_window<false>(shape, p, flags, workspace, stream);
+    return launch_window(shape, p, k_cache, v_cache, flags, workspace, stream);
 }
 
 int santa_decode_kv4(const santa_shape *shape, const void *q, const santa_kv4 *cache, const int32_t *seq_lens,
@@ -180,7 +234,7 @@ int santa_decode_kv4(const santa_shape *shape, const void *q, const santa_kv4 *c
     p.window = window;
     p.sinks = sinks;
     p.out = out;
-    return launch_window<true>(shape, p, flags, workspace, stream);
+    return launch_window(shape, p, nullptr, nullptr, flags, workspace, stream);
 }
 
 }  // extern "C"
