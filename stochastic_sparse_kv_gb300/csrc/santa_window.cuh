@@ -75,7 +75,7 @@ struct WinParams {
 };
 
 struct WinSmem {
-    int ring, bar, seg, flag, wt, nb, prefix, total;
+    int ring, bar, seg, flag, nb, prefix, total;
 };
 
 __host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B, int ns)
@@ -225,6 +225,93 @@ __device__ __forceinline__ void win_store(const WinParams &p, size_t i, float v)
         reinterpret_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(v);
     else
         p.out[i] = v;
+}
+
+// The whole CTA: the n pieces of group gi joined into `part` (a piece) or, when that is null,
+// into the output.  scratch: 16 n + 16 floats; red: WN_NT float4.  Begins and ends with
+// the scratch free.  FAR: the pieces lie in the workspace, written by other CTAs too, and
+// are read past the L1 cache; else in shared memory or the workspace, written by this CTA.
+template <int D, bool FAR, class F>
+__device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, float *scratch, float *red, int gi, float *part)
+{
+    constexpr unsigned FULL = 0xffffffffu;
+    const int tid = threadIdx.x, lane = tid & 31, h = tid >> 5, GD = p.G * D;
+    float *tot = scratch, *wt = scratch + 16, *lt = wt + 8 * n;
+    auto load = [](const float *a) { return FAR ? __ldcg(a) : *a; };
+    auto load4 = [](const float4 *a) { return FAR ? __ldcg(a) : *a; };
+    // warp h: head h's common exponent, the pieces' weights, the sum
+    if (h < p.G) {
+        float C = __int_as_float(0x7f800000);
+        for (int j = lane; j < n; j += 32) {
+            const float *pc = piece_of(j) + GD + h;
+            const float c = load(pc);
+            wt[8 * j + h] = c;
+            lt[8 * j + h] = load(pc + 8);
+            C = fminf(C, c);
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) C = fminf(C, __shfl_xor_sync(FULL, C, m));
+        float L = 0.f;
+        for (int j = lane; j < n; j += 32) {
+            const float w = ex2(C - wt[8 * j + h]);
+            wt[8 * j + h] = w;
+            L = fmaf(w, lt[8 * j + h], L);
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(FULL, L, m);
+        if (lane == 0) {
+            tot[h] = C;
+            tot[8 + h] = L;
+        }
+    }
+    __syncthreads();
+    // four outputs a thread; with fewer than WN_NT of those, slices of the pieces
+    const int nv = GD / 4, ns = WN_NT / nv, v = tid % nv, sl = tid / nv, hv = 4 * v / D;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (sl < ns) {
+#pragma unroll 8
+        for (int j = sl; j < n; j += ns) {
+            const float4 x = load4(reinterpret_cast<const float4 *>(piece_of(j)) + v);
+            const float w = wt[8 * j + hv];
+            o.x = fmaf(w, x.x, o.x);
+            o.y = fmaf(w, x.y, o.y);
+            o.z = fmaf(w, x.z, o.z);
+            o.w = fmaf(w, x.w, o.w);
+        }
+    }
+    if (ns > 1) {
+        reinterpret_cast<float4 *>(red)[tid] = o;
+        __syncthreads();
+        if (sl == 0)
+            for (int s = 1; s < ns; ++s) {
+                const float4 x = reinterpret_cast<const float4 *>(red)[s * nv + v];
+                o.x += x.x;
+                o.y += x.y;
+                o.z += x.z;
+                o.w += x.w;
+            }
+    }
+    if (sl == 0) {
+        if (part) {
+            reinterpret_cast<float4 *>(part)[v] = o;
+            if (v % (D / 4) == 0) {
+                part[GD + hv] = tot[hv];
+                part[GD + 8 + hv] = tot[8 + hv];
+            }
+        } else {
+            const float L = tot[8 + hv];
+            const size_t at = ((size_t)(gi / p.H_kv) * p.H_q + (size_t)(gi % p.H_kv) * p.G) * D + 4 * (size_t)v;
+            o = make_float4(o.x / L, o.y / L, o.z / L, o.w / L);
+            if (p.out_bf16) {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+                *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + at) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+            } else {
+                *reinterpret_cast<float4 *>(p.out + at) = o;
+            }
+        }
+    }
+    __syncthreads();
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -685,81 +772,67 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     }
     __syncthreads();  // (also makes the pieces in the workspace visible to the CTA)
 
-    // ---- join the CTA's pieces group by group, in the order of the list
-    auto piece_of = [&](int i) -> const float * {
-        return (i & 1) ? reinterpret_cast<const float *>(smem + lay.ring + (i >> 1) * NS * STAGE)
-                       : p.first + (size_t)(blockIdx.x * WN_WARPS + (i >> 1)) * PIECE;
-    };
-    for (int i = 0; i < 2 * WN_WARPS;) {
-        const int gi = seg[i];
-        if (gi < 0) {
-            ++i;
-            continue;
-        }
-        int e = i + 1;  // pieces of group gi lie in [i, e)
-        for (int x = i + 1; x < 2 * WN_WARPS; ++x)
-            if (seg[x] == gi) e = x + 1;
-        const int b = gi / p.H_kv, g = gi % p.H_kv;
+    // ---- join the CTA's pieces group by group, in the order of the list.  Scratch: behind the
+    // pieces, which are the first stage of each warp's ring
+    float *scratch = reinterpret_cast<float *>(smem + lay.ring + STAGE);
+    float *red = reinterpret_cast<float *>(smem + lay.ring + (NS + 1) * STAGE);
+    const int mine = lane < 2 * WN_WARPS ? seg[lane] : -1;
+    const unsigned same = __match_any_sync(FULL, mine);
+    unsigned leaders = __ballot_sync(FULL, mine >= 0 && lane == __ffs((int)same) - 1);
+    int open0 = -1, open1 = -1;  // the CTA's groups that other CTAs share: the first, the last
+    while (leaders) {
+        const int i = __ffs((int)leaders) - 1;
+        leaders &= leaders - 1;
+        const int gi = __shfl_sync(FULL, mine, i);
+        const unsigned set = __shfl_sync(FULL, same, i);
+        const int b = gi / p.H_kv;
         const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
-        const int start = prefix[b] + g * cnt;
+        const int start = prefix[b] + gi % p.H_kv * cnt;
         const bool all = t0 <= start && start + cnt <= t1;
-        float *part = p.part + (size_t)(2 * blockIdx.x + (t0 >= start ? 0 : 1)) * PIECE;
-        const size_t orow = (size_t)b * p.H_q + g * p.G;
-        for (int x = tid; x < p.G * D; x += WN_NT) {
-            const int h = x / D;
-            float C = __int_as_float(0x7f800000);
-            for (int j = i; j < e; ++j)
-                if (seg[j] == gi) C = fminf(C, piece_of(j)[p.G * D + h]);
-            float O = 0.f, L = 0.f;
-            for (int j = i; j < e; ++j)
-                if (seg[j] == gi) {
-                    const float *pc = piece_of(j);
-                    const float f = ex2(C - pc[p.G * D + h]);
-                    O = fmaf(f, pc[x], O);
-                    L = fmaf(f, pc[p.G * D + 8 + h], L);
-                }
-            if (all) {
-                win_store(p, orow * D + x, O / L);
-            } else {
-                part[x] = O;
-                if (x % D == 0) {
-                    part[p.G * D + h] = C;
-                    part[p.G * D + 8 + h] = L;
-                }
+        const int slot = t0 >= start ? 0 : 1;
+        if (!all) (slot ? open1 : open0) = gi;
+        // seg[j]: which is the j-th of the group's pieces (the end of a join has freed it)
+        __syncthreads();
+        if (warp == 0 && (set >> lane & 1)) seg[__popc(set & ((1u << lane) - 1))] = lane;
+        __syncthreads();
+        auto piece_of = [&](int j) -> const float * {
+            const int x = seg[j];
+            return (x & 1) ? reinterpret_cast<const float *>(smem + lay.ring + (x >> 1) * NS * STAGE)
+                           : p.first + (size_t)(blockIdx.x * WN_WARPS + (x >> 1)) * PIECE;
+        };
+        win_join<D, false>(p, __popc(set), piece_of, scratch, red, gi, all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE);
+    }
+    if (open0 < 0 && open1 < 0) return;
+
+    // ---- groups that span CTAs: the last to arrive joins
+    __threadfence();
+    __syncthreads();
+    if (tid < 2) {
+        const int gi = tid ? open1 : open0;
+        flag[tid] = 0;
+        if (gi >= 0) {
+            const int b = gi / p.H_kv;
+            const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
+            const int start = prefix[b] + gi % p.H_kv * cnt;
+            const int ca = win_owner(start, NC, T), n = win_owner(start + cnt - 1, NC, T) - ca + 1;
+            if (atomicAdd(p.ctrl + CTRL_GROUPS + gi, 1) == n - 1) {
+                p.ctrl[CTRL_GROUPS + gi] = 0;
+                flag[tid] = n;
+                flag[2 + tid] = 2 * ca + (win_share(ca, NC, T) >= start ? 0 : 1);  // its first piece
             }
         }
-        if (!all) {
-            const int ca = win_owner(start, NC, T), cb = win_owner(start + cnt - 1, NC, T);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int old = atomicAdd(p.ctrl + CTRL_GROUPS + gi, 1);
-                *flag = old == cb - ca;
-                if (old == cb - ca) p.ctrl[CTRL_GROUPS + gi] = 0;
-            }
-            __syncthreads();
-            if (*flag) {
-                __threadfence();
-                auto part_of = [&](int cta) {
-                    return p.part + (size_t)(2 * cta + (win_share(cta, NC, T) >= start ? 0 : 1)) * PIECE;
-                };
-                for (int x = tid; x < p.G * D; x += WN_NT) {
-                    const int h = x / D;
-                    float C = __int_as_float(0x7f800000);
-                    for (int j = ca; j <= cb; ++j) C = fminf(C, __ldcg(part_of(j) + p.G * D + h));
-                    float O = 0.f, L = 0.f;
-                    for (int j = ca; j <= cb; ++j) {
-                        const float *pc = part_of(j);
-                        const float f = ex2(C - __ldcg(pc + p.G * D + h));
-                        O = fmaf(f, __ldcg(pc + x), O);
-                        L = fmaf(f, __ldcg(pc + p.G * D + 8 + h), L);
-                    }
-                    win_store(p, orow * D + x, O / L);
-                }
-            }
-            __syncthreads();
-        }
-        i = e;
+    }
+    __syncthreads();
+    __threadfence();
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int n = flag[x], at = flag[2 + x];
+        if (n == 0) continue;
+        // piece j is the first of CTA ca + j, but for the CTA that the group begins in
+        auto piece_of = [&](int j) -> const float * { return p.part + (size_t)(j ? (at & ~1) + 2 * j : at) * PIECE; };
+        // (the rings are free: n <= WN_MAX_CTAS pieces take 37 KB of them)
+        float *far = reinterpret_cast<float *>(smem + lay.ring);
+        win_join<D, true>(p, n, piece_of, far + 4 * WN_NT, far, x ? open1 : open0, nullptr);
     }
 }
 
