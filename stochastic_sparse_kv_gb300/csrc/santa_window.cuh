@@ -94,20 +94,31 @@ __host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B, int ns)
 
 // ------------------------------------------------------------------ tensor-core pieces
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1)
+// D = A B (+ D): 16 x 16 by 16 x 8, fp32 sums.  BF16: the operands' type, else fp16.
+template <bool BF16>
+__device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1)
+template <bool BF16>
+__device__ __forceinline__ void mma_set(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Transpose of an 8x8 matrix of 16-bit elements held one row of two per lane.
@@ -425,6 +436,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         float o[MT][4];                      // columns 2c, 2c+1 of output rows r, r+8 of each piece
         float l0 = 0.f, l1 = 0.f, c0 = 0.f, c1 = 0.f, thr0 = NEG_INF, thr1 = NEG_INF;
         float ka0 = p.k2_hi, ka1 = p.k2_hi, kb0 = p.k2_lo, kb1 = p.k2_lo;
+        const float second = c < 2 ? 0.f : 1.f;
         bool dead = false;
         for (int t = ta; t < tb; ++t) {
             if (t == ta || t == cg.start) {
@@ -504,9 +516,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 float s[SUB][4];
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
-                    float acc[MT / 2][4];
-#pragma unroll
-                    for (int i = 0; i < MT / 2; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+                    float acc[MT / 2][4];  // chains of two steps
                     if (KV4) {
                         uint32_t a[2][MT][2];  // rows r, r+8: per step two fp16 pairs
 #pragma unroll
@@ -517,9 +527,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                             if (D == 128) {
                                 const uint4 x = *reinterpret_cast<const uint4 *>(st + kr * 64 + c * 16);
                                 w[0] = x.x, w[1] = x.y, w[D / 32 - 2] = x.z, w[D / 32 - 1] = x.w;
-                                const uint32_t b2 = *reinterpret_cast<const uint16_t *>(st + TK * D + kr * 8 + 2 * c);
-                                sc[0] = __byte_perm(b2, 0, 0x4040) << 7;
-                                sc[1] = __byte_perm(b2, 0, 0x4141) << 7;
+                                sc[0] = (uint32_t)st[TK * D + kr * 8 + 2 * c] * 0x00800080u;  // twice, as fp16
+                                sc[1] = (uint32_t)st[TK * D + kr * 8 + 2 * c + 1] * 0x00800080u;
                             } else {
                                 const uint2 x = *reinterpret_cast<const uint2 *>(st + kr * 32 + c * 8);
                                 w[0] = x.x, w[1] = x.y;
@@ -534,8 +543,11 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            mma_f16(acc[i / 2], a[0][i][0], a[1][i][0], a[0][i][1], a[1][i][1], qf[i][0], qf[i][1]);
+                        for (int i = 0; i < MT; i += 2) {
+                            mma_set<false>(acc[i / 2], a[0][i][0], a[1][i][0], a[0][i][1], a[1][i][1], qf[i][0], qf[i][1]);
+                            mma_add<false>(acc[i / 2], a[0][i + 1][0], a[1][i + 1][0], a[0][i + 1][1], a[1][i + 1][1], qf[i + 1][0],
+                                           qf[i + 1][1]);
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < MT / 2; ++i) {  // piece i & 1 of the lane's 16 dimensions of half i / 2
@@ -543,8 +555,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                             const int pc = 2 * c + (i & 1), kr = 16 * u + r;
                             const uint4 x = *reinterpret_cast<const uint4 *>(kt + kr * 128 + ((pc ^ r) << 4));
                             const uint4 y = *reinterpret_cast<const uint4 *>(kt + (kr + 8) * 128 + ((pc ^ r) << 4));
-                            mma_bf16(acc[i], x.x, y.x, x.y, y.y, qf[2 * i][0], qf[2 * i][1]);
-                            mma_bf16(acc[i], x.z, y.z, x.w, y.w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                            mma_set<true>(acc[i], x.x, y.x, x.y, y.y, qf[2 * i][0], qf[2 * i][1]);
+                            mma_add<true>(acc[i], x.z, y.z, x.w, y.w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
                         }
                     }
 #pragma unroll
@@ -554,12 +566,14 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                         for (int i = 0; i < MT / 2; ++i) x[i] = acc[i][e];
                         s[u][e] = MT == 8 ? (x[0] + x[1]) + (x[MT / 2 - 2] + x[MT / 2 - 1]) : x[0] + x[1];
                     }
-                    if (!whole) {
-                        const int ja = k0 + 16 * u + r, jb = ja + 8;
-                        if (!seen(ja)) s[u][0] = s[u][1] = NEG_INF;
-                        if (!seen(jb)) s[u][2] = s[u][3] = NEG_INF;
-                    }
                 }
+                if (!whole)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        const int ja = k0 + 16 * u + r;
+                        if (!seen(ja)) s[u][0] = s[u][1] = NEG_INF;
+                        if (!seen(ja + 8)) s[u][2] = s[u][3] = NEG_INF;
+                    }
 
                 // ---- a new maximum, when it is far above the one that set c
                 float x0 = NEG_INF, x1 = NEG_INF;
@@ -604,11 +618,28 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float a = ex2(fmaf(s[u][2 * y], kb0, fmaf(s[u][2 * y], ka0, c0)));
-                        float b = ex2(fmaf(s[u][2 * y + 1], kb1, fmaf(s[u][2 * y + 1], ka1, c1)));
-                        if (!whole && !seen(k0 + 16 * u + r + 8 * y)) a = b = 0.f;
+                        s[u][2 * y] = ex2(fmaf(s[u][2 * y], kb0, fmaf(s[u][2 * y], ka0, c0)));
+                        s[u][2 * y + 1] = ex2(fmaf(s[u][2 * y + 1], kb1, fmaf(s[u][2 * y + 1], ka1, c1)));
+                    }
+                if (!whole)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            if (!seen(k0 + 16 * u + r + 8 * y)) s[u][2 * y] = s[u][2 * y + 1] = 0.f;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float a = s[u][2 * y], b = s[u][2 * y + 1];
                         l0 += a;
                         l1 += b;
+                        if (KV4 && !WIDE) {
+                            // columns 0-3 the first term, 4-7 what it leaves: second = 0 or 1
+                            const float2 f = unpack_f16(pack_f16(a, b));
+                            pb[u][0][y] = movmatrix(pack_f16(fmaf(-second, f.x, a), fmaf(-second, f.y, b)));
+                            continue;
+                        }
                         uint32_t term[NP];
 #pragma unroll
                         for (int i = 0; i < NP; ++i) {
@@ -628,7 +659,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                             for (int i = 0; i < NP; ++i) pb[u][i % NB][y] = movmatrix(term[i]);
                         } else {
                             pb[u][0][y] = movmatrix(c < 2 ? term[0] : term[1]);
-                            if (!KV4) pb[u][NB - 1][y] = movmatrix(c < 2 ? term[NP - 1] : 0u);
+                            pb[u][NB - 1][y] = movmatrix(c < 2 ? term[NP - 1] : 0u);
                         }
                     }
 
@@ -650,16 +681,21 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                                 vw[u][i][0] = *reinterpret_cast<const uint32_t *>(vt + kk * RB + r * 4);
                             }
                             sb[i] = vsc[kk * (D / 16) + (D == 128 ? r : r >> 1)];
-                            if (!whole && !seen(k0 + kk)) sb[i] = 0;  // what is not seen may be a NaN
                         }
-                        sp[u][0] = (sb[0] | (sb[1] << 16)) << 7;
-                        sp[u][1] = (sb[2] | (sb[3] << 16)) << 7;
+                        sp[u][0] = sb[1] * 0x800000u + sb[0] * 0x80u;  // the key pair's scales as fp16
+                        sp[u][1] = sb[3] * 0x800000u + sb[2] * 0x80u;
                     }
+                    if (!whole)  // what is not seen may be a NaN
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int j = k0 + 16 * u + 2 * c + 8 * y;
+                                sp[u][y] &= (seen(j) ? 0xffffu : 0u) | (seen(j + 1) ? 0xffff0000u : 0u);
+                            }
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         float acc[4][4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
                         for (int u = 0; u < SUB; ++u) {
                             uint32_t a[2][2][4];  // key pair, even or odd dimension, byte
@@ -677,8 +713,12 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                                for (int n = 0; n < NB; ++n)
-                                    mma_f16(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
+                                for (int n = 0; n < NB; ++n) {
+                                    if (u == 0 && n == 0)
+                                        mma_set<false>(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
+                                    else
+                                        mma_add<false>(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
+                                }
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -689,15 +729,18 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                     const uint32_t vt = smem_u32(st + TK * D * 2);
                     uint32_t mk[SUB][2];
 #pragma unroll
-                    for (int u = 0; u < SUB; ++u)
+                    for (int u = 0; u < SUB; ++u) mk[u][0] = mk[u][1] = 0xffffffffu;
+                    if (!whole)  // what is not seen may be a NaN
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int j = k0 + 16 * u + 2 * c + 8 * y;
-                            mk[u][y] = whole ? 0xffffffffu : (seen(j) ? 0xffffu : 0u) | (seen(j + 1) ? 0xffff0000u : 0u);
-                        }
+                        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int j = k0 + 16 * u + 2 * c + 8 * y;
+                                mk[u][y] = (seen(j) ? 0xffffu : 0u) | (seen(j + 1) ? 0xffff0000u : 0u);
+                            }
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        float acc[4];
 #pragma unroll
                         for (int u = 0; u < SUB; ++u) {
                             // matrices: keys 0-7 and 8-15 by dimensions 0-7 and 8-15 of piece i
@@ -706,8 +749,12 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                             uint32_t a[4];
                             ldmatrix_x4_trans(a, vt + (uint32_t)((i / 4) * TK * 128 + kk * 128 + ((pc ^ (kk & 7)) << 4)));
 #pragma unroll
-                            for (int n = 0; n < NB; ++n)
-                                mma_bf16(acc, a[0] & mk[u][0], a[1] & mk[u][0], a[2] & mk[u][1], a[3] & mk[u][1], pb[u][n][0], pb[u][n][1]);
+                            for (int n = 0; n < NB; ++n) {
+                                if (u == 0 && n == 0)
+                                    mma_set<true>(acc, a[0] & mk[u][0], a[1] & mk[u][0], a[2] & mk[u][1], a[3] & mk[u][1], pb[u][n][0], pb[u][n][1]);
+                                else
+                                    mma_add<true>(acc, a[0] & mk[u][0], a[1] & mk[u][0], a[2] & mk[u][1], a[3] & mk[u][1], pb[u][n][0], pb[u][n][1]);
+                            }
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[i][e] += acc[e];
