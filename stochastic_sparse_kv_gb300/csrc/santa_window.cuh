@@ -42,13 +42,19 @@
 
 namespace santa {
 
-constexpr int WN_WARPS = 8;
-constexpr int WN_NT = WN_WARPS * 32;
 constexpr int WN_MAX_CTAS = 512;          // partial slots in the workspace
+constexpr int WN_MAX_WARPS = 12;
+constexpr int WN_RED = 4 * 32 * WN_MAX_WARPS;  // floats of a join's partial sums: 4 x max(G D / 4, threads)
 constexpr float WN_TOP = 9.f;             // log2 of p where a new maximum puts it
 constexpr float WN_SLACK = 6.f;           // and how far above that later ones may be
+constexpr int WN_SETUP = 2;               // tiles that beginning a group costs about as much as
 
-__host__ __device__ constexpr int win_tile(int D, bool kv4) { return kv4 || D == 64 ? 32 : 16; }
+// One CTA to an SM.  4-bit: 12 warps, what 168 registers a thread allow (16 warps of 128
+// spill and are no faster, the conversions' pipe being the limit); bf16: the 8 whose rings fit.
+__host__ __device__ constexpr int win_warps(bool kv4) { return kv4 ? 12 : 8; }
+// Keys of a tile (a ring stage), and of one pass of the arithmetic over it.
+__host__ __device__ constexpr int win_tile(int D, bool kv4) { return kv4 ? 64 : D == 64 ? 32 : 16; }
+__host__ __device__ constexpr int win_pass(int D, bool kv4) { return kv4 || D == 64 ? 32 : 16; }
 __host__ __device__ constexpr int win_stage(int D, bool kv4)
 {
     return kv4 ? win_tile(D, true) * (D + D / 8) : win_tile(D, false) * D * 4;
@@ -63,8 +69,8 @@ struct WinParams {
     const int32_t *seq_lens;
     float *out;
     int32_t *ctrl;
-    float *first;                 // [WN_MAX_CTAS][WN_WARPS] pieces: a warp's first, unfinished group
-    float *part;                  // [WN_MAX_CTAS][2] pieces: a CTA's first and last unfinished groups
+    float *first;                 // [CTAs][warps] pieces: a warp's first group, begun before its share
+    float *part;                  // [CTAs][2] pieces: a group begun before the CTA's share, one not ended in it
     int B, H_q, H_kv, n_max, G;
     int window, sinks;
     int out_bf16;
@@ -80,11 +86,12 @@ struct WinSmem {
 
 __host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B, int ns)
 {
+    const int W = win_warps(kv4);
     WinSmem s{};
     int off = 0;
-    s.ring = off; off += WN_WARPS * ns * win_stage(D, kv4);
-    s.bar = off; off += WN_WARPS * ns * 8;
-    s.seg = off; off += 2 * WN_WARPS * 4;        // group index of each warp's two pieces, or -1
+    s.ring = off; off += W * ns * win_stage(D, kv4);
+    s.bar = off; off += W * ns * 8;
+    s.seg = off; off += 2 * W * 4;               // group index of each warp's two pieces, or -1
     s.flag = off; off += 16;
     s.nb = off; off += (int)align_up((size_t)B * 4, 16);
     s.prefix = off; off += (int)align_up((size_t)(B + 1) * 4, 16);
@@ -158,6 +165,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void add2(float &a, float &b, float x, float y)
+{
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(y));
+}
+
+// (a, b) * (x, y) + (u, v)
+__device__ __forceinline__ float2 fma2(float a, float b, float x, float y, float u, float v)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 s, {%6, %7};\n\t"
+        "fma.rn.f32x2 p, p, q, s;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a), "f"(b), "f"(x), "f"(y), "f"(u), "f"(v));
+    return r;
+}
+
 __device__ __forceinline__ float2 unpack_f16(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 
 // Untiled bulk copy, global to this CTA's shared memory (16-byte aligned, multiple of 16).
@@ -171,6 +198,10 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 }
 
 // ------------------------------------------------------------------ the list of tiles
+//
+// Positions of the list: every group with keys has WN_SETUP positions without work, then one
+// for each of its tiles.  Shares are even in positions, so that a run of short groups
+// (each costs a load of its queries and a result) is not taken for a few tiles.
 
 // A sequence of n keys: tiles [0, ns) cover the sinks, then tiles tw.. up to the last key.
 struct WinTiles {
@@ -188,36 +219,47 @@ __device__ __forceinline__ WinTiles win_tiles(int n, int window, int sinks)
     return t;
 }
 
-// A group of the list: batch row, KV head, its tiles and the list index of the first.
+// Positions of a group with cnt tiles.
+__device__ __forceinline__ int win_span(int cnt) { return cnt > 0 ? cnt + WN_SETUP : 0; }
+
+// A group of the list: batch row, KV head, its tiles and the position of the first tile.
 template <int TK>
 struct WinGroup {
     int b, g, n, start;
     WinTiles t;
 
-    __device__ void seek(int tile, const int *prefix, const int *nb, const WinParams &p)
+    // the group of a position
+    __device__ __forceinline__ void seek(int pos, const int *prefix, const int *nb, const WinParams &p)
     {
         int lo = 0, hi = p.B - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= tile) lo = mid; else hi = mid - 1;
+            if (prefix[mid] <= pos) lo = mid; else hi = mid - 1;
         }
         b = lo;
         n = nb[lo];
         t = win_tiles<TK>(n, p.window, p.sinks);
-        g = (tile - prefix[lo]) / t.cnt;
-        start = prefix[lo] + g * t.cnt;
+        g = (pos - prefix[lo]) / win_span(t.cnt);
+        start = prefix[lo] + g * win_span(t.cnt) + WN_SETUP;
     }
-    __device__ int end() const { return start + t.cnt; }
-    __device__ int index(const WinParams &p) const { return b * p.H_kv + g; }
-    __device__ int key0(int tile) const
+    __device__ __forceinline__ int end() const { return start + t.cnt; }
+    __device__ __forceinline__ int index(const WinParams &p) const { return b * p.H_kv + g; }
+    __device__ __forceinline__ int key0(int pos) const
     {
-        const int i = tile - start;
+        const int i = pos - start;
         return (i < t.ns ? i : t.tw + i - t.ns) * TK;
     }
-    // the group that holds the tile after this one's last (there is one)
-    __device__ void next(const int *nb, const WinParams &p)
+    // the keys of the tile from k0 that may be visible, in whole 16s
+    __device__ __forceinline__ int2 rows(int k0, int sinks) const
     {
-        start += t.cnt;
+        const int lo = k0 < sinks ? k0 : max(k0, t.w0 & ~15);
+        const int hi = min(k0 + TK, k0 < t.tw * TK ? (sinks + 15) & ~15 : (n + 15) & ~15);
+        return make_int2(lo, hi);
+    }
+    // the group after this one (there is one)
+    __device__ __forceinline__ void next(const int *nb, const WinParams &p)
+    {
+        start += win_span(t.cnt);
         if (++g == p.H_kv) {
             g = 0;
             do n = nb[++b]; while (n == 0);
@@ -226,9 +268,9 @@ struct WinGroup {
     }
 };
 
-// First tile of share i of n shares of a list of T tiles, and the share that holds a tile.
+// First position of share i of n shares of T positions, and the share that holds a position.
 __device__ __forceinline__ int win_share(int i, int n, int T) { return (int)((long long)i * T / n); }
-__device__ __forceinline__ int win_owner(int tile, int n, int T) { return (int)((((long long)tile + 1) * n - 1) / T); }
+__device__ __forceinline__ int win_owner(int pos, int n, int T) { return (int)((((long long)pos + 1) * n - 1) / T); }
 
 __device__ __forceinline__ void win_store(const WinParams &p, size_t i, float v)
 {
@@ -239,19 +281,19 @@ __device__ __forceinline__ void win_store(const WinParams &p, size_t i, float v)
 }
 
 // The whole CTA: the n pieces of group gi joined into `part` (a piece) or, when that is null,
-// into the output.  scratch: 16 n + 16 floats; red: WN_NT float4.  Begins and ends with
+// into the output.  scratch: 16 n + 16 floats; red: WN_RED of them.  Begins and ends with
 // the scratch free.  FAR: the pieces lie in the workspace, written by other CTAs too, and
 // are read past the L1 cache; else in shared memory or the workspace, written by this CTA.
-template <int D, bool FAR, class F>
+template <int D, int NT, bool FAR, class F>
 __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, float *scratch, float *red, int gi, float *part)
 {
     constexpr unsigned FULL = 0xffffffffu;
-    const int tid = threadIdx.x, lane = tid & 31, h = tid >> 5, GD = p.G * D;
+    const int tid = threadIdx.x, lane = tid & 31, GD = p.G * D;
     float *tot = scratch, *wt = scratch + 16, *lt = wt + 8 * n;
     auto load = [](const float *a) { return FAR ? __ldcg(a) : *a; };
     auto load4 = [](const float4 *a) { return FAR ? __ldcg(a) : *a; };
-    // warp h: head h's common exponent, the pieces' weights, the sum
-    if (h < p.G) {
+    // a warp a head: its common exponent, the pieces' weights, the sum
+    for (int h = tid >> 5; h < p.G; h += NT / 32) {
         float C = __int_as_float(0x7f800000);
         for (int j = lane; j < n; j += 32) {
             const float *pc = piece_of(j) + GD + h;
@@ -276,10 +318,11 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
         }
     }
     __syncthreads();
-    // four outputs a thread; with fewer than WN_NT of those, slices of the pieces
-    const int nv = GD / 4, ns = WN_NT / nv, v = tid % nv, sl = tid / nv, hv = 4 * v / D;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (sl < ns) {
+    // four outputs a thread; with few outputs, slices of the pieces
+    const int nv = GD / 4, ns = max(1, NT / nv);
+    for (int i = tid; i < ns * nv; i += NT) {
+        const int v = i % nv, sl = i / nv, hv = 4 * v / D;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int j = sl; j < n; j += ns) {
             const float4 x = load4(reinterpret_cast<const float4 *>(piece_of(j)) + v);
@@ -289,20 +332,19 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
             o.z = fmaf(w, x.z, o.z);
             o.w = fmaf(w, x.w, o.w);
         }
+        reinterpret_cast<float4 *>(red)[i] = o;
     }
-    if (ns > 1) {
-        reinterpret_cast<float4 *>(red)[tid] = o;
-        __syncthreads();
-        if (sl == 0)
-            for (int s = 1; s < ns; ++s) {
-                const float4 x = reinterpret_cast<const float4 *>(red)[s * nv + v];
-                o.x += x.x;
-                o.y += x.y;
-                o.z += x.z;
-                o.w += x.w;
-            }
-    }
-    if (sl == 0) {
+    if (ns > 1) __syncthreads();
+    for (int v = tid; v < nv; v += NT) {
+        const int hv = 4 * v / D;
+        float4 o = reinterpret_cast<const float4 *>(red)[v];
+        for (int s = 1; s < ns; ++s) {
+            const float4 x = reinterpret_cast<const float4 *>(red)[s * nv + v];
+            o.x += x.x;
+            o.y += x.y;
+            o.z += x.z;
+            o.w += x.w;
+        }
         if (part) {
             reinterpret_cast<float4 *>(part)[v] = o;
             if (v % (D / 4) == 0) {
@@ -310,9 +352,9 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
                 part[GD + 8 + hv] = tot[8 + hv];
             }
         } else {
-            const float L = tot[8 + hv];
+            const float r = 1.f / tot[8 + hv];
             const size_t at = ((size_t)(gi / p.H_kv) * p.H_q + (size_t)(gi % p.H_kv) * p.G) * D + 4 * (size_t)v;
-            o = make_float4(o.x / L, o.y / L, o.z / L, o.w / L);
+            o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
             if (p.out_bf16) {
                 const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
                 *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + at) =
@@ -331,7 +373,8 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
 template <int D, bool KV4, bool WIDE>
 __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMap *tm_k, const CUtensorMap *tm_v)
 {
-    constexpr int TK = win_tile(D, KV4), SUB = TK / 16, STAGE = win_stage(D, KV4);
+    constexpr int W = win_warps(KV4), NT = 32 * W;
+    constexpr int TK = win_tile(D, KV4), HK = win_pass(D, KV4), SUB = HK / 16, STAGE = win_stage(D, KV4);
     constexpr int MT = D / 16;   // 16-row pieces of the output, and MMA steps of a score
     constexpr int NP = KV4 ? 2 : 3;                     // terms of p
     constexpr int NB = WIDE ? NP : (KV4 ? 1 : 2);       // MMAs they take
@@ -362,7 +405,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 bad = true;
                 n = 0;
             }
-            const int cnt = p.H_kv * win_tiles<TK>(n, p.window, p.sinks).cnt;
+            const int cnt = p.H_kv * win_span(win_tiles<TK>(n, p.window, p.sinks).cnt);
             int x = cnt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -388,36 +431,55 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     const int T = prefix[p.B];
     for (int b = blockIdx.x; b < p.B; b += gridDim.x)  // sequences without keys
         if (nb[b] == 0)
-            for (int i = tid; i < p.H_q * D; i += WN_NT) win_store(p, (size_t)b * p.H_q * D + i, 0.f);
-    const int NC = min((int)gridDim.x, (T + WN_WARPS - 1) / WN_WARPS);  // CTAs with a share
+            for (int i = tid; i < p.H_q * D; i += NT) win_store(p, (size_t)b * p.H_q * D + i, 0.f);
+    const int NC = min((int)gridDim.x, (T + W - 1) / W);  // CTAs with a share
     if ((int)blockIdx.x >= NC) return;
     const int t0 = win_share(blockIdx.x, NC, T), t1 = win_share(blockIdx.x + 1, NC, T);
-    const int ta = t0 + win_share(warp, WN_WARPS, t1 - t0), tb = t0 + win_share(warp + 1, WN_WARPS, t1 - t0);
+    const int ta = t0 + win_share(warp, W, t1 - t0), tb = t0 + win_share(warp + 1, W, t1 - t0);
 
+    WinGroup<TK> cg;  // the group of the tile at hand, t its position
+    int t = ta;
     if (ta < tb) {
+        cg.seek(ta, prefix, nb, p);
+        t = max(ta, cg.start);
+    }
+    if (t < tb) {
         const uint64_t policy = l2_policy_evict_first();
-        // ---- the copies: `ig` is the group of the next tile to fetch
-        WinGroup<TK> ig;
-        ig.seek(ta, prefix, nb, p);
-        WinGroup<TK> cg = ig;
-        int it = ta, is = 0, cs = 0;
+        // ---- a group's queries: head column r (zero in columns without a head).  4-bit: lane c
+        // takes dimensions D/4 c .., four to an MMA step; bf16: 16 c .. of each 64
+        uint4 qraw[MT / 2];
+        auto load_q = [&]() {
+            const int h = WIDE ? r : (r & 3);
+            const uint16_t *qh = p.q + ((size_t)cg.b * p.H_q + cg.g * p.G + h) * D;
+#pragma unroll
+            for (int i = 0; i < MT / 2; ++i)
+                qraw[i] = h >= p.G ? make_uint4(0, 0, 0, 0)
+                          : KV4    ? reinterpret_cast<const uint4 *>(qh + (D / 4) * c)[i]
+                                   : reinterpret_cast<const uint4 *>(qh + (i / 2) * 64 + 16 * c)[i & 1];
+        };
+        load_q();
+
+        // ---- the copies: `ig` is the group of the next tile to fetch, `it` its position
+        WinGroup<TK> ig = cg;
+        int it = t, is = 0, cs = 0, held = 0;  // stages to fill and to use next, copies not waited for
         uint32_t cphase = 0;
+        int fjump = it < ig.start + ig.t.ns ? ig.start + ig.t.ns : ig.end();  // where the rows break off
+        int fk = ig.key0(it);                                                 // the tile's first key
         auto fetch = [&]() {
-            if (it == ig.end()) ig.next(nb, p);
             if (lane == 0) {
                 uint8_t *st = ring + is * STAGE;
-                const int k0 = ig.key0(it);
                 if (KV4) {
-                    const int rows = min(TK, p.n_max - k0);  // 16 or 32: n_max is a multiple of 16
-                    const size_t row = (size_t)ig.index(p) * p.n_max + k0;
-                    mbar_arrive_tx(&bar[is], (uint32_t)(rows * (D + D / 8)));
-                    bulk_load(st, p.k + row * (D / 2), rows * (D / 2), &bar[is], policy);
-                    bulk_load(st + TK * D, p.ks + row * (D / 16), rows * (D / 16), &bar[is], policy);
-                    bulk_load(st + TK * (D / 2), p.v + row * (D / 2), rows * (D / 2), &bar[is], policy);
-                    bulk_load(st + TK * (D + D / 16), p.vs + row * (D / 16), rows * (D / 16), &bar[is], policy);
+                    const int2 rw = ig.rows(fk, p.sinks);
+                    const uint32_t rows = rw.y - rw.x, o = rw.x - fk;  // multiples of 16, as n_max is
+                    const size_t at = (uint32_t)ig.index(p) * (uint32_t)p.n_max + (uint32_t)rw.x;
+                    mbar_arrive_tx(&bar[is], rows * (D + D / 8));
+                    bulk_load(st + o * (D / 2), p.k + at * (D / 2), rows * (D / 2), &bar[is], policy);
+                    bulk_load(st + TK * D + o * (D / 16), p.ks + at * (D / 16), rows * (D / 16), &bar[is], policy);
+                    bulk_load(st + TK * (D / 2) + o * (D / 2), p.v + at * (D / 2), rows * (D / 2), &bar[is], policy);
+                    bulk_load(st + TK * (D + D / 16) + o * (D / 16), p.vs + at * (D / 16), rows * (D / 16), &bar[is], policy);
                 } else {
                     // whole boxes: rows past the group's last key are other keys or zeros, never used
-                    const int row = ig.index(p) * p.n_max + k0;
+                    const int row = ig.index(p) * p.n_max + fk;
                     mbar_arrive_tx(&bar[is], (uint32_t)STAGE);
 #pragma unroll
                     for (int hf = 0; hf < D / 64; ++hf) {
@@ -426,33 +488,305 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                     }
                 }
             }
-            ++it;
             is = is + 1 == NS ? 0 : is + 1;
+            ++held;
+            ++it;
+            fk += TK;
+            if (it == fjump) {  // the sinks end, or the group
+                if (it == ig.end()) {
+                    if (it + WN_SETUP >= tb) {  // no tile left here
+                        it = tb;
+                        return;
+                    }
+                    ig.next(nb, p);
+                    it = ig.start;
+                    const size_t q0 = ((size_t)ig.b * p.H_q + ig.g * p.G) * D;  // its queries, into L2
+                    if (lane * 64 < p.G * D) prefetch_l2(p.q + q0 + lane * 64);
+                }
+                fjump = it < ig.start + ig.t.ns ? ig.start + ig.t.ns : ig.end();
+                fk = ig.key0(it);
+            }
         };
         for (int i = 0; i < NS && it < tb; ++i) fetch();
 
         // ---- the sums
-        uint32_t qf[MT][2];                  // B operand of the scores: head column r
+        uint32_t qf[MT][2];                  // B operand of the scores
         float o[MT][4];                      // columns 2c, 2c+1 of output rows r, r+8 of each piece
         float l0 = 0.f, l1 = 0.f, c0 = 0.f, c1 = 0.f, thr0 = NEG_INF, thr1 = NEG_INF;
         float ka0 = p.k2_hi, ka1 = p.k2_hi, kb0 = p.k2_lo, kb1 = p.k2_lo;
-        const float second = c < 2 ? 0.f : 1.f;
-        bool dead = false;
-        for (int t = ta; t < tb; ++t) {
-            if (t == ta || t == cg.start) {
-                // a group begins: its queries (zero in columns without a head), empty sums
-                const int h = WIDE ? r : (r & 3);
-                const uint16_t *qh = p.q + ((size_t)cg.b * p.H_q + cg.g * p.G + h) * D;
-                const bool live = h < p.G;
+        const float second = c < 2 ? 0.f : -1.f;
+        // ---- one pass: the HK keys from k0, whose rows and scales the pointers are at
+        auto pass = [&](const uint8_t *kc, const uint8_t *vc, const uint8_t *ks, const uint8_t *vs, int k0) {
+            // every key visible: no masks
+            const bool whole = (k0 >= cg.t.w0 || k0 + HK <= p.sinks) && k0 + HK <= cg.n;
+            auto seen = [&](int j) { return j < cg.n && (j >= cg.t.w0 || j < p.sinks); };
+
+            // ---- scores of keys r, r+8 of each 16, columns 2c, 2c+1
+            float s[SUB][4];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                float acc[MT / 2][4];  // chains of two steps
                 if (KV4) {
-                    // lane c holds dimensions D/4 c .. of head r: step t takes 4 of them; scaled
-                    // by the power of two that puts the head's largest near 2^14
+                    uint32_t a[2][MT][2];  // rows r, r+8: per step two fp16 pairs
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int kr = 16 * u + r + 8 * y;
+                        uint32_t w[D / 32];
+                        uint32_t sc[2];
+                        if (D == 128) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(kc + kr * 64 + c * 16);
+                            w[0] = x.x, w[1] = x.y, w[D / 32 - 2] = x.z, w[D / 32 - 1] = x.w;
+                            sc[0] = (uint32_t)ks[kr * 8 + 2 * c] * 0x00800080u;  // twice, as fp16
+                            sc[1] = (uint32_t)ks[kr * 8 + 2 * c + 1] * 0x00800080u;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(kc + kr * 32 + c * 8);
+                            w[0] = x.x, w[1] = x.y;
+                            sc[0] = sc[1] = (uint32_t)ks[kr * 4 + c] * 0x00800080u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j) {
+                            uint32_t h[4];
+                            e2m1_unpack8(w[j], h);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) a[y][2 * j + i / 2][i & 1] = h2mul(h[i], sc[j / 2]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2) {
+                        mma_set<false>(acc[i / 2], a[0][i][0], a[1][i][0], a[0][i][1], a[1][i][1], qf[i][0], qf[i][1]);
+                        mma_add<false>(acc[i / 2], a[0][i + 1][0], a[1][i + 1][0], a[0][i + 1][1], a[1][i + 1][1], qf[i + 1][0],
+                                       qf[i + 1][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < MT / 2; ++i) {  // piece i & 1 of the lane's 16 dimensions of half i / 2
+                        const uint8_t *kt = kc + (i / 2) * TK * 128;
+                        const int pc = 2 * c + (i & 1), kr = 16 * u + r;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(kt + kr * 128 + ((pc ^ r) << 4));
+                        const uint4 y = *reinterpret_cast<const uint4 *>(kt + (kr + 8) * 128 + ((pc ^ r) << 4));
+                        mma_set<true>(acc[i], x.x, y.x, x.y, y.y, qf[2 * i][0], qf[2 * i][1]);
+                        mma_add<true>(acc[i], x.z, y.z, x.w, y.w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    add2(acc[0][e], acc[0][e + 1], acc[1][e], acc[1][e + 1]);
+                    if (MT == 8) {
+                        add2(acc[MT / 2 - 2][e], acc[MT / 2 - 2][e + 1], acc[MT / 2 - 1][e], acc[MT / 2 - 1][e + 1]);
+                        add2(acc[0][e], acc[0][e + 1], acc[MT / 2 - 2][e], acc[MT / 2 - 2][e + 1]);
+                    }
+                    s[u][e] = acc[0][e];
+                    s[u][e + 1] = acc[0][e + 1];
+                }
+            }
+            if (!whole)
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    const int ja = k0 + 16 * u + r;
+                    if (!seen(ja)) s[u][0] = s[u][1] = NEG_INF;
+                    if (!seen(ja + 8)) s[u][2] = s[u][3] = NEG_INF;
+                }
+
+            // ---- a new maximum, when it is far above the one that set c
+            float x0 = NEG_INF, x1 = NEG_INF;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                x0 = fmaxf(x0, fmaxf(s[u][0], s[u][2]));
+                x1 = fmaxf(x1, fmaxf(s[u][1], s[u][3]));
+            }
+            if (__any_sync(FULL, x0 > thr0 || x1 > thr1)) {
+#pragma unroll
+                for (int m = 4; m <= 16; m <<= 1) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(FULL, x0, m));
+                    x1 = fmaxf(x1, __shfl_xor_sync(FULL, x1, m));
+                }
+                float f0 = 1.f, f1 = 1.f;
+                if (x0 > thr0) {
+                    const float cn = fmaf(-x0, ka0, WN_TOP);
+                    f0 = ex2(fminf(cn - c0, 0.f));  // (of empty sums c is not yet set)
+                    c0 = cn;
+                    thr0 = x0 + WN_SLACK / ka0;
+                }
+                if (x1 > thr1) {
+                    const float cn = fmaf(-x1, ka1, WN_TOP);
+                    f1 = ex2(fminf(cn - c1, 0.f));
+                    c1 = cn;
+                    thr1 = x1 + WN_SLACK / ka1;
+                }
+                l0 *= f0;
+                l1 *= f1;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    o[i][0] *= f0;
+                    o[i][1] *= f1;
+                    o[i][2] *= f0;
+                    o[i][3] *= f1;
+                }
+            }
+
+            // ---- p, its sum, and its terms as the B operand of V^T p
+            uint32_t pb[SUB][NB][2];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float2 x = fma2(s[u][2 * y], s[u][2 * y + 1], ka0, ka1, c0, c1);
+                    x = fma2(s[u][2 * y], s[u][2 * y + 1], kb0, kb1, x.x, x.y);
+                    s[u][2 * y] = ex2(x.x);
+                    s[u][2 * y + 1] = ex2(x.y);
+                }
+            if (!whole)
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        if (!seen(k0 + 16 * u + r + 8 * y)) s[u][2 * y] = s[u][2 * y + 1] = 0.f;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float a = s[u][2 * y], b = s[u][2 * y + 1];
+                    add2(l0, l1, a, b);
+                    if (KV4 && !WIDE) {
+                        // columns 0-3 the first term, 4-7 what it leaves: second = 0 or -1
+                        const float2 f = unpack_f16(pack_f16(a, b));
+                        const float2 g = fma2(f.x, f.y, second, second, a, b);
+                        pb[u][0][y] = movmatrix(pack_f16(g.x, g.y));
+                    } else {
+                        uint32_t term[NP];
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) {
+                            if (KV4) {
+                                term[i] = pack_f16(a, b);
+                                const float2 f = unpack_f16(term[i]);
+                                a -= f.x;
+                                b -= f.y;
+                            } else {
+                                term[i] = pack_bf16(a, b);
+                                a -= bf16lo_to_f32(term[i]);
+                                b -= bf16hi_to_f32(term[i]);
+                            }
+                        }
+                        if (WIDE) {
+#pragma unroll
+                            for (int i = 0; i < NP; ++i) pb[u][i % NB][y] = movmatrix(term[i]);
+                        } else {
+                            pb[u][0][y] = movmatrix(c < 2 ? term[0] : term[1]);
+                            pb[u][NB - 1][y] = movmatrix(c < 2 ? term[NP - 1] : 0u);
+                        }
+                    }
+                }
+
+            // ---- o += V^T p, the tile's keys in one chain per piece
+            if (KV4) {
+                constexpr int RB = D / 2, W = D / 64;  // bytes of a row; words of a lane's D/8 dimensions
+                uint32_t vw[SUB][4][W], sp[SUB][2];
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t sb[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = 16 * u + 2 * c + (i & 1) + 8 * (i >> 1);
+                        if (W == 2) {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(vc + kk * RB + r * 8);
+                            vw[u][i][0] = x.x, vw[u][i][W - 1] = x.y;
+                        } else {
+                            vw[u][i][0] = *reinterpret_cast<const uint32_t *>(vc + kk * RB + r * 4);
+                        }
+                        sb[i] = vs[kk * (D / 16) + (D == 128 ? r : r >> 1)];
+                    }
+                    sp[u][0] = sb[1] * 0x800000u + sb[0] * 0x80u;  // the key pair's scales as fp16
+                    sp[u][1] = sb[3] * 0x800000u + sb[2] * 0x80u;
+                }
+                if (!whole)  // what is not seen may be a NaN
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int j = k0 + 16 * u + 2 * c + 8 * y;
+                            sp[u][y] &= (seen(j) ? 0xffffu : 0u) | (seen(j + 1) ? 0xffff0000u : 0u);
+                        }
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    float acc[4][4];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        uint32_t a[2][2][4];  // key pair, even or odd dimension, byte
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t x0w = vw[u][2 * y][w], x1w = vw[u][2 * y + 1][w];
+                            e2m1_unpack8((x0w & 0x0f0f0f0fu) | ((x1w << 4) & 0xf0f0f0f0u), a[y][0]);
+                            e2m1_unpack8(((x0w >> 4) & 0x0f0f0f0fu) | (x1w & 0xf0f0f0f0u), a[y][1]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                a[y][0][i] = h2mul(a[y][0][i], sp[u][y]);
+                                a[y][1][i] = h2mul(a[y][1][i], sp[u][y]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int n = 0; n < NB; ++n) {
+                                if (u == 0 && n == 0)
+                                    mma_set<false>(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
+                                else
+                                    mma_add<false>(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2)
+                            add2(o[4 * w + i][e], o[4 * w + i][e + 1], acc[i][e], acc[i][e + 1]);
+                }
+            } else {
+                const uint32_t vt = smem_u32(vc);
+                uint32_t mk[SUB][2];
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) mk[u][0] = mk[u][1] = 0xffffffffu;
+                if (!whole)  // what is not seen may be a NaN
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int j = k0 + 16 * u + 2 * c + 8 * y;
+                            mk[u][y] = (seen(j) ? 0xffffu : 0u) | (seen(j + 1) ? 0xffff0000u : 0u);
+                        }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    float acc[4];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        // matrices: keys 0-7 and 8-15 by dimensions 0-7 and 8-15 of piece i
+                        const int kk = 16 * u + (lane & 7) + ((lane >> 4) << 3);
+                        const int pc = 2 * (i & 3) + ((lane >> 3) & 1);
+                        uint32_t a[4];
+                        ldmatrix_x4_trans(a, vt + (uint32_t)((i / 4) * TK * 128 + kk * 128 + ((pc ^ (kk & 7)) << 4)));
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            if (u == 0 && n == 0)
+                                mma_set<true>(acc, a[0] & mk[u][0], a[1] & mk[u][0], a[2] & mk[u][1], a[3] & mk[u][1], pb[u][n][0], pb[u][n][1]);
+                            else
+                                mma_add<true>(acc, a[0] & mk[u][0], a[1] & mk[u][0], a[2] & mk[u][1], a[3] & mk[u][1], pb[u][n][0], pb[u][n][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) add2(o[i][e], o[i][e + 1], acc[e], acc[e + 1]);
+                }
+            }
+        };
+
+        bool dead = false, begin = true;
+        while (t < tb) {
+            if (begin) {
+                begin = false;
+                if (KV4) {
+                    // scaled by the power of two that puts the head's largest value near 2^14
                     float x[MT * 4];
                     float big = 0.f;
 #pragma unroll
                     for (int i = 0; i < MT / 2; ++i) {
-                        const uint4 w = live ? reinterpret_cast<const uint4 *>(qh + (D / 4) * c)[i] : make_uint4(0, 0, 0, 0);
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                        const uint32_t u[4] = {qraw[i].x, qraw[i].y, qraw[i].z, qraw[i].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             x[8 * i + 2 * j] = bf16lo_to_f32(u[j]);
@@ -477,15 +811,13 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                     ka1 = p.k2_hi * d1;
                     kb1 = p.k2_lo * d1;
                 } else {
-                    // lane c holds dimensions 16 c .. of each 64: step (half, u, w) takes 4 of them
                     const uint32_t flip = p.qsign < 0.f ? 0x80008000u : 0u;
 #pragma unroll
                     for (int i = 0; i < MT / 2; ++i) {
-                        const uint4 w = live ? reinterpret_cast<const uint4 *>(qh + (i / 2) * 64 + 16 * c)[i & 1] : make_uint4(0, 0, 0, 0);
-                        qf[2 * i][0] = w.x ^ flip;
-                        qf[2 * i][1] = w.y ^ flip;
-                        qf[2 * i + 1][0] = w.z ^ flip;
-                        qf[2 * i + 1][1] = w.w ^ flip;
+                        qf[2 * i][0] = qraw[i].x ^ flip;
+                        qf[2 * i][1] = qraw[i].y ^ flip;
+                        qf[2 * i + 1][0] = qraw[i].z ^ flip;
+                        qf[2 * i + 1][1] = qraw[i].w ^ flip;
                     }
                 }
 #pragma unroll
@@ -499,275 +831,36 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 if (lane == 0) set_dev_error(p.ctrl, DEV_TIMEOUT);
                 int s2 = cs;
                 uint32_t ph = cphase;
-                for (int x = t; x < it; ++x) {
+                for (int x = 0; x < held; ++x) {
                     mbar_wait_bounded(&bar[s2], ph, DRAIN_NS);
                     s2 = s2 + 1 == NS ? 0 : s2 + 1;
                     if (s2 == 0) ph ^= 1u;
                 }
             }
+            const int k0 = cg.key0(t);
             if (!dead) {
+                --held;
                 const uint8_t *st = ring + cs * STAGE;
-                const int k0 = cg.key0(t);
-                // every key of the tile visible: no masks
-                const bool whole = (k0 >= cg.t.w0 || k0 + TK <= p.sinks) && k0 + TK <= cg.n;
-                auto seen = [&](int j) { return j < cg.n && (j >= cg.t.w0 || j < p.sinks); };
-
-                // ---- scores of keys r, r+8 of each 16, columns 2c, 2c+1
-                float s[SUB][4];
-#pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    float acc[MT / 2][4];  // chains of two steps
-                    if (KV4) {
-                        uint32_t a[2][MT][2];  // rows r, r+8: per step two fp16 pairs
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int kr = 16 * u + r + 8 * y;
-                            uint32_t w[D / 32];
-                            uint32_t sc[2];
-                            if (D == 128) {
-                                const uint4 x = *reinterpret_cast<const uint4 *>(st + kr * 64 + c * 16);
-                                w[0] = x.x, w[1] = x.y, w[D / 32 - 2] = x.z, w[D / 32 - 1] = x.w;
-                                sc[0] = (uint32_t)st[TK * D + kr * 8 + 2 * c] * 0x00800080u;  // twice, as fp16
-                                sc[1] = (uint32_t)st[TK * D + kr * 8 + 2 * c + 1] * 0x00800080u;
-                            } else {
-                                const uint2 x = *reinterpret_cast<const uint2 *>(st + kr * 32 + c * 8);
-                                w[0] = x.x, w[1] = x.y;
-                                sc[0] = sc[1] = (uint32_t)st[TK * D + kr * 4 + c] * 0x00800080u;
-                            }
-#pragma unroll
-                            for (int j = 0; j < D / 32; ++j) {
-                                uint32_t h[4];
-                                e2m1_unpack8(w[j], h);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) a[y][2 * j + i / 2][i & 1] = h2mul(h[i], sc[j / 2]);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < MT; i += 2) {
-                            mma_set<false>(acc[i / 2], a[0][i][0], a[1][i][0], a[0][i][1], a[1][i][1], qf[i][0], qf[i][1]);
-                            mma_add<false>(acc[i / 2], a[0][i + 1][0], a[1][i + 1][0], a[0][i + 1][1], a[1][i + 1][1], qf[i + 1][0],
-                                           qf[i + 1][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < MT / 2; ++i) {  // piece i & 1 of the lane's 16 dimensions of half i / 2
-                            const uint8_t *kt = st + (i / 2) * TK * 128;
-                            const int pc = 2 * c + (i & 1), kr = 16 * u + r;
-                            const uint4 x = *reinterpret_cast<const uint4 *>(kt + kr * 128 + ((pc ^ r) << 4));
-                            const uint4 y = *reinterpret_cast<const uint4 *>(kt + (kr + 8) * 128 + ((pc ^ r) << 4));
-                            mma_set<true>(acc[i], x.x, y.x, x.y, y.y, qf[2 * i][0], qf[2 * i][1]);
-                            mma_add<true>(acc[i], x.z, y.z, x.w, y.w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x[MT / 2];
-#pragma unroll
-                        for (int i = 0; i < MT / 2; ++i) x[i] = acc[i][e];
-                        s[u][e] = MT == 8 ? (x[0] + x[1]) + (x[MT / 2 - 2] + x[MT / 2 - 1]) : x[0] + x[1];
-                    }
-                }
-                if (!whole)
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        const int ja = k0 + 16 * u + r;
-                        if (!seen(ja)) s[u][0] = s[u][1] = NEG_INF;
-                        if (!seen(ja + 8)) s[u][2] = s[u][3] = NEG_INF;
-                    }
-
-                // ---- a new maximum, when it is far above the one that set c
-                float x0 = NEG_INF, x1 = NEG_INF;
-#pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    x0 = fmaxf(x0, fmaxf(s[u][0], s[u][2]));
-                    x1 = fmaxf(x1, fmaxf(s[u][1], s[u][3]));
-                }
-                if (__any_sync(FULL, x0 > thr0 || x1 > thr1)) {
-#pragma unroll
-                    for (int m = 4; m <= 16; m <<= 1) {
-                        x0 = fmaxf(x0, __shfl_xor_sync(FULL, x0, m));
-                        x1 = fmaxf(x1, __shfl_xor_sync(FULL, x1, m));
-                    }
-                    float f0 = 1.f, f1 = 1.f;
-                    if (x0 > thr0) {
-                        const float cn = fmaf(-x0, ka0, WN_TOP);
-                        f0 = ex2(fminf(cn - c0, 0.f));  // (of empty sums c is not yet set)
-                        c0 = cn;
-                        thr0 = x0 + WN_SLACK / ka0;
-                    }
-                    if (x1 > thr1) {
-                        const float cn = fmaf(-x1, ka1, WN_TOP);
-                        f1 = ex2(fminf(cn - c1, 0.f));
-                        c1 = cn;
-                        thr1 = x1 + WN_SLACK / ka1;
-                    }
-                    l0 *= f0;
-                    l1 *= f1;
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        o[i][0] *= f0;
-                        o[i][1] *= f1;
-                        o[i][2] *= f0;
-                        o[i][3] *= f1;
-                    }
-                }
-
-                // ---- p, its sum, and its terms as the B operand of V^T p
-                uint32_t pb[SUB][NB][2];
-#pragma unroll
-                for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        s[u][2 * y] = ex2(fmaf(s[u][2 * y], kb0, fmaf(s[u][2 * y], ka0, c0)));
-                        s[u][2 * y + 1] = ex2(fmaf(s[u][2 * y + 1], kb1, fmaf(s[u][2 * y + 1], ka1, c1)));
-                    }
-                if (!whole)
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            if (!seen(k0 + 16 * u + r + 8 * y)) s[u][2 * y] = s[u][2 * y + 1] = 0.f;
-#pragma unroll
-                for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        float a = s[u][2 * y], b = s[u][2 * y + 1];
-                        l0 += a;
-                        l1 += b;
-                        if (KV4 && !WIDE) {
-                            // columns 0-3 the first term, 4-7 what it leaves: second = 0 or 1
-                            const float2 f = unpack_f16(pack_f16(a, b));
-                            pb[u][0][y] = movmatrix(pack_f16(fmaf(-second, f.x, a), fmaf(-second, f.y, b)));
-                            continue;
-                        }
-                        uint32_t term[NP];
-#pragma unroll
-                        for (int i = 0; i < NP; ++i) {
-                            if (KV4) {
-                                term[i] = pack_f16(a, b);
-                                const float2 f = unpack_f16(term[i]);
-                                a -= f.x;
-                                b -= f.y;
-                            } else {
-                                term[i] = pack_bf16(a, b);
-                                a -= bf16lo_to_f32(term[i]);
-                                b -= bf16hi_to_f32(term[i]);
-                            }
-                        }
-                        if (WIDE) {
-#pragma unroll
-                            for (int i = 0; i < NP; ++i) pb[u][i % NB][y] = movmatrix(term[i]);
-                        } else {
-                            pb[u][0][y] = movmatrix(c < 2 ? term[0] : term[1]);
-                            pb[u][NB - 1][y] = movmatrix(c < 2 ? term[NP - 1] : 0u);
-                        }
-                    }
-
-                // ---- o += V^T p, the tile's keys in one chain per piece
                 if (KV4) {
-                    const uint8_t *vt = st + TK * (D / 2), *vsc = st + TK * (D + D / 16);
-                    constexpr int RB = D / 2, W = D / 64;  // bytes of a row; words of a lane's D/8 dimensions
-                    uint32_t vw[SUB][4][W], sp[SUB][2];
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        uint32_t sb[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int kk = 16 * u + 2 * c + (i & 1) + 8 * (i >> 1);
-                            if (W == 2) {
-                                const uint2 x = *reinterpret_cast<const uint2 *>(vt + kk * RB + r * 8);
-                                vw[u][i][0] = x.x, vw[u][i][W - 1] = x.y;
-                            } else {
-                                vw[u][i][0] = *reinterpret_cast<const uint32_t *>(vt + kk * RB + r * 4);
-                            }
-                            sb[i] = vsc[kk * (D / 16) + (D == 128 ? r : r >> 1)];
-                        }
-                        sp[u][0] = sb[1] * 0x800000u + sb[0] * 0x80u;  // the key pair's scales as fp16
-                        sp[u][1] = sb[3] * 0x800000u + sb[2] * 0x80u;
-                    }
-                    if (!whole)  // what is not seen may be a NaN
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int j = k0 + 16 * u + 2 * c + 8 * y;
-                                sp[u][y] &= (seen(j) ? 0xffffu : 0u) | (seen(j + 1) ? 0xffff0000u : 0u);
-                            }
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        float acc[4][4];
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u) {
-                            uint32_t a[2][2][4];  // key pair, even or odd dimension, byte
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t x0w = vw[u][2 * y][w], x1w = vw[u][2 * y + 1][w];
-                                e2m1_unpack8((x0w & 0x0f0f0f0fu) | ((x1w << 4) & 0xf0f0f0f0u), a[y][0]);
-                                e2m1_unpack8(((x0w >> 4) & 0x0f0f0f0fu) | (x1w & 0xf0f0f0f0u), a[y][1]);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    a[y][0][i] = h2mul(a[y][0][i], sp[u][y]);
-                                    a[y][1][i] = h2mul(a[y][1][i], sp[u][y]);
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int n = 0; n < NB; ++n) {
-                                    if (u == 0 && n == 0)
-                                        mma_set<false>(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
-                                    else
-                                        mma_add<false>(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
-                                }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[4 * w + i][e] += acc[i][e];
-                    }
+                    const int2 rw = cg.rows(k0, p.sinks);
+#pragma unroll 1
+                    for (int i = (rw.x - k0) & ~(HK - 1); k0 + i < rw.y; i += HK)
+                        pass(st + i * (D / 2), st + (TK + i) * (D / 2), st + TK * D + i * (D / 16),
+                             st + TK * (D + D / 16) + i * (D / 16), k0 + i);
                 } else {
-                    const uint32_t vt = smem_u32(st + TK * D * 2);
-                    uint32_t mk[SUB][2];
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) mk[u][0] = mk[u][1] = 0xffffffffu;
-                    if (!whole)  // what is not seen may be a NaN
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int j = k0 + 16 * u + 2 * c + 8 * y;
-                                mk[u][y] = (seen(j) ? 0xffffu : 0u) | (seen(j + 1) ? 0xffff0000u : 0u);
-                            }
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        float acc[4];
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u) {
-                            // matrices: keys 0-7 and 8-15 by dimensions 0-7 and 8-15 of piece i
-                            const int kk = 16 * u + (lane & 7) + ((lane >> 4) << 3);
-                            const int pc = 2 * (i & 3) + ((lane >> 3) & 1);
-                            uint32_t a[4];
-                            ldmatrix_x4_trans(a, vt + (uint32_t)((i / 4) * TK * 128 + kk * 128 + ((pc ^ (kk & 7)) << 4)));
-#pragma unroll
-                            for (int n = 0; n < NB; ++n) {
-                                if (u == 0 && n == 0)
-                                    mma_set<true>(acc, a[0] & mk[u][0], a[1] & mk[u][0], a[2] & mk[u][1], a[3] & mk[u][1], pb[u][n][0], pb[u][n][1]);
-                                else
-                                    mma_add<true>(acc, a[0] & mk[u][0], a[1] & mk[u][0], a[2] & mk[u][1], a[3] & mk[u][1], pb[u][n][0], pb[u][n][1]);
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i][e] += acc[e];
-                    }
+                    pass(st, st + TK * D * 2, nullptr, nullptr, k0);
                 }
             }
             __syncwarp();
             cs = cs + 1 == NS ? 0 : cs + 1;
             if (cs == 0) cphase ^= 1u;
             if (!dead && it < tb) fetch();
-            if (t + 1 != cg.end() && t + 1 != tb) continue;
+            ++t;
+            if (t != cg.end() && t != tb) continue;
 
             // ---- the group's last tile here: its result, or a piece of it
+            const bool ended = t == cg.end(), all = ta <= cg.start && ended;
+            if (ended) t += WN_SETUP;
             // sums that no score has set c for are empty (or NaN): they weigh nothing
             if (thr0 == NEG_INF) c0 = -NEG_INF;
             if (thr1 == NEG_INF) c1 = -NEG_INF;
@@ -776,14 +869,14 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 l0 += __shfl_xor_sync(FULL, l0, m);
                 l1 += __shfl_xor_sync(FULL, l1, m);
             }
-            const bool all = ta <= cg.start && cg.end() <= tb;
-            const int slot = t + 1 == tb ? 1 : 0;  // the warp's last group, else its first
-            float *piece = slot ? reinterpret_cast<float *>(ring)
-                                : p.first + (size_t)(blockIdx.x * WN_WARPS + warp) * PIECE;
+            // a piece lies in the warp's ring if it is the warp's last, else in the workspace
+            const int slot = t < tb ? 0 : 1;
+            float *piece = slot ? reinterpret_cast<float *>(ring) : p.first + (size_t)(blockIdx.x * W + warp) * PIECE;
             const size_t orow = (size_t)cg.b * p.H_q + cg.g * p.G;
             // heads of the lane's values: x of column 2c (and y of 2c+1 in wide groups)
             const int hx = WIDE ? 2 * c : 2 * (c & 1) + (c >> 1);
             const float lx = WIDE || c < 2 ? l0 : l1, cx = WIDE || c < 2 ? c0 : c1;
+            const float ix = 1.f / lx, iz = 1.f / l1;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -795,11 +888,11 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                         x = (c < 2 ? x : z) + got;
                     }
                     if (hx < p.G) {
-                        if (all) win_store(p, (orow + hx) * D + dim, x / lx);
+                        if (all) win_store(p, (orow + hx) * D + dim, x * ix);
                         else piece[hx * D + dim] = x;
                     }
                     if (WIDE && hx + 1 < p.G) {
-                        if (all) win_store(p, (orow + hx + 1) * D + dim, z / l1);
+                        if (all) win_store(p, (orow + hx + 1) * D + dim, z * iz);
                         else piece[(hx + 1) * D + dim] = z;
                     }
                 }
@@ -814,7 +907,11 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 }
                 if (lane == 0) seg[2 * warp + slot] = cg.index(p);
             }
-            if (t + 1 < tb) cg.next(nb, p);
+            if (t < tb) {
+                cg.next(nb, p);
+                load_q();
+                begin = true;
+            }
         }
     }
     __syncthreads();  // (also makes the pieces in the workspace visible to the CTA)
@@ -823,10 +920,10 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     // pieces, which are the first stage of each warp's ring
     float *scratch = reinterpret_cast<float *>(smem + lay.ring + STAGE);
     float *red = reinterpret_cast<float *>(smem + lay.ring + (NS + 1) * STAGE);
-    const int mine = lane < 2 * WN_WARPS ? seg[lane] : -1;
+    const int mine = lane < 2 * W ? seg[lane] : -1;
     const unsigned same = __match_any_sync(FULL, mine);
     unsigned leaders = __ballot_sync(FULL, mine >= 0 && lane == __ffs((int)same) - 1);
-    int open0 = -1, open1 = -1;  // the CTA's groups that other CTAs share: the first, the last
+    int open0 = -1, open1 = -1;  // the CTA's groups that other CTAs share: begun before it, begun here
     while (leaders) {
         const int i = __ffs((int)leaders) - 1;
         leaders &= leaders - 1;
@@ -834,9 +931,9 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         const unsigned set = __shfl_sync(FULL, same, i);
         const int b = gi / p.H_kv;
         const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
-        const int start = prefix[b] + gi % p.H_kv * cnt;
-        const bool all = t0 <= start && start + cnt <= t1;
-        const int slot = t0 >= start ? 0 : 1;
+        const int start = prefix[b] + gi % p.H_kv * win_span(cnt) + WN_SETUP;
+        const int slot = t0 <= start ? 1 : 0;  // begun here, or before
+        const bool all = slot && start + cnt <= t1;
         if (!all) (slot ? open1 : open0) = gi;
         // seg[j]: which is the j-th of the group's pieces (the end of a join has freed it)
         __syncthreads();
@@ -845,9 +942,9 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         auto piece_of = [&](int j) -> const float * {
             const int x = seg[j];
             return (x & 1) ? reinterpret_cast<const float *>(smem + lay.ring + (x >> 1) * NS * STAGE)
-                           : p.first + (size_t)(blockIdx.x * WN_WARPS + (x >> 1)) * PIECE;
+                           : p.first + (size_t)(blockIdx.x * W + (x >> 1)) * PIECE;
         };
-        win_join<D, false>(p, __popc(set), piece_of, scratch, red, gi, all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE);
+        win_join<D, NT, false>(p, __popc(set), piece_of, scratch, red, gi, all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE);
     }
     if (open0 < 0 && open1 < 0) return;
 
@@ -860,12 +957,12 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         if (gi >= 0) {
             const int b = gi / p.H_kv;
             const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
-            const int start = prefix[b] + gi % p.H_kv * cnt;
+            const int start = prefix[b] + gi % p.H_kv * win_span(cnt) + WN_SETUP;
             const int ca = win_owner(start, NC, T), n = win_owner(start + cnt - 1, NC, T) - ca + 1;
             if (atomicAdd(p.ctrl + CTRL_GROUPS + gi, 1) == n - 1) {
                 p.ctrl[CTRL_GROUPS + gi] = 0;
                 flag[tid] = n;
-                flag[2 + tid] = 2 * ca + (win_share(ca, NC, T) >= start ? 0 : 1);  // its first piece
+                flag[2 + tid] = ca;
             }
         }
     }
@@ -873,24 +970,23 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     __threadfence();
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        const int n = flag[x], at = flag[2 + x];
+        const int n = flag[x], ca = flag[2 + x];
         if (n == 0) continue;
-        // piece j is the first of CTA ca + j, but for the CTA that the group begins in
-        auto piece_of = [&](int j) -> const float * { return p.part + (size_t)(j ? (at & ~1) + 2 * j : at) * PIECE; };
+        auto piece_of = [&](int j) -> const float * { return p.part + (size_t)(2 * (ca + j) + (j == 0)) * PIECE; };
         // (the rings are free: n <= WN_MAX_CTAS pieces take 37 KB of them)
         float *far = reinterpret_cast<float *>(smem + lay.ring);
-        win_join<D, true>(p, n, piece_of, far + 4 * WN_NT, far, x ? open1 : open0, nullptr);
+        win_join<D, NT, true>(p, n, piece_of, far + WN_RED, far, x ? open1 : open0, nullptr);
     }
 }
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(WN_NT, 2) santa_window_kv4_kernel(const WinParams p)
+__global__ void __launch_bounds__(32 * win_warps(true), 1) santa_window_kv4_kernel(const WinParams p)
 {
     window_body<D, true, WIDE>(p, nullptr, nullptr);
 }
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(WN_NT, 1)
+__global__ void __launch_bounds__(32 * win_warps(false), 1)
     santa_window_bf16_kernel(const WinParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v)
 {
     window_body<D, false, WIDE>(p, &tm_k, &tm_v);

@@ -100,11 +100,13 @@ int check_window(const santa_shape *sh, const void *q, const int32_t *seq_lens, 
     return SANTA_OK;
 }
 
-// CTAs that can hold a share of the shape's tiles: the workspace has pieces for as many.
+// CTAs that can hold a share of the shape's list of tiles (of either cache): the workspace
+// has pieces for as many.
 long long window_ctas(const santa_shape *sh)
 {
-    const long long tiles = (long long)sh->B * sh->H_kv * ((sh->n_max + 15) / 16);
-    return std::min<long long>(WN_MAX_CTAS, (tiles + WN_WARPS - 1) / WN_WARPS);
+    const long long spans = (long long)sh->B * sh->H_kv * ((sh->n_max + 15) / 16 + WN_SETUP);
+    const int w = std::min(win_warps(false), win_warps(true));
+    return std::min<long long>(WN_MAX_CTAS, (spans + w - 1) / w);
 }
 
 const void *window_kernel(int D, bool kv4, bool wide)
@@ -131,7 +133,7 @@ int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void
     const long long cap = window_ctas(sh);
     p.ctrl = reinterpret_cast<int32_t *>(ws);
     p.first = reinterpret_cast<float *>(ws + CTRL_BYTES);
-    p.part = p.first + (size_t)cap * WN_WARPS * win_piece(G, D);
+    p.part = p.first + (size_t)cap * win_warps(kv4) * win_piece(G, D);
     p.B = sh->B;
     p.H_q = sh->H_q;
     p.H_kv = sh->H_kv;
@@ -147,20 +149,18 @@ int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void
 
     int dev, sms, optin, rc;
     if ((rc = device_info(&dev, &sms, &optin))) return rc;
-    // 4-bit: two CTAs to an SM (their registers and rings share it); bf16: one with the whole ring
-    const int room = kv4 ? (optin + 1024) / 2 - 1024 : optin;
     p.nstages = 8;
-    while (p.nstages > 2 && win_smem(D, kv4, sh->B, p.nstages).total > room) --p.nstages;
+    while (p.nstages > 2 && win_smem(D, kv4, sh->B, p.nstages).total > optin) --p.nstages;
     const int smem = win_smem(D, kv4, sh->B, p.nstages).total;
     if (smem > optin) return SANTA_ERR_UNSUPPORTED;
     const void *fn = window_kernel(D, kv4, G > 4);
     int occ = 0;
-    if ((rc = prepare_fn(fn, dev, smem, WN_NT, &occ))) return rc;
+    if ((rc = prepare_fn(fn, dev, smem, 32 * win_warps(kv4), &occ))) return rc;
     const int tile = win_tile(D, kv4);
     const int most = p.window > 0 ? (int)std::min<long long>(sh->n_max, (long long)p.window + p.sinks) : sh->n_max;
     // a group's visible keys touch at most two tiles more than they would fill
-    const long long tiles = (long long)sh->B * sh->H_kv * ((most + tile - 1) / tile + 2);
-    const long long grid = std::min(std::min<long long>(cap, (long long)sms * occ), (tiles + WN_WARPS - 1) / WN_WARPS);
+    const long long spans = (long long)sh->B * sh->H_kv * ((most + tile - 1) / tile + 2 + WN_SETUP);
+    const long long grid = std::min(std::min<long long>(cap, (long long)sms * occ), (spans + win_warps(kv4) - 1) / win_warps(kv4));
     CUtensorMap tm_k, tm_v;
     if (!kv4) {
         const long long rows = (long long)sh->B * sh->H_kv * sh->n_max;
@@ -168,7 +168,7 @@ int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void
         if ((rc = make_map_bf16(&tm_v, v, D, rows, tile))) return rc;
     }
     void *args[] = {&p, &tm_k, &tm_v};
-    if (cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(WN_NT), args, (size_t)smem, (cudaStream_t)stream) != cudaSuccess)
+    if (cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(32 * win_warps(kv4)), args, (size_t)smem, (cudaStream_t)stream) != cudaSuccess)
         return SANTA_ERR_CUDA;
     return SANTA_OK;
 }
@@ -195,7 +195,7 @@ int santa_window_workspace_size(const santa_shape *shape, size_t *bytes)
     if (rc || (rc = check_groups(shape))) return rc;
     if (!bytes) return SANTA_ERR_INVALID_ARG;
     const size_t piece = (size_t)win_piece(shape->H_q / shape->H_kv, shape->d) * sizeof(float);
-    *bytes = align_up(CTRL_BYTES + (size_t)window_ctas(shape) * (WN_WARPS + 2) * piece, 256);
+    *bytes = align_up(CTRL_BYTES + (size_t)window_ctas(shape) * (WN_MAX_WARPS + 2) * piece, 256);
     return SANTA_OK;
 }
 

@@ -337,6 +337,11 @@ def _kv4_dims(cache: KV4Cache):
     return B, H_kv, n_max, half * 2, dev
 
 
+def _kv4_arg(cache: KV4Cache):
+    k, ks, v, vs = cache
+    return ctypes.byref(_Kv4(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr()))
+
+
 class _on_device:
     """The library launches on the current device: make it the tensors' own for the call."""
     __slots__ = ("dev", "ctx")
@@ -355,17 +360,28 @@ class _on_device:
             self.ctx.__exit__(*e)
 
 
-def _stream_on(stream, dev) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+_shapes: dict = {}
+
+
+def _shape_of(key):
+    """(the shape as a C argument, the workspace bytes of a windowed call), kept per shape."""
+    got = _shapes.get(key)
+    if got is None:
+        shape, n = make_shape(*key), ctypes.c_size_t(0)
+        _check(load().santa_window_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "santa_window_workspace_size")
+        if len(_shapes) >= 1024:
+            _shapes.clear()
+        got = _shapes[key] = (ctypes.byref(shape), int(n.value))
+    return got
 
 
 def _call_workspace(nbytes: int, dev, stream) -> torch.Tensor:
-    """The workspace of a call that was given none: one per device and stream, or, inside a
-    stream capture, one of the graph's own (two graphs that share one could not be replayed
-    at the same time, and its clearing has to be part of the graph)."""
+    """The workspace of a call on `stream` that was given none: one per device and stream, or,
+    inside a stream capture, one of the graph's own (two graphs that share one could not be
+    replayed at the same time, and its clearing has to be part of the graph)."""
     if torch.cuda.is_current_stream_capturing():
         return new_workspace(nbytes, dev, stream)
-    return _cached_workspace(nbytes, dev, stream if stream is not None else torch.cuda.current_stream(dev))
+    return _cached_workspace(nbytes, dev, stream)
 
 
 def _move_rows(fn, what: str, cache, k, v, pos, counts, workspace, stream):
@@ -379,11 +395,15 @@ def _move_rows(fn, what: str, cache, k, v, pos, counts, workspace, stream):
     if counts is not None:
         _int_vector(counts, "counts", B, dev)
     rows = _Rows(k.data_ptr(), v.data_ptr(), k.stride()[:3], v.stride()[:3])
+    shape, _ = _shape_of((B, H_kv, H_kv, d, n_max))
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
     with _on_device(dev):
-        rc = fn(ctypes.byref(make_shape(B, H_kv, H_kv, d, n_max)), ctypes.byref(_Kv4(*(t.data_ptr() for t in cache))),
-                ctypes.byref(rows), k.shape[1], pos.data_ptr(), counts.data_ptr() if counts is not None else None,
-                workspace.data_ptr() if workspace is not None else None, _stream_on(stream, dev))
-    _check(rc, what)
+        rc = fn(shape, _kv4_arg(cache), ctypes.byref(rows), k.shape[1], pos.data_ptr(),
+                counts.data_ptr() if counts is not None else None,
+                workspace.data_ptr() if workspace is not None else None, stream.cuda_stream)
+    if rc:
+        _check(rc, what)
 
 
 def kv4_append(cache: KV4Cache, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor,
@@ -407,28 +427,30 @@ def kv4_read(cache: KV4Cache, pos: torch.Tensor, k_out: torch.Tensor, v_out: tor
     return k_out, v_out
 
 
-def _window_call(q, dims, kv_args, fn, what, seq_lens, window, sinks, scale, out, out_dtype, workspace, stream):
+def _window_call(q, dims, cache_args, fn, what, seq_lens, window, sinks, scale, out, out_dtype, workspace, stream):
     B, H_kv, n_max, d, dev = dims
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.device != dev:
+    qs = q.shape
+    if len(qs) != 3 or qs[0] != B or qs[2] != d or q.device != dev:
         raise ValueError("q [B, H_q, d] and the cache's shape or device disagree")
     _int_vector(seq_lens, "seq_lens", B, dev)
-    shape = make_shape(B, q.shape[1], H_kv, d, n_max, scale)
-    n = ctypes.c_size_t(0)
-    lib = load()
-    _check(lib.santa_window_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "santa_window_workspace_size")
+    shape, nbytes = _shape_of((B, qs[1], H_kv, d, n_max, scale))
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+        out = torch.empty(qs, dtype=out_dtype, device=dev)
         if stream is not None:
             out.record_stream(stream)
-    if out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or out.shape != q.shape or \
-            out.device != dev:
+    elif out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or out.shape != qs or out.device != dev:
         raise ValueError("out must be a contiguous fp32 or bf16 [B, H_q, d] tensor on q's device")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
     with _on_device(dev):
-        ws = workspace if workspace is not None else _call_workspace(n.value, dev, stream)
-        rc = getattr(lib, fn)(ctypes.byref(shape), q.data_ptr(), *kv_args, seq_lens.data_ptr(), int(window), int(sinks),
-                              OUT_BF16 if out.dtype == torch.bfloat16 else 0, out.data_ptr(), ws.data_ptr(), ws.numel(),
-                              _stream_on(stream, dev))
-    _check(rc, what)
+        ws = workspace if workspace is not None else _call_workspace(nbytes, dev, stream)
+        rc = fn(shape, q.data_ptr(), *cache_args, seq_lens.data_ptr(), window, sinks,
+                OUT_BF16 if out.dtype == torch.bfloat16 else 0, out.data_ptr(), ws.data_ptr(), ws.numel(),
+                stream.cuda_stream)
+    if rc:
+        _check(rc, what)
     return out
 
 
@@ -443,7 +465,7 @@ def decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.device != k_cache.device:
         raise ValueError("k_cache and v_cache [B, H_kv, n_max, d] disagree")
     return _window_call(q, (*k_cache.shape, k_cache.device), (k_cache.data_ptr(), v_cache.data_ptr()),
-                        "santa_decode_window", "santa_decode_window", seq_lens, window, sinks, scale, out, out_dtype,
+                        load().santa_decode_window, "santa_decode_window", seq_lens, window, sinks, scale, out, out_dtype,
                         workspace, stream)
 
 
@@ -453,6 +475,5 @@ def decode_kv4(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor, window:
     """One step of exact attention over a 4-bit cache: every key, or with window > 0 the last
     `window` keys and the first `sinks`.  Arguments and result as for decode_window."""
     _cuda_bf16(q, "q")
-    dims = _kv4_dims(cache)
-    return _window_call(q, dims, (ctypes.byref(_Kv4(*(t.data_ptr() for t in cache))),), "santa_decode_kv4",
-                        "santa_decode_kv4", seq_lens, window, sinks, scale, out, out_dtype, workspace, stream)
+    return _window_call(q, _kv4_dims(cache), (_kv4_arg(cache),), load().santa_decode_kv4, "santa_decode_kv4", seq_lens,
+                        window, sinks, scale, out, out_dtype, workspace, stream)
