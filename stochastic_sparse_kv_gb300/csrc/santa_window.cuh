@@ -81,7 +81,7 @@ struct WinParams {
 };
 
 struct WinSmem {
-    int ring, bar, seg, flag, nb, prefix, total;
+    int ring, bar, seg, flag, list, nb, prefix, total;
 };
 
 __host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B, int ns)
@@ -93,6 +93,7 @@ __host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B, int ns)
     s.bar = off; off += W * ns * 8;
     s.seg = off; off += 2 * W * 4;               // group index of each warp's two pieces, or -1
     s.flag = off; off += 16;
+    s.list = off; off += 32 * W;
     s.nb = off; off += (int)align_up((size_t)B * 4, 16);
     s.prefix = off; off += (int)align_up((size_t)(B + 1) * 4, 16);
     s.total = off + 1024;
@@ -268,9 +269,28 @@ struct WinGroup {
     }
 };
 
-// First position of share i of n shares of T positions, and the share that holds a position.
-__device__ __forceinline__ int win_share(int i, int n, int T) { return (int)((long long)i * T / n); }
-__device__ __forceinline__ int win_owner(int pos, int n, int T) { return (int)((((long long)pos + 1) * n - 1) / T); }
+// The list's T positions in n shares, the first T % n of them one longer: the first position
+// of share i, and the share that holds a position.
+struct WinShares {
+    int q, rem;
+
+    __device__ __forceinline__ WinShares(int T, int n) : q(T / n), rem(T % n) {}
+    __device__ __forceinline__ int first(int i) const { return i * q + min(i, rem); }
+    __device__ __forceinline__ int owner(int pos) const
+    {
+        const int wide = rem * (q + 1);
+        return pos < wide ? pos / (q + 1) : rem + (pos - wide) / q;
+    }
+};
+
+// One more piece of a group has been written (by this CTA, before a __syncthreads): the count
+// before it.  Later reads by the CTA, after another __syncthreads, see the counted ones.
+__device__ __forceinline__ int win_arrive(int32_t *counter)
+{
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(__cvta_generic_to_global(counter)) : "memory");
+    return old;
+}
 
 __device__ __forceinline__ void win_store(const WinParams &p, size_t i, float v)
 {
@@ -292,6 +312,16 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
     float *tot = scratch, *wt = scratch + 16, *lt = wt + 8 * n;
     auto load = [](const float *a) { return FAR ? __ldcg(a) : *a; };
     auto load4 = [](const float4 *a) { return FAR ? __ldcg(a) : *a; };
+    // four outputs a thread; with few outputs, slices of the pieces.  The first pieces are
+    // on their way while the weights are worked out
+    constexpr int AHEAD = FAR ? 8 : 1;
+    const int nv = GD / 4, ns = max(1, NT / nv);
+    const int v0 = tid % nv, sl0 = tid / nv;
+    float4 ahead[AHEAD];
+    if (tid < ns * nv)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (sl0 + k * ns < n) ahead[k] = load4(reinterpret_cast<const float4 *>(piece_of(sl0 + k * ns)) + v0);
     // a warp a head: its common exponent, the pieces' weights, the sum
     for (int h = tid >> 5; h < p.G; h += NT / 32) {
         float C = __int_as_float(0x7f800000);
@@ -318,21 +348,21 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
         }
     }
     __syncthreads();
-    // four outputs a thread; with few outputs, slices of the pieces
-    const int nv = GD / 4, ns = max(1, NT / nv);
-    for (int i = tid; i < ns * nv; i += NT) {
-        const int v = i % nv, sl = i / nv, hv = 4 * v / D;
+    auto add = [](float4 &o, const float4 &x, float w) {
+        o.x = fmaf(w, x.x, o.x);
+        o.y = fmaf(w, x.y, o.y);
+        o.z = fmaf(w, x.z, o.z);
+        o.w = fmaf(w, x.w, o.w);
+    };
+    if (tid < ns * nv) {
+        const int hv = 4 * v0 / D;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (sl0 + k * ns < n) add(o, ahead[k], wt[8 * (sl0 + k * ns) + hv]);
 #pragma unroll 8
-        for (int j = sl; j < n; j += ns) {
-            const float4 x = load4(reinterpret_cast<const float4 *>(piece_of(j)) + v);
-            const float w = wt[8 * j + hv];
-            o.x = fmaf(w, x.x, o.x);
-            o.y = fmaf(w, x.y, o.y);
-            o.z = fmaf(w, x.z, o.z);
-            o.w = fmaf(w, x.w, o.w);
-        }
-        reinterpret_cast<float4 *>(red)[i] = o;
+        for (int j = sl0 + AHEAD * ns; j < n; j += ns) add(o, load4(reinterpret_cast<const float4 *>(piece_of(j)) + v0), wt[8 * j + hv]);
+        reinterpret_cast<float4 *>(red)[tid] = o;
     }
     if (ns > 1) __syncthreads();
     for (int v = tid; v < nv; v += NT) {
@@ -434,8 +464,10 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             for (int i = tid; i < p.H_q * D; i += NT) win_store(p, (size_t)b * p.H_q * D + i, 0.f);
     const int NC = min((int)gridDim.x, (T + W - 1) / W);  // CTAs with a share
     if ((int)blockIdx.x >= NC) return;
-    const int t0 = win_share(blockIdx.x, NC, T), t1 = win_share(blockIdx.x + 1, NC, T);
-    const int ta = t0 + win_share(warp, W, t1 - t0), tb = t0 + win_share(warp + 1, W, t1 - t0);
+    const WinShares ctas(T, NC);
+    const int t0 = ctas.first(blockIdx.x), t1 = ctas.first(blockIdx.x + 1);
+    const WinShares warps(t1 - t0, W);
+    const int ta = t0 + warps.first(warp), tb = t0 + warps.first(warp + 1);
 
     WinGroup<TK> cg;  // the group of the tile at hand, t its position
     int t = ta;
@@ -920,6 +952,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     // pieces, which are the first stage of each warp's ring
     float *scratch = reinterpret_cast<float *>(smem + lay.ring + STAGE);
     float *red = reinterpret_cast<float *>(smem + lay.ring + (NS + 1) * STAGE);
+    uint8_t *list = reinterpret_cast<uint8_t *>(smem + lay.list) + 32 * warp;
     const int mine = lane < 2 * W ? seg[lane] : -1;
     const unsigned same = __match_any_sync(FULL, mine);
     unsigned leaders = __ballot_sync(FULL, mine >= 0 && lane == __ffs((int)same) - 1);
@@ -935,12 +968,11 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         const int slot = t0 <= start ? 1 : 0;  // begun here, or before
         const bool all = slot && start + cnt <= t1;
         if (!all) (slot ? open1 : open0) = gi;
-        // seg[j]: which is the j-th of the group's pieces (the end of a join has freed it)
-        __syncthreads();
-        if (warp == 0 && (set >> lane & 1)) seg[__popc(set & ((1u << lane) - 1))] = lane;
-        __syncthreads();
+        // list[j]: which is the j-th of the group's pieces, a copy for each warp
+        if (set >> lane & 1) list[__popc(set & ((1u << lane) - 1))] = (uint8_t)lane;
+        __syncwarp();
         auto piece_of = [&](int j) -> const float * {
-            const int x = seg[j];
+            const int x = list[j];
             return (x & 1) ? reinterpret_cast<const float *>(smem + lay.ring + (x >> 1) * NS * STAGE)
                            : p.first + (size_t)(blockIdx.x * W + (x >> 1)) * PIECE;
         };
@@ -949,7 +981,6 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     if (open0 < 0 && open1 < 0) return;
 
     // ---- groups that span CTAs: the last to arrive joins
-    __threadfence();
     __syncthreads();
     if (tid < 2) {
         const int gi = tid ? open1 : open0;
@@ -958,8 +989,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             const int b = gi / p.H_kv;
             const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
             const int start = prefix[b] + gi % p.H_kv * win_span(cnt) + WN_SETUP;
-            const int ca = win_owner(start, NC, T), n = win_owner(start + cnt - 1, NC, T) - ca + 1;
-            if (atomicAdd(p.ctrl + CTRL_GROUPS + gi, 1) == n - 1) {
+            const int ca = ctas.owner(start), n = ctas.owner(start + cnt - 1) - ca + 1;
+            if (win_arrive(p.ctrl + CTRL_GROUPS + gi) == n - 1) {
                 p.ctrl[CTRL_GROUPS + gi] = 0;
                 flag[tid] = n;
                 flag[2 + tid] = ca;
@@ -967,7 +998,6 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         }
     }
     __syncthreads();
-    __threadfence();
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int n = flag[x], ca = flag[2 + x];
