@@ -49,16 +49,18 @@ constexpr float WN_TOP = 9.f;             // log2 of p where a new maximum puts 
 constexpr float WN_SLACK = 6.f;           // and how far above that later ones may be
 constexpr int WN_SETUP = 2;               // tiles that beginning a group costs about as much as
 
-// One CTA to an SM.  4-bit: 12 warps, what 168 registers a thread allow (16 warps of 128
-// spill and are no faster, the conversions' pipe being the limit); bf16: the 8 whose rings fit.
+// One CTA to an SM.  4-bit: 12 warps, what 168 registers a thread allow (16 warps of 128 spill
+// and are slower), each copying its own tiles; bf16: the 8 whose rings fit, and one that
+// issues all of their copies.
 __host__ __device__ constexpr int win_warps(bool kv4) { return kv4 ? 12 : 8; }
-// Keys of a tile (a ring stage), and of one pass of the arithmetic over it.
-__host__ __device__ constexpr int win_tile(int D, bool kv4) { return kv4 ? 64 : D == 64 ? 32 : 16; }
-__host__ __device__ constexpr int win_pass(int D, bool kv4) { return kv4 || D == 64 ? 32 : 16; }
+__host__ __device__ constexpr int win_threads(bool kv4) { return 32 * (kv4 ? win_warps(true) : win_warps(false) + 1); }
+// Keys of a tile, which is a ring stage, and the stages of a warp's ring (what 227 KB hold).
+__host__ __device__ constexpr int win_tile(int D, bool kv4) { return kv4 || D == 64 ? 32 : 16; }
 __host__ __device__ constexpr int win_stage(int D, bool kv4)
 {
     return kv4 ? win_tile(D, true) * (D + D / 8) : win_tile(D, false) * D * 4;
 }
+__host__ __device__ constexpr int win_stages(int D, bool kv4) { return !kv4 ? 3 : D == 128 ? 4 : 8; }
 // A piece of a group's sums: fp32 o[G][D], c[8], l[8].
 __host__ __device__ constexpr int win_piece(int G, int D) { return G * D + 16; }
 
@@ -74,24 +76,24 @@ struct WinParams {
     int B, H_q, H_kv, n_max, G;
     int window, sinks;
     int out_bf16;
-    int nstages;
     float k2_hi, k2_lo;           // |scale| * log2(e) as an unevaluated sum
     float qsign;                  // the sign of scale
     uint64_t wait_ns;  // limit of a stage's wait
 };
 
 struct WinSmem {
-    int ring, bar, seg, flag, list, nb, prefix, total;
+    int ring, bar, seg, stop, flag, list, nb, prefix, total;
 };
 
-__host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B, int ns)
+__host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B)
 {
-    const int W = win_warps(kv4);
+    const int W = win_warps(kv4), ns = win_stages(D, kv4);
     WinSmem s{};
     int off = 0;
     s.ring = off; off += W * ns * win_stage(D, kv4);
-    s.bar = off; off += W * ns * 8;
+    s.bar = off; off += W * ns * 16;             // a full and an empty barrier for each stage
     s.seg = off; off += 2 * W * 4;               // group index of each warp's two pieces, or -1
+    s.stop = off; off += (int)align_up((size_t)W * 4, 16);  // set by a warp that gave up
     s.flag = off; off += 16;
     s.list = off; off += 32 * W;
     s.nb = off; off += (int)align_up((size_t)B * 4, 16);
@@ -107,11 +109,11 @@ template <bool BF16>
 __device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
     if (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -120,11 +122,11 @@ template <bool BF16>
 __device__ __forceinline__ void mma_set(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
     if (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
@@ -133,7 +135,7 @@ __device__ __forceinline__ void mma_set(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
 {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -166,6 +168,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// A barrier of the N threads that work.
+template <int N>
+__device__ __forceinline__ void bar_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ void add2(float &a, float &b, float x, float y)
 {
@@ -188,14 +197,42 @@ __device__ __forceinline__ float2 fma2(float a, float b, float x, float y, float
 
 __device__ __forceinline__ float2 unpack_f16(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 
-// Untiled bulk copy, global to this CTA's shared memory (16-byte aligned, multiple of 16).
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy)
+// Whether the phase of that parity has ended (no waiting).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
 {
+    uint32_t ok;
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
+    return ok != 0;
+}
+
+// Wait for the phase with the given parity; give up after limit_ns.  (A limit below a
+// microsecond, a diagnostic, polls: a suspended wait may outlast it.)
+__device__ __forceinline__ bool win_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (limit_ns >= 1000 ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
+// 16 bytes, global to shared memory, past the L1 cache; groups of them are waited for in order.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ------------------------------------------------------------------ the list of tiles
@@ -283,8 +320,8 @@ struct WinShares {
     }
 };
 
-// One more piece of a group has been written (by this CTA, before a __syncthreads): the count
-// before it.  Later reads by the CTA, after another __syncthreads, see the counted ones.
+// One more piece of a group has been written (by this CTA, before a barrier): the count before
+// it.  Reads by the CTA after another barrier see the counted ones.
 __device__ __forceinline__ int win_arrive(int32_t *counter)
 {
     int old;
@@ -347,7 +384,7 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
             tot[8 + h] = L;
         }
     }
-    __syncthreads();
+    bar_sync<NT>();
     auto add = [](float4 &o, const float4 &x, float w) {
         o.x = fmaf(w, x.x, o.x);
         o.y = fmaf(w, x.y, o.y);
@@ -364,7 +401,7 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
         for (int j = sl0 + AHEAD * ns; j < n; j += ns) add(o, load4(reinterpret_cast<const float4 *>(piece_of(j)) + v0), wt[8 * j + hv]);
         reinterpret_cast<float4 *>(red)[tid] = o;
     }
-    if (ns > 1) __syncthreads();
+    if (ns > 1) bar_sync<NT>();
     for (int v = tid; v < nv; v += NT) {
         const int hv = 4 * v / D;
         float4 o = reinterpret_cast<const float4 *>(red)[v];
@@ -394,7 +431,7 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
             }
         }
     }
-    __syncthreads();
+    bar_sync<NT>();
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -403,8 +440,8 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
 template <int D, bool KV4, bool WIDE>
 __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMap *tm_k, const CUtensorMap *tm_v)
 {
-    constexpr int W = win_warps(KV4), NT = 32 * W;
-    constexpr int TK = win_tile(D, KV4), HK = win_pass(D, KV4), SUB = HK / 16, STAGE = win_stage(D, KV4);
+    constexpr int W = win_warps(KV4), NT = 32 * W;  // warps and threads that work
+    constexpr int TK = win_tile(D, KV4), SUB = TK / 16, STAGE = win_stage(D, KV4), NS = win_stages(D, KV4);
     constexpr int MT = D / 16;   // 16-row pieces of the output, and MMA steps of a score
     constexpr int NP = KV4 ? 2 : 3;                     // terms of p
     constexpr int NB = WIDE ? NP : (KV4 ? 1 : 2);       // MMAs they take
@@ -413,11 +450,13 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    const int NS = p.nstages;
-    const WinSmem lay = win_smem(D, KV4, p.B, NS);
+    const WinSmem lay = win_smem(D, KV4, p.B);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
-    uint8_t *ring = smem + lay.ring + warp * NS * STAGE;
-    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + lay.bar) + warp * NS;
+    // (the copying warp: lane w works for warp w)
+    const int owner = warp < W ? warp : min(lane, W - 1);
+    uint8_t *ring = smem + lay.ring + owner * NS * STAGE;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + lay.bar) + owner * 2 * NS, *empty = full + NS;
+    volatile int *stop = reinterpret_cast<volatile int *>(smem + lay.stop);
     int *seg = reinterpret_cast<int *>(smem + lay.seg);
     int *flag = reinterpret_cast<int *>(smem + lay.flag);
     int *nb = reinterpret_cast<int *>(smem + lay.nb);
@@ -451,23 +490,24 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         if (lane == 0) prefix[p.B] = run;
         if (bad && blockIdx.x == 0) set_dev_error(p.ctrl, DEV_BAD_SEQLEN);
     }
-    if (lane == 0) {
-        for (int s = 0; s < NS; ++s) mbar_init(&bar[s], 1);
+    if (!KV4 && warp == W && lane < W) {
+        for (int s = 0; s < 2 * NS; ++s) mbar_init(&full[s], 1);
         mbar_fence_init();
-        seg[2 * warp] = seg[2 * warp + 1] = -1;
+        stop[lane] = 0;
     }
+    if (tid < 2 * W) seg[tid] = -1;
     __syncthreads();
 
     const int T = prefix[p.B];
     for (int b = blockIdx.x; b < p.B; b += gridDim.x)  // sequences without keys
         if (nb[b] == 0)
-            for (int i = tid; i < p.H_q * D; i += NT) win_store(p, (size_t)b * p.H_q * D + i, 0.f);
+            for (int i = tid; i < p.H_q * D; i += blockDim.x) win_store(p, (size_t)b * p.H_q * D + i, 0.f);
     const int NC = min((int)gridDim.x, (T + W - 1) / W);  // CTAs with a share
     if ((int)blockIdx.x >= NC) return;
     const WinShares ctas(T, NC);
     const int t0 = ctas.first(blockIdx.x), t1 = ctas.first(blockIdx.x + 1);
     const WinShares warps(t1 - t0, W);
-    const int ta = t0 + warps.first(warp), tb = t0 + warps.first(warp + 1);
+    const int ta = t0 + warps.first(owner), tb = t0 + warps.first(owner + 1);
 
     WinGroup<TK> cg;  // the group of the tile at hand, t its position
     int t = ta;
@@ -475,8 +515,68 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         cg.seek(ta, prefix, nb, p);
         t = max(ta, cg.start);
     }
-    if (t < tb) {
+    if (warp == W) {  // (bf16)
+        // ---- the copies: one lane a ring; `t` is the next tile to fetch, of group cg
         const uint64_t policy = l2_policy_evict_first();
+        bool live = lane < W && t < tb;
+        int filled = 0, is = 0;                       // stages filled, the next one to fill
+        uint32_t phase = 1;                           // a fresh barrier lets this parity pass
+        int jump = 0, k0 = 0;                         // where the rows break off; the tile's first key
+        auto follow = [&]() {
+            jump = t < cg.start + cg.t.ns ? cg.start + cg.t.ns : cg.end();
+            k0 = cg.key0(t);
+        };
+        if (live) follow();
+        uint64_t since = globaltimer_ns();
+        while (__any_sync(FULL, live)) {
+            const bool go = live && mbar_test(&empty[is], phase);
+            if (go) {
+                uint8_t *st = ring + is * STAGE;
+                {
+                    // whole boxes: rows past the group's last key are other keys or zeros, never used
+                    const int row = cg.index(p) * p.n_max + k0;
+                    mbar_arrive_tx(&full[is], (uint32_t)STAGE);
+#pragma unroll
+                    for (int hf = 0; hf < D / 64; ++hf) {
+                        tma_load_2d(st + hf * TK * 128, tm_k, hf * 64, row, &full[is], policy);
+                        tma_load_2d(st + TK * D * 2 + hf * TK * 128, tm_v, hf * 64, row, &full[is], policy);
+                    }
+                }
+                ++filled;
+                if (++is == NS) {
+                    is = 0;
+                    phase ^= 1u;
+                }
+                ++t;
+                k0 += TK;
+                if (t == jump) {  // the sinks end, or the group
+                    if (t == cg.end()) {
+                        t += WN_SETUP;
+                        if (t < tb) {
+                            cg.next(nb, p);
+                            const uint16_t *q0 = p.q + ((size_t)cg.b * p.H_q + cg.g * p.G) * D;  // its queries, into L2
+                            for (int i = 0; i < p.G * D; i += 64) prefetch_l2(q0 + i);
+                        }
+                    }
+                    if (t < tb) follow();
+                }
+                live = t < tb;
+            } else if (live && stop[lane]) {
+                live = false;
+            }
+            // (warps that work are never this slow; those that gave up have set `stop`)
+            if (__any_sync(FULL, go)) since = globaltimer_ns();
+            else if (globaltimer_ns() - since > p.wait_ns + DRAIN_NS) {
+                if (live) set_dev_error(p.ctrl, DEV_TIMEOUT);
+                live = false;
+            }
+        }
+        // every copy has landed before the CTA ends
+        if (lane < W)
+            for (int x = max(0, filled - NS); x < filled; ++x) mbar_wait_bounded(&full[x % NS], (uint32_t)(x / NS) & 1u, DRAIN_NS);
+        return;
+    }
+    if (t < tb) {
         // ---- a group's queries: head column r (zero in columns without a head).  4-bit: lane c
         // takes dimensions D/4 c .., four to an MMA step; bf16: 16 c .. of each 64
         uint4 qraw[MT / 2];
@@ -490,56 +590,71 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                                    : reinterpret_cast<const uint4 *>(qh + (i / 2) * 64 + 16 * c)[i & 1];
         };
         load_q();
-
-        // ---- the copies: `ig` is the group of the next tile to fetch, `it` its position
-        WinGroup<TK> ig = cg;
-        int it = t, is = 0, cs = 0, held = 0;  // stages to fill and to use next, copies not waited for
+        int cs = 0;            // the stage to use next
         uint32_t cphase = 0;
-        int fjump = it < ig.start + ig.t.ns ? ig.start + ig.t.ns : ig.end();  // where the rows break off
-        int fk = ig.key0(it);                                                 // the tile's first key
-        auto fetch = [&]() {
-            if (lane == 0) {
-                uint8_t *st = ring + is * STAGE;
-                if (KV4) {
-                    const int2 rw = ig.rows(fk, p.sinks);
-                    const uint32_t rows = rw.y - rw.x, o = rw.x - fk;  // multiples of 16, as n_max is
-                    const size_t at = (uint32_t)ig.index(p) * (uint32_t)p.n_max + (uint32_t)rw.x;
-                    mbar_arrive_tx(&bar[is], rows * (D + D / 8));
-                    bulk_load(st + o * (D / 2), p.k + at * (D / 2), rows * (D / 2), &bar[is], policy);
-                    bulk_load(st + TK * D + o * (D / 16), p.ks + at * (D / 16), rows * (D / 16), &bar[is], policy);
-                    bulk_load(st + TK * (D / 2) + o * (D / 2), p.v + at * (D / 2), rows * (D / 2), &bar[is], policy);
-                    bulk_load(st + TK * (D + D / 16) + o * (D / 16), p.vs + at * (D / 16), rows * (D / 16), &bar[is], policy);
-                } else {
-                    // whole boxes: rows past the group's last key are other keys or zeros, never used
-                    const int row = ig.index(p) * p.n_max + fk;
-                    mbar_arrive_tx(&bar[is], (uint32_t)STAGE);
-#pragma unroll
-                    for (int hf = 0; hf < D / 64; ++hf) {
-                        tma_load_2d(st + hf * TK * 128, tm_k, hf * 64, row, &bar[is], policy);
-                        tma_load_2d(st + TK * D * 2 + hf * TK * 128, tm_v, hf * 64, row, &bar[is], policy);
-                    }
-                }
-            }
-            is = is + 1 == NS ? 0 : is + 1;
-            ++held;
-            ++it;
-            fk += TK;
-            if (it == fjump) {  // the sinks end, or the group
-                if (it == ig.end()) {
-                    if (it + WN_SETUP >= tb) {  // no tile left here
-                        it = tb;
-                        return;
-                    }
-                    ig.next(nb, p);
-                    it = ig.start;
-                    const size_t q0 = ((size_t)ig.b * p.H_q + ig.g * p.G) * D;  // its queries, into L2
-                    if (lane * 64 < p.G * D) prefetch_l2(p.q + q0 + lane * 64);
-                }
-                fjump = it < ig.start + ig.t.ns ? ig.start + ig.t.ns : ig.end();
-                fk = ig.key0(it);
-            }
+
+        // ---- 4-bit: the copies, by all lanes.  `ig` is the group of the next tile to fetch, `it`
+        // its position, fk its first key; every call makes one group of copies
+        WinGroup<TK> ig = cg;
+        int it = t, fjump = 0, fk = 0;
+        auto follow = [&]() {
+            fjump = it < ig.start + ig.t.ns ? ig.start + ig.t.ns : ig.end();
+            fk = ig.key0(it);
         };
-        for (int i = 0; i < NS && it < tb; ++i) fetch();
+        auto fetch = [&](int stage) {
+            if (it < tb) {
+                constexpr int RB = D / 2, NC16 = TK * RB / 512, NS16 = TK * (D / 16) / 16;  // copies a lane; lanes for scales
+                const uint32_t dst = smem_u32(ring + stage * STAGE) + 16 * lane;
+                const size_t at = (uint32_t)ig.index(p) * (uint32_t)p.n_max + (uint32_t)fk;
+                const uint8_t *gk = p.k + at * RB + 16 * lane, *gv = p.v + at * RB + 16 * lane;
+                const uint8_t *gks = p.ks + at * (D / 16) + 16 * lane, *gvs = p.vs + at * (D / 16) + 16 * lane;
+                const int2 rw = ig.rows(fk, p.sinks);  // multiples of 16, as n_max is
+                if (rw.y - rw.x == TK) {
+#pragma unroll
+                    for (int i = 0; i < NC16; ++i) copy16(dst + 512 * i, gk + 512 * i);
+#pragma unroll
+                    for (int i = 0; i < NC16; ++i) copy16(dst + TK * RB + 512 * i, gv + 512 * i);
+                    if (lane < NS16) {
+                        copy16(dst + TK * D, gks);
+                        copy16(dst + TK * (D + D / 16), gvs);
+                    }
+                } else {
+                    const int lo = rw.x - fk, hi = rw.y - fk;
+#pragma unroll
+                    for (int i = 0; i < NC16; ++i) {
+                        const int row = (512 * i + 16 * lane) / RB;
+                        if (row >= lo && row < hi) {
+                            copy16(dst + 512 * i, gk + 512 * i);
+                            copy16(dst + TK * RB + 512 * i, gv + 512 * i);
+                        }
+                    }
+                    const int row = 16 * lane / (D / 16);
+                    if (row >= lo && row < hi) {
+                        copy16(dst + TK * D, gks);
+                        copy16(dst + TK * (D + D / 16), gvs);
+                    }
+                }
+                ++it;
+                fk += TK;
+                if (it == fjump) {  // the sinks end, or the group
+                    if (it == ig.end()) {
+                        it += WN_SETUP;
+                        if (it < tb) {
+                            ig.next(nb, p);
+                            const uint16_t *q0 = p.q + ((size_t)ig.b * p.H_q + ig.g * p.G) * D;  // its queries, into L2
+                            if (lane * 64 < p.G * D) prefetch_l2(q0 + lane * 64);
+                        }
+                    }
+                    if (it < tb) follow();
+                }
+            }
+            copy_commit();
+        };
+        if (KV4) {
+            follow();
+#pragma unroll
+            for (int i = 0; i < NS; ++i) fetch(i);
+        }
 
         // ---- the sums
         uint32_t qf[MT][2];                  // B operand of the scores
@@ -547,10 +662,10 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         float l0 = 0.f, l1 = 0.f, c0 = 0.f, c1 = 0.f, thr0 = NEG_INF, thr1 = NEG_INF;
         float ka0 = p.k2_hi, ka1 = p.k2_hi, kb0 = p.k2_lo, kb1 = p.k2_lo;
         const float second = c < 2 ? 0.f : -1.f;
-        // ---- one pass: the HK keys from k0, whose rows and scales the pointers are at
+        // ---- one tile: the keys from k0, whose rows and scales the pointers are at
         auto pass = [&](const uint8_t *kc, const uint8_t *vc, const uint8_t *ks, const uint8_t *vs, int k0) {
             // every key visible: no masks
-            const bool whole = (k0 >= cg.t.w0 || k0 + HK <= p.sinks) && k0 + HK <= cg.n;
+            const bool whole = (k0 >= cg.t.w0 || k0 + TK <= p.sinks) && k0 + TK <= cg.n;
             auto seen = [&](int j) { return j < cg.n && (j >= cg.t.w0 || j < p.sinks); };
 
             // ---- scores of keys r, r+8 of each 16, columns 2c, 2c+1
@@ -857,36 +972,29 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 l0 = l1 = c0 = c1 = 0.f;
                 thr0 = thr1 = NEG_INF;
             }
-            if (!dead && !__all_sync(FULL, mbar_wait_bounded(&bar[cs], cphase, p.wait_ns))) {
-                // no more copies, no more sums (the pieces still meet): those in flight end first
-                dead = true;
-                if (lane == 0) set_dev_error(p.ctrl, DEV_TIMEOUT);
-                int s2 = cs;
-                uint32_t ph = cphase;
-                for (int x = 0; x < held; ++x) {
-                    mbar_wait_bounded(&bar[s2], ph, DRAIN_NS);
-                    s2 = s2 + 1 == NS ? 0 : s2 + 1;
-                    if (s2 == 0) ph ^= 1u;
+            if (KV4) {
+                copy_wait<NS - 1>();
+                __syncwarp();
+            } else if (!dead && !__all_sync(FULL, win_wait(&full[cs], cphase, p.wait_ns))) {
+                dead = true;  // no more copies, no more sums (the pieces still meet)
+                if (lane == 0) {
+                    set_dev_error(p.ctrl, DEV_TIMEOUT);
+                    stop[warp] = 1;
                 }
             }
             const int k0 = cg.key0(t);
             if (!dead) {
-                --held;
                 const uint8_t *st = ring + cs * STAGE;
-                if (KV4) {
-                    const int2 rw = cg.rows(k0, p.sinks);
-#pragma unroll 1
-                    for (int i = (rw.x - k0) & ~(HK - 1); k0 + i < rw.y; i += HK)
-                        pass(st + i * (D / 2), st + (TK + i) * (D / 2), st + TK * D + i * (D / 16),
-                             st + TK * (D + D / 16) + i * (D / 16), k0 + i);
-                } else {
+                if (KV4)
+                    pass(st, st + TK * (D / 2), st + TK * D, st + TK * (D + D / 16), k0);
+                else
                     pass(st, st + TK * D * 2, nullptr, nullptr, k0);
-                }
             }
             __syncwarp();
+            if (KV4) fetch(cs);
+            else if (!dead && lane == 0) mbar_arrive(&empty[cs]);
             cs = cs + 1 == NS ? 0 : cs + 1;
             if (cs == 0) cphase ^= 1u;
-            if (!dead && it < tb) fetch();
             ++t;
             if (t != cg.end() && t != tb) continue;
 
@@ -946,7 +1054,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             }
         }
     }
-    __syncthreads();  // (also makes the pieces in the workspace visible to the CTA)
+    bar_sync<NT>();  // (also makes the pieces in the workspace visible to the CTA)
 
     // ---- join the CTA's pieces group by group, in the order of the list.  Scratch: behind the
     // pieces, which are the first stage of each warp's ring
@@ -981,7 +1089,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     if (open0 < 0 && open1 < 0) return;
 
     // ---- groups that span CTAs: the last to arrive joins
-    __syncthreads();
+    bar_sync<NT>();
     if (tid < 2) {
         const int gi = tid ? open1 : open0;
         flag[tid] = 0;
@@ -997,7 +1105,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             }
         }
     }
-    __syncthreads();
+    bar_sync<NT>();
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int n = flag[x], ca = flag[2 + x];
@@ -1010,13 +1118,13 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
 }
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(32 * win_warps(true), 1) santa_window_kv4_kernel(const WinParams p)
+__global__ void __launch_bounds__(win_threads(true), 1) santa_window_kv4_kernel(const WinParams p)
 {
     window_body<D, true, WIDE>(p, nullptr, nullptr);
 }
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(32 * win_warps(false), 1)
+__global__ void __launch_bounds__(win_threads(false), 1)
     santa_window_bf16_kernel(const WinParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v)
 {
     window_body<D, false, WIDE>(p, &tm_k, &tm_v);

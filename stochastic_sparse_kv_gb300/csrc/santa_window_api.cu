@@ -149,13 +149,11 @@ int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void
 
     int dev, sms, optin, rc;
     if ((rc = device_info(&dev, &sms, &optin))) return rc;
-    p.nstages = 8;
-    while (p.nstages > 2 && win_smem(D, kv4, sh->B, p.nstages).total > optin) --p.nstages;
-    const int smem = win_smem(D, kv4, sh->B, p.nstages).total;
+    const int smem = win_smem(D, kv4, sh->B).total;
     if (smem > optin) return SANTA_ERR_UNSUPPORTED;
     const void *fn = window_kernel(D, kv4, G > 4);
     int occ = 0;
-    if ((rc = prepare_fn(fn, dev, smem, 32 * win_warps(kv4), &occ))) return rc;
+    if ((rc = prepare_fn(fn, dev, smem, win_threads(kv4), &occ))) return rc;
     const int tile = win_tile(D, kv4);
     const int most = p.window > 0 ? (int)std::min<long long>(sh->n_max, (long long)p.window + p.sinks) : sh->n_max;
     // a group's visible keys touch at most two tiles more than they would fill
@@ -168,7 +166,7 @@ int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void
         if ((rc = make_map_bf16(&tm_v, v, D, rows, tile))) return rc;
     }
     void *args[] = {&p, &tm_k, &tm_v};
-    if (cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(32 * win_warps(kv4)), args, (size_t)smem, (cudaStream_t)stream) != cudaSuccess)
+    if (cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(win_threads(kv4)), args, (size_t)smem, (cudaStream_t)stream) != cudaSuccess)
         return SANTA_ERR_CUDA;
     return SANTA_OK;
 }
