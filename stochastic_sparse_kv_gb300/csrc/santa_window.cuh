@@ -287,6 +287,17 @@ struct WinGroup {
         const int i = pos - start;
         return (i < t.ns ? i : t.tw + i - t.ns) * TK;
     }
+    // tiles whose keys are all seen, but for those of the sinks: first keys lo .. lo + span
+    __device__ __forceinline__ void whole(int &lo, unsigned &span) const
+    {
+        lo = (t.w0 + TK - 1) / TK * TK;
+        const int last = n / TK * TK - TK;
+        span = (unsigned)(last - lo);
+        if (last < lo) {  // none: no tile begins there
+            lo = 1 << 30;
+            span = 0;
+        }
+    }
     // the keys of the tile from k0 that may be visible, in whole 16s
     __device__ __forceinline__ int2 rows(int k0, int sinks) const
     {
@@ -594,22 +605,25 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         uint32_t cphase = 0;
 
         // ---- 4-bit: the copies, by all lanes.  `ig` is the group of the next tile to fetch, `it`
-        // its position, fk its first key; every call makes one group of copies
+        // its position, fk its first key, frow its cache row; the rows break off at `fjump`.
+        // Every call makes one group of copies
         WinGroup<TK> ig = cg;
-        int it = t, fjump = 0, fk = 0;
+        int it = t, fjump = 0, fk = 0, flo = 0;
+        unsigned fspan = 0;
+        uint32_t frow = 0;
         auto follow = [&]() {
             fjump = it < ig.start + ig.t.ns ? ig.start + ig.t.ns : ig.end();
             fk = ig.key0(it);
+            frow = (uint32_t)ig.index(p) * (uint32_t)p.n_max + (uint32_t)fk;
+            ig.whole(flo, fspan);
         };
         auto fetch = [&](int stage) {
             if (it < tb) {
                 constexpr int RB = D / 2, NC16 = TK * RB / 512, NS16 = TK * (D / 16) / 16;  // copies a lane; lanes for scales
-                const uint32_t dst = smem_u32(ring + stage * STAGE) + 16 * lane;
-                const size_t at = (uint32_t)ig.index(p) * (uint32_t)p.n_max + (uint32_t)fk;
-                const uint8_t *gk = p.k + at * RB + 16 * lane, *gv = p.v + at * RB + 16 * lane;
-                const uint8_t *gks = p.ks + at * (D / 16) + 16 * lane, *gvs = p.vs + at * (D / 16) + 16 * lane;
-                const int2 rw = ig.rows(fk, p.sinks);  // multiples of 16, as n_max is
-                if (rw.y - rw.x == TK) {
+                const uint32_t dst = smem_u32(ring) + stage * STAGE + 16 * lane;
+                const uint8_t *gk = p.k + (size_t)frow * RB + 16 * lane, *gv = p.v + (size_t)frow * RB + 16 * lane;
+                const uint8_t *gks = p.ks + (size_t)frow * (D / 16) + 16 * lane, *gvs = p.vs + (size_t)frow * (D / 16) + 16 * lane;
+                if ((unsigned)(fk - flo) <= fspan) {
 #pragma unroll
                     for (int i = 0; i < NC16; ++i) copy16(dst + 512 * i, gk + 512 * i);
 #pragma unroll
@@ -619,8 +633,9 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                         copy16(dst + TK * (D + D / 16), gvs);
                     }
                 } else {
+                    const int2 rw = ig.rows(fk, p.sinks);  // multiples of 16, as n_max is
                     const int lo = rw.x - fk, hi = rw.y - fk;
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < NC16; ++i) {
                         const int row = (512 * i + 16 * lane) / RB;
                         if (row >= lo && row < hi) {
@@ -636,6 +651,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 }
                 ++it;
                 fk += TK;
+                frow += TK;
                 if (it == fjump) {  // the sinks end, or the group
                     if (it == ig.end()) {
                         it += WN_SETUP;
@@ -663,9 +679,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         float ka0 = p.k2_hi, ka1 = p.k2_hi, kb0 = p.k2_lo, kb1 = p.k2_lo;
         const float second = c < 2 ? 0.f : -1.f;
         // ---- one tile: the keys from k0, whose rows and scales the pointers are at
-        auto pass = [&](const uint8_t *kc, const uint8_t *vc, const uint8_t *ks, const uint8_t *vs, int k0) {
-            // every key visible: no masks
-            const bool whole = (k0 >= cg.t.w0 || k0 + TK <= p.sinks) && k0 + TK <= cg.n;
+        // (whole: every one is seen, no masks)
+        auto pass = [&](const uint8_t *kc, const uint8_t *vc, const uint8_t *ks, const uint8_t *vs, int k0, bool whole) {
             auto seen = [&](int j) { return j < cg.n && (j >= cg.t.w0 || j < p.sinks); };
 
             // ---- scores of keys r, r+8 of each 16, columns 2c, 2c+1
@@ -924,9 +939,14 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         };
 
         bool dead = false, begin = true;
+        int k0 = 0, tend = 0, wlo = 0;  // the tile's first key; where the keys break off; whole tiles
+        unsigned wspan = 0;
         while (t < tb) {
             if (begin) {
                 begin = false;
+                k0 = cg.key0(t);
+                tend = min(t < cg.start + cg.t.ns ? cg.start + cg.t.ns : cg.end(), tb);
+                cg.whole(wlo, wspan);
                 if (KV4) {
                     // scaled by the power of two that puts the head's largest value near 2^14
                     float x[MT * 4];
@@ -982,13 +1002,13 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                     stop[warp] = 1;
                 }
             }
-            const int k0 = cg.key0(t);
             if (!dead) {
+                const bool whole = (unsigned)(k0 - wlo) <= wspan;
                 const uint8_t *st = ring + cs * STAGE;
                 if (KV4)
-                    pass(st, st + TK * (D / 2), st + TK * D, st + TK * (D + D / 16), k0);
+                    pass(st, st + TK * (D / 2), st + TK * D, st + TK * (D + D / 16), k0, whole);
                 else
-                    pass(st, st + TK * D * 2, nullptr, nullptr, k0);
+                    pass(st, st + TK * D * 2, nullptr, nullptr, k0, whole);
             }
             __syncwarp();
             if (KV4) fetch(cs);
@@ -996,7 +1016,13 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             cs = cs + 1 == NS ? 0 : cs + 1;
             if (cs == 0) cphase ^= 1u;
             ++t;
-            if (t != cg.end() && t != tb) continue;
+            k0 += TK;
+            if (t != tend) continue;
+            if (t != tb && t != cg.end()) {  // the sinks end
+                tend = min(cg.end(), tb);
+                k0 = cg.key0(t);
+                continue;
+            }
 
             // ---- the group's last tile here: its result, or a piece of it
             const bool ended = t == cg.end(), all = ta <= cg.start && ended;
