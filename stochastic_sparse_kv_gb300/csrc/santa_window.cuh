@@ -43,16 +43,16 @@
 namespace santa {
 
 constexpr int WN_MAX_CTAS = 512;          // partial slots in the workspace
-constexpr int WN_MAX_WARPS = 12;
+constexpr int WN_MAX_WARPS = 16;
 constexpr int WN_RED = 4 * 32 * WN_MAX_WARPS;  // floats of a join's partial sums: 4 x max(G D / 4, threads)
 constexpr float WN_TOP = 9.f;             // log2 of p where a new maximum puts it
 constexpr float WN_SLACK = 6.f;           // and how far above that later ones may be
 constexpr int WN_SETUP = 2;               // tiles that beginning a group costs about as much as
 
-// One CTA to an SM.  4-bit: 12 warps, what 168 registers a thread allow (16 warps of 128 spill
-// and are slower), each copying its own tiles; bf16: the 8 whose rings fit, and one that
-// issues all of their copies.
-__host__ __device__ constexpr int win_warps(bool kv4) { return kv4 ? 12 : 8; }
+// One CTA to an SM.  4-bit: 16 warps, each copying its own tiles (the conversions need the
+// warps: 12 with 168 registers took 119 us where 16 with 128 take 110); bf16: the 8 whose
+// rings fit, and one that issues all of their copies.
+__host__ __device__ constexpr int win_warps(bool kv4) { return kv4 ? 16 : 8; }
 __host__ __device__ constexpr int win_threads(bool kv4) { return 32 * (kv4 ? win_warps(true) : win_warps(false) + 1); }
 // Keys of a tile, which is a ring stage, and the stages of a warp's ring (what 227 KB hold).
 __host__ __device__ constexpr int win_tile(int D, bool kv4) { return kv4 || D == 64 ? 32 : 16; }
@@ -60,7 +60,7 @@ __host__ __device__ constexpr int win_stage(int D, bool kv4)
 {
     return kv4 ? win_tile(D, true) * (D + D / 8) : win_tile(D, false) * D * 4;
 }
-__host__ __device__ constexpr int win_stages(int D, bool kv4) { return !kv4 ? 3 : D == 128 ? 4 : 8; }
+__host__ __device__ constexpr int win_stages(int D, bool kv4) { return !kv4 ? 3 : D == 128 ? 3 : 6; }
 // A piece of a group's sums: fp32 o[G][D], c[8], l[8].
 __host__ __device__ constexpr int win_piece(int G, int D) { return G * D + 16; }
 
@@ -82,7 +82,7 @@ struct WinParams {
 };
 
 struct WinSmem {
-    int ring, bar, seg, stop, flag, list, nb, prefix, total;
+    int ring, bar, seg, stop, flag, list, group, nb, prefix, total;
 };
 
 __host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B)
@@ -96,9 +96,10 @@ __host__ __device__ inline WinSmem win_smem(int D, bool kv4, int B)
     s.stop = off; off += (int)align_up((size_t)W * 4, 16);  // set by a warp that gave up
     s.flag = off; off += 16;
     s.list = off; off += 32 * W;
+    s.group = off; off += 2 * W * 32;            // each warp's groups: of the tile at hand, of the next to fetch
     s.nb = off; off += (int)align_up((size_t)B * 4, 16);
     s.prefix = off; off += (int)align_up((size_t)(B + 1) * 4, 16);
-    s.total = off + 1024;
+    s.total = off + (kv4 ? 0 : 1024);            // (swizzled tiles begin at multiples of 1024)
     return s;
 }
 
@@ -109,11 +110,11 @@ template <bool BF16>
 __device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
     if (BF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -122,11 +123,11 @@ template <bool BF16>
 __device__ __forceinline__ void mma_set(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
     if (BF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
     else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
@@ -135,7 +136,7 @@ __device__ __forceinline__ void mma_set(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
 {
     uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -458,9 +459,9 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     constexpr int NB = WIDE ? NP : (KV4 ? 1 : 2);       // MMAs they take
     constexpr unsigned FULL = 0xffffffffu;
     const float NEG_INF = __int_as_float(0xff800000);
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(16) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t *smem = KV4 ? smem_raw : smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const WinSmem lay = win_smem(D, KV4, p.B);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     // (the copying warp: lane w works for warp w)
@@ -520,22 +521,22 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     const WinShares warps(t1 - t0, W);
     const int ta = t0 + warps.first(owner), tb = t0 + warps.first(owner + 1);
 
-    WinGroup<TK> cg;  // the group of the tile at hand, t its position
+    WinGroup<TK> head;  // the group of the share's first tile, whose position is t
     int t = ta;
     if (ta < tb) {
-        cg.seek(ta, prefix, nb, p);
-        t = max(ta, cg.start);
+        head.seek(ta, prefix, nb, p);
+        t = max(ta, head.start);
     }
     if (warp == W) {  // (bf16)
-        // ---- the copies: one lane a ring; `t` is the next tile to fetch, of group cg
+        // ---- the copies: one lane a ring; `t` is the next tile to fetch, of group `head`
         const uint64_t policy = l2_policy_evict_first();
         bool live = lane < W && t < tb;
         int filled = 0, is = 0;                       // stages filled, the next one to fill
         uint32_t phase = 1;                           // a fresh barrier lets this parity pass
         int jump = 0, k0 = 0;                         // where the rows break off; the tile's first key
         auto follow = [&]() {
-            jump = t < cg.start + cg.t.ns ? cg.start + cg.t.ns : cg.end();
-            k0 = cg.key0(t);
+            jump = t < head.start + head.t.ns ? head.start + head.t.ns : head.end();
+            k0 = head.key0(t);
         };
         if (live) follow();
         uint64_t since = globaltimer_ns();
@@ -545,7 +546,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 uint8_t *st = ring + is * STAGE;
                 {
                     // whole boxes: rows past the group's last key are other keys or zeros, never used
-                    const int row = cg.index(p) * p.n_max + k0;
+                    const int row = head.index(p) * p.n_max + k0;
                     mbar_arrive_tx(&full[is], (uint32_t)STAGE);
 #pragma unroll
                     for (int hf = 0; hf < D / 64; ++hf) {
@@ -561,11 +562,11 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 ++t;
                 k0 += TK;
                 if (t == jump) {  // the sinks end, or the group
-                    if (t == cg.end()) {
+                    if (t == head.end()) {
                         t += WN_SETUP;
                         if (t < tb) {
-                            cg.next(nb, p);
-                            const uint16_t *q0 = p.q + ((size_t)cg.b * p.H_q + cg.g * p.G) * D;  // its queries, into L2
+                            head.next(nb, p);
+                            const uint16_t *q0 = p.q + ((size_t)head.b * p.H_q + head.g * p.G) * D;  // its queries, into L2
                             for (int i = 0; i < p.G * D; i += 64) prefetch_l2(q0 + i);
                         }
                     }
@@ -588,6 +589,18 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         return;
     }
     if (t < tb) {
+        // the groups of the tile at hand and (4-bit) of the next to fetch: seldom needed, so kept
+        // in shared memory; lane 0 writes
+        WinGroup<TK> *groups = reinterpret_cast<WinGroup<TK> *>(smem + lay.group) + 2 * warp;
+        WinGroup<TK> &cg = groups[0], &ig = groups[1];
+        static_assert(sizeof(WinGroup<TK>) == 32, "the layout of shared memory");
+        auto advance = [&](WinGroup<TK> &g) {
+            __syncwarp();
+            if (lane == 0) g.next(nb, p);
+            __syncwarp();
+        };
+        if (lane == 0) cg = ig = head;
+        __syncwarp();
         // ---- a group's queries: head column r (zero in columns without a head).  4-bit: lane c
         // takes dimensions D/4 c .., four to an MMA step; bf16: 16 c .. of each 64
         uint4 qraw[MT / 2];
@@ -607,7 +620,6 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         // ---- 4-bit: the copies, by all lanes.  `ig` is the group of the next tile to fetch, `it`
         // its position, fk its first key, frow its cache row; the rows break off at `fjump`.
         // Every call makes one group of copies
-        WinGroup<TK> ig = cg;
         int it = t, fjump = 0, fk = 0, flo = 0;
         unsigned fspan = 0;
         uint32_t frow = 0;
@@ -656,7 +668,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                     if (it == ig.end()) {
                         it += WN_SETUP;
                         if (it < tb) {
-                            ig.next(nb, p);
+                            advance(ig);
                             const uint16_t *q0 = p.q + ((size_t)ig.b * p.H_q + ig.g * p.G) * D;  // its queries, into L2
                             if (lane * 64 < p.G * D) prefetch_l2(q0 + lane * 64);
                         }
@@ -689,35 +701,32 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             for (int u = 0; u < SUB; ++u) {
                 float acc[MT / 2][4];  // chains of two steps
                 if (KV4) {
-                    uint32_t a[2][MT][2];  // rows r, r+8: per step two fp16 pairs
+                    uint32_t w[2][D / 32], sc[2][2];  // rows r, r+8: codes, scales (twice, as fp16)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int kr = 16 * u + r + 8 * y;
-                        uint32_t w[D / 32];
-                        uint32_t sc[2];
                         if (D == 128) {
                             const uint4 x = *reinterpret_cast<const uint4 *>(kc + kr * 64 + c * 16);
-                            w[0] = x.x, w[1] = x.y, w[D / 32 - 2] = x.z, w[D / 32 - 1] = x.w;
-                            sc[0] = (uint32_t)ks[kr * 8 + 2 * c] * 0x00800080u;  // twice, as fp16
-                            sc[1] = (uint32_t)ks[kr * 8 + 2 * c + 1] * 0x00800080u;
+                            w[y][0] = x.x, w[y][1] = x.y, w[y][D / 32 - 2] = x.z, w[y][D / 32 - 1] = x.w;
+                            sc[y][0] = (uint32_t)ks[kr * 8 + 2 * c] * 0x00800080u;
+                            sc[y][1] = (uint32_t)ks[kr * 8 + 2 * c + 1] * 0x00800080u;
                         } else {
                             const uint2 x = *reinterpret_cast<const uint2 *>(kc + kr * 32 + c * 8);
-                            w[0] = x.x, w[1] = x.y;
-                            sc[0] = sc[1] = (uint32_t)ks[kr * 4 + c] * 0x00800080u;
-                        }
-#pragma unroll
-                        for (int j = 0; j < D / 32; ++j) {
-                            uint32_t h[4];
-                            e2m1_unpack8(w[j], h);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) a[y][2 * j + i / 2][i & 1] = h2mul(h[i], sc[j / 2]);
+                            w[y][0] = x.x, w[y][1] = x.y;
+                            sc[y][0] = sc[y][1] = (uint32_t)ks[kr * 4 + c] * 0x00800080u;
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < MT; i += 2) {
-                        mma_set<false>(acc[i / 2], a[0][i][0], a[1][i][0], a[0][i][1], a[1][i][1], qf[i][0], qf[i][1]);
-                        mma_add<false>(acc[i / 2], a[0][i + 1][0], a[1][i + 1][0], a[0][i + 1][1], a[1][i + 1][1], qf[i + 1][0],
-                                       qf[i + 1][1]);
+                    for (int j = 0; j < D / 32; ++j) {  // a word: two steps
+                        uint32_t a[2][4];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            e2m1_unpack8(w[y][j], a[y]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) a[y][i] = h2mul(a[y][i], sc[y][j / 2]);
+                        }
+                        mma_set<false>(acc[j], a[0][0], a[1][0], a[0][1], a[1][1], qf[2 * j][0], qf[2 * j][1]);
+                        mma_add<false>(acc[j], a[0][2], a[1][2], a[0][3], a[1][3], qf[2 * j + 1][0], qf[2 * j + 1][1]);
                     }
                 } else {
 #pragma unroll
@@ -842,19 +851,13 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             // ---- o += V^T p, the tile's keys in one chain per piece
             if (KV4) {
                 constexpr int RB = D / 2, W = D / 64;  // bytes of a row; words of a lane's D/8 dimensions
-                uint32_t vw[SUB][4][W], sp[SUB][2];
+                uint32_t sp[SUB][2];
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     uint32_t sb[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int kk = 16 * u + 2 * c + (i & 1) + 8 * (i >> 1);
-                        if (W == 2) {
-                            const uint2 x = *reinterpret_cast<const uint2 *>(vc + kk * RB + r * 8);
-                            vw[u][i][0] = x.x, vw[u][i][W - 1] = x.y;
-                        } else {
-                            vw[u][i][0] = *reinterpret_cast<const uint32_t *>(vc + kk * RB + r * 4);
-                        }
                         sb[i] = vs[kk * (D / 16) + (D == 128 ? r : r >> 1)];
                     }
                     sp[u][0] = sb[1] * 0x800000u + sb[0] * 0x80u;  // the key pair's scales as fp16
@@ -876,7 +879,9 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                         uint32_t a[2][2][4];  // key pair, even or odd dimension, byte
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const uint32_t x0w = vw[u][2 * y][w], x1w = vw[u][2 * y + 1][w];
+                            const uint8_t *v0 = vc + (16 * u + 2 * c + 8 * y) * RB + r * 4 * W + 4 * w;
+                            const uint32_t x0w = *reinterpret_cast<const uint32_t *>(v0);
+                            const uint32_t x1w = *reinterpret_cast<const uint32_t *>(v0 + RB);
                             e2m1_unpack8((x0w & 0x0f0f0f0fu) | ((x1w << 4) & 0xf0f0f0f0u), a[y][0]);
                             e2m1_unpack8(((x0w >> 4) & 0x0f0f0f0fu) | (x1w & 0xf0f0f0f0u), a[y][1]);
 #pragma unroll
@@ -938,38 +943,32 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             }
         };
 
-        bool dead = false, begin = true;
-        int k0 = 0, tend = 0, wlo = 0;  // the tile's first key; where the keys break off; whole tiles
-        unsigned wspan = 0;
-        while (t < tb) {
-            if (begin) {
-                begin = false;
-                k0 = cg.key0(t);
-                tend = min(t < cg.start + cg.t.ns ? cg.start + cg.t.ns : cg.end(), tb);
-                cg.whole(wlo, wspan);
+        bool dead = false;
+        for (;;) {  // groups
+            int k0 = cg.key0(t);  // the tile's first key; where the keys break off; whole tiles
+            int tend = min(t < cg.start + cg.t.ns ? cg.start + cg.t.ns : cg.end(), tb), wlo;
+            unsigned wspan;
+            cg.whole(wlo, wspan);
+            {
                 if (KV4) {
                     // scaled by the power of two that puts the head's largest value near 2^14
-                    float x[MT * 4];
-                    float big = 0.f;
+                    uint32_t big = 0;  // its bf16 bits without the sign
 #pragma unroll
                     for (int i = 0; i < MT / 2; ++i) {
                         const uint32_t u[4] = {qraw[i].x, qraw[i].y, qraw[i].z, qraw[i].w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            x[8 * i + 2 * j] = bf16lo_to_f32(u[j]);
-                            x[8 * i + 2 * j + 1] = bf16hi_to_f32(u[j]);
-                        }
+                        for (int j = 0; j < 4; ++j) big = max(big, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
                     }
-#pragma unroll
-                    for (int i = 0; i < MT * 4; ++i) big = fmaxf(big, fabsf(x[i]));
-                    big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
-                    big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
-                    const int e = max(-100, min(127, (int)(__float_as_uint(big) >> 23) - 127)) - 14;
+                    big = max(big, __shfl_xor_sync(FULL, big, 1));
+                    big = max(big, __shfl_xor_sync(FULL, big, 2));
+                    const int e = max(-100, min(127, (int)(big >> 7) - 127)) - 14;
                     const float up = p.qsign * exp2i(-e);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        qf[i][0] = pack_f16(x[4 * i] * up, x[4 * i + 1] * up);
-                        qf[i][1] = pack_f16(x[4 * i + 2] * up, x[4 * i + 3] * up);
+                    for (int i = 0; i < MT / 2; ++i) {
+                        qf[2 * i][0] = pack_f16(bf16lo_to_f32(qraw[i].x) * up, bf16hi_to_f32(qraw[i].x) * up);
+                        qf[2 * i][1] = pack_f16(bf16lo_to_f32(qraw[i].y) * up, bf16hi_to_f32(qraw[i].y) * up);
+                        qf[2 * i + 1][0] = pack_f16(bf16lo_to_f32(qraw[i].z) * up, bf16hi_to_f32(qraw[i].z) * up);
+                        qf[2 * i + 1][1] = pack_f16(bf16lo_to_f32(qraw[i].w) * up, bf16hi_to_f32(qraw[i].w) * up);
                     }
                     const int h0 = WIDE ? 2 * c : (2 * c) & 3;  // heads of this lane's columns
                     const float d0 = exp2i(__shfl_sync(FULL, e, h0 * 4)), d1 = exp2i(__shfl_sync(FULL, e, h0 * 4 + 4));
@@ -992,36 +991,36 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 l0 = l1 = c0 = c1 = 0.f;
                 thr0 = thr1 = NEG_INF;
             }
-            if (KV4) {
-                copy_wait<NS - 1>();
-                __syncwarp();
-            } else if (!dead && !__all_sync(FULL, win_wait(&full[cs], cphase, p.wait_ns))) {
-                dead = true;  // no more copies, no more sums (the pieces still meet)
-                if (lane == 0) {
-                    set_dev_error(p.ctrl, DEV_TIMEOUT);
-                    stop[warp] = 1;
+            for (;;) {  // tiles
+                if (KV4) {
+                    copy_wait<NS - 1>();
+                    __syncwarp();
+                } else if (!dead && !__all_sync(FULL, win_wait(&full[cs], cphase, p.wait_ns))) {
+                    dead = true;  // no more copies, no more sums (the pieces still meet)
+                    if (lane == 0) {
+                        set_dev_error(p.ctrl, DEV_TIMEOUT);
+                        stop[warp] = 1;
+                    }
                 }
-            }
-            if (!dead) {
-                const bool whole = (unsigned)(k0 - wlo) <= wspan;
-                const uint8_t *st = ring + cs * STAGE;
-                if (KV4)
-                    pass(st, st + TK * (D / 2), st + TK * D, st + TK * (D + D / 16), k0, whole);
-                else
-                    pass(st, st + TK * D * 2, nullptr, nullptr, k0, whole);
-            }
-            __syncwarp();
-            if (KV4) fetch(cs);
-            else if (!dead && lane == 0) mbar_arrive(&empty[cs]);
-            cs = cs + 1 == NS ? 0 : cs + 1;
-            if (cs == 0) cphase ^= 1u;
-            ++t;
-            k0 += TK;
-            if (t != tend) continue;
-            if (t != tb && t != cg.end()) {  // the sinks end
-                tend = min(cg.end(), tb);
+                if (!dead) {
+                    const bool whole = (unsigned)(k0 - wlo) <= wspan;
+                    const uint8_t *st = ring + cs * STAGE;
+                    if (KV4)
+                        pass(st, st + TK * (D / 2), st + TK * D, st + TK * (D + D / 16), k0, whole);
+                    else
+                        pass(st, st + TK * D * 2, nullptr, nullptr, k0, whole);
+                }
+                __syncwarp();
+                if (KV4) fetch(cs);
+                else if (!dead && lane == 0) mbar_arrive(&empty[cs]);
+                cs = cs + 1 == NS ? 0 : cs + 1;
+                if (cs == 0) cphase ^= 1u;
+                ++t;
+                k0 += TK;
+                if (t != tend) continue;
+                if (t == tb || t == cg.end()) break;
+                tend = min(cg.end(), tb);  // the sinks end
                 k0 = cg.key0(t);
-                continue;
             }
 
             // ---- the group's last tile here: its result, or a piece of it
@@ -1073,11 +1072,9 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 }
                 if (lane == 0) seg[2 * warp + slot] = cg.index(p);
             }
-            if (t < tb) {
-                cg.next(nb, p);
-                load_q();
-                begin = true;
-            }
+            if (t >= tb) break;
+            advance(cg);
+            load_q();
         }
     }
     bar_sync<NT>();  // (also makes the pieces in the workspace visible to the CTA)
