@@ -61,8 +61,8 @@ __host__ __device__ constexpr int win_stage(int D, bool kv4)
     return kv4 ? win_tile(D, true) * (D + D / 8) : win_tile(D, false) * D * 4;
 }
 __host__ __device__ constexpr int win_stages(int D, bool kv4) { return !kv4 ? 3 : D == 128 ? 3 : 6; }
-// A piece of a group's sums: fp32 o[G][D], c[8], l[8].
-__host__ __device__ constexpr int win_piece(int G, int D) { return G * D + 16; }
+// A piece of a group's sums: fp32 o[G][D + 4] (the heads' rows in different banks), c[8], l[8].
+__host__ __device__ constexpr int win_piece(int G, int D) { return G * (D + 4) + 16; }
 
 struct WinParams {
     const uint16_t *q;            // bf16 [B][H_q][D]
@@ -349,36 +349,51 @@ __device__ __forceinline__ void win_store(const WinParams &p, size_t i, float v)
         p.out[i] = v;
 }
 
-// The whole CTA: the n pieces of group gi joined into `part` (a piece) or, when that is null,
-// into the output.  scratch: 16 n + 16 floats; red: WN_RED of them.  Begins and ends with
-// the scratch free.  FAR: the pieces lie in the workspace, written by other CTAs too, and
-// are read past the L1 cache; else in shared memory or the workspace, written by this CTA.
-template <int D, int NT, bool FAR, class F>
-__device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, float *scratch, float *red, int gi, float *part)
+// Where the pieces of a group lie: those of a CTA's warps (list[j]: piece 2 w + 1 of warp w in its
+// ring, 2 w in the workspace) or, list null, those of CTAs (the first one's second, then firsts).
+struct WinPieces {
+    const uint8_t *list;
+    const float *ring, *near;
+    int ring_step, step;
+
+    __device__ __forceinline__ const float *at(int j) const
+    {
+        if (!list) return near + (size_t)(2 * j + (j == 0)) * step;
+        const int x = list[j];
+        return (x & 1) ? ring + (x >> 1) * ring_step : near + (size_t)(x >> 1) * step;
+    }
+};
+
+// All NT threads: the n pieces of group gi joined into `part` (a piece) or, when that is null,
+// into the output.  red: WN_RED floats; scratch: 16 n + 16.  Begins and ends with both free.
+// FAR: the pieces were written by other CTAs too and are read past the L1 cache.
+template <int D, int NT, bool FAR>
+__device__ __forceinline__ void win_join(const WinParams &p, int n, const WinPieces pieces, float *red, float *scratch, int gi, float *part)
 {
     constexpr unsigned FULL = 0xffffffffu;
-    const int tid = threadIdx.x, lane = tid & 31, GD = p.G * D;
+    constexpr int AHEAD = 8, HS = D + 4;
+    const int tid = threadIdx.x, lane = tid & 31, GS = p.G * HS;
     float *tot = scratch, *wt = scratch + 16, *lt = wt + 8 * n;
     auto load = [](const float *a) { return FAR ? __ldcg(a) : *a; };
-    auto load4 = [](const float4 *a) { return FAR ? __ldcg(a) : *a; };
-    // four outputs a thread; with few outputs, slices of the pieces.  The first pieces are
-    // on their way while the weights are worked out
-    constexpr int AHEAD = FAR ? 8 : 1;
-    const int nv = GD / 4, ns = max(1, NT / nv);
-    const int v0 = tid % nv, sl0 = tid / nv;
+    auto load4 = [](const float *a) {
+        return FAR ? __ldcg(reinterpret_cast<const float4 *>(a)) : *reinterpret_cast<const float4 *>(a);
+    };
+    // four outputs a thread; with few outputs, slices of the pieces.  The first pieces are on
+    // their way while the weights are worked out (indexes past the last are those of the last:
+    // a load under a condition would be waited for before the next)
+    const int nv = p.G * (D / 4), ns = max(1, NT / nv);
+    const int v0 = tid % nv, sl0 = tid / nv, h0 = v0 / (D / 4), at0 = h0 * HS + 4 * (v0 % (D / 4));
     float4 ahead[AHEAD];
-    if (tid < ns * nv)
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (sl0 + k * ns < n) ahead[k] = load4(reinterpret_cast<const float4 *>(piece_of(sl0 + k * ns)) + v0);
+    for (int k = 0; k < AHEAD; ++k) ahead[k] = load4(pieces.at(min(sl0 + k * ns, n - 1)) + at0);
     // a warp a head: its common exponent, the pieces' weights, the sum
     for (int h = tid >> 5; h < p.G; h += NT / 32) {
         float C = __int_as_float(0x7f800000);
         for (int j = lane; j < n; j += 32) {
-            const float *pc = piece_of(j) + GD + h;
-            const float c = load(pc);
+            const float *pc = pieces.at(j) + GS + h;
+            const float c = load(pc), l = load(pc + 8);
             wt[8 * j + h] = c;
-            lt[8 * j + h] = load(pc + 8);
+            lt[8 * j + h] = l;
             C = fminf(C, c);
         }
 #pragma unroll
@@ -403,44 +418,35 @@ __device__ __forceinline__ void win_join(const WinParams &p, int n, F piece_of, 
         o.z = fmaf(w, x.z, o.z);
         o.w = fmaf(w, x.w, o.w);
     };
-    if (tid < ns * nv) {
-        const int hv = 4 * v0 / D;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (sl0 + k * ns < n) add(o, ahead[k], wt[8 * (sl0 + k * ns) + hv]);
-#pragma unroll 8
-        for (int j = sl0 + AHEAD * ns; j < n; j += ns) add(o, load4(reinterpret_cast<const float4 *>(piece_of(j)) + v0), wt[8 * j + hv]);
-        reinterpret_cast<float4 *>(red)[tid] = o;
+    for (int k = 0; k < AHEAD; ++k)
+        if (sl0 + k * ns < n) add(o, ahead[k], wt[8 * (sl0 + k * ns) + h0]);
+    for (int j = sl0 + AHEAD * ns; j < n; j += 4 * ns) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ahead[k] = load4(pieces.at(min(j + k * ns, n - 1)) + at0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j + k * ns < n) add(o, ahead[k], wt[8 * (j + k * ns) + h0]);
     }
+    if (tid < ns * nv) reinterpret_cast<float4 *>(red)[tid] = o;
     if (ns > 1) bar_sync<NT>();
-    for (int v = tid; v < nv; v += NT) {
-        const int hv = 4 * v / D;
-        float4 o = reinterpret_cast<const float4 *>(red)[v];
-        for (int s = 1; s < ns; ++s) {
-            const float4 x = reinterpret_cast<const float4 *>(red)[s * nv + v];
-            o.x += x.x;
-            o.y += x.y;
-            o.z += x.z;
-            o.w += x.w;
-        }
+    if (tid < nv) {
+        for (int s = 1; s < ns; ++s) add(o, reinterpret_cast<const float4 *>(red)[s * nv + tid], 1.f);
         if (part) {
-            reinterpret_cast<float4 *>(part)[v] = o;
-            if (v % (D / 4) == 0) {
-                part[GD + hv] = tot[hv];
-                part[GD + 8 + hv] = tot[8 + hv];
+            *reinterpret_cast<float4 *>(part + at0) = o;
+            if (tid % (D / 4) == 0) {
+                part[GS + h0] = tot[h0];
+                part[GS + 8 + h0] = tot[8 + h0];
             }
         } else {
-            const float r = 1.f / tot[8 + hv];
-            const size_t at = ((size_t)(gi / p.H_kv) * p.H_q + (size_t)(gi % p.H_kv) * p.G) * D + 4 * (size_t)v;
+            const float r = 1.f / tot[8 + h0];
+            const size_t at = ((size_t)(gi / p.H_kv) * p.H_q + (size_t)(gi % p.H_kv) * p.G) * D + 4 * (size_t)tid;
             o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
-            if (p.out_bf16) {
-                const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
-                *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(p.out) + at) =
-                    make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-            } else {
+            if (p.out_bf16)
+                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p.out) + at) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+            else
                 *reinterpret_cast<float4 *>(p.out + at) = o;
-            }
         }
     }
     bar_sync<NT>();
@@ -680,7 +686,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         };
         if (KV4) {
             follow();
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < NS; ++i) fetch(i);
         }
 
@@ -1038,40 +1044,56 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             const int slot = t < tb ? 0 : 1;
             float *piece = slot ? reinterpret_cast<float *>(ring) : p.first + (size_t)(blockIdx.x * W + warp) * PIECE;
             const size_t orow = (size_t)cg.b * p.H_q + cg.g * p.G;
-            // heads of the lane's values: x of column 2c (and y of 2c+1 in wide groups)
+            // heads of the lane's values: x of column 2c (and z of 2c+1 in wide groups)
             const int hx = WIDE ? 2 * c : 2 * (c & 1) + (c >> 1);
             const float lx = WIDE || c < 2 ? l0 : l1, cx = WIDE || c < 2 ? c0 : c1;
-            const float ix = 1.f / lx, iz = 1.f / l1;
+            const float ix = all ? 1.f / lx : 1.f, iz = all ? 1.f / l1 : 1.f;
+            if (!WIDE)  // columns j and j + 4 hold terms of the same head: lanes c, c ^ 2
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+                for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int dim = KV4 ? (D / 8) * r + 2 * i + y : 16 * i + 8 * y + r;
-                    float x = o[i][2 * y], z = o[i][2 * y + 1];
-                    if (!WIDE) {  // columns j and j + 4 hold terms of the same head: lanes c, c ^ 2
-                        const float got = __shfl_xor_sync(FULL, c < 2 ? z : x, 2);
-                        x = (c < 2 ? x : z) + got;
+                    for (int e = 0; e < 4; e += 2) {
+                        const float got = __shfl_xor_sync(FULL, c < 2 ? o[i][e + 1] : o[i][e], 2);
+                        o[i][e] = (c < 2 ? o[i][e] : o[i][e + 1]) + got;
                     }
-                    if (hx < p.G) {
-                        if (all) win_store(p, (orow + hx) * D + dim, x * ix);
-                        else piece[hx * D + dim] = x;
+#pragma unroll
+            for (int x = 0; x < (WIDE ? 2 : 1); ++x) {
+                const int h = hx + x;
+                const float inv = x ? iz : ix;
+                if (h >= p.G) continue;
+                if (KV4) {
+                    // D/8 dimensions in a row, from D/8 r
+                    const size_t at = (orow + h) * D + (D / 8) * r;
+                    float *dst = all ? p.out + at : piece + h * (D + 4) + (D / 8) * r;
+                    if (all && p.out_bf16) {
+#pragma unroll
+                        for (int i = 0; i < MT; i += 4)
+                            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(p.out) + at + 2 * i) =
+                                make_uint4(pack_bf16(o[i][x] * inv, o[i][x + 2] * inv), pack_bf16(o[i + 1][x] * inv, o[i + 1][x + 2] * inv),
+                                           pack_bf16(o[i + 2][x] * inv, o[i + 2][x + 2] * inv),
+                                           pack_bf16(o[i + 3][x] * inv, o[i + 3][x + 2] * inv));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < MT; i += 2)
+                            *reinterpret_cast<float4 *>(dst + 2 * i) =
+                                make_float4(o[i][x] * inv, o[i][x + 2] * inv, o[i + 1][x] * inv, o[i + 1][x + 2] * inv);
                     }
-                    if (WIDE && hx + 1 < p.G) {
-                        if (all) win_store(p, (orow + hx + 1) * D + dim, z * iz);
-                        else piece[(hx + 1) * D + dim] = z;
-                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int dim = 16 * i + 8 * y + r;
+                            if (all) win_store(p, (orow + h) * D + dim, o[i][x + 2 * y] * inv);
+                            else piece[h * (D + 4) + dim] = o[i][x + 2 * y];
+                        }
                 }
-            if (!all) {
-                if (r == 0 && hx < p.G) {
-                    piece[p.G * D + hx] = cx;
-                    piece[p.G * D + 8 + hx] = lx;
-                    if (WIDE && hx + 1 < p.G) {
-                        piece[p.G * D + hx + 1] = c1;
-                        piece[p.G * D + 8 + hx + 1] = l1;
-                    }
+                if (!all && r == 0) {
+                    piece[p.G * (D + 4) + h] = x ? c1 : cx;
+                    piece[p.G * (D + 4) + 8 + h] = x ? l1 : lx;
                 }
-                if (lane == 0) seg[2 * warp + slot] = cg.index(p);
             }
+            if (!all && lane == 0) seg[2 * warp + slot] = cg.index(p);
             if (t >= tb) break;
             advance(cg);
             load_q();
@@ -1102,12 +1124,9 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         // list[j]: which is the j-th of the group's pieces, a copy for each warp
         if (set >> lane & 1) list[__popc(set & ((1u << lane) - 1))] = (uint8_t)lane;
         __syncwarp();
-        auto piece_of = [&](int j) -> const float * {
-            const int x = list[j];
-            return (x & 1) ? reinterpret_cast<const float *>(smem + lay.ring + (x >> 1) * NS * STAGE)
-                           : p.first + (size_t)(blockIdx.x * W + (x >> 1)) * PIECE;
-        };
-        win_join<D, NT, false>(p, __popc(set), piece_of, scratch, red, gi, all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE);
+        const WinPieces pieces{list, reinterpret_cast<const float *>(smem + lay.ring), p.first + (size_t)blockIdx.x * W * PIECE,
+                               NS * STAGE / 4, PIECE};
+        win_join<D, NT, false>(p, __popc(set), pieces, red, scratch, gi, all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE);
     }
     if (open0 < 0 && open1 < 0) return;
 
@@ -1133,22 +1152,22 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     for (int x = 0; x < 2; ++x) {
         const int n = flag[x], ca = flag[2 + x];
         if (n == 0) continue;
-        auto piece_of = [&](int j) -> const float * { return p.part + (size_t)(2 * (ca + j) + (j == 0)) * PIECE; };
-        // (the rings are free: n <= WN_MAX_CTAS pieces take 37 KB of them)
+        // (the rings are free: n <= WN_MAX_CTAS pieces take 41 KB of them)
         float *far = reinterpret_cast<float *>(smem + lay.ring);
-        win_join<D, NT, true>(p, n, piece_of, far + WN_RED, far, x ? open1 : open0, nullptr);
+        const WinPieces pieces{nullptr, nullptr, p.part + (size_t)2 * ca * PIECE, 0, PIECE};
+        win_join<D, NT, true>(p, n, pieces, far, far + WN_RED, x ? open1 : open0, nullptr);
     }
 }
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(win_threads(true), 1) santa_window_kv4_kernel(const WinParams p)
+__global__ void __launch_bounds__(win_threads(true), 1) santa_window_kv4_kernel(const __grid_constant__ WinParams p)
 {
     window_body<D, true, WIDE>(p, nullptr, nullptr);
 }
 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(win_threads(false), 1)
-    santa_window_bf16_kernel(const WinParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v)
+    santa_window_bf16_kernel(const __grid_constant__ WinParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v)
 {
     window_body<D, false, WIDE>(p, &tm_k, &tm_v);
 }
