@@ -375,13 +375,22 @@ def _shape_of(key):
     return got
 
 
-def _call_workspace(nbytes: int, dev, stream) -> torch.Tensor:
+def _raw_stream(stream, dev) -> int:
+    """The CUDA handle of `stream`, or of the current one on `dev` (looked up without making a
+    torch.cuda.Stream, which would be a tenth of a small call)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _call_workspace(nbytes: int, dev, stream, raw: int) -> torch.Tensor:
     """The workspace of a call on `stream` that was given none: one per device and stream, or,
     inside a stream capture, one of the graph's own (two graphs that share one could not be
     replayed at the same time, and its clearing has to be part of the graph)."""
     if torch.cuda.is_current_stream_capturing():
         return new_workspace(nbytes, dev, stream)
-    return _cached_workspace(nbytes, dev, stream)
+    ws = _ws_cache.get((dev, raw))
+    if ws is None or ws.numel() < nbytes:
+        ws = _ws_cache[(dev, raw)] = new_workspace(nbytes, dev, stream if stream is not None else torch.cuda.current_stream(dev))
+    return ws
 
 
 def _move_rows(fn, what: str, cache, k, v, pos, counts, workspace, stream):
@@ -396,12 +405,10 @@ def _move_rows(fn, what: str, cache, k, v, pos, counts, workspace, stream):
         _int_vector(counts, "counts", B, dev)
     rows = _Rows(k.data_ptr(), v.data_ptr(), k.stride()[:3], v.stride()[:3])
     shape, _ = _shape_of((B, H_kv, H_kv, d, n_max))
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     with _on_device(dev):
         rc = fn(shape, _kv4_arg(cache), ctypes.byref(rows), k.shape[1], pos.data_ptr(),
                 counts.data_ptr() if counts is not None else None,
-                workspace.data_ptr() if workspace is not None else None, stream.cuda_stream)
+                workspace.data_ptr() if workspace is not None else None, _raw_stream(stream, dev))
     if rc:
         _check(rc, what)
 
@@ -442,13 +449,11 @@ def _window_call(q, dims, cache_args, fn, what, seq_lens, window, sinks, scale, 
             out.record_stream(stream)
     elif out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or out.shape != qs or out.device != dev:
         raise ValueError("out must be a contiguous fp32 or bf16 [B, H_q, d] tensor on q's device")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     with _on_device(dev):
-        ws = workspace if workspace is not None else _call_workspace(nbytes, dev, stream)
+        raw = _raw_stream(stream, dev)
+        ws = workspace if workspace is not None else _call_workspace(nbytes, dev, stream, raw)
         rc = fn(shape, q.data_ptr(), *cache_args, seq_lens.data_ptr(), window, sinks,
-                OUT_BF16 if out.dtype == torch.bfloat16 else 0, out.data_ptr(), ws.data_ptr(), ws.numel(),
-                stream.cuda_stream)
+                OUT_BF16 if out.dtype == torch.bfloat16 else 0, out.data_ptr(), ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc, what)
     return out
