@@ -11,12 +11,18 @@
 // without a second scale per tensor.  A group that holds a NaN or an infinity gets the
 // scale 0xff (a NaN): the whole group reads back as NaN.
 //
-// Exactness.  A code has at most 2 significant bits and a scale 4, so x^ has at most 6 and
-// a magnitude in [2^-18, 61440]: fp16 and bf16 both hold it exactly, and reading rounds
-// nothing.  When writing, max|x| / 6 and |x| / s are quotients of short integers (8 by 2 and
-// 8 by 4 significant bits): a quotient is either a tie of the coarser format exactly or at
-// least 2^-12 (relative) away from one, and the fp32 quotient (2^-24) decides as the real
-// number would.
+// Exactness.  A code has at most 2 significant bits and a scale 4, so x^ has at most 6 and a
+// magnitude in [2^-18, 61440]: fp16 and bf16 both hold it exactly, and reading rounds nothing.
+// Writing rounds the quotients max|x| / 6 and |x| / s as the real numbers: they are quotients of
+// integers of 8 bits by 2 and by 4 bits, a border of the rounding (5 and 3 bits) times its
+// divisor is an integer of the same grid as the dividend, so a quotient lies on a border exactly
+// or at least 2^-8 of itself away.  An fp32 product with the reciprocal (off by less than 2^-21)
+// rounded to fewer bits in between (2^-16, and 2^-12 absolute) is on the border or on the same
+// side of it.
+//
+// Both kernels move 2.56 bytes a value and are bound by that: one thread takes one group, in one
+// 32-byte access where the rows allow it.  (Dividing exactly, 16 times a group, took twice the
+// time of the memory traffic.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -34,9 +40,10 @@ constexpr uint32_t UE5M3_NAN = 0xFF;
 __device__ __forceinline__ uint32_t ue5m3_scale(uint32_t amax)
 {
     if (amax >= 0x7f80u) return UE5M3_NAN;
-    const float want = __fdiv_rn(__uint_as_float(amax << 16), 6.f);
+    const float sixth = __uint_as_float(amax << 16) * (1.f / 6.f);
+    const uint32_t u = (__float_as_uint(sixth) + 0x80u) & ~0xffu;  // 16 bits
+    const float want = __uint_as_float(u);
     if (want < 0x1p-14f) return (uint32_t)__float2int_rn(want * 0x1p17f);  // below the normal range
-    const uint32_t u = __float_as_uint(want);
     const uint32_t r = (u + 0x7ffffu + ((u >> 20) & 1u)) >> 20;            // 8 exponent, 3 mantissa bits
     return min(r - ((127u - 15u) << 3), UE5M3_MAX);
 }
@@ -56,6 +63,15 @@ __device__ __forceinline__ uint32_t e2m1_pack8(const float (&x)[8])
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(r)
         : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+
+// The sign bits of eight bf16 values (pairs in w[0..3]) as those of their codes.
+__device__ __forceinline__ uint32_t signs8(const uint32_t *w)
+{
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r |= ((w[i] >> 12) & 8u) << (8 * i) | ((w[i] >> 24) & 0x80u) << (8 * i);
     return r;
 }
 
@@ -89,86 +105,98 @@ struct Kv4Move {
     int B, H_kv, D, n_max, T;
 };
 
-// One thread moves one group (32 bytes of bf16, 8 bytes of codes, 1 of scale); consecutive
-// threads take the groups of a row, then the tokens of a head, so that a warp's cache side
-// is contiguous.  Returns whether the thread has a live group.
-__device__ __forceinline__ bool kv4_group(const Kv4Move &m, size_t &crow, int &grp, const uint16_t *&src)
+// The group of a thread: blockIdx.y is a (batch row, head) pair, z is K or V; consecutive threads
+// take the groups of a row, then the tokens, so that a warp's cache side is contiguous.
+// Returns whether the thread has a live group; its place in the cache and its bf16 values.
+template <int D>
+__device__ __forceinline__ bool kv4_group(const Kv4Move &m, size_t &crow, int &grp, uint16_t *&row)
 {
-    const int ng = m.D / KV_GROUP;
-    const uint32_t idx = blockIdx.x * (uint32_t)KV_NT + threadIdx.x;
-    const uint32_t row = idx / (uint32_t)ng;
-    grp = (int)(idx % (uint32_t)ng);
-    const uint32_t bh = row / (uint32_t)m.T;
-    const int t = (int)(row % (uint32_t)m.T);
-    const int b = (int)(bh / (uint32_t)m.H_kv), h = (int)(bh % (uint32_t)m.H_kv);
-    if (b >= m.B) return false;
-    const int which = blockIdx.y;
+    constexpr int NG = D / KV_GROUP;
+    const int idx = blockIdx.x * blockDim.x + threadIdx.x;
+    const int t = idx / NG;
+    grp = idx % NG;
+    const int b = (int)(blockIdx.y / (unsigned)m.H_kv), h = (int)(blockIdx.y % (unsigned)m.H_kv);
     const int first = m.pos[b], cnt = m.counts ? m.counts[b] : m.T;
     if (first < 0 || cnt < 0 || cnt > m.T || first > m.n_max - cnt) {
-        if (m.ctrl && which == 0 && h == 0 && t == 0 && grp == 0) set_dev_error(m.ctrl, DEV_BAD_POSITION);
+        if (m.ctrl && idx == 0 && h == 0 && blockIdx.z == 0) set_dev_error(m.ctrl, DEV_BAD_POSITION);
         return false;
     }
     if (t >= cnt) return false;
-    crow = ((size_t)b * m.H_kv + h) * m.n_max + (size_t)(first + t);
-    src = m.row[which] + (b * m.sb[which] + t * m.st[which] + h * m.sh[which] + grp * KV_GROUP);
+    crow = (size_t)blockIdx.y * m.n_max + (size_t)(first + t);
+    row = m.row[blockIdx.z] + (b * m.sb[blockIdx.z] + t * m.st[blockIdx.z] + h * m.sh[blockIdx.z] + grp * KV_GROUP);
     return true;
 }
 
-// New rows into the cache.
+// New rows into the cache.  WIDE: the rows are 32-byte aligned.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(KV_NT) santa_kv4_append_kernel(const Kv4Move m)
 {
     size_t crow;
     int grp;
-    const uint16_t *src;
-    if (!kv4_group(m, crow, grp, src)) return;
-    const uint4 *s4 = reinterpret_cast<const uint4 *>(src);
-    const uint4 a = s4[0], b = s4[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint16_t *row;
+    if (!kv4_group<D>(m, crow, grp, row)) return;
+    uint32_t w[8];
+    if (WIDE) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(__cvta_generic_to_global(row)));
+    } else {
+        const uint4 a = reinterpret_cast<const uint4 *>(row)[0], b = reinterpret_cast<const uint4 *>(row)[1];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
     uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    for (int i = 0; i < 8; ++i) amax = __vmaxu2(amax, w[i] & 0x7fff7fffu);
+    amax = max(amax & 0xffffu, amax >> 16);
     const uint32_t sc = ue5m3_scale(amax);
     uint32_t c[2] = {0, 0};
     if (sc != 0 && sc != UE5M3_NAN) {
-        const float s = __half2float(ue5m3_half(sc));
+        const float inv = __frcp_rn(__half2float(ue5m3_half(sc)));
+        constexpr float R = 0x1.8p12f;  // adding it rounds |x| < 2^11 to multiples of 2^-11
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __fdiv_rn(bf16lo_to_f32(w[4 * j + i]), s);
-                x[2 * i + 1] = __fdiv_rn(bf16hi_to_f32(w[4 * j + i]), s);
+                x[2 * i] = __fsub_rn(__fadd_rn(bf16lo_to_f32(w[4 * j + i]) * inv, R), R);
+                x[2 * i + 1] = __fsub_rn(__fadd_rn(bf16hi_to_f32(w[4 * j + i]) * inv, R), R);
             }
-            c[j] = e2m1_pack8(x);
+            c[j] = e2m1_pack8(x) | signs8(w + 4 * j);
         }
     }
-    const int which = blockIdx.y;
-    *reinterpret_cast<uint2 *>(m.code[which] + crow * (m.D / 2) + grp * 8) = make_uint2(c[0], c[1]);
-    m.scale[which][crow * (m.D / KV_GROUP) + grp] = (uint8_t)sc;
+    *reinterpret_cast<uint2 *>(m.code[blockIdx.z] + crow * (D / 2) + grp * 8) = make_uint2(c[0], c[1]);
+    m.scale[blockIdx.z][crow * (D / KV_GROUP) + grp] = (uint8_t)sc;
 }
 
 // Cache rows back to bf16.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(KV_NT) santa_kv4_read_kernel(const Kv4Move m)
 {
     size_t crow;
     int grp;
-    const uint16_t *src;
-    if (!kv4_group(m, crow, grp, src)) return;
-    const int which = blockIdx.y;
-    const uint2 c = *reinterpret_cast<const uint2 *>(m.code[which] + crow * (m.D / 2) + grp * 8);
-    const float s = __half2float(ue5m3_half(m.scale[which][crow * (m.D / KV_GROUP) + grp]));
-    uint4 *dst = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(src));
+    uint16_t *row;
+    if (!kv4_group<D>(m, crow, grp, row)) return;
+    const uint2 c = *reinterpret_cast<const uint2 *>(m.code[blockIdx.z] + crow * (D / 2) + grp * 8);
+    const float s = __half2float(ue5m3_half(m.scale[blockIdx.z][crow * (D / KV_GROUP) + grp]));
+    uint32_t o[8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        uint32_t h[4], o[4];
+        uint32_t h[4];
         e2m1_unpack8(j ? c.y : c.x, h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
             const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
-            o[i] = *reinterpret_cast<const uint32_t *>(&v);
+            o[4 * j + i] = *reinterpret_cast<const uint32_t *>(&v);
         }
-        dst[j] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (WIDE) {
+        asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]),
+                     "r"(o[5]), "r"(o[6]), "r"(o[7]), "l"(__cvta_generic_to_global(row))
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(row)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4 *>(row)[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 

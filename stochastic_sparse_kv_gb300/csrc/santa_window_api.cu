@@ -23,13 +23,27 @@ int check_cache(const santa_shape *sh, const santa_kv4 *c)
     return SANTA_OK;
 }
 
+const void *move_kernel(int D, bool read, bool wide)
+{
+    switch ((D == 128) * 4 + read * 2 + wide) {
+    case 0: return (const void *)santa_kv4_append_kernel<64, false>;
+    case 1: return (const void *)santa_kv4_append_kernel<64, true>;
+    case 2: return (const void *)santa_kv4_read_kernel<64, false>;
+    case 3: return (const void *)santa_kv4_read_kernel<64, true>;
+    case 4: return (const void *)santa_kv4_append_kernel<128, false>;
+    case 5: return (const void *)santa_kv4_append_kernel<128, true>;
+    case 6: return (const void *)santa_kv4_read_kernel<128, false>;
+    default: return (const void *)santa_kv4_read_kernel<128, true>;
+    }
+}
+
 // The checks and the launch shared by append and read.  `distinct`: the rows are written, so
 // no two may share memory.
 int move_rows(const santa_shape *sh, const santa_kv4 *c, const santa_rows *r, int32_t T, const int32_t *pos,
               const int32_t *counts, void *workspace, void *stream, bool distinct)
 {
-    const int rc = check_cache(sh, c);
-    if (rc) return rc;
+    int rc = check_cache(sh, c);
+    if (rc || (rc = check_groups(sh))) return rc;
     if (!r || !r->k || !r->v || !pos || T < 0) return SANTA_ERR_INVALID_ARG;
     if (!aligned(r->k, 16) || !aligned(r->v, 16) || !aligned(pos, 4) || (counts && !aligned(counts, 4)) ||
         (workspace && !aligned(workspace, 256)))
@@ -79,12 +93,16 @@ int move_rows(const santa_shape *sh, const santa_kv4 *c, const santa_rows *r, in
     m.D = sh->d;
     m.n_max = sh->n_max;
     m.T = T;
-    const dim3 grid((unsigned)((groups * T + KV_NT - 1) / KV_NT), 2);
-    if (distinct)
-        santa_kv4_read_kernel<<<grid, KV_NT, 0, (cudaStream_t)stream>>>(m);
-    else
-        santa_kv4_append_kernel<<<grid, KV_NT, 0, (cudaStream_t)stream>>>(m);
-    return cudaGetLastError() == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
+    // 32-byte accesses where every row begins at one
+    bool wide = aligned(r->k, 32) && aligned(r->v, 32);
+    for (int i = 0; i < 3; ++i)
+        if (dims[i] > 1) wide = wide && r->k_stride[i] % 16 == 0 && r->v_stride[i] % 16 == 0;
+    const int row_groups = T * (sh->d / KV_GROUP);
+    const int threads = std::min(KV_NT, (row_groups + 31) / 32 * 32);
+    const dim3 grid((unsigned)((row_groups + threads - 1) / threads), (unsigned)(sh->B * sh->H_kv), 2);
+    void *args[] = {&m};
+    const void *fn = move_kernel(sh->d, distinct, wide);
+    return cudaLaunchKernel(fn, grid, dim3((unsigned)threads), args, 0, (cudaStream_t)stream) == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
 }
 
 int check_window(const santa_shape *sh, const void *q, const int32_t *seq_lens, int32_t window, int32_t sinks,

@@ -116,6 +116,37 @@ def test_ragged_counts_and_strides(d):
             assert torch.all(vo[b, c:] == 9)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shift,pad", [(8, 0), (0, 8), (8, 8), (16, 16), (24, 0)])
+def test_rows_aligned_to_16_bytes_only(d, shift, pad):
+    """K and V at 16-byte offsets of their own, head strides that are odd multiples of 8."""
+    g = gen(shift + pad)
+    B, T, H_kv, n_max = 2, 19, 3, 32
+    room = rand(g, B, T, H_kv, d + pad).to(DEV).reshape(-1)
+
+    def rows_at(offset):
+        buf = torch.full((offset + room.numel() + 32,), 3.0, dtype=torch.bfloat16, device=DEV)
+        buf[offset:offset + room.numel()] = room
+        return torch.as_strided(buf, (B, T, H_kv, d), (T * H_kv * (d + pad), H_kv * (d + pad), d + pad, 1), offset), buf
+
+    (k, _), (v, _) = rows_at(shift), rows_at(0)
+    cache = santa.new_kv4_cache(B, H_kv, n_max, d)
+    santa.kv4_append(cache, k, v, ints([3, 13]))
+    c, s = kv4_util.quantise(k.cpu().transpose(1, 2).contiguous())
+    for b, p in ((0, 3), (1, 13)):
+        for got in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+            assert np.array_equal(got[0][b, :, p:p + T].cpu().numpy(), c[b])
+            assert np.array_equal(got[1][b, :, p:p + T].cpu().numpy(), s[b])
+    (ko, kbuf), (vo, vbuf) = rows_at(shift), rows_at(0)
+    before = kbuf.clone()
+    santa.kv4_read(cache, ints([3, 13]), ko, vo)
+    ref = kv4_util.values(c, s)
+    assert np.array_equal(ko.cpu().transpose(1, 2).double().numpy(), ref)
+    assert np.array_equal(vo.cpu().transpose(1, 2).double().numpy(), ref)
+    ko.copy_(k)
+    assert torch.equal(kbuf, before)          # nothing beside the rows was written
+
+
 def test_every_largest_magnitude_and_every_quotient():
     """Every finite bf16 as a group's largest magnitude (all scales, ties and the ends of the
     range), beside values of all smaller sizes; and every bf16 mantissa against every scale
