@@ -17,7 +17,7 @@
 // integers of 8 bits by 2 and by 4 bits, a border of the rounding (5 and 3 bits) times its
 // divisor is an integer of the same grid as the dividend, so a quotient lies on a border exactly
 // or at least 2^-8 of itself away.  An fp32 product with the reciprocal (off by less than 2^-21)
-// rounded to fewer bits in between (2^-16, and 2^-12 absolute) is on the border or on the same
+// rounded to 16 bits is on the border or on the same
 // side of it.
 //
 // Both kernels move 2.56 bytes a value and are bound by that: one thread takes one group, in one
@@ -66,12 +66,23 @@ __device__ __forceinline__ uint32_t e2m1_pack8(const float (&x)[8])
     return r;
 }
 
-// The sign bits of eight bf16 values (pairs in w[0..3]) as those of their codes.
-__device__ __forceinline__ uint32_t signs8(const uint32_t *w)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void add2(float &a, float &b, float x, float y)
 {
-    uint32_t r = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r |= ((w[i] >> 12) & 8u) << (8 * i) | ((w[i] >> 24) & 0x80u) << (8 * i);
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(y));
+}
+
+// (a, b) * (x, y) + (u, v)
+__device__ __forceinline__ float2 fma2(float a, float b, float x, float y, float u, float v)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 s, {%6, %7};\n\t"
+        "fma.rn.f32x2 p, p, q, s;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a), "f"(b), "f"(x), "f"(y), "f"(u), "f"(v));
     return r;
 }
 
@@ -152,16 +163,20 @@ __global__ void __launch_bounds__(KV_NT) santa_kv4_append_kernel(const Kv4Move m
     uint32_t c[2] = {0, 0};
     if (sc != 0 && sc != UE5M3_NAN) {
         const float inv = __frcp_rn(__half2float(ue5m3_half(sc)));
-        constexpr float R = 0x1.8p12f;  // adding it rounds |x| < 2^11 to multiples of 2^-11
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __fsub_rn(__fadd_rn(bf16lo_to_f32(w[4 * j + i]) * inv, R), R);
-                x[2 * i + 1] = __fsub_rn(__fadd_rn(bf16hi_to_f32(w[4 * j + i]) * inv, R), R);
+                // t rounded to 16 bits: u - (u - t) with u = (2^8 + 1) t (Veltkamp's splitting)
+                const float2 t = fma2(bf16lo_to_f32(w[4 * j + i]), bf16hi_to_f32(w[4 * j + i]), inv, inv, -0.f, -0.f);
+                const float2 u = fma2(t.x, t.y, 257.f, 257.f, -0.f, -0.f);
+                const float2 d = fma2(t.x, t.y, -1.f, -1.f, u.x, u.y);
+                const float2 y = fma2(d.x, d.y, -1.f, -1.f, u.x, u.y);
+                x[2 * i] = y.x;
+                x[2 * i + 1] = y.y;
             }
-            c[j] = e2m1_pack8(x) | signs8(w + 4 * j);
+            c[j] = e2m1_pack8(x);
         }
     }
     *reinterpret_cast<uint2 *>(m.code[blockIdx.z] + crow * (D / 2) + grp * 8) = make_uint2(c[0], c[1]);

@@ -176,26 +176,6 @@ __device__ __forceinline__ void bar_sync()
     asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ void add2(float &a, float &b, float x, float y)
-{
-    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
-        "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
-        : "+f"(a), "+f"(b)
-        : "f"(x), "f"(y));
-}
-
-// (a, b) * (x, y) + (u, v)
-__device__ __forceinline__ float2 fma2(float a, float b, float x, float y, float u, float v)
-{
-    float2 r;
-    asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 s, {%6, %7};\n\t"
-        "fma.rn.f32x2 p, p, q, s;\n\tmov.b64 {%0, %1}, p;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a), "f"(b), "f"(x), "f"(y), "f"(u), "f"(v));
-    return r;
-}
-
 __device__ __forceinline__ float2 unpack_f16(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
 
 // Whether the phase of that parity has ended (no waiting).
