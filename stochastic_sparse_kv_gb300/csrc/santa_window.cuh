@@ -312,15 +312,6 @@ struct WinShares {
     }
 };
 
-// One more piece of a group has been written (by this CTA, before a barrier): the count before
-// it.  Reads by the CTA after another barrier see the counted ones.
-__device__ __forceinline__ int win_arrive(int32_t *counter)
-{
-    int old;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(__cvta_generic_to_global(counter)) : "memory");
-    return old;
-}
-
 __device__ __forceinline__ void win_store(const WinParams &p, size_t i, float v)
 {
     if (p.out_bf16)
@@ -1112,19 +1103,28 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
 
     // ---- groups that span CTAs: the last to arrive joins
     bar_sync<NT>();
-    if (tid < 2) {
-        const int gi = tid ? open1 : open0;
-        flag[tid] = 0;
+    if (warp == 0) {
+        // lanes 0 and 1 arrive for the two at once: one fence for what the CTA wrote, one round
+        // trip (the lanes one after the other, each with its fences, took 2.5 us more)
+        const int gi = lane == 0 ? open0 : lane == 1 ? open1 : -1;
+        int ca = 0, n = 0, old = -1;
         if (gi >= 0) {
             const int b = gi / p.H_kv;
             const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
             const int start = prefix[b] + gi % p.H_kv * win_span(cnt) + WN_SETUP;
-            const int ca = ctas.owner(start), n = ctas.owner(start + cnt - 1) - ca + 1;
-            if (win_arrive(p.ctrl + CTRL_GROUPS + gi) == n - 1) {
-                p.ctrl[CTRL_GROUPS + gi] = 0;
-                flag[tid] = n;
-                flag[2 + tid] = ca;
-            }
+            ca = ctas.owner(start);
+            n = ctas.owner(start + cnt - 1) - ca + 1;
+        }
+        __syncwarp();
+        __threadfence();
+        if (gi >= 0) old = atomicAdd(p.ctrl + CTRL_GROUPS + gi, 1);
+        __syncwarp();
+        __threadfence();
+        const bool last = gi >= 0 && old == n - 1;
+        if (last) p.ctrl[CTRL_GROUPS + gi] = 0;
+        if (lane < 2) {
+            flag[lane] = last ? n : 0;
+            flag[2 + lane] = ca;
         }
     }
     bar_sync<NT>();
