@@ -47,6 +47,7 @@ constexpr int WN_MAX_WARPS = 16;
 constexpr int WN_RED = 4 * 32 * WN_MAX_WARPS;  // floats of a join's partial sums: 4 x max(G D / 4, threads)
 constexpr float WN_TOP = 9.f;             // log2 of p where a new maximum puts it
 constexpr float WN_SLACK = 6.f;           // and how far above that later ones may be
+constexpr int WN_ALONE = 4;               // tiles a warp up to which a group stays in one CTA
 constexpr int WN_SETUP = 2;               // tiles that beginning a group costs about as much as
 
 // One CTA to an SM.  4-bit: 16 warps, each copying its own tiles (the conversions need the
@@ -454,7 +455,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
 
     // ---- setup: checked lengths and the list's prefix, barriers
     if (warp == 0) {
-        int run = 0;
+        int run = 0, longest = 0;
         bool bad = false;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
@@ -463,7 +464,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 bad = true;
                 n = 0;
             }
-            const int cnt = p.H_kv * win_span(win_tiles<TK>(n, p.window, p.sinks).cnt);
+            const int tiles = win_tiles<TK>(n, p.window, p.sinks).cnt, cnt = p.H_kv * win_span(tiles);
+            longest = max(longest, tiles);
             int x = cnt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -476,7 +478,11 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             }
             run += __shfl_sync(FULL, x, 31);
         }
-        if (lane == 0) prefix[p.B] = run;
+        longest = __reduce_max_sync(FULL, longest);
+        if (lane == 0) {
+            prefix[p.B] = run;
+            flag[0] = longest;
+        }
         if (bad && blockIdx.x == 0) set_dev_error(p.ctrl, DEV_BAD_SEQLEN);
     }
     if (!KV4 && warp == W && lane < W) {
@@ -491,10 +497,19 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     for (int b = blockIdx.x; b < p.B; b += gridDim.x)  // sequences without keys
         if (nb[b] == 0)
             for (int i = tid; i < p.H_q * D; i += blockDim.x) win_store(p, (size_t)b * p.H_q * D + i, 0.f);
-    const int NC = min((int)gridDim.x, (T + W - 1) / W);  // CTAs with a share
+    // Few short groups: a CTA for each.  Else even shares of the list, which split groups between
+    // CTAs and join them through the workspace: that takes 6 us (fence, arrival, join), as
+    // long as WN_ALONE more tiles a warp.
+    const bool alone = p.B * p.H_kv <= (int)gridDim.x && flag[0] <= WN_ALONE * W;
+    const int NC = alone ? p.B * p.H_kv : min((int)gridDim.x, (T + W - 1) / W);  // CTAs with a share
     if ((int)blockIdx.x >= NC) return;
     const WinShares ctas(T, NC);
-    const int t0 = ctas.first(blockIdx.x), t1 = ctas.first(blockIdx.x + 1);
+    int t0 = ctas.first(blockIdx.x), t1 = ctas.first(blockIdx.x + 1);
+    if (alone) {
+        const int b = blockIdx.x / p.H_kv, span = win_span(win_tiles<TK>(nb[b], p.window, p.sinks).cnt);
+        t0 = prefix[b] + blockIdx.x % p.H_kv * span;
+        t1 = t0 + span;
+    }
     const WinShares warps(t1 - t0, W);
     const int ta = t0 + warps.first(owner), tb = t0 + warps.first(owner + 1);
 

@@ -124,7 +124,7 @@ long long window_ctas(const santa_shape *sh)
 {
     const long long spans = (long long)sh->B * sh->H_kv * ((sh->n_max + 15) / 16 + WN_SETUP);
     const int w = std::min(win_warps(false), win_warps(true));
-    return std::min<long long>(WN_MAX_CTAS, (spans + w - 1) / w);
+    return std::min<long long>(WN_MAX_CTAS, std::max<long long>((spans + w - 1) / w, (long long)sh->B * sh->H_kv));
 }
 
 const void *window_kernel(int D, bool kv4, bool wide)
@@ -176,7 +176,8 @@ int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void
     const int most = p.window > 0 ? (int)std::min<long long>(sh->n_max, (long long)p.window + p.sinks) : sh->n_max;
     // a group's visible keys touch at most two tiles more than they would fill
     const long long spans = (long long)sh->B * sh->H_kv * ((most + tile - 1) / tile + 2 + WN_SETUP);
-    const long long grid = std::min(std::min<long long>(cap, (long long)sms * occ), (spans + win_warps(kv4) - 1) / win_warps(kv4));
+    const long long want = std::max((spans + win_warps(kv4) - 1) / win_warps(kv4), (long long)sh->B * sh->H_kv);
+    const long long grid = std::min(std::min<long long>(cap, (long long)sms * occ), want);
     CUtensorMap tm_k, tm_v;
     if (!kv4) {
         const long long rows = (long long)sh->B * sh->H_kv * sh->n_max;
