@@ -116,102 +116,121 @@ struct Kv4Move {
     int B, H_kv, D, n_max, T;
 };
 
-// The group of a thread: blockIdx.y is a (batch row, head) pair, z is K or V; consecutive threads
+// A thread's group, of K and of V: blockIdx.y is a (batch row, head) pair; consecutive threads
 // take the groups of a row, then the tokens, so that a warp's cache side is contiguous.
 // Returns whether the thread has a live group; its place in the cache and its bf16 values.
 template <int D>
-__device__ __forceinline__ bool kv4_group(const Kv4Move &m, size_t &crow, int &grp, uint16_t *&row)
+__device__ __forceinline__ bool kv4_group(const Kv4Move &m, size_t &place, uint16_t *(&row)[2])
 {
     constexpr int NG = D / KV_GROUP;
     const int idx = blockIdx.x * blockDim.x + threadIdx.x;
-    const int t = idx / NG;
-    grp = idx % NG;
+    const int t = idx / NG, grp = idx % NG;
     const int b = (int)(blockIdx.y / (unsigned)m.H_kv), h = (int)(blockIdx.y % (unsigned)m.H_kv);
     const int first = m.pos[b], cnt = m.counts ? m.counts[b] : m.T;
     if (first < 0 || cnt < 0 || cnt > m.T || first > m.n_max - cnt) {
-        if (m.ctrl && idx == 0 && h == 0 && blockIdx.z == 0) set_dev_error(m.ctrl, DEV_BAD_POSITION);
+        if (m.ctrl && idx == 0 && h == 0) set_dev_error(m.ctrl, DEV_BAD_POSITION);
         return false;
     }
     if (t >= cnt) return false;
-    crow = (size_t)blockIdx.y * m.n_max + (size_t)(first + t);
-    row = m.row[blockIdx.z] + (b * m.sb[blockIdx.z] + t * m.st[blockIdx.z] + h * m.sh[blockIdx.z] + grp * KV_GROUP);
+    place = ((size_t)blockIdx.y * m.n_max + (size_t)(first + t)) * NG + grp;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) row[i] = m.row[i] + (b * m.sb[i] + t * m.st[i] + h * m.sh[i] + grp * KV_GROUP);
     return true;
+}
+
+// Code and scale of one group: its bf16 bits in pairs.
+__device__ __forceinline__ uint2 kv4_encode(const uint32_t (&w)[8], uint32_t &scale)
+{
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = __vmaxu2(amax, w[i] & 0x7fff7fffu);
+    amax = max(amax & 0xffffu, amax >> 16);
+    scale = ue5m3_scale(amax);
+    if (scale == 0 || scale == UE5M3_NAN) return make_uint2(0, 0);
+    const float inv = __frcp_rn(__half2float(ue5m3_half(scale)));
+    uint32_t c[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // t rounded to 16 bits: u - (u - t) with u = (2^8 + 1) t (Veltkamp's splitting)
+            const float2 t = fma2(bf16lo_to_f32(w[4 * j + i]), bf16hi_to_f32(w[4 * j + i]), inv, inv, -0.f, -0.f);
+            const float2 u = fma2(t.x, t.y, 257.f, 257.f, -0.f, -0.f);
+            const float2 d = fma2(t.x, t.y, -1.f, -1.f, u.x, u.y);
+            const float2 y = fma2(d.x, d.y, -1.f, -1.f, u.x, u.y);
+            x[2 * i] = y.x;
+            x[2 * i + 1] = y.y;
+        }
+        c[j] = e2m1_pack8(x);
+    }
+    return make_uint2(c[0], c[1]);
 }
 
 // New rows into the cache.  WIDE: the rows are 32-byte aligned.
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(KV_NT) santa_kv4_append_kernel(const Kv4Move m)
 {
-    size_t crow;
-    int grp;
-    uint16_t *row;
-    if (!kv4_group<D>(m, crow, grp, row)) return;
-    uint32_t w[8];
-    if (WIDE) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(__cvta_generic_to_global(row)));
-    } else {
-        const uint4 a = reinterpret_cast<const uint4 *>(row)[0], b = reinterpret_cast<const uint4 *>(row)[1];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    }
-    uint32_t amax = 0;
+    size_t place;
+    uint16_t *row[2];
+    if (!kv4_group<D>(m, place, row)) return;
+    uint32_t w[2][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = __vmaxu2(amax, w[i] & 0x7fff7fffu);
-    amax = max(amax & 0xffffu, amax >> 16);
-    const uint32_t sc = ue5m3_scale(amax);
-    uint32_t c[2] = {0, 0};
-    if (sc != 0 && sc != UE5M3_NAN) {
-        const float inv = __frcp_rn(__half2float(ue5m3_half(sc)));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // t rounded to 16 bits: u - (u - t) with u = (2^8 + 1) t (Veltkamp's splitting)
-                const float2 t = fma2(bf16lo_to_f32(w[4 * j + i]), bf16hi_to_f32(w[4 * j + i]), inv, inv, -0.f, -0.f);
-                const float2 u = fma2(t.x, t.y, 257.f, 257.f, -0.f, -0.f);
-                const float2 d = fma2(t.x, t.y, -1.f, -1.f, u.x, u.y);
-                const float2 y = fma2(d.x, d.y, -1.f, -1.f, u.x, u.y);
-                x[2 * i] = y.x;
-                x[2 * i + 1] = y.y;
-            }
-            c[j] = e2m1_pack8(x);
+    for (int i = 0; i < 2; ++i) {
+        if (WIDE) {
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3]), "=r"(w[i][4]), "=r"(w[i][5]), "=r"(w[i][6]),
+                           "=r"(w[i][7])
+                         : "l"(__cvta_generic_to_global(row[i])));
+        } else {
+            const uint4 a = reinterpret_cast<const uint4 *>(row[i])[0], b = reinterpret_cast<const uint4 *>(row[i])[1];
+            w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w, w[i][4] = b.x, w[i][5] = b.y, w[i][6] = b.z, w[i][7] = b.w;
         }
     }
-    *reinterpret_cast<uint2 *>(m.code[blockIdx.z] + crow * (D / 2) + grp * 8) = make_uint2(c[0], c[1]);
-    m.scale[blockIdx.z][crow * (D / KV_GROUP) + grp] = (uint8_t)sc;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t sc;
+        reinterpret_cast<uint2 *>(m.code[i])[place] = kv4_encode(w[i], sc);
+        m.scale[i][place] = (uint8_t)sc;
+    }
 }
 
 // Cache rows back to bf16.
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(KV_NT) santa_kv4_read_kernel(const Kv4Move m)
 {
-    size_t crow;
-    int grp;
-    uint16_t *row;
-    if (!kv4_group<D>(m, crow, grp, row)) return;
-    const uint2 c = *reinterpret_cast<const uint2 *>(m.code[blockIdx.z] + crow * (D / 2) + grp * 8);
-    const float s = __half2float(ue5m3_half(m.scale[blockIdx.z][crow * (D / KV_GROUP) + grp]));
-    uint32_t o[8];
+    size_t place;
+    uint16_t *row[2];
+    if (!kv4_group<D>(m, place, row)) return;
+    uint2 c[2];
+    float s[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        uint32_t h[4];
-        e2m1_unpack8(j ? c.y : c.x, h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-            const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
-            o[4 * j + i] = *reinterpret_cast<const uint32_t *>(&v);
-        }
+    for (int i = 0; i < 2; ++i) {
+        c[i] = reinterpret_cast<const uint2 *>(m.code[i])[place];
+        s[i] = __half2float(ue5m3_half(m.scale[i][place]));
     }
-    if (WIDE) {
-        asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]),
-                     "r"(o[5]), "r"(o[6]), "r"(o[7]), "l"(__cvta_generic_to_global(row))
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(row)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<uint4 *>(row)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t h[4];
+            e2m1_unpack8(j ? c[i].y : c[i].x, h);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[x]));
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s[i], f.y * s[i]);
+                o[4 * j + x] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+        }
+        if (WIDE) {
+            asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]),
+                         "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "l"(__cvta_generic_to_global(row[i]))
+                         : "memory");
+        } else {
+            reinterpret_cast<uint4 *>(row[i])[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            reinterpret_cast<uint4 *>(row[i])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
     }
 }
 

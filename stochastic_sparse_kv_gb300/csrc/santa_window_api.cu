@@ -99,7 +99,7 @@ int move_rows(const santa_shape *sh, const santa_kv4 *c, const santa_rows *r, in
         if (dims[i] > 1) wide = wide && r->k_stride[i] % 16 == 0 && r->v_stride[i] % 16 == 0;
     const int row_groups = T * (sh->d / KV_GROUP);
     const int threads = std::min(KV_NT, (row_groups + 31) / 32 * 32);
-    const dim3 grid((unsigned)((row_groups + threads - 1) / threads), (unsigned)(sh->B * sh->H_kv), 2);
+    const dim3 grid((unsigned)((row_groups + threads - 1) / threads), (unsigned)(sh->B * sh->H_kv));
     void *args[] = {&m};
     const void *fn = move_kernel(sh->d, distinct, wide);
     return cudaLaunchKernel(fn, grid, dim3((unsigned)threads), args, 0, (cudaStream_t)stream) == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
