@@ -250,6 +250,7 @@ int santa_decode_static(const santa_shape *shape, const void *q, const void *k_c
  *          the such number nearest max|x| / 6, ties to even, at most 10240 (0xE2).  As bits
  *          it is bits 7-14 of the fp16 of the same value.  0xFF (a NaN) where the group
  *          holds a NaN or an infinity: the whole group then reads back as NaN.
+ *          No other code above 0xE2 is ever written.
  *   codes  4 bits each: sign (bit 3) and index into {0, .5, 1, 1.5, 2, 3, 4, 6} (bits 0-2),
  *          the value nearest x / scale, ties to the even index, saturating at 6.  Byte i of
  *          a row holds values 2i (low half) and 2i + 1 (high half).
@@ -283,7 +284,8 @@ typedef struct {
  *  workspace any workspace of this library, or NULL: only its device error word is used.
  *            A batch row with pos < 0, counts outside [0, T] or pos + counts > n_max is
  *            skipped and sets SANTA_DEV_BAD_POSITION there
- * B * H_kv * T * d / 16 must be below 2^31.  The caller advances its sequence lengths.
+ * B * H_kv * T * d / 16 must be below 2^31, B * H_kv at most 16320.  The caller advances its
+ * sequence lengths.  One launch; it can be captured, positions and counts are read when it runs.
  */
 int santa_kv4_append(const santa_shape *shape, const santa_kv4 *cache, const santa_rows *rows, int32_t T,
                      const int32_t *pos, const int32_t *counts, void *workspace, void *stream);
@@ -292,7 +294,7 @@ int santa_kv4_append(const santa_shape *shape, const santa_kv4 *cache, const san
  * santa_kv4_read -- rows of a 4-bit cache back as bf16 (exact: every held value is a bf16).
  * Arguments as for santa_kv4_append, with `rows` written instead: cache row pos[b] + t goes
  * to row (b, t) for t < counts[b], and the other rows stay as they were.  No two rows may
- * share memory: in order of size, each stride must step over all that the smaller ones span
+ * share memory, of K or of V: in order of size, each stride must step over all that the smaller ones span
  * (SANTA_ERR_INVALID_ARG otherwise).  For example, with the strides of a bf16 cache
  * [B, H_kv, n, d] it fills the cache that santa_decode samples.
  */
@@ -310,14 +312,17 @@ int santa_kv4_read(const santa_shape *shape, const santa_kv4 *cache, const santa
 
 /*
  * santa_window_workspace_size -- bytes of workspace santa_decode_window and santa_decode_kv4
- * need for this shape (the same for both).  Pure host computation.
+ * need for this shape (the same for both; a workspace of santa_workspace_size may be smaller).
+ * Returns SANTA_OK, SANTA_ERR_INVALID_ARG or SANTA_ERR_UNSUPPORTED (limits as for santa_decode,
+ * among them B * H_kv <= 16320).  Pure host computation.
  */
 int santa_window_workspace_size(const santa_shape *shape, size_t *bytes);
 
 /*
  * santa_decode_window -- over a bf16 cache.  q, k_cache, v_cache, seq_lens, out, workspace and
  * stream as for santa_decode; window >= 0; sinks >= 0 (ignored when window = 0); flags 0 or
- * SANTA_OUT_BF16.  n_b = 0 gives zeros.
+ * SANTA_OUT_BF16.  n_b = 0 gives zeros.  One launch.  Results do not depend on timing: the same
+ * call on the same device gives the same bits.
  */
 int santa_decode_window(const santa_shape *shape, const void *q, const void *k_cache, const void *v_cache,
                         const int32_t *seq_lens, int32_t window, int32_t sinks, int32_t flags, float *out,

@@ -157,6 +157,8 @@ int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void
     p.H_kv = sh->H_kv;
     p.n_max = sh->n_max;
     p.G = G;
+    p.window = std::min(p.window, sh->n_max);  // (larger ones see no more; no sum below overflows)
+    p.sinks = std::min(p.sinks, sh->n_max);
     p.out_bf16 = (flags & SANTA_OUT_BF16) ? 1 : 0;
     const float scale = sh->scale != 0.f ? sh->scale : (float)(1.0 / std::sqrt((double)D));
     const double k2 = std::fabs((double)scale) * 1.4426950408889634;

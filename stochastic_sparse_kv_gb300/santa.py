@@ -430,6 +430,8 @@ def kv4_read(cache: KV4Cache, pos: torch.Tensor, k_out: torch.Tensor, v_out: tor
     kv4_append) for t < counts[b] (default T); other rows stay as they were.  Exact.  For a
     bf16 cache [B, H_kv, n, d] pass its transpose(1, 2).  Returns (k_out, v_out)."""
     if k_out.dim() != 4 or k_out.shape[1] != 0:
+        if k_out.is_cuda and k_out.data_ptr() == v_out.data_ptr():
+            raise ValueError("k_out and v_out are the same rows")
         _move_rows(load().santa_kv4_read, "santa_kv4_read", cache, k_out, v_out, pos, counts, workspace, stream)
     return k_out, v_out
 
@@ -440,6 +442,8 @@ def _window_call(q, dims, cache_args, fn, what, seq_lens, window, sinks, scale, 
     if len(qs) != 3 or qs[0] != B or qs[2] != d or q.device != dev:
         raise ValueError("q [B, H_q, d] and the cache's shape or device disagree")
     _int_vector(seq_lens, "seq_lens", B, dev)
+    if window >= 1 << 31 or sinks >= 1 << 31:
+        raise ValueError("window and sinks are 32-bit numbers")
     shape, nbytes = _shape_of((B, qs[1], H_kv, d, n_max, scale))
     if out is None:
         if out_dtype not in (torch.float32, torch.bfloat16):

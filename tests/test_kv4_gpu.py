@@ -283,6 +283,38 @@ def test_attention_many_splits_and_many_rows(op, B, H_kv, n, window):
 
 
 @pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("n", [511, 512, 513, 2047, 2048, 2049])
+def test_where_groups_begin_to_be_split(op, n):
+    """Few groups around the length up to which each has one CTA to itself, a short one and an
+    empty one among them, and the same with more groups than SMs."""
+    n_max = -(-n // 16) * 16
+    q, k, v = inputs(n, [n, 5, 0], 8, 2, 128, n_max)
+    check(op, q, k, v, [n, 5, 0])
+    q, k, v = inputs(n, [n // 16] * 100, 4, 2, 64, 144)
+    check(op, q, k, v, [min(n // 16 + b, 144) for b in range(100)])
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_many_batch_rows(op):
+    """1024 batch rows (the most there may be), empty and short ones."""
+    seq = [(7 * b) % 49 for b in range(1024)]
+    q, k, v = inputs(1, seq, 2, 2, 64, 48)
+    check(op, q, k, v, seq)
+    check(op, q, k, v, seq, 16, 2)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_windows_and_sinks_beyond_the_cache(op):
+    seq = [100, 33]
+    q, k, v = inputs(2, seq, 4, 2, 64, 112)
+    big = 2 ** 31 - 1
+    every = check(op, q, k, v, seq)
+    assert torch.equal(check(op, q, k, v, seq, big, big), every)
+    assert torch.equal(check(op, q, k, v, seq, big, 0), every)
+    check(op, q, k, v, seq, 7, big)
+
+
+@pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("std,scale", [(0.0, 0.0), (0.1, 0.0), (3.0, 1e-3), (12.0, 0.0), (3.0, -0.1)])
 def test_flat_and_peaked_scores_and_other_scales(op, std, scale):
     seq = [400, 1000]
@@ -563,6 +595,14 @@ def test_binding_refuses_mismatched_tensors():
         santa.decode_window(q, kc, kc[:, :, :20], pos, 4)
     with pytest.raises(ValueError):
         santa.decode_window(q, kc.transpose(1, 2), kc, pos, 4)
+    with pytest.raises(ValueError):
+        santa.decode_kv4(q, cache, pos, window=1 << 31)
+    with pytest.raises(ValueError):                 # K and V read into the same rows
+        santa.kv4_read(cache, pos, x, x)
+    with pytest.raises(santa.SantaError) as e:      # queries that begin between two 16-byte boundaries
+        room = z(2 * 4 * 64 + 8, dtype=torch.bfloat16, device=DEV)
+        santa.decode_kv4(room[4:4 + 512].view(2, 4, 64), cache, pos)
+    assert e.value.status == -2
     with pytest.raises(santa.SantaError) as e:
         santa.decode_kv4(q, cache, pos, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
     assert e.value.status == -3
