@@ -183,11 +183,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// A barrier of the N threads that work.
+// A barrier of N threads (1: all that work; 2, 3: its halves).
 template <int N>
-__device__ __forceinline__ void bar_sync()
+__device__ __forceinline__ void bar_sync(int id = 1)
 {
-    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
 }
 
 __device__ __forceinline__ float2 unpack_f16(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
@@ -326,6 +326,9 @@ struct WinShares {
     }
 };
 
+// Orders this thread's accesses, and those of others that it has seen, for the whole GPU.
+__device__ __forceinline__ void fence_acq_rel() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 __device__ __forceinline__ void win_store(const WinParams &p, size_t i, float v)
 {
     if (p.out_bf16)
@@ -349,92 +352,107 @@ struct WinPieces {
     }
 };
 
-// All NT threads: the n pieces of group gi joined into `part` (a piece) or, when that is null,
-// into the output.  red: WN_RED floats; scratch: 16 n + 16.  Begins and ends with both free.
-// FAR: the pieces were written by other CTAs too and are read past the L1 cache.
+// NT threads (tid of them, barrier bar): the n pieces of group gi joined into `part` (a piece) or,
+// when that is null, into the output.  red: WN_RED floats; scratch: 16 n + 16.  Begins and
+// ends with both free.  FAR: the pieces were written by other CTAs too and are read past the
+// L1 cache.
 template <int D, int NT, bool FAR>
-__device__ __forceinline__ void win_join(const WinParams &p, int n, const WinPieces pieces, float *red, float *scratch, int gi, float *part)
+__device__ __forceinline__ void win_join(const WinParams &p, int tid, int bar, int n, const WinPieces pieces, float *red, float *scratch,
+                                         int gi, float *part)
 {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int AHEAD = 8, HS = D + 4;
-    const int tid = threadIdx.x, lane = tid & 31, GS = p.G * HS;
+    const int lane = tid & 31, GS = p.G * HS;
     float *tot = scratch, *wt = scratch + 16, *lt = wt + 8 * n;
     auto load = [](const float *a) { return FAR ? __ldcg(a) : *a; };
     auto load4 = [](const float *a) {
         return FAR ? __ldcg(reinterpret_cast<const float4 *>(a)) : *reinterpret_cast<const float4 *>(a);
     };
-    // four outputs a thread; with few outputs, slices of the pieces.  The first pieces are on
+    // four outputs a thread; with few outputs, ns slices of the pieces.  The first pieces are on
     // their way while the weights are worked out (indexes past the last are those of the last:
     // a load under a condition would be waited for before the next)
-    const int nv = p.G * (D / 4), ns = max(1, NT / nv);
-    const int v0 = tid % nv, sl0 = tid / nv, h0 = v0 / (D / 4), at0 = h0 * HS + 4 * (v0 % (D / 4));
+    const int nv = p.G * (D / 4), cols = min(nv, NT), ns = NT / cols, sl = tid / cols;
+    int v = tid % cols, h = v / (D / 4), at = h * HS + 4 * (v % (D / 4));
     float4 ahead[AHEAD];
+    auto fetch = [&]() {
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) ahead[k] = load4(pieces.at(min(sl0 + k * ns, n - 1)) + at0);
+        for (int k = 0; k < AHEAD; ++k) ahead[k] = load4(pieces.at(min(sl + k * ns, n - 1)) + at);
+    };
+    fetch();
     // a warp a head: its common exponent, the pieces' weights, the sum
-    for (int h = tid >> 5; h < p.G; h += NT / 32) {
+    for (int hd = tid >> 5; hd < p.G; hd += NT / 32) {
         float C = __int_as_float(0x7f800000);
         for (int j = lane; j < n; j += 32) {
-            const float *pc = pieces.at(j) + GS + h;
+            const float *pc = pieces.at(j) + GS + hd;
             const float c = load(pc), l = load(pc + 8);
-            wt[8 * j + h] = c;
-            lt[8 * j + h] = l;
+            wt[8 * j + hd] = c;
+            lt[8 * j + hd] = l;
             C = fminf(C, c);
         }
 #pragma unroll
         for (int m = 16; m; m >>= 1) C = fminf(C, __shfl_xor_sync(FULL, C, m));
         float L = 0.f;
         for (int j = lane; j < n; j += 32) {
-            const float w = ex2(C - wt[8 * j + h]);
-            wt[8 * j + h] = w;
-            L = fmaf(w, lt[8 * j + h], L);
+            const float w = ex2(C - wt[8 * j + hd]);
+            wt[8 * j + hd] = w;
+            L = fmaf(w, lt[8 * j + hd], L);
         }
 #pragma unroll
         for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(FULL, L, m);
         if (lane == 0) {
-            tot[h] = C;
-            tot[8 + h] = L;
+            tot[hd] = C;
+            tot[8 + hd] = L;
         }
     }
-    bar_sync<NT>();
+    bar_sync<NT>(bar);
     auto add = [](float4 &o, const float4 &x, float w) {
         o.x = fmaf(w, x.x, o.x);
         o.y = fmaf(w, x.y, o.y);
         o.z = fmaf(w, x.z, o.z);
         o.w = fmaf(w, x.w, o.w);
     };
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (;;) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-        if (sl0 + k * ns < n) add(o, ahead[k], wt[8 * (sl0 + k * ns) + h0]);
-    for (int j = sl0 + AHEAD * ns; j < n; j += 4 * ns) {
+        for (int k = 0; k < AHEAD; ++k)
+            if (sl + k * ns < n) add(o, ahead[k], wt[8 * (sl + k * ns) + h]);
+        for (int j = sl + AHEAD * ns; j < n; j += 4 * ns) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ahead[k] = load4(pieces.at(min(j + k * ns, n - 1)) + at0);
+            for (int k = 0; k < 4; ++k) ahead[k] = load4(pieces.at(min(j + k * ns, n - 1)) + at);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (j + k * ns < n) add(o, ahead[k], wt[8 * (j + k * ns) + h0]);
-    }
-    if (tid < ns * nv) reinterpret_cast<float4 *>(red)[tid] = o;
-    if (ns > 1) bar_sync<NT>();
-    if (tid < nv) {
-        for (int s = 1; s < ns; ++s) add(o, reinterpret_cast<const float4 *>(red)[s * nv + tid], 1.f);
-        if (part) {
-            *reinterpret_cast<float4 *>(part + at0) = o;
-            if (tid % (D / 4) == 0) {
-                part[GS + h0] = tot[h0];
-                part[GS + 8 + h0] = tot[8 + h0];
-            }
-        } else {
-            const float r = 1.f / tot[8 + h0];
-            const size_t at = ((size_t)(gi / p.H_kv) * p.H_q + (size_t)(gi % p.H_kv) * p.G) * D + 4 * (size_t)tid;
-            o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
-            if (p.out_bf16)
-                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p.out) + at) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-            else
-                *reinterpret_cast<float4 *>(p.out + at) = o;
+            for (int k = 0; k < 4; ++k)
+                if (j + k * ns < n) add(o, ahead[k], wt[8 * (j + k * ns) + h]);
         }
+        if (ns > 1) {
+            reinterpret_cast<float4 *>(red)[tid] = o;
+            bar_sync<NT>(bar);
+            if (sl == 0)
+                for (int s = 1; s < ns; ++s) add(o, reinterpret_cast<const float4 *>(red)[s * cols + tid], 1.f);
+        }
+        if (sl == 0) {
+            if (part) {
+                *reinterpret_cast<float4 *>(part + at) = o;
+                if (v % (D / 4) == 0) {
+                    part[GS + h] = tot[h];
+                    part[GS + 8 + h] = tot[8 + h];
+                }
+            } else {
+                const float r = 1.f / tot[8 + h];
+                const size_t to = ((size_t)(gi / p.H_kv) * p.H_q + (size_t)(gi % p.H_kv) * p.G) * D + 4 * (size_t)v;
+                o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+                if (p.out_bf16)
+                    *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p.out) + to) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                else
+                    *reinterpret_cast<float4 *>(p.out + to) = o;
+            }
+        }
+        v += NT;  // (more outputs than threads: ns = 1)
+        if (v >= nv) break;
+        h = v / (D / 4);
+        at = h * HS + 4 * (v % (D / 4));
+        fetch();
     }
-    bar_sync<NT>();
+    bar_sync<NT>(bar);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -1125,7 +1143,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         __syncwarp();
         const WinPieces pieces{list, reinterpret_cast<const float *>(smem + lay.ring), p.first + (size_t)blockIdx.x * W * PIECE,
                                NS * STAGE / 4, PIECE};
-        win_join<D, NT, false>(p, __popc(set), pieces, red, scratch, gi, all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE);
+        win_join<D, NT, false>(p, tid, 1, __popc(set), pieces, red, scratch, gi, all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE);
     }
     if (open0 < 0 && open1 < 0) return;
 
@@ -1144,26 +1162,24 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             n = ctas.owner(start + cnt - 1) - ca + 1;
         }
         __syncwarp();
-        __threadfence();
+        fence_acq_rel();
         if (gi >= 0) old = atomicAdd(p.ctrl + CTRL_GROUPS + gi, 1);
-        __syncwarp();
-        __threadfence();
         const bool last = gi >= 0 && old == n - 1;
         if (last) p.ctrl[CTRL_GROUPS + gi] = 0;
+        if (__any_sync(FULL, last)) fence_acq_rel();
         if (lane < 2) {
             flag[lane] = last ? n : 0;
             flag[2 + lane] = ca;
         }
     }
     bar_sync<NT>();
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int n = flag[x], ca = flag[2 + x];
-        if (n == 0) continue;
+    // half of the threads for each of the two (one after the other took 2.3 us more)
+    const int x = warp >= W / 2, n = flag[x], ca = flag[2 + x];
+    if (n > 0) {
         // (the rings are free: n <= WN_MAX_CTAS pieces take 41 KB of them)
-        float *far = reinterpret_cast<float *>(smem + lay.ring);
+        float *far = reinterpret_cast<float *>(smem + lay.ring) + x * (WN_RED + 16 * WN_MAX_CTAS + 16);
         const WinPieces pieces{nullptr, nullptr, p.part + (size_t)2 * ca * PIECE, 0, PIECE};
-        win_join<D, NT, true>(p, n, pieces, far, far + WN_RED, x ? open1 : open0, nullptr);
+        win_join<D, NT / 2, true>(p, tid - x * (NT / 2), 2 + x, n, pieces, far, far + WN_RED, x ? open1 : open0, nullptr);
     }
 }
 
