@@ -567,15 +567,13 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             const bool go = live && mbar_test(&empty[is], phase);
             if (go) {
                 uint8_t *st = ring + is * STAGE;
-                {
-                    // whole boxes: rows past the group's last key are other keys or zeros, never used
-                    const int row = head.index(p) * p.n_max + k0;
-                    mbar_arrive_tx(&full[is], (uint32_t)STAGE);
+                // whole boxes: rows past the group's last key are other keys or zeros, never used
+                const int row = head.index(p) * p.n_max + k0;
+                mbar_arrive_tx(&full[is], (uint32_t)STAGE);
 #pragma unroll
-                    for (int hf = 0; hf < D / 64; ++hf) {
-                        tma_load_2d(st + hf * TK * 128, tm_k, hf * 64, row, &full[is], policy);
-                        tma_load_2d(st + TK * D * 2 + hf * TK * 128, tm_v, hf * 64, row, &full[is], policy);
-                    }
+                for (int hf = 0; hf < D / 64; ++hf) {
+                    tma_load_2d(st + hf * TK * 128, tm_k, hf * 64, row, &full[is], policy);
+                    tma_load_2d(st + TK * D * 2 + hf * TK * 128, tm_v, hf * 64, row, &full[is], policy);
                 }
                 ++filled;
                 if (++is == NS) {
@@ -972,48 +970,46 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             int tend = min(t < cg.start + cg.t.ns ? cg.start + cg.t.ns : cg.end(), tb), wlo;
             unsigned wspan;
             cg.whole(wlo, wspan);
-            {
-                if (KV4) {
-                    // scaled by the power of two that puts the head's largest value near 2^14
-                    uint32_t big = 0;  // its bf16 bits without the sign
+            if (KV4) {
+                // scaled by the power of two that puts the head's largest value near 2^14
+                uint32_t big = 0;  // its bf16 bits without the sign
 #pragma unroll
-                    for (int i = 0; i < MT / 2; ++i) {
-                        const uint32_t u[4] = {qraw[i].x, qraw[i].y, qraw[i].z, qraw[i].w};
+                for (int i = 0; i < MT / 2; ++i) {
+                    const uint32_t u[4] = {qraw[i].x, qraw[i].y, qraw[i].z, qraw[i].w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) big = max(big, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
-                    }
-                    big = max(big, __shfl_xor_sync(FULL, big, 1));
-                    big = max(big, __shfl_xor_sync(FULL, big, 2));
-                    const int e = max(-100, min(127, (int)(big >> 7) - 127)) - 14;
-                    const float up = p.qsign * exp2i(-e);
-#pragma unroll
-                    for (int i = 0; i < MT / 2; ++i) {
-                        qf[2 * i][0] = pack_f16(bf16lo_to_f32(qraw[i].x) * up, bf16hi_to_f32(qraw[i].x) * up);
-                        qf[2 * i][1] = pack_f16(bf16lo_to_f32(qraw[i].y) * up, bf16hi_to_f32(qraw[i].y) * up);
-                        qf[2 * i + 1][0] = pack_f16(bf16lo_to_f32(qraw[i].z) * up, bf16hi_to_f32(qraw[i].z) * up);
-                        qf[2 * i + 1][1] = pack_f16(bf16lo_to_f32(qraw[i].w) * up, bf16hi_to_f32(qraw[i].w) * up);
-                    }
-                    const int h0 = WIDE ? 2 * c : (2 * c) & 3;  // heads of this lane's columns
-                    const float d0 = exp2i(__shfl_sync(FULL, e, h0 * 4)), d1 = exp2i(__shfl_sync(FULL, e, h0 * 4 + 4));
-                    ka0 = p.k2_hi * d0;
-                    kb0 = p.k2_lo * d0;
-                    ka1 = p.k2_hi * d1;
-                    kb1 = p.k2_lo * d1;
-                } else {
-                    const uint32_t flip = p.qsign < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-                    for (int i = 0; i < MT / 2; ++i) {
-                        qf[2 * i][0] = qraw[i].x ^ flip;
-                        qf[2 * i][1] = qraw[i].y ^ flip;
-                        qf[2 * i + 1][0] = qraw[i].z ^ flip;
-                        qf[2 * i + 1][1] = qraw[i].w ^ flip;
-                    }
+                    for (int j = 0; j < 4; ++j) big = max(big, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
                 }
+                big = max(big, __shfl_xor_sync(FULL, big, 1));
+                big = max(big, __shfl_xor_sync(FULL, big, 2));
+                const int e = max(-100, min(127, (int)(big >> 7) - 127)) - 14;
+                const float up = p.qsign * exp2i(-e);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-                l0 = l1 = c0 = c1 = 0.f;
-                thr0 = thr1 = NEG_INF;
+                for (int i = 0; i < MT / 2; ++i) {
+                    qf[2 * i][0] = pack_f16(bf16lo_to_f32(qraw[i].x) * up, bf16hi_to_f32(qraw[i].x) * up);
+                    qf[2 * i][1] = pack_f16(bf16lo_to_f32(qraw[i].y) * up, bf16hi_to_f32(qraw[i].y) * up);
+                    qf[2 * i + 1][0] = pack_f16(bf16lo_to_f32(qraw[i].z) * up, bf16hi_to_f32(qraw[i].z) * up);
+                    qf[2 * i + 1][1] = pack_f16(bf16lo_to_f32(qraw[i].w) * up, bf16hi_to_f32(qraw[i].w) * up);
+                }
+                const int h0 = WIDE ? 2 * c : (2 * c) & 3;  // heads of this lane's columns
+                const float d0 = exp2i(__shfl_sync(FULL, e, h0 * 4)), d1 = exp2i(__shfl_sync(FULL, e, h0 * 4 + 4));
+                ka0 = p.k2_hi * d0;
+                kb0 = p.k2_lo * d0;
+                ka1 = p.k2_hi * d1;
+                kb1 = p.k2_lo * d1;
+            } else {
+                const uint32_t flip = p.qsign < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+                for (int i = 0; i < MT / 2; ++i) {
+                    qf[2 * i][0] = qraw[i].x ^ flip;
+                    qf[2 * i][1] = qraw[i].y ^ flip;
+                    qf[2 * i + 1][0] = qraw[i].z ^ flip;
+                    qf[2 * i + 1][1] = qraw[i].w ^ flip;
+                }
             }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            l0 = l1 = c0 = c1 = 0.f;
+            thr0 = thr1 = NEG_INF;
             for (;;) {  // tiles
                 if (KV4) {
                     copy_wait<NS - 1>();
@@ -1118,32 +1114,48 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     }
     bar_sync<NT>();  // (also makes the pieces in the workspace visible to the CTA)
 
-    // ---- join the CTA's pieces group by group, in the order of the list.  Scratch: behind the
-    // pieces, which are the first stage of each warp's ring
-    float *scratch = reinterpret_cast<float *>(smem + lay.ring + STAGE);
-    float *red = reinterpret_cast<float *>(smem + lay.ring + (NS + 1) * STAGE);
+    // ---- join the CTA's pieces group by group, in the order of the list, two groups at a time by
+    // half of the threads each (two are usual, where a share ends one and begins the next).
+    // Scratch: behind the pieces, which are the first stage of each warp's ring
+    const int half = warp >= W / 2;
+    float *scratch = reinterpret_cast<float *>(smem + lay.ring + 2 * half * NS * STAGE + STAGE);
+    float *red = scratch + NS * STAGE / 4;
     uint8_t *list = reinterpret_cast<uint8_t *>(smem + lay.list) + 32 * warp;
     const int mine = lane < 2 * W ? seg[lane] : -1;
     const unsigned same = __match_any_sync(FULL, mine);
     unsigned leaders = __ballot_sync(FULL, mine >= 0 && lane == __ffs((int)same) - 1);
     int open0 = -1, open1 = -1;  // the CTA's groups that other CTAs share: begun before it, begun here
     while (leaders) {
-        const int i = __ffs((int)leaders) - 1;
-        leaders &= leaders - 1;
-        const int gi = __shfl_sync(FULL, mine, i);
-        const unsigned set = __shfl_sync(FULL, same, i);
-        const int b = gi / p.H_kv;
-        const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
-        const int start = prefix[b] + gi % p.H_kv * win_span(cnt) + WN_SETUP;
-        const int slot = t0 <= start ? 1 : 0;  // begun here, or before
-        const bool all = slot && start + cnt <= t1;
-        if (!all) (slot ? open1 : open0) = gi;
-        // list[j]: which is the j-th of the group's pieces, a copy for each warp
-        if (set >> lane & 1) list[__popc(set & ((1u << lane) - 1))] = (uint8_t)lane;
-        __syncwarp();
-        const WinPieces pieces{list, reinterpret_cast<const float *>(smem + lay.ring), p.first + (size_t)blockIdx.x * W * PIECE,
-                               NS * STAGE / 4, PIECE};
-        win_join<D, NT, false>(p, tid, 1, __popc(set), pieces, red, scratch, gi, all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE);
+        int gi = -1;
+        unsigned set = 0;
+        float *part = nullptr;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (!leaders) continue;
+            const int i = __ffs((int)leaders) - 1;
+            leaders &= leaders - 1;
+            const int g = __shfl_sync(FULL, mine, i);
+            const unsigned who = __shfl_sync(FULL, same, i);
+            const int b = g / p.H_kv;
+            const int cnt = win_tiles<TK>(nb[b], p.window, p.sinks).cnt;
+            const int start = prefix[b] + g % p.H_kv * win_span(cnt) + WN_SETUP;
+            const int slot = t0 <= start ? 1 : 0;  // begun here, or before
+            const bool all = slot && start + cnt <= t1;
+            if (!all) (slot ? open1 : open0) = g;
+            if (k == half) {
+                gi = g;
+                set = who;
+                part = all ? nullptr : p.part + (size_t)(2 * blockIdx.x + slot) * PIECE;
+            }
+        }
+        if (gi >= 0) {
+            // list[j]: which is the j-th of the group's pieces, a copy for each warp
+            if (set >> lane & 1) list[__popc(set & ((1u << lane) - 1))] = (uint8_t)lane;
+            __syncwarp();
+            const WinPieces pieces{list, reinterpret_cast<const float *>(smem + lay.ring), p.first + (size_t)blockIdx.x * W * PIECE,
+                                   NS * STAGE / 4, PIECE};
+            win_join<D, NT / 2, false>(p, tid - half * (NT / 2), 2 + half, __popc(set), pieces, red, scratch, gi, part);
+        }
     }
     if (open0 < 0 && open1 < 0) return;
 
@@ -1174,12 +1186,12 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     }
     bar_sync<NT>();
     // half of the threads for each of the two (one after the other took 2.3 us more)
-    const int x = warp >= W / 2, n = flag[x], ca = flag[2 + x];
+    const int n = flag[half], ca = flag[2 + half];
     if (n > 0) {
         // (the rings are free: n <= WN_MAX_CTAS pieces take 41 KB of them)
-        float *far = reinterpret_cast<float *>(smem + lay.ring) + x * (WN_RED + 16 * WN_MAX_CTAS + 16);
+        float *far = reinterpret_cast<float *>(smem + lay.ring) + half * (WN_RED + 16 * WN_MAX_CTAS + 16);
         const WinPieces pieces{nullptr, nullptr, p.part + (size_t)2 * ca * PIECE, 0, PIECE};
-        win_join<D, NT / 2, true>(p, tid - x * (NT / 2), 2 + x, n, pieces, far, far + WN_RED, x ? open1 : open0, nullptr);
+        win_join<D, NT / 2, true>(p, tid - half * (NT / 2), 2 + half, n, pieces, far, far + WN_RED, half ? open1 : open0, nullptr);
     }
 }
 
