@@ -37,16 +37,17 @@
 // list, so results do not depend on timing.
 //
 // What bounds it.  bf16: the cache's bytes.  16 rows, window 8192 + 16 sinks of 32k keys,
-// d = 128, 8 KV heads: 538 MB in 83 us, 6.5 TB/s, 0.97 of the measured copy rate.
-// 4-bit: the conversions.  Per 32 keys of a KV head a warp converts 256 bytes of codes a lane:
-// 128 cvt (a half-rate pipe) and 128 multiplies by scales of about 560 instructions; 16 rows
-// of 32k keys, 604 MB, take 110 us, 5.5 TB/s, 0.82 of the copy rate, at 0.6 of the issue slots.
-// Without the arithmetic the copies alone take 95 us.  What it took from 162 us: chains that
-// begin at zero in the MMA, two fp32 operations an instruction, copies by the lanes that use
-// them (bulk copies of a tile by one lane: 126 us; by warps of their own: 139 us), 16 warps
-// without spills, seldom used state in shared memory.
-// Small calls: a single group 4.4 us, and about 6 us more where groups span CTAs (fence,
-// arrival, join).
+// d = 128, 8 KV heads: 538 MB in 80-84 us, 6.4-6.7 TB/s, 0.96-1.0 of the measured copy rate.
+// 4-bit: 16 rows of 32k keys, 604 MB, take 108 us, 5.6 TB/s, 0.83 of the copy rate.  No unit
+// is full (half that batch: 640 warp instructions per 32 keys of a KV head, 0.62 of the issue
+// slots, 0.48 of the ALU pipe, which the 128 conversions among them take at half rate, 0.25 of
+// the tensor pipe); with four warps to a scheduler neither copies nor arithmetic hide the
+// other wholly.  An earlier state's copies took 94-96 us without the arithmetic.  What it
+// took from 162 us: chains that begin at zero in the MMA, two fp32 operations an instruction,
+// copies by the lanes that use them (bulk copies of a tile by one lane: 126 us against 113; by
+// warps of their own: 139-143 against 127), 16 warps (12 of 168 registers: 119 against 110),
+// seldom used state in shared memory, joins side by side.
+// Small calls: a group of 32 keys 4.6 us in one CTA; groups that span CTAs 12 us and more.
 #pragma once
 
 #include "santa_kv4.cuh"
@@ -60,12 +61,14 @@ constexpr int WN_MAX_WARPS = 16;
 constexpr int WN_RED = 4 * 32 * WN_MAX_WARPS;  // floats of a join's partial sums: 4 x max(G D / 4, threads)
 constexpr float WN_TOP = 9.f;             // log2 of p where a new maximum puts it
 constexpr float WN_SLACK = 6.f;           // and how far above that later ones may be
-constexpr int WN_ALONE = 4;               // tiles a warp up to which a group stays in one CTA
+// Tiles a warp up to which a group stays in one CTA (one sequence, d = 128; alone against
+// split: 4-bit 1024 keys, 2 tiles, 11.2 and 12.4 us, 2048 keys, 4 tiles, 14.9 and 12.4; bf16
+// 256 keys, 2 tiles, 8.3 and 9.4, 512 keys, 4 tiles, 10.7 and 9.4).
+constexpr int WN_ALONE = 2;
 constexpr int WN_SETUP = 2;               // tiles that beginning a group costs about as much as
 
-// One CTA to an SM.  4-bit: 16 warps, each copying its own tiles (the conversions need the
-// warps: 12 with 168 registers took 119 us where 16 with 128 take 110); bf16: the 8 whose
-// rings fit, and one that issues all of their copies.
+// One CTA to an SM.  4-bit: 16 warps, each copying its own tiles; bf16: the 8 whose rings fit,
+// and one that issues all of their copies.
 __host__ __device__ constexpr int win_warps(bool kv4) { return kv4 ? 16 : 8; }
 __host__ __device__ constexpr int win_threads(bool kv4) { return 32 * (kv4 ? win_warps(true) : win_warps(false) + 1); }
 // Keys of a tile, which is a ring stage, and the stages of a warp's ring (what 227 KB hold).

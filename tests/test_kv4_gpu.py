@@ -295,6 +295,18 @@ def test_where_groups_begin_to_be_split(op, n):
 
 
 @pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("n", [255, 256, 257, 1023, 1024, 1025])
+def test_where_short_groups_begin_to_be_split(op, n):
+    """Few groups around the length up to which each has one CTA to itself, a short one and an
+    empty one among them, and the same with more groups than SMs."""
+    n_max = -(-n // 16) * 16
+    q, k, v = inputs(n, [n, 5, 0], 8, 2, 128, n_max)
+    check(op, q, k, v, [n, 5, 0])
+    q, k, v = inputs(n, [n // 16] * 100, 4, 2, 64, 144)
+    check(op, q, k, v, [min(n // 16 + b, 144) for b in range(100)])
+
+
+@pytest.mark.parametrize("op", OPS)
 def test_many_batch_rows(op):
     """1024 batch rows (the most there may be), empty and short ones."""
     seq = [(7 * b) % 49 for b in range(1024)]
