@@ -147,6 +147,20 @@ def test_rows_aligned_to_16_bytes_only(d, shift, pad):
     assert torch.equal(kbuf, before)          # nothing beside the rows was written
 
 
+def test_strides_of_single_dimensions_are_not_read():
+    """One row of one head, its batch, token and head strides any numbers."""
+    g = gen(3)
+    room = rand(g, 2, 128).to(DEV)
+    k, v = (torch.as_strided(room, (1, 1, 1, 128), st, 128 * i) for i, st in enumerate([(0, 0, 0, 1), (7, 3, 1, 1)]))
+    cache = santa.new_kv4_cache(1, 1, 16, 128)
+    santa.kv4_append(cache, k, v, ints([5]))
+    out = torch.zeros(3, 128, dtype=torch.bfloat16, device=DEV)
+    ko, vo = (torch.as_strided(out, (1, 1, 1, 128), st, 128 * i) for i, st in enumerate([(1, 5, 0, 1), (0, 0, 0, 1)]))
+    santa.kv4_read(cache, ints([5]), ko, vo)
+    ref = kv4_util.values(*kv4_util.quantise(room.cpu()))
+    assert np.array_equal(out[:2].cpu().double().numpy(), ref) and torch.all(out[2] == 0)
+
+
 def test_every_largest_magnitude_and_every_quotient():
     """Every finite bf16 as a group's largest magnitude (all scales, ties and the ends of the
     range), beside values of all smaller sizes; and every bf16 mantissa against every scale
