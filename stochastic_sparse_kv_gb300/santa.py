@@ -145,23 +145,56 @@ def _stream_ptr(stream) -> int | None:
 
 
 def new_workspace(nbytes: int, device, stream=None) -> torch.Tensor:
-    """A zero-initialised workspace (torch allocation, 256-byte aligned)."""
+    """A zero-initialised workspace (torch allocation, 256-byte aligned), for calls on `stream`."""
+    if stream is not None:
+        with _current(stream, device):
+            return new_workspace(nbytes, device)
     ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
     _check(load().santa_workspace_init(ctypes.c_void_p(ws.data_ptr()), ws.numel(),
-                                       ctypes.c_void_p(_stream_ptr(stream))), "santa_workspace_init")
+                                       ctypes.c_void_p(_stream_ptr(None))), "santa_workspace_init")
     return ws
 
 
-_ws_cache: dict = {}
+def _current(stream, device):
+    """A context in which `stream` is the current one.  What a call on an explicit stream
+    allocates is allocated in it: torch hands a block's memory on in the order of the stream that
+    the block was allocated on, and a capture is the stream's that is captured."""
+    dev = torch.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, dev)
+    if dev.index is not None and stream.device != dev:
+        raise ValueError(f"the stream is not one of {dev}")
+    return torch.cuda.stream(stream)
+
+
+_ws_cache: dict = {}     # (kind of call, device, stream) -> workspace
+_ws_captured: dict = {}  # address -> workspace whose address a captured decode() holds: never freed
+
+
+def _own_workspace(kind: str, nbytes: int, dev, raw) -> torch.Tensor:
+    """The workspace of a call on the current stream (handle `raw`) that was given none: one for each
+    kind of call, device and stream, allocated on that stream, so that a smaller one is not
+    reused before the calls on it have ended.  Inside a capture it is one of the graph's own,
+    cleared in the graph (two graphs that share one could not be replayed at the same time);
+    decode() takes the stream's own there if a call before the capture has made it."""
+    ws = _ws_cache.get((kind, dev, raw))
+    if ws is not None and ws.numel() < nbytes:
+        ws = None
+    if torch.cuda.is_current_stream_capturing():
+        if ws is None or kind != "decode":
+            return new_workspace(nbytes, dev)
+        _ws_captured[ws.data_ptr()] = ws
+    elif ws is None:
+        ws = _ws_cache[(kind, dev, raw)] = new_workspace(nbytes, dev)
+    return ws
 
 
 def _cached_workspace(nbytes: int, device, stream) -> torch.Tensor:
-    key = (torch.device(device), _stream_ptr(stream))
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = new_workspace(nbytes, device, stream)
-        _ws_cache[key] = ws
-    return ws
+    """The workspace of decode()."""
+    if stream is not None:
+        with _current(stream, device):
+            return _cached_workspace(nbytes, device, None)
+    return _own_workspace("decode", nbytes, torch.device(device), _stream_ptr(None))
 
 
 def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_lens: torch.Tensor,
@@ -188,6 +221,15 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_le
         raise ValueError("k_cache/v_cache/q shapes disagree")
     shape = make_shape(B, H_q, H_kv, d, n_max, scale)
     dev = q.device
+    if stream is not None:
+        caller = torch.cuda.current_stream(dev)
+        with _current(stream, dev):
+            got = decode(q, k_cache, v_cache, seq_lens, S, m, seed, scale, out, idx_out, want_idx, workspace, None,
+                         group_dedup, out_dtype, bernoulli, two_pass)
+        for t, given in zip(got, (out, idx_out)):
+            if t is not None and given is None:  # the caller may use it on its own stream
+                t.record_stream(caller)
+        return got
     if out is None:
         out = torch.empty(B, H_q, d, dtype=out_dtype, device=dev)
     if out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or out.shape != (B, H_q, d):
@@ -195,7 +237,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_le
     if m != DENSE and want_idx and idx_out is None:
         idx_out = torch.empty(B, H_q, S, dtype=torch.int32, device=dev)
     nbytes = workspace_size(shape, S if m != DENSE else 1, m)
-    ws = workspace if workspace is not None else _cached_workspace(nbytes, dev, stream)
+    ws = workspace if workspace is not None else _cached_workspace(nbytes, dev, None)
     mf = m | (GROUP_DEDUP if (group_dedup and m != DENSE) else 0) | (OUT_BF16 if out.dtype == torch.bfloat16 else 0) \
         | (BERNOULLI_QK if bernoulli else 0) | (TWO_PASS if (two_pass and m != DENSE) else 0)
     rc = load().santa_decode(ctypes.byref(shape), ctypes.c_void_p(q.data_ptr()),
@@ -203,7 +245,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_le
                              ctypes.c_void_p(seq_lens.data_ptr()), int(S), mf, ctypes.c_uint64(seed),
                              ctypes.c_void_p(out.data_ptr()),
                              ctypes.c_void_p(idx_out.data_ptr() if (idx_out is not None and m != DENSE) else 0),
-                             ctypes.c_void_p(ws.data_ptr()), ws.numel(), ctypes.c_void_p(_stream_ptr(stream)))
+                             ctypes.c_void_p(ws.data_ptr()), ws.numel(), ctypes.c_void_p(_stream_ptr(None)))
     _check(rc, "santa_decode")
     return out, (idx_out if m != DENSE else None)
 
@@ -381,18 +423,6 @@ def _raw_stream(stream, dev) -> int:
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _call_workspace(nbytes: int, dev, stream, raw: int) -> torch.Tensor:
-    """The workspace of a call on `stream` that was given none: one per device and stream, or,
-    inside a stream capture, one of the graph's own (two graphs that share one could not be
-    replayed at the same time, and its clearing has to be part of the graph)."""
-    if torch.cuda.is_current_stream_capturing():
-        return new_workspace(nbytes, dev, stream)
-    ws = _ws_cache.get((dev, raw))
-    if ws is None or ws.numel() < nbytes:
-        ws = _ws_cache[(dev, raw)] = new_workspace(nbytes, dev, stream if stream is not None else torch.cuda.current_stream(dev))
-    return ws
-
-
 def _move_rows(fn, what: str, cache, k, v, pos, counts, workspace, stream):
     B, H_kv, n_max, d, dev = _kv4_dims(cache)
     for t, name in ((k, "K rows"), (v, "V rows")):
@@ -444,18 +474,23 @@ def _window_call(q, dims, cache_args, fn, what, seq_lens, window, sinks, scale, 
     _int_vector(seq_lens, "seq_lens", B, dev)
     if window >= 1 << 31 or sinks >= 1 << 31:
         raise ValueError("window and sinks are 32-bit numbers")
+    if stream is not None:
+        caller = torch.cuda.current_stream(dev)
+        with _current(stream, dev):
+            got = _window_call(q, dims, cache_args, fn, what, seq_lens, window, sinks, scale, out, out_dtype, workspace, None)
+        if out is None:  # the caller may use it on its own stream
+            got.record_stream(caller)
+        return got
     shape, nbytes = _shape_of((B, qs[1], H_kv, d, n_max, scale))
     if out is None:
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
         out = torch.empty(qs, dtype=out_dtype, device=dev)
-        if stream is not None:
-            out.record_stream(stream)
     elif out.dtype not in (torch.float32, torch.bfloat16) or not out.is_contiguous() or out.shape != qs or out.device != dev:
         raise ValueError("out must be a contiguous fp32 or bf16 [B, H_q, d] tensor on q's device")
     with _on_device(dev):
-        raw = _raw_stream(stream, dev)
-        ws = workspace if workspace is not None else _call_workspace(nbytes, dev, stream, raw)
+        raw = _raw_stream(None, dev)
+        ws = workspace if workspace is not None else _own_workspace("window", nbytes, dev, raw)
         rc = fn(shape, q.data_ptr(), *cache_args, seq_lens.data_ptr(), window, sinks,
                 OUT_BF16 if out.dtype == torch.bfloat16 else 0, out.data_ptr(), ws.data_ptr(), ws.numel(), raw)
     if rc:
