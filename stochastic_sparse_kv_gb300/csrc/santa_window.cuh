@@ -17,9 +17,10 @@
 //    registers to become fp16 anyway: a tcgen05 tile (M = 128 from shared memory or TMEM)
 //    would add a store and a load of every converted value to save the MMA issue slots,
 //    16 of about 280 per 16 keys.
-//  * p = 2^(k2 s + c), with c set so that the largest p so far lies in (2^3, 2^15]: c moves
-//    only when a score exceeds the one that set it by more than 2^6, so most tiles rescale
-//    nothing, and a piece's sums are scaled by exactly 2^c.
+//  * p = 2^(k2 (s - m) + 9), m a score so far, with which the largest p so far lies in [2^9, 2^15]:
+//    m moves only when p would exceed that, so most tiles rescale nothing.  The difference of
+//    two scores is taken before it is scaled: k2 s - k2 m, each rounded at the size of the
+//    score, left the range of p at scores of 1e8 and more.
 //  * output: A = V^T (16 of the d dimensions by 16 keys), B = p.  movmatrix turns the score
 //    accumulators into that operand in registers.
 //
@@ -78,7 +79,7 @@ __host__ __device__ constexpr int win_stage(int D, bool kv4)
     return kv4 ? win_tile(D, true) * (D + D / 8) : win_tile(D, false) * D * 4;
 }
 __host__ __device__ constexpr int win_stages(int D, bool kv4) { return !kv4 ? 3 : D == 128 ? 3 : 5; }
-// A piece of a group's sums: fp32 o[G][D + 4] (the heads' rows in different banks), c[8], l[8].
+// A piece of a group's sums: fp32 o[G][D + 4] (the heads' rows in different banks), m[8], l[8].
 __host__ __device__ constexpr int win_piece(int G, int D) { return G * (D + 4) + 16; }
 
 struct WinParams {
@@ -356,15 +357,17 @@ struct WinPieces {
 };
 
 // NT threads (tid of them, barrier bar): the n pieces of group gi joined into `part` (a piece) or,
-// when that is null, into the output.  red: WN_RED floats; scratch: 16 n + 16.  Begins and
+// when that is null, into the output.  red: WN_RED floats; scratch: 16 n + 16; factor: of
+// the pieces' m.  Begins and
 // ends with both free.  FAR: the pieces were written by other CTAs too and are read past the
 // L1 cache.
 template <int D, int NT, bool FAR>
-__device__ __forceinline__ void win_join(const WinParams &p, int tid, int bar, int n, const WinPieces pieces, float *red, float *scratch,
-                                         int gi, float *part)
+__device__ __forceinline__ void win_join(const WinParams &p, float factor, int tid, int bar, int n, const WinPieces pieces, float *red,
+                                         float *scratch, int gi, float *part)
 {
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int AHEAD = 8, HS = D + 4;
+    const float NEG_INF = __int_as_float(0xff800000);
     const int lane = tid & 31, GS = p.G * HS;
     float *tot = scratch, *wt = scratch + 16, *lt = wt + 8 * n;
     auto load = [](const float *a) { return FAR ? __ldcg(a) : *a; };
@@ -382,28 +385,28 @@ __device__ __forceinline__ void win_join(const WinParams &p, int tid, int bar, i
         for (int k = 0; k < AHEAD; ++k) ahead[k] = load4(pieces.at(min(sl + k * ns, n - 1)) + at);
     };
     fetch();
-    // a warp a head: its common exponent, the pieces' weights, the sum
+    // a warp a head: the largest of the pieces' m, their weights, the sum
     for (int hd = tid >> 5; hd < p.G; hd += NT / 32) {
-        float C = __int_as_float(0x7f800000);
+        float M = NEG_INF;
         for (int j = lane; j < n; j += 32) {
             const float *pc = pieces.at(j) + GS + hd;
-            const float c = load(pc), l = load(pc + 8);
-            wt[8 * j + hd] = c;
+            const float m = load(pc), l = load(pc + 8);
+            wt[8 * j + hd] = m;
             lt[8 * j + hd] = l;
-            C = fminf(C, c);
+            M = fmaxf(M, m);
         }
 #pragma unroll
-        for (int m = 16; m; m >>= 1) C = fminf(C, __shfl_xor_sync(FULL, C, m));
+        for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, m));
         float L = 0.f;
         for (int j = lane; j < n; j += 32) {
-            const float w = ex2(C - wt[8 * j + hd]);
+            const float w = ex2((wt[8 * j + hd] - M) * factor);
             wt[8 * j + hd] = w;
             L = fmaf(w, lt[8 * j + hd], L);
         }
 #pragma unroll
         for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(FULL, L, m);
         if (lane == 0) {
-            tot[hd] = C;
+            tot[hd] = M;
             tot[8 + hd] = L;
         }
     }
@@ -711,7 +714,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         // ---- the sums
         uint32_t qf[MT][2];                  // B operand of the scores
         float o[MT][4];                      // columns 2c, 2c+1 of output rows r, r+8 of each piece
-        float l0 = 0.f, l1 = 0.f, c0 = 0.f, c1 = 0.f, thr0 = NEG_INF, thr1 = NEG_INF;
+        float l0 = 0.f, l1 = 0.f, m0 = 0.f, m1 = 0.f, thr0 = NEG_INF, thr1 = NEG_INF;
         float ka0 = p.k2_hi, ka1 = p.k2_hi, kb0 = p.k2_lo, kb1 = p.k2_lo;
         const float second = c < 2 ? 0.f : -1.f;
         // ---- one tile: the keys from k0, whose rows and scales the pointers are at
@@ -782,7 +785,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                     if (!seen(ja + 8)) s[u][2] = s[u][3] = NEG_INF;
                 }
 
-            // ---- a new maximum, when it is far above the one that set c
+            // ---- a new maximum, when it is far above m
             float x0 = NEG_INF, x1 = NEG_INF;
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
@@ -797,16 +800,14 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 }
                 float f0 = 1.f, f1 = 1.f;
                 if (x0 > thr0) {
-                    const float cn = fmaf(-x0, ka0, WN_TOP);
-                    f0 = ex2(fminf(cn - c0, 0.f));  // (of empty sums c is not yet set)
-                    c0 = cn;
-                    thr0 = x0 + WN_SLACK / ka0;
+                    f0 = ex2(fminf((m0 - x0) * ka0, 0.f));  // (of empty sums m is not yet set)
+                    m0 = x0;
+                    thr0 = __fadd_rd(x0, WN_SLACK / ka0);  // (rounded up, it could pass the range of p)
                 }
                 if (x1 > thr1) {
-                    const float cn = fmaf(-x1, ka1, WN_TOP);
-                    f1 = ex2(fminf(cn - c1, 0.f));
-                    c1 = cn;
-                    thr1 = x1 + WN_SLACK / ka1;
+                    f1 = ex2(fminf((m1 - x1) * ka1, 0.f));
+                    m1 = x1;
+                    thr1 = __fadd_rd(x1, WN_SLACK / ka1);
                 }
                 l0 *= f0;
                 l1 *= f1;
@@ -825,7 +826,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    float2 x = fma2(s[u][2 * y], s[u][2 * y + 1], ka0, ka1, c0, c1);
+                    add2(s[u][2 * y], s[u][2 * y + 1], -m0, -m1);
+                    float2 x = fma2(s[u][2 * y], s[u][2 * y + 1], ka0, ka1, WN_TOP, WN_TOP);
                     x = fma2(s[u][2 * y], s[u][2 * y + 1], kb0, kb1, x.x, x.y);
                     s[u][2 * y] = ex2(x.x);
                     s[u][2 * y + 1] = ex2(x.y);
@@ -1011,7 +1013,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-            l0 = l1 = c0 = c1 = 0.f;
+            l0 = l1 = m0 = m1 = 0.f;
             thr0 = thr1 = NEG_INF;
             for (;;) {  // tiles
                 if (KV4) {
@@ -1048,9 +1050,15 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             // ---- the group's last tile here: its result, or a piece of it
             const bool ended = t == cg.end(), all = ta <= cg.start && ended;
             if (ended) t += WN_SETUP;
-            // sums that no score has set c for are empty (or NaN): they weigh nothing
-            if (thr0 == NEG_INF) c0 = -NEG_INF;
-            if (thr1 == NEG_INF) c1 = -NEG_INF;
+            // sums that no score has set m for are empty (or NaN): they weigh nothing
+            if (thr0 == NEG_INF) m0 = NEG_INF;
+            if (thr1 == NEG_INF) m1 = NEG_INF;
+            if (KV4 && !all) {
+                // m of all pieces of a head in one unit: times the power of two that ka holds (from the
+                // difference of the exponents), and 2^-24, so that it cannot overflow
+                m0 *= __int_as_float(__float_as_int(ka0) - __float_as_int(p.k2_hi) + 0x3f800000) * 0x1p-24f;
+                m1 *= __int_as_float(__float_as_int(ka1) - __float_as_int(p.k2_hi) + 0x3f800000) * 0x1p-24f;
+            }
 #pragma unroll
             for (int m = 4; m <= 16; m <<= 1) {
                 l0 += __shfl_xor_sync(FULL, l0, m);
@@ -1062,7 +1070,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             const size_t orow = (size_t)cg.b * p.H_q + cg.g * p.G;
             // heads of the lane's values: x of column 2c (and z of 2c+1 in wide groups)
             const int hx = WIDE ? 2 * c : 2 * (c & 1) + (c >> 1);
-            const float lx = WIDE || c < 2 ? l0 : l1, cx = WIDE || c < 2 ? c0 : c1;
+            const float lx = WIDE || c < 2 ? l0 : l1, mx = WIDE || c < 2 ? m0 : m1;
             const float ix = all ? 1.f / lx : 1.f, iz = all ? 1.f / l1 : 1.f;
             if (!WIDE)  // columns j and j + 4 hold terms of the same head: lanes c, c ^ 2
 #pragma unroll
@@ -1105,7 +1113,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                         }
                 }
                 if (!all && r == 0) {
-                    piece[p.G * (D + 4) + h] = x ? c1 : cx;
+                    piece[p.G * (D + 4) + h] = x ? m1 : mx;
                     piece[p.G * (D + 4) + 8 + h] = x ? l1 : lx;
                 }
             }
@@ -1121,6 +1129,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     // half of the threads each (two are usual, where a share ends one and begins the next).
     // Scratch: behind the pieces, which are the first stage of each warp's ring
     const int half = warp >= W / 2;
+    const float factor = KV4 ? p.k2_hi * 0x1p24f : p.k2_hi;
     float *scratch = reinterpret_cast<float *>(smem + lay.ring + 2 * half * NS * STAGE + STAGE);
     float *red = scratch + NS * STAGE / 4;
     uint8_t *list = reinterpret_cast<uint8_t *>(smem + lay.list) + 32 * warp;
@@ -1157,7 +1166,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             __syncwarp();
             const WinPieces pieces{list, reinterpret_cast<const float *>(smem + lay.ring), p.first + (size_t)blockIdx.x * W * PIECE,
                                    NS * STAGE / 4, PIECE};
-            win_join<D, NT / 2, false>(p, tid - half * (NT / 2), 2 + half, __popc(set), pieces, red, scratch, gi, part);
+            win_join<D, NT / 2, false>(p, factor, tid - half * (NT / 2), 2 + half, __popc(set), pieces, red, scratch, gi, part);
         }
     }
     if (open0 < 0 && open1 < 0) return;
@@ -1194,7 +1203,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         // (the rings are free: n <= WN_MAX_CTAS pieces take 41 KB of them)
         float *far = reinterpret_cast<float *>(smem + lay.ring) + half * (WN_RED + 16 * WN_MAX_CTAS + 16);
         const WinPieces pieces{nullptr, nullptr, p.part + (size_t)2 * ca * PIECE, 0, PIECE};
-        win_join<D, NT / 2, true>(p, tid - half * (NT / 2), 2 + half, n, pieces, far, far + WN_RED, half ? open1 : open0, nullptr);
+        win_join<D, NT / 2, true>(p, factor, tid - half * (NT / 2), 2 + half, n, pieces, far, far + WN_RED, half ? open1 : open0, nullptr);
     }
 }
 

@@ -1,0 +1,72 @@
+"""Numerics of the windowed and 4-bit attention kernels at scores, weights and lengths where
+fp32 arithmetic gives the answer and narrower steps on the way would not.
+
+Scores here are sums with one product that is not zero, so that they are exact in fp32: what is
+tested is what follows, the softmax and the weighted sum.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from stochastic_sparse_kv_gb300 import santa
+from tests import kv4_util
+
+DEV = "cuda"
+OPS = ["kv4", "window"]
+NINF = float("-inf")
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def attend(op, q, k, v, seq, window=0, sinks=0, scale=0.0):
+    """(the kernel's output, the definition's in 64 bits); q, k, v CPU bf16."""
+    sl = torch.tensor(seq, dtype=torch.int32, device=DEV)
+    if op == "kv4":
+        parts = [torch.from_numpy(x) for t in (k, v) for x in kv4_util.quantise(t)]
+        kr, vr = kv4_util.values(parts[0].numpy(), parts[1].numpy()), kv4_util.values(parts[2].numpy(), parts[3].numpy())
+        out = santa.decode_kv4(q.to(DEV), santa.KV4Cache(*(x.to(DEV) for x in parts)), sl, window, sinks, scale)
+    else:
+        kr, vr = k.double().numpy(), v.double().numpy()
+        out = santa.decode_window(q.to(DEV), k.to(DEV), v.to(DEV), sl, window, sinks, scale)
+    return out.cpu().double().numpy(), kv4_util.attention(q, kr, vr, seq, window, sinks, scale)
+
+
+# ------------------------------------------------------------------ very large scores
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("d,H_kv,G", [(128, 2, 4), (128, 1, 8), (64, 2, 2), (64, 1, 8)])
+@pytest.mark.parametrize("n", [48, 5008])
+def test_scores_of_any_finite_size(op, d, H_kv, G, n):
+    """Products of 1e3 to 1e37 of both signs: one key leads, or two do by exactly the same score,
+    and the next is a step of the key's format behind.  Steps of at least 1/32 of a score of
+    1e3 / sqrt(d): the others weigh less than 2^-5 there and nothing above; the weights are in
+    the reference.  Tolerance: a weight is off by less than 1e-6 (exponent, its rounding), the
+    output by twice that of max|v|."""
+    g = gen(n + G)
+    sizes = [1e3, 1e6, 3e7, 1e8, 2e8, 5e8, 1e9, 3e9, 1e12, 1e20, 1e30, 1e37]
+    B = len(sizes)
+    q = torch.zeros(B, H_kv * G, d)
+    for b, s in enumerate(sizes):
+        q[b, :, 5] = s * (1 + torch.rand(H_kv * G, generator=g))
+    q[:, 1::2] *= -1
+    q[:, :, 5] /= 6 * 2.0 ** 5
+    k = torch.zeros(B, H_kv, n, d)
+    grid = torch.tensor([0.5, 1, 1.5, 2, 3, 4])
+    k[..., 5] = grid[torch.randint(0, 6, (B, H_kv, n), generator=g)] * 2.0 ** 5
+    k[..., 5] *= torch.randint(0, 2, (B, H_kv, n), generator=g) * 2 - 1
+    k[..., 6] = 6 * 2.0 ** 5                       # the group's largest: its scale is 2^5
+    lead = torch.randint(0, n, (B, H_kv, 3), generator=g)
+    for b in range(B):
+        for h in range(H_kv):
+            k[b, h, lead[b, h, 0], 5] = 6 * 2.0 ** 5
+            k[b, h, lead[b, h, 1], 5] = -6 * 2.0 ** 5
+            if b % 2:
+                k[b, h, lead[b, h, 2], 5] = 6 * 2.0 ** 5
+    v = torch.randn(B, H_kv, n, d, generator=g)
+    got, want = attend(op, q.bfloat16(), k.bfloat16(), v.bfloat16(), [n - b % 3 for b in range(B)])
+    assert np.abs(got - want).max() <= 2e-6 * float(v.abs().max())
