@@ -20,7 +20,9 @@
 //  * p = 2^(k2 (s - m) + 9), m a score so far, with which the largest p so far lies in [2^9, 2^15]:
 //    m moves only when p would exceed that, so most tiles rescale nothing.  The difference of
 //    two scores is taken before it is scaled: k2 s - k2 m, each rounded at the size of the
-//    score, left the range of p at scores of 1e8 and more.
+//    score, left the range of p at scores of 1e8 and more.  k2 = |scale| log2 e is one fp32
+//    number: its rounding moves p by 2^-25 x ln 2 of p, x = log2(2^9 / p), at most 2^-25 of the
+//    leading weight (a second term would turn a score of minus infinity into a NaN).
 //  * output: A = V^T (16 of the d dimensions by 16 keys), B = p.  movmatrix turns the score
 //    accumulators into that operand in registers.
 //
@@ -94,7 +96,7 @@ struct WinParams {
     int B, H_q, H_kv, n_max, G;
     int window, sinks;
     int out_bf16;
-    float k2_hi, k2_lo;           // |scale| * log2(e) as an unevaluated sum
+    float k2;                     // |scale| * log2(e)
     float qsign;                  // the sign of scale
     uint64_t wait_ns;             // bf16: limit of a stage's wait
 };
@@ -399,7 +401,7 @@ __device__ __forceinline__ void win_join(const WinParams &p, float factor, int t
         for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, m));
         float L = 0.f;
         for (int j = lane; j < n; j += 32) {
-            const float w = ex2((wt[8 * j + hd] - M) * factor);
+            const float w = M == NEG_INF ? 1.f : ex2((wt[8 * j + hd] - M) * factor);  // (all empty: empty)
             wt[8 * j + hd] = w;
             L = fmaf(w, lt[8 * j + hd], L);
         }
@@ -715,7 +717,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         uint32_t qf[MT][2];                  // B operand of the scores
         float o[MT][4];                      // columns 2c, 2c+1 of output rows r, r+8 of each piece
         float l0 = 0.f, l1 = 0.f, m0 = 0.f, m1 = 0.f, thr0 = NEG_INF, thr1 = NEG_INF;
-        float ka0 = p.k2_hi, ka1 = p.k2_hi, kb0 = p.k2_lo, kb1 = p.k2_lo;
+        float ka0 = p.k2, ka1 = p.k2;
         const float second = c < 2 ? 0.f : -1.f;
         // ---- one tile: the keys from k0, whose rows and scales the pointers are at
         // (whole: every one is seen, no masks)
@@ -827,8 +829,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     add2(s[u][2 * y], s[u][2 * y + 1], -m0, -m1);
-                    float2 x = fma2(s[u][2 * y], s[u][2 * y + 1], ka0, ka1, WN_TOP, WN_TOP);
-                    x = fma2(s[u][2 * y], s[u][2 * y + 1], kb0, kb1, x.x, x.y);
+                    const float2 x = fma2(s[u][2 * y], s[u][2 * y + 1], ka0, ka1, WN_TOP, WN_TOP);
                     s[u][2 * y] = ex2(x.x);
                     s[u][2 * y + 1] = ex2(x.y);
                 }
@@ -997,10 +998,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 }
                 const int h0 = WIDE ? 2 * c : (2 * c) & 3;  // heads of this lane's columns
                 const float d0 = exp2i(__shfl_sync(FULL, e, h0 * 4)), d1 = exp2i(__shfl_sync(FULL, e, h0 * 4 + 4));
-                ka0 = p.k2_hi * d0;
-                kb0 = p.k2_lo * d0;
-                ka1 = p.k2_hi * d1;
-                kb1 = p.k2_lo * d1;
+                ka0 = p.k2 * d0;
+                ka1 = p.k2 * d1;
             } else {
                 const uint32_t flip = p.qsign < 0.f ? 0x80008000u : 0u;
 #pragma unroll
@@ -1056,8 +1055,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
             if (KV4 && !all) {
                 // m of all pieces of a head in one unit: times the power of two that ka holds (from the
                 // difference of the exponents), and 2^-24, so that it cannot overflow
-                m0 *= __int_as_float(__float_as_int(ka0) - __float_as_int(p.k2_hi) + 0x3f800000) * 0x1p-24f;
-                m1 *= __int_as_float(__float_as_int(ka1) - __float_as_int(p.k2_hi) + 0x3f800000) * 0x1p-24f;
+                m0 *= __int_as_float(__float_as_int(ka0) - __float_as_int(p.k2) + 0x3f800000) * 0x1p-24f;
+                m1 *= __int_as_float(__float_as_int(ka1) - __float_as_int(p.k2) + 0x3f800000) * 0x1p-24f;
             }
 #pragma unroll
             for (int m = 4; m <= 16; m <<= 1) {
@@ -1129,7 +1128,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     // half of the threads each (two are usual, where a share ends one and begins the next).
     // Scratch: behind the pieces, which are the first stage of each warp's ring
     const int half = warp >= W / 2;
-    const float factor = KV4 ? p.k2_hi * 0x1p24f : p.k2_hi;
+    const float factor = KV4 ? p.k2 * 0x1p24f : p.k2;
     float *scratch = reinterpret_cast<float *>(smem + lay.ring + 2 * half * NS * STAGE + STAGE);
     float *red = scratch + NS * STAGE / 4;
     uint8_t *list = reinterpret_cast<uint8_t *>(smem + lay.list) + 32 * warp;

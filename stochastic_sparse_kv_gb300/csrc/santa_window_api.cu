@@ -161,9 +161,7 @@ int launch_window(const santa_shape *sh, WinParams &p, const void *k, const void
     p.sinks = std::min(p.sinks, sh->n_max);
     p.out_bf16 = (flags & SANTA_OUT_BF16) ? 1 : 0;
     const float scale = sh->scale != 0.f ? sh->scale : (float)(1.0 / std::sqrt((double)D));
-    const double k2 = std::fabs((double)scale) * 1.4426950408889634;
-    p.k2_hi = (float)k2;
-    p.k2_lo = (float)(k2 - (double)p.k2_hi);
+    p.k2 = (float)(std::fabs((double)scale) * 1.4426950408889634);
     p.qsign = scale < 0.f ? -1.f : 1.f;
     p.wait_ns = wait_limit_ns();
 

@@ -4,7 +4,6 @@ fp32 arithmetic gives the answer and narrower steps on the way would not.
 Scores here are sums with one product that is not zero, so that they are exact in fp32: what is
 tested is what follows, the softmax and the weighted sum.
 """
-import math
 
 import numpy as np
 import pytest
@@ -70,3 +69,23 @@ def test_scores_of_any_finite_size(op, d, H_kv, G, n):
     v = torch.randn(B, H_kv, n, d, generator=g)
     got, want = attend(op, q.bfloat16(), k.bfloat16(), v.bfloat16(), [n - b % 3 for b in range(B)])
     assert np.abs(got - want).max() <= 2e-6 * float(v.abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, 0.25, -0.1])
+def test_a_score_of_minus_infinity_weighs_nothing(d, scale):
+    """Keys that hold an infinity against a query of the other sign (so that the score is minus
+    infinity), in visible places: single ones, whole tiles before any other key, and whole shares
+    of other CTAs."""
+    g = gen(d)
+    n, B, H_kv, G = 6000, 3, 2, 4
+    q = torch.randn(B, H_kv * G, d, generator=g)
+    q[:, :, 3] = 1
+    k, v = torch.randn(B, H_kv, n, d, generator=g) * 0.25, torch.randn(B, H_kv, n, d, generator=g)
+    bad = float("inf") if scale < 0 else NINF
+    k[0, :, torch.randint(0, n, (50,), generator=g), 3] = bad
+    k[1, :, :2500, 3] = bad
+    k[2, :, 100:, 3] = bad
+    got, want = attend("window", q.bfloat16(), k.bfloat16(), v.bfloat16(), [n, n, n], scale=scale)
+    assert np.abs(got - want).max() <= 1e-4 * float(v.abs().max())      # (scores are long sums here)
