@@ -29,7 +29,9 @@
 // Precision.  The result is fp32, and the tensor cores round operands to 11 (fp16) or 8
 // (bf16) bits and truncate their sums, so: 4-bit values are exact in fp16, q is bf16 times a
 // power of two, products are exact; p is split into two fp16 or three bf16 terms (22 or 24
-// bits; groups of at most 4 heads put the first two terms side by side in the 8 columns);
+// bits; groups of at most 4 heads put the first two terms side by side in the 8 columns).  The
+// second fp16 term is held times 2^11: fp16 ends at 2^-24, and without the factor a p below
+// 2^-25 left the numerator and stayed in the denominator;
 // at most two MMA steps are chained before the partial sum is added in fp32 with rounding.
 // Error against 64 bits 4.6e-7 (relative, 32k keys), as of fp32 arithmetic throughout; one
 // serial fp32 sum over the keys had 4e-6.
@@ -64,6 +66,7 @@ constexpr int WN_MAX_WARPS = 16;
 constexpr int WN_RED = 4 * 32 * WN_MAX_WARPS;  // floats of a join's partial sums: 4 x max(G D / 4, threads)
 constexpr float WN_TOP = 9.f;             // log2 of p where a new maximum puts it
 constexpr float WN_SLACK = 6.f;           // and how far above that later ones may be
+constexpr float WN_LOW = 2048.f;          // 4-bit: the factor of the second term of p, whose steps are those of 2^-35
 // Tiles a warp up to which a group stays in one CTA (one sequence, d = 128; alone against
 // split: 4-bit 1024 keys, 2 tiles, 11.2 and 12.4 us, 2048 keys, 4 tiles, 14.9 and 12.4; bf16
 // 256 keys, 2 tiles, 8.3 and 9.4, 512 keys, 4 tiles, 10.7 and 9.4).
@@ -472,8 +475,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
     constexpr int W = win_warps(KV4), NT = 32 * W;  // warps and threads that work
     constexpr int TK = win_tile(D, KV4), SUB = TK / 16, STAGE = win_stage(D, KV4), NS = win_stages(D, KV4);
     constexpr int MT = D / 16;   // 16-row pieces of the output, and MMA steps of a score
-    constexpr int NP = KV4 ? 2 : 3;                     // terms of p
-    constexpr int NB = WIDE ? NP : (KV4 ? 1 : 2);       // MMAs they take
+    constexpr int NB = KV4 ? (WIDE ? 2 : 1) : (WIDE ? 3 : 2);  // MMAs that the terms of p take (4-bit: two, bf16: three)
     constexpr unsigned FULL = 0xffffffffu;
     const float NEG_INF = __int_as_float(0xff800000);
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -718,7 +720,7 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         float o[MT][4];                      // columns 2c, 2c+1 of output rows r, r+8 of each piece
         float l0 = 0.f, l1 = 0.f, m0 = 0.f, m1 = 0.f, thr0 = NEG_INF, thr1 = NEG_INF;
         float ka0 = p.k2, ka1 = p.k2;
-        const float second = c < 2 ? 0.f : -1.f;
+        const float second = c < 2 ? 0.f : -1.f, low = c < 2 ? 1.f : WN_LOW;
         // ---- one tile: the keys from k0, whose rows and scales the pointers are at
         // (whole: every one is seen, no masks)
         auto pass = [&](const uint8_t *kc, const uint8_t *vc, const uint8_t *ks, const uint8_t *vs, int k0, bool whole) {
@@ -845,32 +847,30 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 for (int y = 0; y < 2; ++y) {
                     float a = s[u][2 * y], b = s[u][2 * y + 1];
                     add2(l0, l1, a, b);
-                    if (KV4 && !WIDE) {
-                        // columns 0-3 the first term, 4-7 what it leaves: second = 0 or -1
-                        const float2 f = unpack_f16(pack_f16(a, b));
-                        const float2 g = fma2(f.x, f.y, second, second, a, b);
-                        pb[u][0][y] = movmatrix(pack_f16(g.x, g.y));
+                    if (KV4) {
+                        // what the first term leaves, times WN_LOW, is the second.  Up to 4 heads: columns
+                        // 0-3 hold the first, 4-7 the second (second = 0 or -1)
+                        const uint32_t t = pack_f16(a, b);
+                        const float2 f = unpack_f16(t);
+                        const float take = WIDE ? -1.f : second, by = WIDE ? WN_LOW : low;
+                        float2 g = fma2(f.x, f.y, take, take, a, b);
+                        g = fma2(g.x, g.y, by, by, -0.f, -0.f);
+                        pb[u][NB - 1][y] = movmatrix(pack_f16(g.x, g.y));
+                        if (WIDE) pb[u][0][y] = movmatrix(t);
                     } else {
-                        uint32_t term[NP];
+                        uint32_t term[3];
 #pragma unroll
-                        for (int i = 0; i < NP; ++i) {
-                            if (KV4) {
-                                term[i] = pack_f16(a, b);
-                                const float2 f = unpack_f16(term[i]);
-                                a -= f.x;
-                                b -= f.y;
-                            } else {
-                                term[i] = pack_bf16(a, b);
-                                a -= bf16lo_to_f32(term[i]);
-                                b -= bf16hi_to_f32(term[i]);
-                            }
+                        for (int i = 0; i < 3; ++i) {
+                            term[i] = pack_bf16(a, b);
+                            a -= bf16lo_to_f32(term[i]);
+                            b -= bf16hi_to_f32(term[i]);
                         }
                         if (WIDE) {
 #pragma unroll
-                            for (int i = 0; i < NP; ++i) pb[u][i % NB][y] = movmatrix(term[i]);
+                            for (int i = 0; i < 3; ++i) pb[u][i % NB][y] = movmatrix(term[i]);
                         } else {
                             pb[u][0][y] = movmatrix(c < 2 ? term[0] : term[1]);
-                            pb[u][NB - 1][y] = movmatrix(c < 2 ? term[NP - 1] : 0u);
+                            pb[u][NB - 1][y] = movmatrix(c < 2 ? term[2] : 0u);
                         }
                     }
                 }
@@ -900,38 +900,50 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                         }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    float acc[4][4];
+                    // (wide groups: each term in sums of its own, two of a word's four bytes at a time)
+                    constexpr int NI = WIDE ? 2 : 4;
 #pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        uint32_t a[2][2][4];  // key pair, even or odd dimension, byte
+                    for (int i0 = 0; i0 < 4; i0 += NI) {
+                        float acc[NB][NI][4];
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint8_t *v0 = vc + (16 * u + 2 * c + 8 * y) * RB + r * 4 * W + 4 * w;
-                            const uint32_t x0w = *reinterpret_cast<const uint32_t *>(v0);
-                            const uint32_t x1w = *reinterpret_cast<const uint32_t *>(v0 + RB);
-                            e2m1_unpack8((x0w & 0x0f0f0f0fu) | ((x1w << 4) & 0xf0f0f0f0u), a[y][0]);
-                            e2m1_unpack8(((x0w >> 4) & 0x0f0f0f0fu) | (x1w & 0xf0f0f0f0u), a[y][1]);
+                        for (int u = 0; u < SUB; ++u) {
+                            uint32_t a[2][2][4];  // key pair, even or odd dimension, byte
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                a[y][0][i] = h2mul(a[y][0][i], sp[u][y]);
-                                a[y][1][i] = h2mul(a[y][1][i], sp[u][y]);
+                            for (int y = 0; y < 2; ++y) {
+                                const uint8_t *v0 = vc + (16 * u + 2 * c + 8 * y) * RB + r * 4 * W + 4 * w;
+                                const uint32_t x0w = *reinterpret_cast<const uint32_t *>(v0);
+                                const uint32_t x1w = *reinterpret_cast<const uint32_t *>(v0 + RB);
+                                e2m1_unpack8((x0w & 0x0f0f0f0fu) | ((x1w << 4) & 0xf0f0f0f0u), a[y][0]);
+                                e2m1_unpack8(((x0w >> 4) & 0x0f0f0f0fu) | (x1w & 0xf0f0f0f0u), a[y][1]);
+#pragma unroll
+                                for (int i = i0; i < i0 + NI; ++i) {
+                                    a[y][0][i] = h2mul(a[y][0][i], sp[u][y]);
+                                    a[y][1][i] = h2mul(a[y][1][i], sp[u][y]);
+                                }
                             }
+#pragma unroll
+                            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                                for (int n = 0; n < NB; ++n) {
+                                    const int j = i0 + i;
+                                    if (u == 0)
+                                        mma_set<false>(acc[n][i], a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j], pb[u][n][0], pb[u][n][1]);
+                                    else
+                                        mma_add<false>(acc[n][i], a[0][0][j], a[0][1][j], a[1][0][j], a[1][1][j], pb[u][n][0], pb[u][n][1]);
+                                }
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < NI; ++i)
 #pragma unroll
-                            for (int n = 0; n < NB; ++n) {
-                                if (u == 0 && n == 0)
-                                    mma_set<false>(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
-                                else
-                                    mma_add<false>(acc[i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[u][n][0], pb[u][n][1]);
+                            for (int e = 0; e < 4; e += 2) {
+                                float *to = &o[4 * w + i0 + i][e];
+                                if (WIDE) {
+                                    const float2 t = fma2(acc[NB - 1][i][e], acc[NB - 1][i][e + 1], 1.f / WN_LOW, 1.f / WN_LOW, to[0], to[1]);
+                                    to[0] = t.x, to[1] = t.y;
+                                }
+                                add2(to[0], to[1], acc[0][i][e], acc[0][i][e + 1]);
                             }
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2)
-                            add2(o[4 * w + i][e], o[4 * w + i][e + 1], acc[i][e], acc[i][e + 1]);
                 }
             } else {
                 const uint32_t vt = smem_u32(vc);
@@ -1076,6 +1088,10 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
+                        if (KV4 && c >= 2) {
+                            o[i][e] *= 1.f / WN_LOW;
+                            o[i][e + 1] *= 1.f / WN_LOW;
+                        }
                         const float got = __shfl_xor_sync(FULL, c < 2 ? o[i][e + 1] : o[i][e], 2);
                         o[i][e] = (c < 2 ? o[i][e] : o[i][e + 1]) + got;
                     }

@@ -4,6 +4,7 @@ fp32 arithmetic gives the answer and narrower steps on the way would not.
 Scores here are sums with one product that is not zero, so that they are exact in fp32: what is
 tested is what follows, the softmax and the weighted sum.
 """
+import math
 
 import numpy as np
 import pytest
@@ -89,3 +90,24 @@ def test_a_score_of_minus_infinity_weighs_nothing(d, scale):
     k[2, :, 100:, 3] = bad
     got, want = attend("window", q.bfloat16(), k.bfloat16(), v.bfloat16(), [n, n, n], scale=scale)
     assert np.abs(got - want).max() <= 1e-4 * float(v.abs().max())      # (scores are long sums here)
+
+
+# ------------------------------------------------------------------ very small weights
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("d,G", [(64, 4), (64, 8), (128, 4), (128, 8)])
+@pytest.mark.parametrize("bits", [30, 33, 36])
+@pytest.mark.parametrize("n,lead", [(32, 0), (32, 17), (32, 31), (3008, 0), (3008, 1500), (3008, 3007)])
+def test_many_keys_of_very_small_weight(op, d, G, bits, n, lead):
+    """One key leads and the others weigh less than 2^-bits of it (2^-37.1 at the least): v is 0 at
+    the first and 6 at the others, so that the output is their share.  With the leading weight at
+    2^9 theirs is 2^-28.1; held to 2^-35, half a step is 2^-7.9 of it."""
+    q, k, v = torch.zeros(1, G, d), torch.zeros(1, 1, n, d), torch.full((1, 1, n, d), 6.0)
+    q[:, :, 0] = 1.0
+    k[..., 0] = -6.0
+    k[0, 0, lead, 0] = 0
+    v[0, 0, lead] = 0
+    scale = bits * math.log(2) / 6 * 1.03
+    got, want = attend(op, q.bfloat16(), k.bfloat16(), v.bfloat16(), [n], scale=scale)
+    assert np.abs(got / want - 1).max() <= 2.0 ** -7
