@@ -111,3 +111,81 @@ def test_many_keys_of_very_small_weight(op, d, G, bits, n, lead):
     scale = bits * math.log(2) / 6 * 1.03
     got, want = attend(op, q.bfloat16(), k.bfloat16(), v.bfloat16(), [n], scale=scale)
     assert np.abs(got / want - 1).max() <= 2.0 ** -7
+
+
+# ------------------------------------------------------------------ the terms of a weight
+
+def two_keys(seed, d, H_kv, G, B=48, n=48):
+    """Two keys that weigh 1 and w = exp(-q t), t and q of many sizes, at any two places of the
+    sequence; the others nothing.  v is 0 and 6: the output is 6 w / (1 + w)."""
+    g = gen(seed)
+    q, k, v = torch.zeros(B, H_kv * G, d), torch.zeros(B, H_kv, n, d), torch.zeros(B, H_kv, n, d)
+    q[:, :, 9] = 0.25 + torch.rand(B, H_kv * G, generator=g)
+    k[..., 9] = -1024
+    v[...] = torch.randn(B, H_kv, n, 1, generator=g)
+    for b in range(B):
+        for h in range(H_kv):
+            i, j = torch.randperm(n, generator=g)[:2].tolist()
+            k[b, h, i, 9], k[b, h, j, 9] = 0, -torch.rand(1, generator=g).item()
+            v[b, h, i], v[b, h, j] = 0, 6
+    return q.bfloat16(), k.bfloat16(), v.bfloat16()
+
+
+# Error of 6 w / (1 + w).  w: its exponent is rounded near 2^3 (2^-21 ln 2), the factor log2 e by
+# 2^-25 of at most 2.2, two exponentials are off by 2^-22 each: less than 9e-7, times 6 w / (1 + w)^2,
+# at most 6 / 4.  The weight in two or three terms 2^-23, their sum and products in the tensor cores
+# three steps of 2^-23, the sum of weights, the reciprocal and the product 2^-24, 2^-23 and 2^-24:
+# six times 2^-23, times 6 w / (1 + w), at most 3.
+TOL_TWO = 9e-7 * 1.5 + 6 * 2.0 ** -23 * 3
+
+
+def many_keys(seed, d, H_kv, G, B=8, n=64):
+    """Keys of comparable weight (scores within 4), v of both signs."""
+    g = gen(seed)
+    q, k = torch.zeros(B, H_kv * G, d), torch.zeros(B, H_kv, n, d)
+    q[:, :, 9] = 0.25 + torch.rand(B, H_kv * G, generator=g)
+    k[..., 9] = 3 * torch.rand(B, H_kv, n, generator=g)
+    return q.bfloat16(), k.bfloat16(), torch.randn(B, H_kv, n, d, generator=g).bfloat16()
+
+
+# Error of sum p v / sum p, relative to max|v|: twice that of a weight (9e-7); the tensor cores' sums,
+# at most 6 steps of 2^-23 in a row, 64 / 16 additions of them and 8 of a lane's weights, 2^-24 each, and
+# as much again as the exchange of both, the reciprocal and the product take.
+TOL_MANY = 2 * 9e-7 + (12 + 4 + 8 + 6) * 2.0 ** -24
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_a_weight_keeps_its_bits(op, d, G):
+    q, k, v = two_keys(d + G, d, 2, G)
+    got, want = attend(op, q, k, v, [48] * 48, scale=1.0)
+    assert np.abs(got - want).max() <= TOL_TWO
+    q, k, v = many_keys(d + G, d, 2, G)
+    got, want = attend(op, q, k, v, [64] * 8, scale=1.0)
+    assert np.abs(got - want).max() <= TOL_MANY * float(v.abs().max())
+
+
+def error_with(terms, op, q, k, v):
+    """Largest error of the output in 64 bits when each weight is the sum of its first `terms` terms."""
+    if op == "kv4":
+        k, v = (torch.from_numpy(kv4_util.values(*kv4_util.quantise(x))) for x in (k, v))
+    s = torch.einsum("bhgd,bhnd->bhgn", q.double().view(k.shape[0], k.shape[1], -1, q.shape[-1]), k.double())
+    p = torch.exp(s - s.amax(-1, keepdim=True)) * 512
+    kept = torch.zeros_like(p)
+    for _ in range(terms):
+        kept += (p - kept).to(torch.float16 if op == "kv4" else torch.bfloat16).double()
+    return float(torch.einsum("bhgn,bhnd->bhgd", (p - kept) / p.sum(-1, keepdim=True), v.double()).abs().max())
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_the_tolerances_would_show_a_lost_term(op, d, G):
+    """The same inputs with the last term of each weight left out (many keys: all but the first):
+    beyond twice the tolerance."""
+    q, k, v = two_keys(d + G, d, 2, G)
+    assert error_with(1 if op == "kv4" else 2, op, q, k, v) > 2 * TOL_TWO
+    q, k, v = many_keys(d + G, d, 2, G)
+    assert error_with(1, op, q, k, v) > 2 * TOL_MANY * float(v.abs().max())
