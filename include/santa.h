@@ -237,7 +237,7 @@ int santa_device_status(void *workspace, int32_t *code, void *stream);
  *    (different streams without ordering, or several host threads) race on the buffer:
  *    order them on one stream.
  */
-#define SANTA_STATIC_SCRATCH_BYTES ((size_t)16 << 20)
+#define SANTA_STATIC_SCRATCH_BYTES (((size_t)16 << 20) + 65536)  /* the control block and 16 MiB */
 int santa_decode_static(const santa_shape *shape, const void *q, const void *k_cache,
                         const void *v_cache, const int32_t *seq_lens, int32_t S, int32_t mode,
                         uint64_t seed, float *out, int32_t *idx_out, void *stream);

@@ -33,7 +33,7 @@ EXPORTS = ("santa_workspace_size", "santa_workspace_init", "santa_decode", "sant
            "santa_window_workspace_size")
 ERR_DEVICE = -6
 ERR_SCRATCH = -7
-STATIC_SCRATCH_BYTES = 16 << 20
+STATIC_SCRATCH_BYTES = (16 << 20) + 65536
 
 
 class SantaError(RuntimeError):
