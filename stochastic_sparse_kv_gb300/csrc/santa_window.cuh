@@ -31,10 +31,14 @@
 // power of two, products are exact; p is split into two fp16 or three bf16 terms (22 or 24
 // bits; groups of at most 4 heads put the first two terms side by side in the 8 columns).  The
 // second fp16 term is held times 2^11: fp16 ends at 2^-24, and without the factor a p below
-// 2^-25 left the numerator and stayed in the denominator;
-// at most two MMA steps are chained before the partial sum is added in fp32 with rounding.
-// Error against 64 bits 4.6e-7 (relative, 32k keys), as of fp32 arithmetic throughout; one
-// serial fp32 sum over the keys had 4e-6.
+// 2^-25 left the numerator and stayed in the denominator.  Few MMA steps are chained before
+// their sum is added in fp32 with rounding: two in a score and, in V^T p, two for 4 bits and for
+// bf16 at d = 128 with up to 4 heads a group, three with 8 heads, four and six at d = 64.
+// (A factor of q below 2^-31 of its head's largest is rounded to a step of 2^-38 of that.)
+// Error against 64 bits, over 4 x 32k and 64 x 4k keys, 1 to 8 heads a group and both d, relative
+// to the largest output: 4 bits 2.1e-7 to 6.9e-7, bf16 3.7e-7 to 1.1e-6, root mean square
+// 1.8e-7 to 3.5e-7 and 3.6e-7 to 5.3e-7 (fp32 products and sums of a library: 3.3e-7 to
+// 1.3e-6); one serial fp32 sum over 32k keys had 4e-6.
 //
 // Groups that one warp holds whole are finished by it.  Pieces of others meet in shared
 // memory (their CTA joins them) and, where a group spans CTAs, in the workspace: the last
