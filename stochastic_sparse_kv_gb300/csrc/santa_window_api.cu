@@ -97,8 +97,8 @@ int move_rows(const santa_shape *sh, const santa_kv4 *c, const santa_rows *r, in
     bool wide = aligned(r->k, 32) && aligned(r->v, 32);
     for (int i = 0; i < 3; ++i)
         if (dims[i] > 1) wide = wide && r->k_stride[i] % 16 == 0 && r->v_stride[i] % 16 == 0;
-    const int row_groups = T * (sh->d / KV_GROUP);
-    const int threads = std::min(KV_NT, (row_groups + 31) / 32 * 32);
+    const long long row_groups = (long long)T * (sh->d / KV_GROUP);
+    const long long threads = std::min<long long>(KV_NT, (row_groups + 31) / 32 * 32);
     const dim3 grid((unsigned)((row_groups + threads - 1) / threads), (unsigned)(sh->B * sh->H_kv));
     void *args[] = {&m};
     const void *fn = move_kernel(sh->d, distinct, wide);

@@ -147,6 +147,22 @@ def test_rows_aligned_to_16_bytes_only(d, shift, pad):
     assert torch.equal(kbuf, before)          # nothing beside the rows was written
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_as_many_tokens_as_there_may_be(d):
+    """2^31 - 1 groups, or the most below: one prompt of which few tokens are live, its token stride 0."""
+    T = ((1 << 31) - 1) // (d // 16)
+    row = rand(gen(d), 1, 1, 1, d).to(DEV)
+    cache = santa.new_kv4_cache(1, 1, 16, d)
+    santa.kv4_append(cache, row.expand(1, T, 1, d), row.expand(1, T, 1, d), ints([6]), ints([3]))
+    c, s = kv4_util.quantise(row.cpu())
+    for codes, scales in (cache[:2], cache[2:]):
+        live = np.zeros(16, dtype=bool)
+        live[6:9] = True
+        assert np.array_equal(codes[0, 0, 6:9].cpu().numpy(), np.repeat(c.reshape(1, -1), 3, 0))
+        assert np.array_equal(scales[0, 0, 6:9].cpu().numpy(), np.repeat(s.reshape(1, -1), 3, 0))
+        assert not codes[0, 0, ~live].any() and not scales[0, 0, ~live].any()
+
+
 def test_strides_of_single_dimensions_are_not_read():
     """One row of one head, its batch, token and head strides any numbers."""
     g = gen(3)
