@@ -68,6 +68,7 @@ int move_rows(const santa_shape *sh, const santa_kv4 *c, const santa_rows *r, in
             const int x = order[i];
             if (dims[x] <= 1) continue;
             if (st[x] < extent) return SANTA_ERR_INVALID_ARG;
+            if (dims[x] - 1 > ((1ll << 60) - extent) / st[x]) return SANTA_ERR_INVALID_ARG;  // no memory is that large
             extent += st[x] * (dims[x] - 1);
         }
     }
