@@ -472,7 +472,7 @@ def _window_call(q, dims, cache_args, fn, what, seq_lens, window, sinks, scale, 
     if len(qs) != 3 or qs[0] != B or qs[2] != d or q.device != dev:
         raise ValueError("q [B, H_q, d] and the cache's shape or device disagree")
     _int_vector(seq_lens, "seq_lens", B, dev)
-    if window >= 1 << 31 or sinks >= 1 << 31:
+    if not (-1 << 31 <= window < 1 << 31 and -1 << 31 <= sinks < 1 << 31):
         raise ValueError("window and sinks are 32-bit numbers")
     if stream is not None:
         caller = torch.cuda.current_stream(dev)

@@ -103,6 +103,13 @@ def test_a_workspace_that_a_captured_decode_holds_is_never_freed(host, monkeypat
     assert santa._cached_workspace(1000, CPU, t) is not inside
 
 
+@pytest.mark.parametrize("window,sinks", [(1 << 31, 0), ((1 << 32) + 5, 0), (5 - (1 << 32), 0), (4, 5 - (1 << 32))])
+def test_windows_that_32_bits_do_not_hold_are_refused(host, window, sinks):
+    with pytest.raises(ValueError, match="32-bit"):
+        santa._window_call(torch.zeros(1, 8, 128), (1, 1, 64, 128, CPU), (None,), lambda *a: 0, "call",
+                           torch.zeros(1, dtype=torch.int32), window, sinks, 0.0, torch.empty(1, 8, 128), torch.float32, None, None)
+
+
 def test_a_stream_of_another_device_is_refused(monkeypatch):
     class Other:
         cuda_stream, device = 7, torch.device("cuda", 1)
