@@ -65,7 +65,8 @@ def test_read_refuses_rows_that_share_memory(lib):
     assert call((4096, 128, 128)) == -1        # tokens inside one another's heads
     assert call((4096, 128, 384)) == -1        # head-major, heads closer than 4 tokens
     # tokens 2^39 apart reach past 2^63, batch rows 2^40 apart lie among them
-    assert call((1 << 40, 1 << 39, 64), T=(1 << 28) - 1, B=2, H_q=1, H_kv=1, d=64) == -1
+    far = (1 << 40, 1 << 39, 64)
+    assert lib.santa_kv4_read(shape(B=2, H_q=1, H_kv=1, d=64), kv(), rows(ks=far, vs=far), (1 << 28) - 1, A, None, None, STREAM) == -1
     # strides of dimensions of size 1 (or 0) are not read; nothing to do, so nothing is enqueued
     # (one row with such strides is read in test_kv4_gpu.py)
     assert call((-3, 1, 7), T=0, B=1, H_kv=1) == 0
