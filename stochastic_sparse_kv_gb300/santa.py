@@ -307,9 +307,15 @@ def set_wait_limit(limit_ns: int) -> None:
 
 
 def sample_points(B: int, H_q: int, S: int, mode, seed: int, device="cuda", stream=None) -> torch.Tensor:
+    if stream is not None:
+        caller = torch.cuda.current_stream(device)
+        with _current(stream, device):
+            t = sample_points(B, H_q, S, mode, seed, device)
+        t.record_stream(caller)
+        return t
     t = torch.empty(B, H_q, S, dtype=torch.float64, device=device)
     _check(load().santa_sample_points(int(B), int(H_q), int(S), _mode(mode), ctypes.c_uint64(seed),
-                                      ctypes.c_void_p(t.data_ptr()), ctypes.c_void_p(_stream_ptr(stream))),
+                                      ctypes.c_void_p(t.data_ptr()), ctypes.c_void_p(_stream_ptr(None))),
            "santa_sample_points")
     return t
 
@@ -318,10 +324,16 @@ def ternary_query(q: torch.Tensor, seed: int, stream=None) -> torch.Tensor:
     """santa_ternary_query: each head's Bernoulli qK^T draw (bf16 [B,H_q,d])."""
     if q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous() or q.dim() != 3:
         raise ValueError("q must be a contiguous bf16 CUDA tensor [B, H_q, d]")
+    if stream is not None:
+        caller = torch.cuda.current_stream(q.device)
+        with _current(stream, q.device):
+            out = ternary_query(q, seed)
+        out.record_stream(caller)
+        return out
     B, H_q, d = q.shape
     out = torch.empty_like(q)
     _check(load().santa_ternary_query(int(B), int(H_q), int(d), ctypes.c_void_p(q.data_ptr()), ctypes.c_uint64(seed),
-                                      ctypes.c_void_p(out.data_ptr()), ctypes.c_void_p(_stream_ptr(stream))),
+                                      ctypes.c_void_p(out.data_ptr()), ctypes.c_void_p(_stream_ptr(None))),
            "santa_ternary_query")
     return out
 

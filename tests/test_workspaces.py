@@ -158,6 +158,28 @@ def test_growing_on_an_explicit_stream_without_synchronising():
 
 
 @pytest.mark.gpu
+def test_draws_on_an_explicit_stream_use_memory_of_that_stream():
+    """Memory that work still running on the current stream has given back is not written by another stream."""
+    q = workloads.make_q(64, 32, 128, 3.0, torch.Generator().manual_seed(1)).to(DEV)
+    calls = [lambda **kw: santa.sample_points(64, 32, 256, "stratified", 7, **kw), lambda **kw: santa.ternary_query(q, 7, **kw)]
+    want = [c().clone() for c in calls]
+    side = torch.cuda.Stream()
+    big = torch.ones(1 << 28, device=DEV)
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        for _ in range(4):
+            for _ in range(20):
+                big.mul_(1.0)                                    # the current stream is busy
+            gone = torch.full_like(w, 3)                         # written late, given back at once
+            at = gone.data_ptr()
+            del gone
+            got = c(stream=side)
+            assert got.data_ptr() != at
+            torch.cuda.synchronize()
+            assert torch.equal(got, w)
+
+
+@pytest.mark.gpu
 def test_two_captured_branches_with_explicit_streams():
     """Two branches of one graph, forked from the captured stream, each a call on its own stream."""
     p, r = _problem(4000, 1), _problem(3008, 2)
