@@ -115,7 +115,7 @@ struct Kv4Move {
     long long sb[2], st[2], sh[2];    // batch, token, head
     const int32_t *pos, *counts;      // first cache row of each batch row; live tokens (NULL: T)
     int32_t *ctrl;                    // device error word (or NULL)
-    int B, H_kv, D, n_max, T;
+    int H_kv, n_max, T;
 };
 
 // A thread's group, of K and of V: blockIdx.y is a (batch row, head) pair; consecutive threads

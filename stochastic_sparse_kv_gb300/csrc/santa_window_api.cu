@@ -89,9 +89,7 @@ int move_rows(const santa_shape *sh, const santa_kv4 *c, const santa_rows *r, in
     m.pos = pos;
     m.counts = counts;
     m.ctrl = static_cast<int32_t *>(workspace);
-    m.B = sh->B;
     m.H_kv = sh->H_kv;
-    m.D = sh->d;
     m.n_max = sh->n_max;
     m.T = T;
     // 32-byte accesses where every row begins at one
