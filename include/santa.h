@@ -253,7 +253,8 @@ int santa_decode_static(const santa_shape *shape, const void *q, const void *k_c
  *          No other code above 0xE2 is ever written.
  *   codes  4 bits each: sign (bit 3) and index into {0, .5, 1, 1.5, 2, 3, 4, 6} (bits 0-2),
  *          the value nearest x / scale, ties to the even index, saturating at 6.  Byte i of
- *          a row holds values 2i (low half) and 2i + 1 (high half).
+ *          a row holds values 2i (low half) and 2i + 1 (high half).  In a group whose scale is
+ *          0 or 0xFF every code is 0, the sign too.
  * A code stands for sign * value * scale, which bf16 holds exactly.  Largest magnitude held:
  * 61440; smallest: 2^-18.
  */
@@ -295,7 +296,8 @@ int santa_kv4_append(const santa_shape *shape, const santa_kv4 *cache, const san
  * Arguments as for santa_kv4_append, with `rows` written instead: cache row pos[b] + t goes
  * to row (b, t) for t < counts[b], and the other rows stay as they were.  No two rows may
  * share memory, of K or of V: in order of size, each stride must step over all that the smaller ones span
- * (SANTA_ERR_INVALID_ARG otherwise).  For example, with the strides of a bf16 cache
+ * (SANTA_ERR_INVALID_ARG otherwise).  K rows and V rows must not share memory with one another
+ * either; that is not checked.  For example, with the strides of a bf16 cache
  * [B, H_kv, n, d] it fills the cache that santa_decode samples.
  */
 int santa_kv4_read(const santa_shape *shape, const santa_kv4 *cache, const santa_rows *rows, int32_t T,
@@ -307,7 +309,9 @@ int santa_kv4_read(const santa_shape *shape, const santa_kv4 *cache, const santa
  * decoding token being the last of its n_b = seq_lens[b] keys:
  *   window = 0   every key j < n_b
  *   window > 0   the last `window` keys (j >= n_b - window) and the first `sinks` ones
- * Keys that are not visible are not read into the result, whatever they hold (NaN too).
+ * Keys that are not visible are not read into the result, whatever they hold (NaN too).  A visible
+ * key with a score of minus infinity weighs nothing; when every visible score of a head is, its
+ * output is NaN, as it is with a score that is NaN or plus infinity.
  */
 
 /*

@@ -515,7 +515,9 @@ def decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None, stream=None):
     """One step of exact attention over the last `window` keys of each sequence and its first
     `sinks` (window = 0: every key).  q [B, H_q, d], k/v [B, H_kv, n_max, d] bf16, seq_lens
-    [B] int32, all on one CUDA device.  Returns out [B, H_q, d], fp32 or bf16."""
+    [B] int32, all on one CUDA device.  Returns out [B, H_q, d], fp32 or bf16.  On an explicit `stream`,
+    the call and all that it allocates are that stream's: order its inputs and its result with
+    the current stream as for any work on another one."""
     for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
         _cuda_bf16(t, name)
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.device != k_cache.device:
