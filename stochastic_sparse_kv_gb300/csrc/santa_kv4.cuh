@@ -22,8 +22,8 @@
 //
 // Both kernels move 2.56 bytes a value and are bound by that: one thread takes one group of K
 // and of V, in one 32-byte access where the rows allow it.  4 rows of 32k tokens, 8 heads, d = 128:
-// read back in 104 us, 6.6 TB/s, 0.98 of the measured copy rate (16-byte accesses and index
-// divisions: 127 us).  8k tokens written and read back in 54 us, 51 at the copy rate (dividing
+// read back in 103-105 us, 6.6 TB/s, 0.98 of the measured copy rate (16-byte accesses and index
+// divisions: 127 us).  8k tokens written and read back in 53-54 us, 51 at the copy rate (dividing
 // exactly, 16 times a group: 85 us).
 #pragma once
 

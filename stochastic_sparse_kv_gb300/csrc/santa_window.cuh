@@ -46,17 +46,20 @@
 // list, so results do not depend on timing.
 //
 // What bounds it.  bf16: the cache's bytes.  16 rows, window 8192 + 16 sinks of 32k keys,
-// d = 128, 8 KV heads: 538 MB in 80-84 us, 6.4-6.7 TB/s, 0.96-1.0 of the measured copy rate.
-// 4-bit: 16 rows of 32k keys, 604 MB, take 108 us, 5.6 TB/s, 0.83 of the copy rate.  No unit
-// is full (half that batch: 640 warp instructions per 32 keys of a KV head, 0.62 of the issue
-// slots, 0.48 of the ALU pipe, which the 128 conversions among them take at half rate, 0.25 of
+// d = 128, 8 KV heads: 538 MB in 81-83 us, 6.5-6.7 TB/s, 0.97-0.99 of the measured copy rate.
+// 4-bit: 16 rows of 32k keys, 604 MB, take 107-108 us, 5.6 TB/s, 0.84 of the copy rate (8 heads a
+// group 122 us; d = 64, half the bytes, 72 us, 8 heads a group 77).  No unit
+// is full (half that batch: 636 warp instructions per 32 keys of a KV head, 0.62 of the issue
+// slots, 0.47 of the ALU pipe, which the 128 conversions among them take at half rate, 0.25 of
 // the tensor pipe); with four warps to a scheduler neither copies nor arithmetic hide the
 // other wholly.  An earlier state's copies took 94-96 us without the arithmetic.  What it
 // took from 162 us: chains that begin at zero in the MMA, two fp32 operations an instruction,
 // copies by the lanes that use them (bulk copies of a tile by one lane: 126 us against 113; by
-// warps of their own: 139-143 against 127), 16 warps (12 of 168 registers: 119 against 110),
+// warps of their own: 139-143 against 127), 16 warps (12 of 168 registers: 119 against 110; the
+// 128 registers of 16 spill at d = 128: 8 bytes, with 8 heads a group 32 stored and 76 loaded),
 // seldom used state in shared memory, joins side by side.
-// Small calls: a group of 32 keys 4.6 us in one CTA; groups that span CTAs 12 us and more.
+// Small calls: a group of 32 keys 3.8-7.0 us in one CTA; one that spans CTAs 9 us (bf16) or
+// 11 us (4 bits) and more.
 #pragma once
 
 #include "santa_kv4.cuh"
@@ -71,9 +74,11 @@ constexpr int WN_RED = 4 * 32 * WN_MAX_WARPS;  // floats of a join's partial sum
 constexpr float WN_TOP = 9.f;             // log2 of p where a new maximum puts it
 constexpr float WN_SLACK = 6.f;           // and how far above that later ones may be
 constexpr float WN_LOW = 2048.f;          // 4-bit: the factor of the second term of p, whose steps are those of 2^-35
-// Tiles a warp up to which a group stays in one CTA (one sequence, d = 128; alone against
-// split: 4-bit 1024 keys, 2 tiles, 11.2 and 12.4 us, 2048 keys, 4 tiles, 14.9 and 12.4; bf16
-// 256 keys, 2 tiles, 8.3 and 9.4, 512 keys, 4 tiles, 10.7 and 9.4).
+// Tiles a warp up to which a group stays in one CTA.  One sequence of 8 KV heads, 4 heads a group,
+// alone against split, at 2 tiles and at 4: 4-bit d = 128 1024 keys 11.2 and 12.4 us, 2048 keys
+// 14.7 and 12.5; d = 64 8.7 and 11.0, 10.7 and 11.0; bf16 d = 128 256 keys 8.1 and 9.2, 512 keys
+// 10.4 and 9.2; d = 64 512 keys 7.3 and 9.1, 1024 keys 8.8 and 9.1.  (d = 64 could go to 4, for
+// 0.3 us; with 8 sequences 1.2.)
 constexpr int WN_ALONE = 2;
 constexpr int WN_SETUP = 2;               // tiles that beginning a group costs about as much as
 
@@ -543,8 +548,8 @@ __device__ __forceinline__ void window_body(const WinParams &p, const CUtensorMa
         if (nb[b] == 0)
             for (int i = tid; i < p.H_q * D; i += blockDim.x) win_store(p, (size_t)b * p.H_q * D + i, 0.f);
     // Few short groups: a CTA for each.  Else even shares of the list, which split groups between
-    // CTAs and join them through the workspace: that takes 6 us (fence, arrival, join), as
-    // long as WN_ALONE more tiles a warp.
+    // CTAs and join them through the workspace: fence, arrival and join make a group of 128 keys
+    // 2.3-3.6 us (bf16) or 5.5-6 us (4 bits) longer than one CTA would be.
     const bool alone = p.B * p.H_kv <= (int)gridDim.x && flag[0] <= WN_ALONE * W;
     const int NC = alone ? p.B * p.H_kv : min((int)gridDim.x, (T + W - 1) / W);  // CTAs with a share
     if ((int)blockIdx.x >= NC) return;
