@@ -158,6 +158,30 @@ def test_growing_on_an_explicit_stream_without_synchronising():
 
 
 @pytest.mark.gpu
+def test_streams_given_as_handles_and_plans_on_a_stream():
+    """Any object that holds a CUDA stream handle will do, and a plan keeps to its stream."""
+    class Handle:
+        def __init__(self, s):
+            self.cuda_stream = s.cuda_stream
+
+    p = _problem(2000, 8)
+    want = [op().clone() for op in _ops(p)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (Handle(side), torch.cuda.ExternalStream(side.cuda_stream), side):
+        got = [op(stream=s) for op in _ops(p)]
+        assert santa.new_workspace(70000, DEV, s).numel() == 70000
+        side.synchronize()
+        assert all(torch.equal(a, w) for a, w in zip(got, want))
+    q, k, v, _, sl = p
+    plan = santa.DecodePlan(q, k, v, sl, 64, "systematic", two_pass=True, stream=side)
+    _ops(_problem(8000, 9))[2](stream=side)              # a larger call on the plan's stream
+    out, _ = plan(3)
+    side.synchronize()
+    assert torch.equal(out, want[2])
+
+
+@pytest.mark.gpu
 def test_draws_on_an_explicit_stream_use_memory_of_that_stream():
     """Memory that work still running on the current stream has given back is not written by another stream."""
     q = workloads.make_q(64, 32, 128, 3.0, torch.Generator().manual_seed(1)).to(DEV)
