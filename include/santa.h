@@ -93,6 +93,7 @@ extern "C" {
 #define SANTA_DEV_BAD_SEQLEN 1      /* some seq_lens[b] outside [0, n_max]; treated as 0 */
 #define SANTA_DEV_TIMEOUT 2         /* a bounded wait on a shared-memory barrier gave up */
 #define SANTA_DEV_BAD_POSITION 4    /* a row's pos / counts outside the cache; the row is skipped */
+#define SANTA_DEV_BAD_PAGE 8        /* a needed entry of a page table names no page */
 
 /* Problem shape.  scale = 0 selects 1/sqrt(d) rounded to fp32. */
 typedef struct {
@@ -338,6 +339,152 @@ int santa_decode_window(const santa_shape *shape, const void *q, const void *k_c
 int santa_decode_kv4(const santa_shape *shape, const void *q, const santa_kv4 *cache, const int32_t *seq_lens,
                      int32_t window, int32_t sinks, int32_t flags, float *out, void *workspace,
                      size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ rotary positions
+ *
+ * A head at position p is rotated pair by pair: features (x, y) of pair i become
+ * (x cos a - y sin a, x sin a + y cos a) times `amplitude`, a = p f_i.  The pairs cover the first
+ * `rot` features; the others stay as they are.  Frequencies f_i are held in 64-bit fixed point as
+ * turns a position, so that the angle of any position is exact (a product modulo 2^64) before one
+ * conversion to fp32.
+ */
+#define SANTA_ROPE_HALVES 0         /* pair i is the features (i, i + rot/2) */
+#define SANTA_ROPE_PAIRS 1          /* pair i is the features (2i, 2i + 1) */
+
+typedef struct {
+    const uint64_t *turns;  /* device [rot/2], 8-byte aligned: f_i / (2 pi) in units of 2^-64 */
+    int32_t rot;            /* 16..d, a multiple of 16 (SANTA_ERR_UNSUPPORTED otherwise) */
+    int32_t layout;         /* SANTA_ROPE_HALVES or SANTA_ROPE_PAIRS */
+    float amplitude;        /* factor of the rotated features: 1, or what santa_rope_turns gives */
+} santa_rotation;
+
+/* How frequencies are scaled for contexts longer than the trained one.  f_i = base^(-2i/rot):
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   BASE    base' = base factor^(rot / (rot - 2)) in its place
+ *   BANDS   f_i above `high` turns over the original context, f_i / factor below `low` turns,
+ *           in between the blend that is linear in the number of turns
+ *   RAMP    f_i above `high` turns, f_i / factor below `low` turns, in between a blend that is
+ *           linear in i, its ends rounded outwards to whole pairs; amplitude
+ *           0.1 ln(factor) + 1 */
+#define SANTA_ROPE_SCALE_NONE 0
+#define SANTA_ROPE_SCALE_LINEAR 1
+#define SANTA_ROPE_SCALE_BASE 2
+#define SANTA_ROPE_SCALE_BANDS 3
+#define SANTA_ROPE_SCALE_RAMP 4
+
+typedef struct {
+    double base;            /* above 1 (10000, 500000, ...) */
+    int32_t scaling;        /* SANTA_ROPE_SCALE_* */
+    double factor;          /* at least 1: how much longer (NONE does not read it) */
+    double low, high;       /* 0 < low < high: turns over the original context (BANDS, RAMP) */
+    int32_t original;       /* positions of the original context, at least 1 (BANDS, RAMP) */
+} santa_rope_spec;
+
+/*
+ * santa_rope_turns -- the table and the amplitude of a santa_rotation, on the host: turns
+ * [rot/2] and *amplitude are host memory; copy the table to the device once.  rot: a multiple of
+ * 2 of at least 2 here.  Pure host computation, in doubles.
+ */
+int santa_rope_turns(const santa_rope_spec *spec, int32_t rot, uint64_t *turns, float *amplitude);
+
+/*
+ * santa_rope -- rotate rows to their positions.
+ *
+ *  B, T, H, d  batch rows 1..1024, tokens, heads 1..1024, head dimension 64 or 128; T = 0 does
+ *              nothing; B * T * H * d / 16 below 2^31
+ *  x, out      device bf16 [B, T, H, d], 16-byte aligned; strides in elements for (batch,
+ *              token, head) as for santa_rows.  Rows of `out` may not share memory (as for
+ *              santa_kv4_read); out = x with the same strides rotates in place, any other
+ *              overlap of the two is not allowed (not checked)
+ *  pos         device int32 [B]: position of each batch row's first token, not negative
+ *  counts      device int32 [B] or NULL: live tokens (padded prompts).  Rows t >= counts[b] of
+ *              `out` stay as they were
+ *  workspace   any workspace of this library, or NULL: only its device error word is used.  A
+ *              batch row with pos < 0, counts outside [0, T] or pos + counts > 2^31 - 1 is skipped
+ *              and sets SANTA_DEV_BAD_POSITION there
+ * Products in fp32, one rounding to bf16.  One launch; it can be captured, positions and counts
+ * are read when it runs.
+ */
+int santa_rope(int32_t B, int32_t T, int32_t H, int32_t d, const void *x, const int64_t x_stride[3], void *out,
+               const int64_t out_stride[3], const santa_rotation *rotation, const int32_t *pos, const int32_t *counts,
+               void *workspace, void *stream);
+
+/* ------------------------------------------------------------------ a paged cache
+ *
+ * A bf16 cache whose sequences hold pages of a common pool, in any order.  Key j of sequence b is
+ * row j % page of page table[b][j / page].  The pool and the table are the caller's: pages are
+ * handed out by writing the table, on the stream of the calls, and may stand in many tables (a
+ * prefix that sequences share) as long as nothing is written to them.
+ */
+typedef struct {
+    void *k, *v;            /* device bf16 [n_pages, H_kv, page, d], contiguous, 16-byte aligned */
+    const int32_t *table;   /* device int32 [B, n_max / page], contiguous; entries that no call needs may
+                             * hold anything */
+    int32_t n_pages;        /* pages of the pool; n_pages * H_kv * page < 2^31 */
+    int32_t page;           /* tokens a page: 16, 32, 64, 128 or 256 */
+} santa_paged;
+
+/* In the calls below shape->n_max is the longest sequence that the table has room for, a multiple
+ * of `page` up to 524288 (SANTA_ERR_UNSUPPORTED otherwise); B * H_kv * n_max is not limited. */
+
+/*
+ * santa_paged_append -- write new K and V rows into their pages, K rotated on the way.
+ *
+ *  shape     B, H_q, H_kv, d and n_max
+ *  rows      the new rows [B, T, H_kv, d] (read only), as for santa_kv4_append
+ *  pos       device int32 [B]: position of each batch row's first new token
+ *  counts    device int32 [B] or NULL: live tokens; nothing else is written
+ *  rotation  of K and q, or NULL: no rotation
+ *  q, q_out  NULL, or the same tokens' queries [B, T, H_q, d] and where they go rotated, in the
+ *            same launch (strides and overlap as for santa_rope)
+ *  workspace any workspace of this library, or NULL: only its device error word is used.  A batch row
+ *            with pos < 0, counts outside [0, T] or pos + counts > n_max is skipped
+ *            (SANTA_DEV_BAD_POSITION); a token whose table entry is outside [0, n_pages) is not
+ *            written, but its query is rotated (SANTA_DEV_BAD_PAGE)
+ * No two live tokens may go to the same row of the same page (not checked).  B * T * (H_q +
+ * 2 H_kv) * d / 16 below 2^31.  One launch; it can be captured, the table, positions and counts are read
+ * when it runs.
+ */
+int santa_paged_append(const santa_shape *shape, const santa_paged *cache, const santa_rows *rows, int32_t T,
+                       const int32_t *pos, const int32_t *counts, const santa_rotation *rotation, const void *q,
+                       const int64_t q_stride[3], void *q_out, const int64_t q_out_stride[3], void *workspace,
+                       void *stream);
+
+/*
+ * santa_attend_workspace_size -- bytes of workspace that santa_attend_paged needs for this shape
+ * and T (n_max is not read).  Pure host computation.
+ */
+int santa_attend_workspace_size(const santa_shape *shape, int32_t T, size_t *bytes);
+
+/*
+ * santa_attend_paged -- exact causal attention of a chunk of new tokens, one (a decode step) to
+ * `T` a sequence, over a paged cache that holds their K and V already (santa_paged_append).
+ *
+ * Token t of sequence b, t < counts[b], has position P = pos[b] + t and sees key j when
+ *   j <= P  and  (window == 0  or  j > P - window  or  j < sinks)
+ * (with T = 1, what santa_decode_window sees with seq_lens = pos + 1).  Keys that a token does not
+ * see are not read into its result, whatever they hold (NaN too).  A visible key with a score of minus
+ * infinity weighs nothing; a token all of whose visible scores are has a NaN result, as with a
+ * score that is NaN or plus infinity.
+ *
+ *  q         device bf16 [B, T, H_q, d], 16-byte aligned; q_stride in elements for (batch, token,
+ *            head): multiples of 8, not negative, those of dimensions of size 1 are not read
+ *  T         tokens per batch row, 0..524288; 0 does nothing
+ *  pos       device int32 [B]: tokens in the cache before the chunk
+ *  counts    device int32 [B] or NULL: how many of the T tokens are live
+ *  window    >= 0; sinks >= 0 (ignored when window = 0); shape->scale >= 0
+ *  out       device bf16 [B, T, H_q, d], contiguous; rows t >= counts[b] stay as they were
+ *  workspace of santa_attend_workspace_size bytes, 256-byte aligned, initialised once
+ * A batch row with pos < 0, counts outside [0, T] or pos + counts > n_max is skipped
+ * (SANTA_DEV_BAD_POSITION).  Keys of a page outside [0, n_pages) count as zeros, K and V
+ * (SANTA_DEV_BAD_PAGE).  Scores and sums in fp32, weights rounded to bf16 (and summed as
+ * rounded), the result rounded once.  One launch; it can be captured.  Results do not depend on timing:
+ * the same call on the same device gives the same bits.
+ */
+int santa_attend_paged(const santa_shape *shape, const void *q, const int64_t q_stride[3], const santa_paged *cache,
+                       int32_t T, const int32_t *pos, const int32_t *counts, int32_t window, int32_t sinks, void *out,
+                       void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * santa_timeline_buffer -- for reading where a call's time goes: in a library built with

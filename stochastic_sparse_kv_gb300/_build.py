@@ -13,9 +13,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsanta.so")
-UNITS = ["santa_api.cu", "santa_window_api.cu", "santa_kernels_d128.cu", "santa_kernels_d64.cu"]
+UNITS = ["santa_api.cu", "santa_window_api.cu", "santa_paged_api.cu", "santa_kernels_d128.cu", "santa_kernels_d64.cu"]
 HEADERS = ["santa_common.cuh", "santa_sample.cuh", "santa_tcgen05.cuh", "santa_score.cuh", "santa_gather.cuh", "santa_dense.cuh",
-           "santa_cluster.cuh", "santa_kernels.h", "santa_host.h", "santa_kv4.cuh", "santa_window.cuh"]
+           "santa_cluster.cuh", "santa_kernels.h", "santa_host.h", "santa_kv4.cuh", "santa_window.cuh",
+           "santa_rope.cuh", "santa_attend.cuh"]
 # the timeline build: the same sources with %globaltimer stamps (santa_timeline_buffer)
 TIMELINE_LIB = os.path.join(HERE, "libsanta_timeline.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -33,6 +33,7 @@ enum : int { CTRL_ERR = 0, CTRL_WORK = 1, CTRL_EXIT = 2, CTRL_GROUPS = 64 };
 constexpr int DEV_BAD_SEQLEN = 1;
 constexpr int DEV_TIMEOUT = 2;
 constexpr int DEV_BAD_POSITION = 4;
+constexpr int DEV_BAD_PAGE = 8;
 // Limit of the end-of-kernel drains (MMAs still running, TMA fills not yet consumed):
 // never the caller's shorter limit, so that an aborted CTA frees TMEM and exits only
 // after its asynchronous work has completed.

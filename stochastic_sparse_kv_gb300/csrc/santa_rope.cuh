@@ -1,0 +1,134 @@
+// santa_rope.cuh -- rotary positions, and the rows of new tokens written into a paged cache,
+// sm_103a.
+//
+//   (x, y) -> A (x cos a - y sin a, x sin a + y cos a),  a = p f_i
+//
+// for the pairs i of a head's first `rot` features at position p.  f_i is held as turns a position
+// in units of 2^-64, so that p f_i modulo one turn is one 64-bit product modulo 2^64: exact, at any
+// position, with no fp64 (slow on this part) and no reduction of a large angle.  Its signed value
+// over 2^63 is the angle in half turns, in [-1, 1), rounded once to fp32.
+//
+// One kernel serves the rotation alone and a step's q, K and V together: the heads of a token are
+// those of q, then K, then V.  Bound by bytes, 4 a value.
+#pragma once
+
+#include "santa_common.cuh"
+
+namespace santa {
+
+constexpr int RP_NT = 256;
+constexpr int RP_VALUES = 16;             // features a thread moves of a row
+
+// Rows of one kind; strides in elements for (batch, token, head).
+struct RopeRows {
+    const uint16_t *src;
+    uint16_t *dst;
+    long long sb, st, sh;                 // of src
+    long long db, dt, dh;                 // of dst (rows; pages are addressed through the table)
+};
+
+struct RopeParams {
+    RopeRows q, k, v;
+    int H_q, H_kv;                        // heads of q, of K and of V (H_kv = 0: q alone)
+    int T, B, rot;                        // rot = 0: nothing is rotated
+    int groups;                           // threads that share a token's heads: each takes every groups-th
+    const uint64_t *turns;
+    float amplitude;
+    const int32_t *pos, *counts;          // counts NULL: T
+    int last;                             // largest pos + counts
+    const int32_t *table;                 // [B][cols]
+    int cols, n_pages, page_shift;
+    int32_t *ctrl;                        // device error word (or NULL)
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A thread's 16 features as two 16-byte accesses, and what it does with them.
+template <int D, bool PAIRS>
+__global__ void __launch_bounds__(RP_NT) santa_rope_kernel(const RopeParams p)
+{
+    constexpr int NU = D / RP_VALUES;
+    const int b = blockIdx.y;
+    const int idx = blockIdx.x * blockDim.x + threadIdx.x;
+    const int c = idx % NU, slot = idx / NU;
+    const int g = slot % p.groups, t = slot / p.groups;
+    const int first = p.pos[b], cnt = p.counts ? p.counts[b] : p.T;
+    if (first < 0 || cnt < 0 || cnt > p.T || first > p.last - cnt) {
+        if (p.ctrl && idx == 0) set_dev_error(p.ctrl, DEV_BAD_POSITION);
+        return;
+    }
+    if (t >= cnt) return;
+    const int at = first + t;
+    const bool turn = RP_VALUES * c < p.rot;
+    // where the two halves of this thread's features begin
+    const int f0 = PAIRS || !turn ? RP_VALUES * c : 8 * c;
+    const int f1 = PAIRS || !turn ? f0 + 8 : p.rot / 2 + 8 * c;
+    float cs[8], sn[8];
+    if (turn) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t a = (uint64_t)(uint32_t)at * p.turns[8 * c + i];
+            sincospif(__ll2float_rn((long long)a) * 0x1p-63f, &sn[i], &cs[i]);
+            cs[i] *= p.amplitude;
+            sn[i] *= p.amplitude;
+        }
+    }
+    // this token's row 0 of its page (head 0)
+    long long place = -1;
+    if (p.H_kv > 0) {
+        const int entry = p.table[(size_t)b * p.cols + (at >> p.page_shift)];
+        if ((unsigned)entry < (unsigned)p.n_pages)
+            place = (((long long)entry * p.H_kv << p.page_shift) + (at & ((1 << p.page_shift) - 1))) * D;
+        else if (p.ctrl && g == 0 && c == 0)
+            set_dev_error(p.ctrl, DEV_BAD_PAGE);
+    }
+    const int heads = p.H_q + 2 * p.H_kv;
+    for (int h = g; h < heads; h += p.groups) {
+        const uint16_t *src;
+        uint16_t *dst;
+        bool rotate = turn;
+        if (h < p.H_q) {
+            src = p.q.src + (b * p.q.sb + t * p.q.st + h * p.q.sh);
+            dst = p.q.dst + (b * p.q.db + t * p.q.dt + h * p.q.dh);
+        } else {
+            if (place < 0) break;
+            const bool value = h - p.H_q >= p.H_kv;
+            const RopeRows &r = value ? p.v : p.k;
+            const int hk = h - p.H_q - (value ? p.H_kv : 0);
+            src = r.src + (b * r.sb + t * r.st + hk * r.sh);
+            dst = r.dst + (place + ((long long)hk << p.page_shift) * D);
+            rotate = turn && !value;
+        }
+        // (a row of V is copied in the same two pieces)
+        uint4 u = *reinterpret_cast<const uint4 *>(src + f0), w = *reinterpret_cast<const uint4 *>(src + f1);
+        if (rotate) {
+            uint32_t a[4] = {u.x, u.y, u.z, u.w}, e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (PAIRS) {
+                    // words 0-3 hold pairs 0-3 of this thread, words 4-7 pairs 4-7
+                    const float x0 = bf16lo_to_f32(a[i]), y0 = bf16hi_to_f32(a[i]);
+                    const float x1 = bf16lo_to_f32(e[i]), y1 = bf16hi_to_f32(e[i]);
+                    a[i] = bf16x2(x0 * cs[i] - y0 * sn[i], x0 * sn[i] + y0 * cs[i]);
+                    e[i] = bf16x2(x1 * cs[4 + i] - y1 * sn[4 + i], x1 * sn[4 + i] + y1 * cs[4 + i]);
+                } else {
+                    const float x0 = bf16lo_to_f32(a[i]), x1 = bf16hi_to_f32(a[i]);
+                    const float y0 = bf16lo_to_f32(e[i]), y1 = bf16hi_to_f32(e[i]);
+                    a[i] = bf16x2(x0 * cs[2 * i] - y0 * sn[2 * i], x1 * cs[2 * i + 1] - y1 * sn[2 * i + 1]);
+                    e[i] = bf16x2(x0 * sn[2 * i] + y0 * cs[2 * i], x1 * sn[2 * i + 1] + y1 * cs[2 * i + 1]);
+                }
+            }
+            u = make_uint4(a[0], a[1], a[2], a[3]);
+            w = make_uint4(e[0], e[1], e[2], e[3]);
+        }
+        *reinterpret_cast<uint4 *>(dst + f0) = u;
+        *reinterpret_cast<uint4 *>(dst + f1) = w;
+    }
+}
+
+}  // namespace santa

@@ -23,14 +23,17 @@ GROUP_DEDUP = 0x100  # or-ed into a sampling mode: V rows loaded once per KV-hea
 OUT_BF16 = 0x200     # or-ed into any mode: out is bf16 (the fp32 result rounded once)
 BERNOULLI_QK = 0x400  # or-ed into any mode: score with each head's ternary query draw
 TWO_PASS = 0x800      # or-ed into a sampling mode: never the single-pass cluster kernel
-DEV_BAD_SEQLEN, DEV_TIMEOUT, DEV_BAD_POSITION = 1, 2, 4
+DEV_BAD_SEQLEN, DEV_TIMEOUT, DEV_BAD_POSITION, DEV_BAD_PAGE = 1, 2, 4, 8
+ROPE_LAYOUTS = {"halves": 0, "pairs": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 # every symbol include/santa.h declares
 EXPORTS = ("santa_workspace_size", "santa_workspace_init", "santa_decode", "santa_sample_points",
            "santa_device_status", "santa_status_string", "santa_version", "santa_decode_static",
            "santa_set_wait_limit", "santa_ternary_query", "santa_call_info", "santa_timeline_buffer",
            "santa_kv4_append", "santa_kv4_read", "santa_decode_kv4", "santa_decode_window",
-           "santa_window_workspace_size")
+           "santa_window_workspace_size", "santa_rope_turns", "santa_rope", "santa_paged_append",
+           "santa_attend_workspace_size", "santa_attend_paged")
 ERR_DEVICE = -6
 ERR_SCRATCH = -7
 STATIC_SCRATCH_BYTES = (16 << 20) + 65536
@@ -54,6 +57,21 @@ class _Kv4(ctypes.Structure):
 class _Rows(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
                 ("v_stride", ctypes.c_int64 * 3)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("amplitude", ctypes.c_float)]
+
+
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("scaling", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("original", ctypes.c_int32)]
+
+
+class _Paged(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -109,6 +127,15 @@ def load(path: str | None = None):
         lib.santa_decode_window.restype = ctypes.c_int
         lib.santa_window_workspace_size.argtypes = [shp, ctypes.POINTER(sz)]
         lib.santa_window_workspace_size.restype = ctypes.c_int
+        i64p, rtp, pgp = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(_Rotation), ctypes.POINTER(_Paged)
+        lib.santa_rope_turns.argtypes = [ctypes.POINTER(_RopeSpec), i32, ctypes.POINTER(u64), ctypes.POINTER(ctypes.c_float)]
+        lib.santa_rope.argtypes = [i32, i32, i32, i32, vp, i64p, vp, i64p, rtp, vp, vp, vp, vp]
+        lib.santa_paged_append.argtypes = [shp, pgp, rwp, i32, vp, vp, rtp, vp, i64p, vp, i64p, vp, vp]
+        lib.santa_attend_workspace_size.argtypes = [shp, i32, ctypes.POINTER(sz)]
+        lib.santa_attend_paged.argtypes = [shp, vp, i64p, pgp, i32, vp, vp, i32, i32, vp, vp, sz, vp]
+        for f in (lib.santa_rope_turns, lib.santa_rope, lib.santa_paged_append, lib.santa_attend_workspace_size,
+                  lib.santa_attend_paged):
+            f.restype = ctypes.c_int
         lib.santa_version.argtypes = []
         lib.santa_version.restype = ctypes.c_int
         _lib, _lib_path = lib, os.path.realpath(p)
@@ -535,3 +562,228 @@ def decode_kv4(q: torch.Tensor, cache: KV4Cache, seq_lens: torch.Tensor, window:
     _cuda_bf16(q, "q")
     return _window_call(q, _kv4_dims(cache), (_kv4_arg(cache),), load().santa_decode_kv4, "santa_decode_kv4", seq_lens,
                         window, sinks, scale, out, out_dtype, workspace, stream)
+
+
+# ------------------------------------------------------------------ rotary positions, paged cache
+
+class RopeTable(NamedTuple):
+    """Rotary frequencies: turns int64 [rot/2] on the device (the bits of unsigned numbers, turns a
+    position in units of 2^-64), the number of features they rotate, how those pair up ("halves":
+    (i, i + rot/2); "pairs": (2i, 2i + 1)), and a factor of the rotated features."""
+    turns: torch.Tensor
+    rot: int
+    layout: str = "halves"
+    amplitude: float = 1.0
+
+
+def rope_table(rot: int, base: float = 10000.0, layout: str = "halves", scaling: str = "none", factor: float = 1.0,
+               low: float = 1.0, high: float = 4.0, original: int = 8192, device="cuda") -> RopeTable:
+    """Frequencies base^(-2i/rot), scaled for long contexts: "linear", "base", "bands" or "ramp"
+    (santa_rope_spec in santa.h has the formulas; `low` and `high` are turns over the `original`
+    context).  rot: a multiple of 16 up to the head dimension."""
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"layout is one of {list(ROPE_LAYOUTS)}, scaling one of {list(ROPE_SCALINGS)}")
+    spec = _RopeSpec(base, ROPE_SCALINGS[scaling], factor, low, high, original)
+    turns, amplitude = (ctypes.c_uint64 * max(int(rot) // 2, 1))(), ctypes.c_float(0)
+    _check(load().santa_rope_turns(ctypes.byref(spec), int(rot), turns, ctypes.byref(amplitude)), "santa_rope_turns")
+    bits = torch.tensor([x - (1 << 64) if x >> 63 else x for x in turns], dtype=torch.int64)
+    return RopeTable(bits.to(device), int(rot), layout, float(amplitude.value))
+
+
+class PagedCache(NamedTuple):
+    """A bf16 cache in pages: k and v [n_pages, H_kv, page, d], table int32 [B, columns]; key j of
+    sequence b is row j % page of page table[b, j // page].  Contiguous, on one CUDA device."""
+    k: torch.Tensor
+    v: torch.Tensor
+    table: torch.Tensor
+
+
+def new_paged_cache(n_pages: int, H_kv: int, page: int, d: int, B: int, columns: int, device="cuda") -> PagedCache:
+    """An empty pool and a table whose entries name no page yet (-1)."""
+    k, v = (torch.zeros(n_pages, H_kv, page, d, dtype=torch.bfloat16, device=device) for _ in range(2))
+    return PagedCache(k, v, torch.full((B, columns), -1, dtype=torch.int32, device=device))
+
+
+def _rotation_arg(table: RopeTable, dev):
+    t = table.turns
+    if t.dtype != torch.int64 or t.device != dev or t.shape != (table.rot // 2,) or not t.is_contiguous():
+        raise ValueError("a rope table holds contiguous int64 turns [rot/2] on the inputs' device")
+    if table.layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout is one of {list(ROPE_LAYOUTS)}")
+    return ctypes.byref(_Rotation(t.data_ptr(), table.rot, ROPE_LAYOUTS[table.layout], table.amplitude))
+
+
+_strides = ctypes.c_int64 * 3
+
+
+def _row_tensor(t: torch.Tensor, name: str, shape, dev):
+    if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 4 or t.stride(3) != 1:
+        raise ValueError(f"{name} must be a bf16 tensor [B, T, H, d] on the inputs' device, contiguous in d")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    return t.data_ptr(), _strides(*t.stride()[:3])
+
+
+def _on_stream(stream, dev, call, made):
+    """call() with `stream` current; what it returns is the caller's to use on its own one (`made`)."""
+    caller = torch.cuda.current_stream(dev)
+    with _current(stream, dev):
+        got = call()
+    if made and got is not None:
+        got.record_stream(caller)
+    return got
+
+
+def _out_rows(x: torch.Tensor, counts) -> torch.Tensor:
+    """Rows for a result: those that no live token writes are zeros."""
+    return (torch.empty if counts is None else torch.zeros)(x.shape, dtype=torch.bfloat16, device=x.device)
+
+
+def rope(x: torch.Tensor, table: RopeTable, pos: torch.Tensor, counts: torch.Tensor | None = None,
+         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows x [B, T, H, d] (bf16, any strides that are multiples of 8) rotated to the positions
+    pos[b] + t (int32 [B]), for t < counts[b] (default T).  Into `out` (x itself: in place), whose
+    other rows stay as they were; without it into new rows, the others zero."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev = x.device
+    if stream is not None:
+        return _on_stream(stream, dev, lambda: rope(x, table, pos, counts, out, workspace), out is None)
+    x_ptr, x_st = _row_tensor(x, "x", None, dev)
+    B, T, H, d = x.shape
+    _int_vector(pos, "pos", B, dev)
+    if counts is not None:
+        _int_vector(counts, "counts", B, dev)
+    rotation = _rotation_arg(table, dev)
+    if out is None:
+        out = _out_rows(x, counts)
+    o_ptr, o_st = _row_tensor(out, "out", x.shape, dev)
+    if T == 0:
+        return out
+    with _on_device(dev):
+        rc = load().santa_rope(B, T, H, d, x_ptr, x_st, o_ptr, o_st, rotation, pos.data_ptr(),
+                               counts.data_ptr() if counts is not None else None,
+                               workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
+    if rc:
+        _check(rc, "santa_rope")
+    return out
+
+
+def _paged_dims(cache: PagedCache):
+    """(B, H_kv, n_max, d, page, device) of a checked cache."""
+    k, v, table = cache
+    dev = k.device
+    if k.dim() != 4 or v.shape != k.shape or not k.is_cuda:
+        raise ValueError("a paged cache holds CUDA tensors k and v [n_pages, H_kv, page, d]")
+    for t in (k, v):
+        if t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
+            raise ValueError("a paged cache holds contiguous bf16 tensors on one CUDA device")
+    if table.dtype != torch.int32 or table.device != dev or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("a paged cache's table is a contiguous int32 tensor [B, columns] on its device")
+    _, H_kv, page, d = k.shape
+    return table.shape[0], H_kv, table.shape[1] * page, d, page, dev
+
+
+def _paged_arg(cache: PagedCache):
+    k, v, table = cache
+    return ctypes.byref(_Paged(k.data_ptr(), v.data_ptr(), table.data_ptr(), k.shape[0], k.shape[2]))
+
+
+def paged_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, pos: torch.Tensor,
+                 counts: torch.Tensor | None = None, rope: RopeTable | None = None, q: torch.Tensor | None = None,
+                 q_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Write new rows [B, T, H_kv, d] (bf16, any strides that are multiples of 8) to positions
+    pos[b] + t of a paged cache, for t < counts[b] (default T), K rotated by `rope` if one is given.
+    With it, the same tokens' queries q [B, T, H_q, d] can be rotated in the same launch: into
+    q_out (q itself: in place) or into new rows, which are returned.  Batch rows that would leave
+    the table, and tokens without a page, are not written; give a `workspace` to have that reported
+    by device_status (DEV_BAD_POSITION, DEV_BAD_PAGE)."""
+    B, H_kv, n_max, d, _, dev = _paged_dims(cache)
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if q is not None and rope is None:
+        raise ValueError("q is rotated: give a rope table")
+    if stream is not None:
+        return _on_stream(stream, dev, lambda: paged_append(cache, k_new, v_new, pos, counts, rope, q, q_out, workspace),
+                          q_out is None)
+    T = k_new.shape[1] if k_new.dim() == 4 else -1
+    k_ptr, k_st = _row_tensor(k_new, "K rows", (B, T, H_kv, d), dev)
+    v_ptr, v_st = _row_tensor(v_new, "V rows", (B, T, H_kv, d), dev)
+    _int_vector(pos, "pos", B, dev)
+    if counts is not None:
+        _int_vector(counts, "counts", B, dev)
+    H_q, q_arg = H_kv, (None,) * 4
+    if q is not None:
+        H_q = q.shape[2] if q.dim() == 4 else 0
+        q_args = _row_tensor(q, "q", (B, T, H_q, d), dev)
+        if q_out is None:
+            q_out = _out_rows(q, counts)
+        q_arg = (*q_args, *_row_tensor(q_out, "q_out", q.shape, dev))
+    rotation = _rotation_arg(rope, dev) if rope is not None else None
+    if T == 0:
+        return q_out
+    shape = make_shape(B, H_q, H_kv, d, n_max)
+    with _on_device(dev):
+        rc = load().santa_paged_append(ctypes.byref(shape), _paged_arg(cache), ctypes.byref(_Rows(k_ptr, v_ptr, k_st, v_st)), T,
+                                       pos.data_ptr(), counts.data_ptr() if counts is not None else None, rotation, *q_arg,
+                                       workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
+    if rc:
+        _check(rc, "santa_paged_append")
+    return q_out
+
+
+_attend_shapes: dict = {}
+
+
+def _attend_shape_of(key):
+    """(the shape as a C argument, the workspace bytes of attend_paged), kept per shape and T."""
+    got = _attend_shapes.get(key)
+    if got is None:
+        shape, n = make_shape(*key[:-1]), ctypes.c_size_t(0)
+        _check(load().santa_attend_workspace_size(ctypes.byref(shape), key[-1], ctypes.byref(n)),
+               "santa_attend_workspace_size")
+        if len(_attend_shapes) >= 1024:
+            _attend_shapes.clear()
+        got = _attend_shapes[key] = (ctypes.byref(shape), int(n.value))
+    return got
+
+
+def attend_paged(q: torch.Tensor, cache: PagedCache, pos: torch.Tensor, counts: torch.Tensor | None = None, window: int = 0,
+                 sinks: int = 0, scale: float = 0.0, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Causal attention of T new tokens a sequence (1: a decode step) over a paged cache that holds
+    their K and V already.  q [B, T, H_q, d] (bf16, any strides that are multiples of 8); token t < counts[b]
+    (default T) sits at pos[b] + t (int32 [B]) and sees the keys up to its own, with window > 0 the
+    last `window` of them and the first `sinks`.  Returns bf16 [B, T, H_q, d]: `out`, whose other rows
+    stay as they were, or new rows, the others zero.  On an explicit `stream`, the call and all that it
+    allocates are that stream's: order its inputs and its result with the current stream as for any
+    work on another one."""
+    B, H_kv, n_max, d, _, dev = _paged_dims(cache)
+    if not (-1 << 31 <= window < 1 << 31 and -1 << 31 <= sinks < 1 << 31):
+        raise ValueError("window and sinks are 32-bit numbers")
+    if stream is not None:
+        return _on_stream(stream, dev, lambda: attend_paged(q, cache, pos, counts, window, sinks, scale, out, workspace),
+                          out is None)
+    q_ptr, q_st = _row_tensor(q, "q", None, dev)
+    if q.shape[0] != B or q.shape[3] != d:
+        raise ValueError("q [B, T, H_q, d] and the cache's shape disagree")
+    _int_vector(pos, "pos", B, dev)
+    if counts is not None:
+        _int_vector(counts, "counts", B, dev)
+    T = q.shape[1]
+    shape, nbytes = _attend_shape_of((B, q.shape[2], H_kv, d, n_max, scale, T))
+    if out is None:
+        out = _out_rows(q, counts)
+    elif out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != q.shape or out.device != dev:
+        raise ValueError("out must be a contiguous bf16 tensor [B, T, H_q, d] on q's device")
+    if T == 0:
+        return out
+    with _on_device(dev):
+        raw = _raw_stream(None, dev)
+        ws = workspace if workspace is not None else _own_workspace("attend", nbytes, dev, raw)
+        rc = load().santa_attend_paged(shape, q_ptr, q_st, _paged_arg(cache), T, pos.data_ptr(),
+                                       counts.data_ptr() if counts is not None else None, window, sinks, out.data_ptr(),
+                                       ws.data_ptr(), ws.numel(), raw)
+    if rc:
+        _check(rc, "santa_attend_paged")
+    return out
