@@ -300,6 +300,23 @@ int make_map_bf16(CUtensorMap *map, const void *base, int D, long long rows, int
     return r == CUDA_SUCCESS ? SANTA_OK : SANTA_ERR_CUDA;
 }
 
+int make_map_rows(CUtensorMap *map, const void *base, int D, int H, int T, int B, const int64_t stride[3], int heads, int tokens)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return SANTA_ERR_CUDA;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    // (the stride of a dimension of size 1 is not the caller's to get right)
+    const cuuint64_t row = (cuuint64_t)D * 2;
+    const cuuint64_t strides[3] = {H > 1 ? (cuuint64_t)stride[2] * 2 : row, T > 1 ? (cuuint64_t)stride[1] * 2 : row,
+                                   B > 1 ? (cuuint64_t)stride[0] * 2 : row};
+    const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)tokens, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SANTA_OK : SANTA_ERR_CUDA;
+}
+
 namespace {
 
 // The single-pass cluster kernel, when it applies: one cluster of C CTAs per (b, KV head),

@@ -4,64 +4,750 @@
 //   visible(j):  j <= P  and  (window == 0  or  j > P - window  or  j < sinks)
 //
 // for the token at position P.
+//
+// Rows and items.  The G query heads of a KV head and consecutive tokens share K and V: they are
+// the rows of one product, token by token, 128 to a tile (a row of the MMA, a lane of TMEM).  An
+// item is NQ tiles (NQ = 1 where the whole chunk is one) of one sequence and KV head, with the
+// tiles of 128 keys that any of its tokens sees.
+//
+// Shares.  The list of all items' key tiles, over sequences, row tiles and KV heads, is cut into
+// equal contiguous shares, one a CTA, one CTA an SM: any mix of prompts, decode steps, lengths and
+// windows fills the GPU, without a queue.  An item that spans CTAs leaves pieces (the running
+// maximum and sum, and the sum over V, of each row) in the workspace; the last CTA to arrive joins
+// them in the order of the list, so results do not depend on timing.
+//
+// Warps of a CTA:
+//  * a producer warp: the item's q rows by one tiled TMA copy (strides of any projection's slice),
+//    then K and V of each tile, page by page, a lane a page, into a ring of stages;
+//  * an MMA warp, one thread of which issues S = Q K^T (both from shared memory) and O += P V, P
+//    read from TMEM and V from shared memory as it lies (keys as rows: MN-major);
+//  * four softmax warps a row tile, a thread a row: scores from TMEM to registers, their maximum,
+//    p = 2^(k2 (s - m)), rounded to bf16 and written to TMEM over the scores; the sum l of the
+//    rounded values, so that a rounding moves numerator and denominator alike.  m is a score so
+//    far and moves only when one exceeds it by 2^AT_SLACK, so that O in TMEM is seldom rescaled.
+// With two row tiles one is in the tensor cores while the other is in its softmax; with one, the
+// next tile's scores are (two score buffers).
+//
+// Masks.  A tile that all the item's tokens see whole takes no mask.  In the others the scores of
+// hidden keys become minus infinity.  p is 0 there, but 0 times a NaN or an infinity in V is not:
+// in those tiles such values are set to zero in shared memory, and when one belongs to a key that
+// some token sees, the rows that see it get it added at the end.  That also covers what a page
+// holds behind the last key.
 #pragma once
 
-#include "santa_common.cuh"
+#include "santa_kv4.cuh"
+#include "santa_tcgen05.cuh"
 
 namespace santa {
 
+constexpr int AT_ROWS = 128;              // rows of a tile: (token, head) pairs
+constexpr int AT_KEYS = 128;              // keys of a tile
+constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
+constexpr int AT_SETUP = 2;               // what an item costs beside its tiles, in tiles
+constexpr int AT_MIN_SHARE = 4;           // a share's least size, in tiles
+constexpr float AT_SLACK = 8.f;           // log2 of the largest p
+constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
+constexpr int AT_MISC = 2048;             // of it for barriers and the like
+constexpr int AT_STAGES_MAX = 12;
+
+__host__ __device__ constexpr int at_threads(int NQ) { return NQ * 128 + 64; }
+__host__ __device__ constexpr int at_qbytes(int D, int NQ) { return NQ * AT_ROWS * D * 2; }
+__host__ __device__ constexpr int at_stage_bytes(int D) { return AT_KEYS * D * 2; }
+__host__ __device__ constexpr int at_stages(int D, int NQ)
+{
+    const int n = (AT_SMEM - 1024 - AT_MISC - at_qbytes(D, NQ)) / at_stage_bytes(D);
+    return n < AT_STAGES_MAX ? n : AT_STAGES_MAX;
+}
+__host__ __device__ constexpr int at_smem(int D, int NQ)
+{
+    return 1024 + at_qbytes(D, NQ) + at_stages(D, NQ) * at_stage_bytes(D) + AT_MISC;
+}
+
+// Row tiles of an item, and rows that a piece holds, by the rows T * G of a sequence and KV head.
+__host__ __device__ constexpr int at_nq(long long rows) { return rows > AT_ROWS ? 2 : 1; }
+__host__ __device__ constexpr int at_piece_rows(long long rows) { return rows > AT_ROWS ? 2 * AT_ROWS : (int)rows; }
+
 struct AttendParams {
-    const uint16_t *q;
-    long long q_sb, q_st, q_sh;   // elements, for (batch, token, head)
-    const uint16_t *k, *v;
+    const uint16_t *v;            // the pool (the slow path of values that are not finite)
     const int32_t *table, *pos, *counts;
     uint16_t *out;
     int32_t *ctrl;
-    int B, T, H_q, H_kv, G, n_max, cols, n_pages, page_shift;
-    int window, sinks;
+    float *part;                  // [cta][2][piece rows][D] sums over V
+    float *part_ml;               // [cta][2][piece rows][2] maximum, sum
+    int B, T, H_q, H_kv, lg_g, n_max, cols, n_pages, page_shift;
+    int window, sinks, piece_rows;
     float k2;                     // scale log2 e
     uint64_t wait_ns;
 };
 
-// One warp a (token, head): the plainest form.
-template <int D>
-__global__ void __launch_bounds__(128) santa_attend_kernel(const AttendParams p)
+struct AtSmem {
+    uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
+    uint64_t qfull, qempty;
+    uint64_t sfull[2], pfull[2];  // NQ = 2: of a row tile; NQ = 1: of a score buffer
+    uint64_t ofull[2], oempty[2], wg[2];
+    uint64_t drain;
+    long long sums[2 * 16];
+    long long total, start_base;
+    int start_pair, last;
+    uint32_t tmem;
+    int bad_v;                    // a value that is not finite was set to zero
+    int timeout;
+    int fills, fills_used;        // stages filled, and their fills seen by the MMA thread
+    int qfills, qfills_used;
+    int is_last[2];
+    int arrived[2][2];            // [slot][row tile]: arrivals of this CTA's pieces
+};
+static_assert(sizeof(AtSmem) <= AT_MISC, "barriers and the like");
+
+// A batch row's tokens; none where pos and counts leave the cache.
+__device__ __forceinline__ void at_row(const AttendParams &p, int b, int &first, int &cnt)
 {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (w >= (long long)p.T * p.H_q) return;
-    const int b = blockIdx.y, t = (int)(w / p.H_q), h = (int)(w % p.H_q);
-    const int first = p.pos[b], cnt = p.counts ? p.counts[b] : p.T;
+    first = p.pos[b];
+    cnt = p.counts ? p.counts[b] : p.T;
     if (first < 0 || cnt < 0 || cnt > p.T || first > p.n_max - cnt) {
-        if (w == 0 && lane == 0) set_dev_error(p.ctrl, DEV_BAD_POSITION);
-        return;
+        if (blockIdx.x == 0) set_dev_error(p.ctrl, DEV_BAD_POSITION);
+        cnt = 0;
     }
-    if (t >= cnt) return;
-    const int P = first + t;
-    float q[E], o[E], m = __int_as_float(0xff800000), l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        q[e] = bf16lo_to_f32(p.q[b * p.q_sb + t * p.q_st + h * p.q_sh + lane * E + e]);
-        o[e] = 0.f;
+}
+
+// The key tiles of row tile group qt of a batch row.
+struct AtItem {
+    int first, t0, t1;            // position of token 0; first and last live token
+    int lo;                       // least key in the window of any of the tokens
+    int nsink, tlo, L;            // tile i is i below nsink, else tlo + i - nsink
+    __device__ __forceinline__ int key(int i) const { return (i < nsink ? i : tlo + i - nsink) * AT_KEYS; }
+};
+
+template <int NQ>
+__device__ __forceinline__ int at_item(const AttendParams &p, int first, int cnt, int qt, AtItem &it)
+{
+    const int tpi = (NQ * AT_ROWS) >> p.lg_g;
+    it.L = 0;
+    it.first = first;
+    it.t0 = qt * tpi;
+    if (it.t0 >= cnt) return 0;
+    it.t1 = min(it.t0 + tpi, cnt) - 1;
+    const int kmax = first + it.t1;
+    it.lo = p.window > 0 ? max(0, first + it.t0 - p.window + 1) : 0;
+    it.tlo = it.lo / AT_KEYS;
+    it.nsink = (min(p.sinks, kmax + 1) + AT_KEYS - 1) / AT_KEYS;  // (p.sinks is 0 without a window)
+    if (it.nsink > 0 && it.nsink >= it.tlo) it.tlo = it.nsink = 0;
+    it.L = it.nsink + kmax / AT_KEYS - it.tlo + 1;
+    return it.L;
+}
+
+// The items of a share [f0, f1) of the list, one after another.
+template <int NQ>
+struct AtWalk {
+    long long f0, f1, base;
+    int b, qt, h, qts, first, cnt;
+    AtItem it;
+    int i0, i1;                   // this share's tiles of the item
+
+    __device__ __forceinline__ void begin(const AttendParams &p, long long f0_, long long f1_, long long base_, int pair)
+    {
+        f0 = f0_, f1 = f1_;
+        qts = (p.T + ((NQ * AT_ROWS) >> p.lg_g) - 1) / ((NQ * AT_ROWS) >> p.lg_g);
+        b = pair / qts, qt = pair % qts;
+        at_row(p, b, first, cnt);
+        const int cost = AT_SETUP + at_item<NQ>(p, first, cnt, qt, it);
+        h = (int)((f0 - base_) / cost);
+        base = base_ + (long long)h * cost;
     }
-    const int lo = p.window > 0 ? max(0, P - p.window + 1) : 0;
-    for (int j = p.sinks > 0 && lo > 0 ? 0 : lo; j <= P; ++j) {
-        if (j >= p.sinks && j < lo) j = lo;
-        const int page = p.table[(size_t)b * p.cols + (j >> p.page_shift)];
-        const bool good = (unsigned)page < (unsigned)p.n_pages;
-        if (!good && lane == 0) set_dev_error(p.ctrl, DEV_BAD_PAGE);
-        const long long row = ((((long long)(good ? page : 0) * p.H_kv + h / p.G) << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s += q[e] * (good ? bf16lo_to_f32(p.k[row + lane * E + e]) : 0.f);
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float mn = fmaxf(m, s), ref = mn == __int_as_float(0xff800000) ? 0.f : mn;
-        const float f = exp2f((m - ref) * p.k2), w1 = exp2f((s - ref) * p.k2);
-        m = mn;
-        l = l * f + w1;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + w1 * (good ? bf16lo_to_f32(p.v[row + lane * E + e]) : 0.f);
+    __device__ __forceinline__ void step(const AttendParams &p)
+    {
+        base += AT_SETUP + it.L;
+        if (++h < p.H_kv) return;
+        h = 0;
+        do {
+            if (++qt >= qts || qt * ((NQ * AT_ROWS) >> p.lg_g) >= cnt) {
+                qt = 0;
+                if (++b >= p.B) return;
+                at_row(p, b, first, cnt);
+            }
+        } while (at_item<NQ>(p, first, cnt, qt, it) == 0);
     }
-    for (int e = 0; e < E; ++e)
-        p.out[(((size_t)b * p.T + t) * p.H_q + h) * D + lane * E + e] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e] / l));
+    // Moves to the first item at or after this one of which the share holds a tile.
+    __device__ __forceinline__ bool seek(const AttendParams &p)
+    {
+        for (;; step(p)) {
+            if (base >= f1 || b >= p.B) return false;
+            const long long a = f0 - base - AT_SETUP, e = f1 - base - AT_SETUP;
+            i0 = (int)max(0ll, min(a, (long long)it.L));
+            i1 = (int)max(0ll, min(e, (long long)it.L));
+            if (i0 < i1) return true;
+        }
+    }
+    __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == it.L; }
+    __device__ __forceinline__ int live_rows(const AttendParams &p) const { return (it.t1 - it.t0 + 1) << p.lg_g; }
+    // whether all tokens of the item see all keys of tile i
+    __device__ __forceinline__ bool open(const AttendParams &p, int key) const
+    {
+        return key + AT_KEYS - 1 <= it.first + it.t0 &&
+               (p.window == 0 || key > it.first + it.t1 - p.window || key + AT_KEYS <= p.sinks);
+    }
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// (a, b) * (x, y)
+__device__ __forceinline__ void mul2(float &a, float &b, float x, float y)
+{
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(y));
+}
+
+__device__ __forceinline__ uint32_t at_bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Whether one of the bf16 halves of w is not finite; bit 15 and bit 31 say which.
+__device__ __forceinline__ uint32_t at_not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// bits 0 .. x-1
+__device__ __forceinline__ uint32_t at_low_bits(int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; }
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(at_threads(NQ), 1)
+    santa_attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v)
+{
+    constexpr int NT_ = at_threads(NQ);
+    constexpr int NW = NT_ / 32;
+    constexpr int NS = at_stages(D, NQ);
+    constexpr int SB = at_stage_bytes(D);
+    constexpr int PANELS = D / 64;
+    constexpr int PANEL = AT_KEYS * 128;       // bytes of 64 columns of a tile
+    constexpr int W_PROD = NQ * 4, W_MMA = W_PROD + 1;
+    constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_KEYS), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
+    constexpr uint32_t O_COL = 256;            // scores in columns 0-255, outputs behind them
+    constexpr uint32_t P_COL = 64;             // weights over the upper half of their scores
+    constexpr unsigned FULL = 0xffffffffu;
+    static_assert(NS >= 4, "ring");
+    const float NEG_INF = __int_as_float(0xff800000);
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t *qs = smem;
+    uint8_t *ring = smem + at_qbytes(D, NQ);
+    AtSmem &sh = *reinterpret_cast<AtSmem *>(ring + NS * SB);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // ---- the list's size, and where this CTA's share begins
+    const int tpi = (NQ * AT_ROWS) >> p.lg_g;
+    const int qts = (p.T + tpi - 1) / tpi;
+    const long long pairs = (long long)p.B * qts;
+    const long long per = (pairs + NT_ - 1) / NT_;
+    const long long x0 = min(pairs, per * tid), x1 = min(pairs, x0 + per);
+    long long mine = 0;
+    {
+        int b_at = -1, first = 0, cnt = 0;
+        for (long long x = x0; x < x1; ++x) {
+            const int b = (int)(x / qts), qt = (int)(x % qts);
+            if (b != b_at) at_row(p, b_at = b, first, cnt);
+            AtItem it;
+            const int L = at_item<NQ>(p, first, cnt, qt, it);
+            if (L) mine += (long long)p.H_kv * (AT_SETUP + L);
+        }
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(FULL, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) sh.sums[warp] = incl;
+    __syncthreads();
+    long long total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const long long s = sh.sums[w];
+        if (w < warp) before += s;
+        total += s;
+    }
+    const long long ctas = max(1ll, min((long long)gridDim.x, total / AT_MIN_SHARE));
+    const long long cta = blockIdx.x;
+    if (total == 0 || cta >= ctas) return;
+    const long long f0 = total * cta / ctas, f1 = total * (cta + 1) / ctas;
+    if (before <= f0 && f0 < before + mine) {
+        int b_at = -1, first = 0, cnt = 0;
+        for (long long x = x0; x < x1; ++x) {
+            const int b = (int)(x / qts), qt = (int)(x % qts);
+            if (b != b_at) at_row(p, b_at = b, first, cnt);
+            AtItem it;
+            const int L = at_item<NQ>(p, first, cnt, qt, it);
+            const long long cost = L ? (long long)p.H_kv * (AT_SETUP + L) : 0;
+            if (f0 < before + cost) {
+                sh.start_pair = (int)x;
+                sh.start_base = before;
+                break;
+            }
+            before += cost;
+        }
+    }
+    // the CTA whose share holds unit x of the list
+    auto owner = [&](long long x) { return (int)(((x + 1) * ctas - 1) / total); };
+
+    // ---- setup: TMEM, barriers
+    if (warp == W_MMA) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == W_PROD && lane == 0) {
+        tma_prefetch_map(&tm_q);
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_v);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        mbar_init(&sh.qfull, 1);
+        mbar_init(&sh.qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.sfull[i], 1);
+            mbar_init(&sh.pfull[i], 4);
+            mbar_init(&sh.ofull[i], 1);
+            mbar_init(&sh.oempty[i], 4);
+            mbar_init(&sh.wg[i], 4);
+            for (int j = 0; j < 2; ++j) sh.arrived[i][j] = 0;
+        }
+        mbar_init(&sh.drain, 1);
+        mbar_fence_init();
+        sh.bad_v = sh.timeout = 0;
+        sh.fills = sh.fills_used = sh.qfills = sh.qfills_used = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = sh.tmem;
+    AtWalk<NQ> w;
+    w.begin(p, f0, f1, sh.start_base, sh.start_pair);
+    auto failed = [&]() {
+        set_dev_error(p.ctrl, DEV_TIMEOUT);
+        sh.timeout = 1;
+    };
+
+    if (warp == W_PROD) {
+        // ================= producer
+        const int page = 1 << p.page_shift, box = min(page, AT_KEYS);
+        const int rows_all = (p.n_pages * p.H_kv) << p.page_shift;   // (below 2^31) beyond the pool: zeros
+        int n = 0, items = 0, stage = 0, phase = 1;
+        bool ok = true;
+        for (; ok && w.seek(p); w.step(p), ++items) {
+            const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
+            if (items > 0 && !__all_sync(FULL, mbar_wait_bounded(&sh.qempty, (items - 1) & 1, p.wait_ns))) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                mbar_arrive_tx(&sh.qfull, (uint32_t)(nq * AT_ROWS * D * 2));
+                for (int i = 0; i < nq; ++i)
+                    for (int c = 0; c < PANELS; ++c)
+                        tma_load_4d(qs + (i * PANELS + c) * (AT_ROWS * 128), &tm_q, c * 64, w.h << p.lg_g,
+                                    w.it.t0 + i * (AT_ROWS >> p.lg_g), w.b, &sh.qfull);
+                sh.qfills = items + 1;
+            }
+            const int kmax = w.it.first + w.it.t1;
+            for (int i = w.i0; ok && i < w.i1; ++i, ++n) {
+                const int key = w.it.key(i);
+                const int boxes = (min(AT_KEYS, kmax + 1 - key) + box - 1) / box;
+                // a lane a (page, panel) box
+                const int bi = lane / PANELS, c = lane % PANELS;
+                int row = 0;
+                if (bi < boxes) {
+                    const int j = key + bi * box;
+                    const int entry = p.table[(size_t)w.b * p.cols + (j >> p.page_shift)];
+                    if ((unsigned)entry < (unsigned)p.n_pages) {
+                        row = ((entry * p.H_kv + w.h) << p.page_shift) + (j & (page - 1));
+                    } else {
+                        row = rows_all;
+                        set_dev_error(p.ctrl, DEV_BAD_PAGE);
+                    }
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!__all_sync(FULL, mbar_wait_bounded(&sh.empty[stage], phase, p.wait_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_tx(&sh.full[stage], (uint32_t)(boxes * box * D * 2));
+                        sh.fills = 2 * n + kv + 1;
+                    }
+                    __syncwarp();
+                    if (bi < boxes)
+                        tma_load_2d_plain(ring + stage * SB + c * PANEL + bi * box * 128, kv ? &tm_v : &tm_k, c * 64, row,
+                                          &sh.full[stage]);
+                    if (++stage == NS) stage = 0, phase ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) failed();
+        __syncwarp();
+    } else if (warp == W_MMA) {
+        // ================= MMA issuer: one thread
+        if (lane == 0) {
+            int n = 0, items = 0;
+            int nt[2] = {0, 0};       // tiles of each row tile so far
+            int no[2] = {0, 0};       // its items so far
+            const uint32_t qaddr = smem_u32(qs);
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (ok && !mbar_wait_bounded(bar, parity, p.wait_ns)) ok = false;
+                return ok;
+            };
+            // fill f of the ring (K of tile n: 2n, V: 2n + 1) has landed
+            auto landed = [&](int f) {
+                if (wait(&sh.full[f % NS], (f / NS) & 1) && sh.fills_used < f + 1) sh.fills_used = f + 1;
+                return ok;
+            };
+            auto scores = [&](int q, int f, int buf) {
+                const uint32_t k = smem_u32(ring + (f % NS) * SB), a = qaddr + q * AT_ROWS * D * 2;
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    tc_mma_bf16(tbase + buf * AT_KEYS, umma_desc_sw128(a + (x / 4) * (AT_ROWS * 128) + (x % 4) * 32),
+                                umma_desc_sw128(k + (x / 4) * PANEL + (x % 4) * 32), ID_S, x != 0);
+                tc_commit(&sh.sfull[buf]);
+            };
+            for (; ok && w.seek(p); w.step(p), ++items) {
+                const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
+                const int L = w.i1 - w.i0;
+                if (!wait(&sh.qfull, items & 1)) break;
+                sh.qfills_used = items + 1;
+                if (!landed(2 * n)) break;
+                tc_fence_after();
+                for (int q = 0; q < nq; ++q) scores(q, 2 * n, NQ == 2 ? q : nt[0] & 1);
+                tc_commit(&sh.empty[(2 * n) % NS]);
+                if (L == 1) tc_commit(&sh.qempty);
+                for (int j = 0; ok && j < L; ++j, ++n) {
+                    const bool more = j + 1 < L;
+                    if (NQ == 1 && more) {
+                        if (!landed(2 * n + 2)) break;
+                        scores(0, 2 * n + 2, (nt[0] + 1) & 1);
+                        tc_commit(&sh.empty[(2 * n + 2) % NS]);
+                        if (j + 2 == L) tc_commit(&sh.qempty);
+                    }
+                    for (int q = 0; ok && q < nq; ++q) {
+                        const int buf = NQ == 2 ? q : nt[0] & 1;
+                        if (!wait(&sh.pfull[buf], (NQ == 2 ? nt[q] : nt[0] >> 1) & 1)) break;
+                        if (q == 0 && !landed(2 * n + 1)) break;
+                        if (j == 0 && no[q] > 0 && !wait(&sh.oempty[q], (no[q] - 1) & 1)) break;
+                        tc_fence_after();
+                        const uint32_t v = smem_u32(ring + ((2 * n + 1) % NS) * SB);
+#pragma unroll
+                        for (int x = 0; x < AT_KEYS / 16; ++x)
+                            tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, umma_desc_sw128_mn(v + x * 2048, PANEL),
+                                           ID_O, j != 0 || x != 0);
+                        tc_commit(&sh.ofull[q]);
+                        ++nt[q];
+                        if (j == 0) ++no[q];
+                        if (NQ == 2 && more) {
+                            if (q == 0 && !landed(2 * n + 2)) break;
+                            tc_fence_after();
+                            scores(q, 2 * n + 2, q);
+                        }
+                        if (q == nq - 1) {
+                            tc_commit(&sh.empty[(2 * n + 1) % NS]);
+                            if (NQ == 2 && more) {
+                                tc_commit(&sh.empty[(2 * n + 2) % NS]);
+                                if (j + 2 == L) tc_commit(&sh.qempty);
+                            }
+                        }
+                    }
+                }
+            }
+            if (!ok) failed();
+            tc_commit(&sh.drain);
+            mbar_wait_bounded(&sh.drain, 0u, DRAIN_NS);
+        }
+        __syncwarp();
+    } else if (warp < W_PROD) {
+        // ================= softmax of row tile q: thread = row = TMEM lane
+        const int q = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t t_o = tbase + lanes + O_COL + q * D;
+        int n = 0, n0 = 0;            // tiles of this row tile so far, and of the CTA
+        uint32_t wg_phase = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok) ok = __all_sync(FULL, mbar_wait_bounded(bar, parity, p.wait_ns));
+            return ok;
+        };
+        // rendezvous of the four warps (a bounded wait, unlike bar.sync)
+        auto wg_sync = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.wg[q]);
+            wait(&sh.wg[q], wg_phase);
+            wg_phase ^= 1u;
+            return ok;
+        };
+        for (; ok && w.seek(p); n0 += w.i1 - w.i0, w.step(p)) {
+            const int live = w.live_rows(p) - q * AT_ROWS;   // of this row tile
+            if (live <= 0) continue;
+            const bool warp_live = 32 * (warp & 3) < live;
+            const int t = w.it.t0 + ((q * AT_ROWS + row) >> p.lg_g);
+            const int P = w.it.first + t;
+            const int lo = p.window > 0 ? P - p.window + 1 : 0;
+            const int kmax = w.it.first + w.it.t1;
+            float m = NEG_INF, l = 0.f;
+            int i = w.i0;
+            for (; i < w.i1; ++i, ++n) {
+                const int buf = NQ == 2 ? q : n & 1;
+                const uint32_t t_s = tbase + lanes + buf * AT_KEYS;
+                const int key = w.it.key(i);
+                const bool open = w.open(p, key);
+                if (!wait(&sh.sfull[buf], (NQ == 2 ? n : n >> 1) & 1)) break;
+                if (!open && q == 0) {
+                    // values of V that are not finite become zeros
+                    const int f = 2 * (n0 + i - w.i0) + 1;
+                    if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
+                    uint8_t *v = ring + (f % NS) * SB;
+#pragma unroll 4
+                    for (int c = tid; c < SB / 16; c += 128) {
+                        uint4 x = reinterpret_cast<uint4 *>(v)[c];
+                        const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
+                        if (b0 | b1 | b2 | b3) {
+                            x.x &= ~((b0 >> 15) * 0xffffu);
+                            x.y &= ~((b1 >> 15) * 0xffffu);
+                            x.z &= ~((b2 >> 15) * 0xffffu);
+                            x.w &= ~((b3 >> 15) * 0xffffu);
+                            reinterpret_cast<uint4 *>(v)[c] = x;
+                            const int j = key + (c % (PANEL / 16)) / 8;
+                            if (j <= kmax && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (warp_live) {
+                    tc_fence_after();
+                    // the upper half of the scores stays in registers from here to its weights, the lower
+                    // half is read again: 128 of them, beside all else, would not fit 168 registers
+                    uint32_t lo_s[64], hi_s[64];
+                    tmem_ld32_start(t_s, lo_s);
+                    tmem_ld32_start(t_s + 32, lo_s + 32);
+                    tmem_ld_wait();
+                    tmem_ready<64>(lo_s);
+                    tmem_ld32_start(t_s + 64, hi_s);
+                    tmem_ld32_start(t_s + 96, hi_s + 32);
+                    const int ub = P + 1 - key, lb = lo - key, sk = p.sinks - key;
+                    auto hide = [&](uint32_t *s, int c0) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 32) {
+                            const int at = c0 + c;
+                            const uint32_t seen = at_low_bits(ub - at) & (~at_low_bits(lb - at) | at_low_bits(sk - at));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
+                        }
+                    };
+                    float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+                    auto most = [&](const uint32_t *s) {
+#pragma unroll
+                        for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1])));
+                    };
+                    if (!open) hide(lo_s, 0);
+                    most(lo_s);
+                    tmem_ld_wait();
+                    tmem_ready<64>(hi_s);
+                    if (!open) hide(hi_s, 64);
+                    most(hi_s);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
+                    if (__any_sync(FULL, grow)) {
+                        const float f = grow ? (m == NEG_INF ? 0.f : ex2((m - top) * p.k2)) : 1.f;
+                        if (grow) m = top;
+                        l *= f;
+                        if (i > w.i0) {
+                            if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32_start(t_o + 32 * c, o);
+                                tmem_ld_wait();
+                                tmem_ready<32>(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(t_o + 32 * c, o);
+                            }
+                        }
+                    }
+                    const float ref = m == NEG_INF ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    auto weigh = [&](uint32_t *s, int c0) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float a = __uint_as_float(s[32 * c + 2 * e]), b = __uint_as_float(s[32 * c + 2 * e + 1]);
+                                add2(a, b, -ref, -ref);
+                                mul2(a, b, p.k2, p.k2);
+                                pk[e] = at_bf16x2(ex2(a), ex2(b));
+                                add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], bf16lo_to_f32(pk[e]), bf16hi_to_f32(pk[e]));
+                            }
+                            tmem_st16(t_s + P_COL + (c0 + 32 * c) / 2, pk);
+                        }
+                    };
+                    weigh(hi_s, 64);
+                    tmem_ld32_start(t_s, lo_s);
+                    tmem_ld32_start(t_s + 32, lo_s + 32);
+                    tmem_ld_wait();
+                    tmem_ready<64>(lo_s);
+                    if (!open) hide(lo_s, 0);
+                    weigh(lo_s, 0);
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.pfull[buf]);
+            }
+            if (!ok) break;
+            // (a parity tells only two phases apart.  The last scores follow the product of two tiles
+            // before with two buffers, of the tile before with one: the phase between is waited for)
+            if (NQ == 1 && n > 1 && !wait(&sh.ofull[q], (n - 2) & 1)) break;
+            if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
+            tc_fence_after();
+
+            // ---- the item's (or the piece's) sums
+            const bool whole = w.whole(), mine_live = row < live;
+            const bool fix = *reinterpret_cast<volatile int *>(&sh.bad_v) != 0;
+            const int slot = w.i0 > 0 ? 0 : 1;
+            const float inv = whole ? 1.f / l : 1.f;
+            float *piece = p.part + ((size_t)(blockIdx.x * 2 + slot) * p.piece_rows + q * AT_ROWS + row) * D;
+            uint16_t *out = p.out + (((size_t)w.b * p.T + t) * p.H_q + (w.h << p.lg_g) + ((q * AT_ROWS + row) & ((1 << p.lg_g) - 1))) * D;
+            if (warp_live) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32_start(t_o + 32 * c, o);
+                    tmem_ld_wait();
+                    tmem_ready<32>(o);
+                    if (fix && mine_live) {
+                        // values that are not finite, of the keys that this row sees
+                        for (int x = w.i0; x < w.i1; ++x) {
+                            const int key = w.it.key(x);
+                            if (w.open(p, key)) continue;
+                            for (int j = key; j < key + AT_KEYS && j <= P; ++j) {
+                                if (j < lo && j >= p.sinks) continue;
+                                const int entry = p.table[(size_t)w.b * p.cols + (j >> p.page_shift)];
+                                if ((unsigned)entry >= (unsigned)p.n_pages) continue;
+                                const uint32_t *v = reinterpret_cast<const uint32_t *>(
+                                    p.v + ((((long long)entry * p.H_kv + w.h) << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D + 32 * c);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const uint32_t u = v[e], bad = at_not_finite(u);
+                                    if (bad & 0x8000u) o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + bf16lo_to_f32(u));
+                                    if (bad >> 31) o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + bf16hi_to_f32(u));
+                                }
+                            }
+                        }
+                    }
+                    if (!mine_live) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 x;
+                            x.x = at_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                            x.y = at_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                            x.z = at_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                            x.w = at_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                            *reinterpret_cast<uint4 *>(out + 32 * c + e) = x;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            __stcg(reinterpret_cast<uint4 *>(piece + 32 * c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.oempty[q]);
+            if (whole) continue;
+
+            // ---- a piece: the last CTA of the item to arrive joins them all
+            if (mine_live)
+                __stcg(reinterpret_cast<float2 *>(p.part_ml + ((size_t)(blockIdx.x * 2 + slot) * p.piece_rows + q * AT_ROWS + row) * 2),
+                       make_float2(m, l));
+            __threadfence();
+            if (!wg_sync()) break;
+            const int c0 = owner(w.base + AT_SETUP), c1 = owner(w.base + AT_SETUP + w.it.L - 1);
+            if (row == 0) {
+                int32_t *arrivals = p.ctrl + CTRL_GROUPS + 2 * c0 + q;
+                sh.arrived[slot][q] = 1;
+                const bool last = atomicAdd(arrivals, 1) == c1 - c0;
+                if (last) *arrivals = 0;
+                sh.is_last[q] = last;
+                __threadfence();
+            }
+            if (!wg_sync()) break;
+            if (!sh.is_last[q]) continue;
+            __threadfence();
+            const int rows_live = min(live, AT_ROWS);
+            auto at = [&](int c, int r) { return (size_t)(c * 2 + (c == c0 ? 1 : 0)) * p.piece_rows + q * AT_ROWS + r; };
+            for (int x = row; x < rows_live * (D / 4); x += 128) {
+                const int r = x / (D / 4), e = x % (D / 4);
+                float M = NEG_INF;
+                for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + at(c, r) * 2));
+                float sl = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+#pragma unroll 4
+                for (int c = c0; c <= c1; ++c) {
+                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c, r) * 2));
+                    const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c, r) * D) + e);
+                    const float f = ml.x == NEG_INF ? 0.f : ex2((ml.x - M) * p.k2);
+                    sl = fmaf(f, ml.y, sl);
+                    o0 = fmaf(f, o.x, o0), o1 = fmaf(f, o.y, o1), o2 = fmaf(f, o.z, o2), o3 = fmaf(f, o.w, o3);
+                }
+                const float inv = 1.f / sl;
+                const int R = q * AT_ROWS + r;
+                uint16_t *dst = p.out + (((size_t)w.b * p.T + w.it.t0 + (R >> p.lg_g)) * p.H_q + (w.h << p.lg_g) + (R & ((1 << p.lg_g) - 1))) * D;
+                *reinterpret_cast<uint2 *>(dst + 4 * e) = make_uint2(at_bf16x2(o0 * inv, o1 * inv), at_bf16x2(o2 * inv, o3 * inv));
+            }
+        }
+        if (!ok && lane == 0) failed();
+        __syncwarp();
+    }
+
+    // ---- teardown: every MMA has completed (drained above); release TMEM.  After a timeout, copies
+    // that were not waited for get a bounded wait to land, and pieces that did not arrive do, so that
+    // the counters are zero again after the last CTA.
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+    if (warp == W_PROD && lane == 0 && sh.timeout) {
+        for (int f = sh.fills_used; f < sh.fills; ++f)
+            if (!mbar_wait_bounded(&sh.full[f % NS], (f / NS) & 1, DRAIN_NS)) break;
+        if (sh.qfills_used < sh.qfills) mbar_wait_bounded(&sh.qfull, (sh.qfills - 1) & 1, DRAIN_NS);
+        AtWalk<NQ> a;
+        a.begin(p, f0, f1, sh.start_base, sh.start_pair);
+        for (; a.seek(p); a.step(p)) {
+            if (a.whole()) continue;
+            const int c0 = owner(a.base + AT_SETUP), c1 = owner(a.base + AT_SETUP + a.it.L - 1);
+            for (int q = 0; q < NQ && a.live_rows(p) > q * AT_ROWS; ++q) {
+                int32_t *arrivals = p.ctrl + CTRL_GROUPS + 2 * c0 + q;
+                if (!sh.arrived[a.i0 > 0 ? 0 : 1][q] && atomicAdd(arrivals, 1) == c1 - c0) *arrivals = 0;
+            }
+        }
+    }
 }
 
 }  // namespace santa

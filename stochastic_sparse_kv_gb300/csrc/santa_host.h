@@ -28,4 +28,8 @@ uint64_t wait_limit_ns();
 // Row-major bf16 matrix [rows][D] as a 2-D tensor map: boxes of 64 columns x box_rows rows.
 int make_map_bf16(CUtensorMap *map, const void *base, int D, long long rows, int box_rows);
 
+// bf16 rows [B][T][H][D] with strides in elements for (batch, token, head) as a 4-D tensor map:
+// boxes of 64 columns x heads x tokens of one batch row.
+int make_map_rows(CUtensorMap *map, const void *base, int D, int H, int T, int B, const int64_t stride[3], int heads, int tokens);
+
 }  // namespace santa

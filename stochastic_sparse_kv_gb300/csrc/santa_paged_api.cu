@@ -207,7 +207,8 @@ int santa_attend_workspace_size(const santa_shape *shape, int32_t T, size_t *byt
     if (rc) return rc;
     if (!bytes || T < 0) return SANTA_ERR_INVALID_ARG;
     if (shape->B > BMAX || T > NMAX_LIMIT) return SANTA_ERR_UNSUPPORTED;
-    *bytes = CTRL_BYTES;
+    const size_t rows = (size_t)at_piece_rows((long long)T * (shape->H_q / shape->H_kv));
+    *bytes = align_up(CTRL_BYTES + (size_t)AT_MAX_CTAS * 2 * rows * (shape->d + 2) * sizeof(float), 256);
     return SANTA_OK;
 }
 
@@ -223,33 +224,60 @@ int santa_attend_paged(const santa_shape *shape, const void *q, const int64_t q_
     size_t need = 0;
     if ((rc = santa_attend_workspace_size(shape, T, &need)) || (rc = check_strides(q_stride, shape->B, T, shape->H_q, shape->d, false)))
         return rc;
+    // (a tensor copy's strides are below 2^40 bytes)
+    const long long dims[3] = {shape->B, T, shape->H_q};
+    for (int i = 0; i < 3; ++i)
+        if (dims[i] > 1 && q_stride[i] >= (1ll << 39)) return SANTA_ERR_INVALID_ARG;
     const double k2 = (shape->scale != 0.f ? (double)shape->scale : 1.0 / std::sqrt((double)shape->d)) * 1.4426950408889634;
     if (!std::isfinite((float)k2)) return SANTA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < need) return SANTA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SANTA_ERR_MISALIGNED;
     if (T == 0) return SANTA_OK;
     AttendParams p{};
-    p.q = static_cast<const uint16_t *>(q);
-    p.q_sb = q_stride[0], p.q_st = q_stride[1], p.q_sh = q_stride[2];
-    p.k = static_cast<const uint16_t *>(cache->k);
     p.v = static_cast<const uint16_t *>(cache->v);
     p.table = cache->table;
     p.pos = pos, p.counts = counts;
     p.out = static_cast<uint16_t *>(out);
-    p.ctrl = static_cast<int32_t *>(workspace);
-    p.B = shape->B, p.T = T, p.H_q = shape->H_q, p.H_kv = shape->H_kv, p.G = shape->H_q / shape->H_kv;
+    const int D = shape->d, G = shape->H_q / shape->H_kv, NQ = at_nq((long long)T * G);
+    p.B = shape->B, p.T = T, p.H_q = shape->H_q, p.H_kv = shape->H_kv, p.lg_g = log2_of(G);
     p.n_max = shape->n_max;
     p.cols = shape->n_max / cache->page;
     p.n_pages = cache->n_pages;
     p.page_shift = log2_of(cache->page);
     p.window = std::min(window, shape->n_max);  // (larger ones see no more; no sum below overflows)
     p.sinks = p.window > 0 ? std::min(sinks, shape->n_max) : 0;
+    p.piece_rows = at_piece_rows((long long)T * G);
     p.k2 = (float)k2;
     p.wait_ns = wait_limit_ns();
-    const dim3 grid((unsigned)(((long long)T * p.H_q + 3) / 4), (unsigned)p.B);
-    void *args[] = {&p};
-    const void *fn = shape->d == 128 ? (const void *)santa_attend_kernel<128> : (const void *)santa_attend_kernel<64>;
-    return cudaLaunchKernel(fn, grid, dim3(128), args, 0, (cudaStream_t)stream) == cudaSuccess ? SANTA_OK : SANTA_ERR_CUDA;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.ctrl = reinterpret_cast<int32_t *>(ws);
+    p.part = reinterpret_cast<float *>(ws + CTRL_BYTES);
+    p.part_ml = p.part + (size_t)AT_MAX_CTAS * 2 * p.piece_rows * D;
+
+    int dev, sms, optin, occ = 0;
+    if ((rc = device_info(&dev, &sms, &optin))) return rc;
+    const void *fn = D == 128 ? (NQ == 2 ? (const void *)santa_attend_kernel<128, 2> : (const void *)santa_attend_kernel<128, 1>)
+                              : (NQ == 2 ? (const void *)santa_attend_kernel<64, 2> : (const void *)santa_attend_kernel<64, 1>);
+    const int smem = at_smem(D, NQ);
+    if (smem > optin) return SANTA_ERR_UNSUPPORTED;
+    if ((rc = prepare_fn(fn, dev, smem, at_threads(NQ), &occ))) return rc;
+    // no more shares than the longest sequences would give
+    const long long qts = ((long long)T * G + NQ * AT_ROWS - 1) / (NQ * AT_ROWS);
+    const long long most = p.window > 0 ? std::min<long long>(p.n_max, (long long)p.window + p.sinks + (NQ * AT_ROWS) / G) : p.n_max;
+    const long long units = (most + AT_KEYS - 1) / AT_KEYS + 2 + AT_SETUP;
+    const long long want = (units * shape->B * shape->H_kv * qts + AT_MIN_SHARE - 1) / AT_MIN_SHARE;
+    const long long grid = std::min<long long>(std::min(sms, AT_MAX_CTAS), want);
+    CUtensorMap tm_q, tm_k, tm_v;
+    const long long rows = (long long)cache->n_pages * shape->H_kv * cache->page;
+    const int box = std::min<int>(cache->page, AT_KEYS);
+    if ((rc = make_map_rows(&tm_q, q, D, shape->H_q, T, shape->B, q_stride, G, AT_ROWS / G)) ||
+        (rc = make_map_bf16(&tm_k, cache->k, D, rows, box)) || (rc = make_map_bf16(&tm_v, cache->v, D, rows, box)))
+        return rc;
+    void *args[] = {&p, &tm_q, &tm_k, &tm_v};
+    return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)at_threads(NQ)), args, (size_t)smem, (cudaStream_t)stream) ==
+                   cudaSuccess
+               ? SANTA_OK
+               : SANTA_ERR_CUDA;
 }
 
 }  // extern "C"

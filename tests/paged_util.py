@@ -83,9 +83,8 @@ def attention(q, k, v, table, pos, counts=None, window=0, sinks=0, scale=0.0):
                 w /= w.sum(-1, keepdims=True)
                 o = np.einsum("hgn,hnd->hgd", w, vb[:, j])
                 out[b, t] = o.reshape(H_q, d)
-                if np.isfinite(o).all():
-                    spread[b, t] = np.stack([np.einsum("gn,ngd->gd", w[h], np.abs(vb[h, j][:, None] - o[h][None]))
-                                             for h in range(H_kv)]).reshape(H_q, d)
+                spread[b, t] = np.stack([np.einsum("gn,ngd->gd", w[h], np.abs(vb[h, j][:, None] - o[h][None]))
+                                         for h in range(H_kv)]).reshape(H_q, d)
     return out, spread
 
 
@@ -94,7 +93,7 @@ def attention(q, k, v, table, pos, counts=None, window=0, sinks=0, scale=0.0):
 # (v_j - o) / (1 + sum p_j e_j).  Scores are fp32 sums of d products, off by d steps of 2^-24 of
 # their size at most, exponentials by 2^-21: together 2^-10 of a weight for scores up to 2^6.
 def tolerance(out, spread):
-    return 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2.0 ** -10) * 1.01 * spread + 2.0 ** -22 * np.abs(out).max(initial=0.0)
+    return 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2.0 ** -10) * 1.01 * spread + 2.0 ** -22 * np.nanmax(np.abs(out), initial=0.0)
 
 
 def pages(gen, lengths, page, columns, spare=2):
