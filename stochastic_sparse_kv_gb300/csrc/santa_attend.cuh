@@ -83,7 +83,7 @@ struct AttendParams {
 struct AtSmem {
     uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
     uint64_t qfull, qempty;
-    uint64_t sfull[2], pfull[2];  // NQ = 2: of a row tile; NQ = 1: of a score buffer
+    uint64_t sfull[2], phalf[2], pfull[2];  // NQ = 2: of a row tile; NQ = 1: of a score buffer
     uint64_t ofull[2], oempty[2], wg[2];
     uint64_t drain;
     long long sums[2 * 16];
@@ -195,20 +195,26 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
-// (a, b) * (x, y)
-__device__ __forceinline__ void mul2(float &a, float &b, float x, float y)
-{
-    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
-        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
-        : "+f"(a), "+f"(b)
-        : "f"(x), "f"(y));
-}
-
 __device__ __forceinline__ uint32_t at_bf16x2(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Weights are 2^(k2 s - r), r = k2 m rounded to fp32: its rounding moves all weights of a row alike.  Where
+// that could be by more than 2^0.5 (scores of a size that no model has), they are 2^(k2 (s - m))
+// instead, r = k2 m exactly.
+constexpr float AT_FAR = 0x1p24f;
+__device__ __forceinline__ bool at_far(float m, float k2) { return fabsf(m * k2) >= AT_FAR; }
+
+// 2^(r of m - r of n): what sums of weights taken with m are multiplied with to be sums taken with n.
+__device__ __forceinline__ float at_ratio(float m, float n, float k2)
+{
+    const float rm = m * k2, rn = n * k2;
+    const float x = at_far(m, k2) ? (at_far(n, k2) ? (m - n) * k2 : fmaf(m, k2, -rn))
+                                  : (at_far(n, k2) ? fmaf(-n, k2, rm) : rm - rn);
+    return ex2(x);
 }
 
 // Whether one of the bf16 halves of w is not finite; bit 15 and bit 31 say which.
@@ -316,6 +322,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         mbar_init(&sh.qempty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.sfull[i], 1);
+            mbar_init(&sh.phalf[i], 4);
             mbar_init(&sh.pfull[i], 4);
             mbar_init(&sh.ofull[i], 1);
             mbar_init(&sh.oempty[i], 4);
@@ -440,15 +447,23 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     }
                     for (int q = 0; ok && q < nq; ++q) {
                         const int buf = NQ == 2 ? q : nt[0] & 1;
-                        if (!wait(&sh.pfull[buf], (NQ == 2 ? nt[q] : nt[0] >> 1) & 1)) break;
+                        const uint32_t parity = (NQ == 2 ? nt[q] : nt[0] >> 1) & 1;
                         if (q == 0 && !landed(2 * n + 1)) break;
+                        if (!wait(&sh.phalf[buf], parity)) break;
                         if (j == 0 && no[q] > 0 && !wait(&sh.oempty[q], (no[q] - 1) & 1)) break;
                         tc_fence_after();
                         const uint32_t v = smem_u32(ring + ((2 * n + 1) % NS) * SB);
+                        // the upper keys' weights come first
 #pragma unroll
-                        for (int x = 0; x < AT_KEYS / 16; ++x)
+                        for (int x = AT_KEYS / 32; x < AT_KEYS / 16; ++x)
                             tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, umma_desc_sw128_mn(v + x * 2048, PANEL),
-                                           ID_O, j != 0 || x != 0);
+                                           ID_O, j != 0 || x != AT_KEYS / 32);
+                        if (!wait(&sh.pfull[buf], parity)) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = 0; x < AT_KEYS / 32; ++x)
+                            tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, umma_desc_sw128_mn(v + x * 2048, PANEL),
+                                           ID_O, 1);
                         tc_commit(&sh.ofull[q]);
                         ++nt[q];
                         if (j == 0) ++no[q];
@@ -568,7 +583,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
                     if (__any_sync(FULL, grow)) {
-                        const float f = grow ? (m == NEG_INF ? 0.f : ex2((m - top) * p.k2)) : 1.f;
+                        const float f = grow ? (m == NEG_INF ? 0.f : at_ratio(m, top, p.k2)) : 1.f;
                         if (grow) m = top;
                         l *= f;
                         if (i > w.i0) {
@@ -587,17 +602,22 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                         }
                     }
                     const float ref = m == NEG_INF ? 0.f : m;
+                    const bool far = at_far(ref, p.k2), any_far = __any_sync(FULL, far);
+                    const float off = far ? 0.f : -(ref * p.k2), sub = far ? ref : 0.f;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
                     auto weigh = [&](uint32_t *s, int c0) {
+                        if (any_far) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
+                        }
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             uint32_t pk[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                float a = __uint_as_float(s[32 * c + 2 * e]), b = __uint_as_float(s[32 * c + 2 * e + 1]);
-                                add2(a, b, -ref, -ref);
-                                mul2(a, b, p.k2, p.k2);
-                                pk[e] = at_bf16x2(ex2(a), ex2(b));
+                                const float2 x = fma2(__uint_as_float(s[32 * c + 2 * e]), __uint_as_float(s[32 * c + 2 * e + 1]), p.k2,
+                                                      p.k2, off, off);
+                                pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
                                 add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], bf16lo_to_f32(pk[e]), bf16hi_to_f32(pk[e]));
                             }
                             tmem_st16(t_s + P_COL + (c0 + 32 * c) / 2, pk);
@@ -606,12 +626,18 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     weigh(hi_s, 64);
                     tmem_ld32_start(t_s, lo_s);
                     tmem_ld32_start(t_s + 32, lo_s + 32);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.phalf[buf]);
                     tmem_ld_wait();
                     tmem_ready<64>(lo_s);
                     if (!open) hide(lo_s, 0);
                     weigh(lo_s, 0);
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_st_wait();
+                } else if (lane == 0) {
+                    mbar_arrive(&sh.phalf[buf]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -710,7 +736,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 for (int c = c0; c <= c1; ++c) {
                     const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c, r) * 2));
                     const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c, r) * D) + e);
-                    const float f = ml.x == NEG_INF ? 0.f : ex2((ml.x - M) * p.k2);
+                    const float f = ml.x == NEG_INF ? 0.f : at_ratio(ml.x, M, p.k2);
                     sl = fmaf(f, ml.y, sl);
                     o0 = fmaf(f, o.x, o0), o1 = fmaf(f, o.y, o1), o2 = fmaf(f, o.z, o2), o3 = fmaf(f, o.w, o3);
                 }

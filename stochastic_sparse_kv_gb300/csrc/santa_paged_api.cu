@@ -89,7 +89,12 @@ int launch_rope(RopeParams &p, int d, const santa_rotation *rotation, void *stre
         p.turns = rotation->turns;
         p.amplitude = rotation->amplitude;
     }
-    p.groups = (int)heads;
+    int dev, sms, optin, rc;
+    if ((rc = device_info(&dev, &sms, &optin))) return rc;
+    // as many rows to a thread as leave every SM its threads twice over
+    const long long all = heads * p.B * p.T * (d / RP_VALUES);
+    const long long each = std::min<long long>(RP_HEADS, std::max<long long>(1, all / (2ll * 2048 * sms)));
+    p.groups = (int)((heads + each - 1) / each);
     const bool pairs = rotation && rotation->layout == SANTA_ROPE_PAIRS;
     const void *fn = d == 128 ? (pairs ? (const void *)santa_rope_kernel<128, true> : (const void *)santa_rope_kernel<128, false>)
                               : (pairs ? (const void *)santa_rope_kernel<64, true> : (const void *)santa_rope_kernel<64, false>);

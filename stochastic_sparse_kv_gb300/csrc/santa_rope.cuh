@@ -18,6 +18,8 @@ namespace santa {
 
 constexpr int RP_NT = 256;
 constexpr int RP_VALUES = 16;             // features a thread moves of a row
+constexpr int RP_AHEAD = 4;               // rows that a thread has in flight
+constexpr int RP_HEADS = 8;               // rows a thread moves at the most (its angles serve them all)
 
 // Rows of one kind; strides in elements for (batch, token, head).
 struct RopeRows {
@@ -88,46 +90,58 @@ __global__ void __launch_bounds__(RP_NT) santa_rope_kernel(const RopeParams p)
             set_dev_error(p.ctrl, DEV_BAD_PAGE);
     }
     const int heads = p.H_q + 2 * p.H_kv;
-    for (int h = g; h < heads; h += p.groups) {
-        const uint16_t *src;
-        uint16_t *dst;
-        bool rotate = turn;
-        if (h < p.H_q) {
-            src = p.q.src + (b * p.q.sb + t * p.q.st + h * p.q.sh);
-            dst = p.q.dst + (b * p.q.db + t * p.q.dt + h * p.q.dh);
-        } else {
-            if (place < 0) break;
-            const bool value = h - p.H_q >= p.H_kv;
-            const RopeRows &r = value ? p.v : p.k;
-            const int hk = h - p.H_q - (value ? p.H_kv : 0);
-            src = r.src + (b * r.sb + t * r.st + hk * r.sh);
-            dst = r.dst + (place + ((long long)hk << p.page_shift) * D);
-            rotate = turn && !value;
-        }
-        // (a row of V is copied in the same two pieces)
-        uint4 u = *reinterpret_cast<const uint4 *>(src + f0), w = *reinterpret_cast<const uint4 *>(src + f1);
-        if (rotate) {
-            uint32_t a[4] = {u.x, u.y, u.z, u.w}, e[4] = {w.x, w.y, w.z, w.w};
+    // RP_AHEAD rows are read before the first of them is used
+    for (int h0 = g; h0 < heads; h0 += RP_AHEAD * p.groups) {
+        uint4 u[RP_AHEAD], w[RP_AHEAD];
+        uint16_t *dst[RP_AHEAD];
+        bool rotate[RP_AHEAD];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (PAIRS) {
-                    // words 0-3 hold pairs 0-3 of this thread, words 4-7 pairs 4-7
-                    const float x0 = bf16lo_to_f32(a[i]), y0 = bf16hi_to_f32(a[i]);
-                    const float x1 = bf16lo_to_f32(e[i]), y1 = bf16hi_to_f32(e[i]);
-                    a[i] = bf16x2(x0 * cs[i] - y0 * sn[i], x0 * sn[i] + y0 * cs[i]);
-                    e[i] = bf16x2(x1 * cs[4 + i] - y1 * sn[4 + i], x1 * sn[4 + i] + y1 * cs[4 + i]);
-                } else {
-                    const float x0 = bf16lo_to_f32(a[i]), x1 = bf16hi_to_f32(a[i]);
-                    const float y0 = bf16lo_to_f32(e[i]), y1 = bf16hi_to_f32(e[i]);
-                    a[i] = bf16x2(x0 * cs[2 * i] - y0 * sn[2 * i], x1 * cs[2 * i + 1] - y1 * sn[2 * i + 1]);
-                    e[i] = bf16x2(x0 * sn[2 * i] + y0 * cs[2 * i], x1 * sn[2 * i + 1] + y1 * cs[2 * i + 1]);
-                }
+        for (int x = 0; x < RP_AHEAD; ++x) {
+            const int h = h0 + x * p.groups;
+            const uint16_t *src;
+            dst[x] = nullptr;
+            if (h >= heads || (h >= p.H_q && place < 0)) continue;
+            if (h < p.H_q) {
+                src = p.q.src + (b * p.q.sb + t * p.q.st + h * p.q.sh);
+                dst[x] = p.q.dst + (b * p.q.db + t * p.q.dt + h * p.q.dh);
+                rotate[x] = turn;
+            } else {
+                const bool value = h - p.H_q >= p.H_kv;
+                const int hk = h - p.H_q - (value ? p.H_kv : 0);
+                src = value ? p.v.src + (b * p.v.sb + t * p.v.st + hk * p.v.sh) : p.k.src + (b * p.k.sb + t * p.k.st + hk * p.k.sh);
+                dst[x] = (value ? p.v.dst : p.k.dst) + (place + ((long long)hk << p.page_shift) * D);
+                rotate[x] = turn && !value;
             }
-            u = make_uint4(a[0], a[1], a[2], a[3]);
-            w = make_uint4(e[0], e[1], e[2], e[3]);
+            // (a row of V is copied in the same two pieces)
+            u[x] = *reinterpret_cast<const uint4 *>(src + f0);
+            w[x] = *reinterpret_cast<const uint4 *>(src + f1);
         }
-        *reinterpret_cast<uint4 *>(dst + f0) = u;
-        *reinterpret_cast<uint4 *>(dst + f1) = w;
+#pragma unroll
+        for (int x = 0; x < RP_AHEAD; ++x) {
+            if (!dst[x]) continue;
+            if (rotate[x]) {
+                uint32_t a[4] = {u[x].x, u[x].y, u[x].z, u[x].w}, e[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (PAIRS) {
+                        // words 0-3 hold pairs 0-3 of this thread, words 4-7 pairs 4-7
+                        const float x0 = bf16lo_to_f32(a[i]), y0 = bf16hi_to_f32(a[i]);
+                        const float x1 = bf16lo_to_f32(e[i]), y1 = bf16hi_to_f32(e[i]);
+                        a[i] = bf16x2(x0 * cs[i] - y0 * sn[i], x0 * sn[i] + y0 * cs[i]);
+                        e[i] = bf16x2(x1 * cs[4 + i] - y1 * sn[4 + i], x1 * sn[4 + i] + y1 * cs[4 + i]);
+                    } else {
+                        const float x0 = bf16lo_to_f32(a[i]), x1 = bf16hi_to_f32(a[i]);
+                        const float y0 = bf16lo_to_f32(e[i]), y1 = bf16hi_to_f32(e[i]);
+                        a[i] = bf16x2(x0 * cs[2 * i] - y0 * sn[2 * i], x1 * cs[2 * i + 1] - y1 * sn[2 * i + 1]);
+                        e[i] = bf16x2(x0 * sn[2 * i] + y0 * cs[2 * i], x1 * sn[2 * i + 1] + y1 * cs[2 * i + 1]);
+                    }
+                }
+                u[x] = make_uint4(a[0], a[1], a[2], a[3]);
+                w[x] = make_uint4(e[0], e[1], e[2], e[3]);
+            }
+            *reinterpret_cast<uint4 *>(dst[x] + f0) = u[x];
+            *reinterpret_cast<uint4 *>(dst[x] + f1) = w[x];
+        }
     }
 }
 
