@@ -21,7 +21,7 @@
 //    then K and V of each tile, page by page, a lane a page, into a ring of stages;
 //  * an MMA warp, one thread of which issues S = Q K^T (both from shared memory) and O += P V, P
 //    read from TMEM and V from shared memory as it lies (keys as rows: MN-major);
-//  * four softmax warps a row tile, a thread a row: scores from TMEM to registers, their maximum,
+//  * eight softmax warps a row tile, two threads a row: scores from TMEM to registers, their maximum,
 //    p = 2^(k2 (s - m)), rounded to bf16 and written to TMEM over the scores; the sum l of the
 //    rounded values, so that a rounding moves numerator and denominator alike.  m is a score so
 //    far and moves only when one exceeds it by 2^AT_SLACK, so that O in TMEM is seldom rescaled.
@@ -47,20 +47,20 @@ constexpr int AT_SETUP = 2;               // what an item costs beside its tiles
 constexpr int AT_MIN_SHARE = 4;           // a share's least size, in tiles
 constexpr float AT_SLACK = 8.f;           // log2 of the largest p
 constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
-constexpr int AT_MISC = 2048;             // of it for barriers and the like
-constexpr int AT_STAGES_MAX = 12;
+constexpr int AT_MISC = 3072;             // of it for barriers and the like
+constexpr int AT_STAGES_MAX = 8;
 
-__host__ __device__ constexpr int at_threads(int NQ) { return NQ * 128 + 64; }
+__host__ __device__ constexpr int at_threads(int NQ) { return NQ * 256 + 64; }
 __host__ __device__ constexpr int at_qbytes(int D, int NQ) { return NQ * AT_ROWS * D * 2; }
 __host__ __device__ constexpr int at_stage_bytes(int D) { return AT_KEYS * D * 2; }
 __host__ __device__ constexpr int at_stages(int D, int NQ)
 {
-    const int n = (AT_SMEM - 1024 - AT_MISC - at_qbytes(D, NQ)) / at_stage_bytes(D);
+    const int n = (AT_SMEM - AT_MISC - at_qbytes(D, NQ)) / at_stage_bytes(D);
     return n < AT_STAGES_MAX ? n : AT_STAGES_MAX;
 }
 __host__ __device__ constexpr int at_smem(int D, int NQ)
 {
-    return 1024 + at_qbytes(D, NQ) + at_stages(D, NQ) * at_stage_bytes(D) + AT_MISC;
+    return at_qbytes(D, NQ) + at_stages(D, NQ) * at_stage_bytes(D) + AT_MISC;
 }
 
 // Row tiles of an item, and rows that a piece holds, by the rows T * G of a sequence and KV head.
@@ -79,25 +79,6 @@ struct AttendParams {
     float k2;                     // scale log2 e
     uint64_t wait_ns;
 };
-
-struct AtSmem {
-    uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
-    uint64_t qfull, qempty;
-    uint64_t sfull[2], phalf[2], pfull[2];  // NQ = 2: of a row tile; NQ = 1: of a score buffer
-    uint64_t ofull[2], oempty[2], wg[2];
-    uint64_t drain;
-    long long sums[2 * 16];
-    long long total, start_base;
-    int start_pair, last;
-    uint32_t tmem;
-    int bad_v;                    // a value that is not finite was set to zero
-    int timeout;
-    int fills, fills_used;        // stages filled, and their fills seen by the MMA thread
-    int qfills, qfills_used;
-    int is_last[2];
-    int arrived[2][2];            // [slot][row tile]: arrivals of this CTA's pieces
-};
-static_assert(sizeof(AtSmem) <= AT_MISC, "barriers and the like");
 
 // A batch row's tokens; none where pos and counts leave the cache.
 __device__ __forceinline__ void at_row(const AttendParams &p, int b, int &first, int &cnt)
@@ -136,17 +117,16 @@ __device__ __forceinline__ int at_item(const AttendParams &p, int first, int cnt
     return it.L;
 }
 
-// The items of a share [f0, f1) of the list, one after another.
+// The items of the share [f0, f1) of the list, one after another.
 template <int NQ>
 struct AtWalk {
-    long long f0, f1, base;
+    long long base;
     int b, qt, h, qts, first, cnt;
     AtItem it;
     int i0, i1;                   // this share's tiles of the item
 
-    __device__ __forceinline__ void begin(const AttendParams &p, long long f0_, long long f1_, long long base_, int pair)
+    __device__ __forceinline__ void begin(const AttendParams &p, long long f0, long long base_, int pair)
     {
-        f0 = f0_, f1 = f1_;
         qts = (p.T + ((NQ * AT_ROWS) >> p.lg_g) - 1) / ((NQ * AT_ROWS) >> p.lg_g);
         b = pair / qts, qt = pair % qts;
         at_row(p, b, first, cnt);
@@ -168,7 +148,7 @@ struct AtWalk {
         } while (at_item<NQ>(p, first, cnt, qt, it) == 0);
     }
     // Moves to the first item at or after this one of which the share holds a tile.
-    __device__ __forceinline__ bool seek(const AttendParams &p)
+    __device__ __forceinline__ bool seek(const AttendParams &p, long long f0, long long f1)
     {
         for (;; step(p)) {
             if (base >= f1 || b >= p.B) return false;
@@ -187,6 +167,31 @@ struct AtWalk {
                (p.window == 0 || key > it.first + it.t1 - p.window || key + AT_KEYS <= p.sinks);
     }
 };
+
+template <int NQ>
+struct AtSmem {
+    uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
+    uint64_t qfull, qempty;
+    uint64_t sfull[2], phalf[2], pfull[2];  // NQ = 2: of a row tile; NQ = 1: of a score buffer
+    uint64_t ofull[2], oempty[2], wg[2];
+    uint64_t drain;
+    long long total, start_base;
+    int start_pair, last;
+    uint32_t tmem;
+    int bad_v;                    // a value that is not finite was set to zero
+    int timeout;
+    int fills, fills_used;        // stages filled, and their fills seen by the MMA thread
+    int qfills, qfills_used;
+    int is_last[2];
+    int arrived[2][2];            // [slot][row tile]: arrivals of this CTA's pieces
+    AtWalk<NQ> walk[NQ * 4];      // of the pairs of softmax warps: not in their registers
+    int more[NQ * 4];
+    union {
+        long long sums[20];
+        float swap[NQ][AT_ROWS][2];   // between the two threads of a row: maxima, sums
+    };
+};
+static_assert(sizeof(AtSmem<2>) <= AT_MISC && sizeof(AtSmem<1>) <= AT_MISC, "barriers and the like");
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -217,6 +222,13 @@ __device__ __forceinline__ float at_ratio(float m, float n, float k2)
     return ex2(x);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Whether one of the bf16 halves of w is not finite; bit 15 and bit 31 say which.
 __device__ __forceinline__ uint32_t at_not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
@@ -234,20 +246,18 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     constexpr int SB = at_stage_bytes(D);
     constexpr int PANELS = D / 64;
     constexpr int PANEL = AT_KEYS * 128;       // bytes of 64 columns of a tile
-    constexpr int W_PROD = NQ * 4, W_MMA = W_PROD + 1;
+    constexpr int W_PROD = NQ * 8, W_MMA = W_PROD + 1;
     constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_KEYS), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
     constexpr uint32_t O_COL = 256;            // scores in columns 0-255, outputs behind them
-    constexpr uint32_t P_COL = 64;             // weights over the upper half of their scores
+    constexpr uint32_t P_COL = 0;              // weights over the lower half of their scores
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(NS >= 4, "ring");
     const float NEG_INF = __int_as_float(0xff800000);
 
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    uint8_t *qs = smem;
-    uint8_t *ring = smem + at_qbytes(D, NQ);
-    AtSmem &sh = *reinterpret_cast<AtSmem *>(ring + NS * SB);
+    extern __shared__ __align__(1024) uint8_t at_shared[];
+    uint8_t *qs = at_shared;
+    uint8_t *ring = at_shared + at_qbytes(D, NQ);
+    AtSmem<NQ> &sh = *reinterpret_cast<AtSmem<NQ> *>(ring + NS * SB);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // ---- the list's size, and where this CTA's share begins
@@ -322,11 +332,11 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         mbar_init(&sh.qempty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.sfull[i], 1);
-            mbar_init(&sh.phalf[i], 4);
-            mbar_init(&sh.pfull[i], 4);
+            mbar_init(&sh.phalf[i], 8);
+            mbar_init(&sh.pfull[i], 8);
             mbar_init(&sh.ofull[i], 1);
-            mbar_init(&sh.oempty[i], 4);
-            mbar_init(&sh.wg[i], 4);
+            mbar_init(&sh.oempty[i], 8);
+            mbar_init(&sh.wg[i], 8);
             for (int j = 0; j < 2; ++j) sh.arrived[i][j] = 0;
         }
         mbar_init(&sh.drain, 1);
@@ -338,8 +348,6 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = sh.tmem;
-    AtWalk<NQ> w;
-    w.begin(p, f0, f1, sh.start_base, sh.start_pair);
     auto failed = [&]() {
         set_dev_error(p.ctrl, DEV_TIMEOUT);
         sh.timeout = 1;
@@ -349,9 +357,11 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         // ================= producer
         const int page = 1 << p.page_shift, box = min(page, AT_KEYS);
         const int rows_all = (p.n_pages * p.H_kv) << p.page_shift;   // (below 2^31) beyond the pool: zeros
+        AtWalk<NQ> w;
+        w.begin(p, f0, sh.start_base, sh.start_pair);
         int n = 0, items = 0, stage = 0, phase = 1;
         bool ok = true;
-        for (; ok && w.seek(p); w.step(p), ++items) {
+        for (; ok && w.seek(p, f0, f1); w.step(p), ++items) {
             const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
             if (items > 0 && !__all_sync(FULL, mbar_wait_bounded(&sh.qempty, (items - 1) & 1, p.wait_ns))) {
                 ok = false;
@@ -405,6 +415,8 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     } else if (warp == W_MMA) {
         // ================= MMA issuer: one thread
         if (lane == 0) {
+            AtWalk<NQ> w;
+            w.begin(p, f0, sh.start_base, sh.start_pair);
             int n = 0, items = 0;
             int nt[2] = {0, 0};       // tiles of each row tile so far
             int no[2] = {0, 0};       // its items so far
@@ -419,15 +431,17 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 if (wait(&sh.full[f % NS], (f / NS) & 1) && sh.fills_used < f + 1) sh.fills_used = f + 1;
                 return ok;
             };
+            // (descriptors are made where they are used: kept for the whole loop they fill the registers)
             auto scores = [&](int q, int f, int buf) {
-                const uint32_t k = smem_u32(ring + (f % NS) * SB), a = qaddr + q * AT_ROWS * D * 2;
+                uint64_t k = umma_desc_sw128(smem_u32(ring + (f % NS) * SB)), a = umma_desc_sw128(qaddr + q * AT_ROWS * D * 2);
+                asm volatile("" : "+l"(k), "+l"(a));
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    tc_mma_bf16(tbase + buf * AT_KEYS, umma_desc_sw128(a + (x / 4) * (AT_ROWS * 128) + (x % 4) * 32),
-                                umma_desc_sw128(k + (x / 4) * PANEL + (x % 4) * 32), ID_S, x != 0);
+                    tc_mma_bf16(tbase + buf * AT_KEYS, a + ((x / 4) * (AT_ROWS * 128) + (x % 4) * 32) / 16,
+                                k + ((x / 4) * PANEL + (x % 4) * 32) / 16, ID_S, x != 0);
                 tc_commit(&sh.sfull[buf]);
             };
-            for (; ok && w.seek(p); w.step(p), ++items) {
+            for (; ok && w.seek(p, f0, f1); w.step(p), ++items) {
                 const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
                 const int L = w.i1 - w.i0;
                 if (!wait(&sh.qfull, items & 1)) break;
@@ -452,18 +466,23 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                         if (!wait(&sh.phalf[buf], parity)) break;
                         if (j == 0 && no[q] > 0 && !wait(&sh.oempty[q], (no[q] - 1) & 1)) break;
                         tc_fence_after();
-                        const uint32_t v = smem_u32(ring + ((2 * n + 1) % NS) * SB);
-                        // the upper keys' weights come first
+                        uint64_t v = umma_desc_sw128_mn(smem_u32(ring + ((2 * n + 1) % NS) * SB), PANEL);
+                        asm volatile("" : "+l"(v));
+                        // the weights come in two parts: the first 32 and the next 32 of each 64 keys
 #pragma unroll
-                        for (int x = AT_KEYS / 32; x < AT_KEYS / 16; ++x)
-                            tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, umma_desc_sw128_mn(v + x * 2048, PANEL),
-                                           ID_O, j != 0 || x != AT_KEYS / 32);
-                        if (!wait(&sh.pfull[buf], parity)) break;
-                        tc_fence_after();
+                        for (int part = 0; part < 2; ++part) {
+                            if (part) {
+                                if (!wait(&sh.pfull[buf], parity)) break;
+                                tc_fence_after();
+                            }
 #pragma unroll
-                        for (int x = 0; x < AT_KEYS / 32; ++x)
-                            tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, umma_desc_sw128_mn(v + x * 2048, PANEL),
-                                           ID_O, 1);
+                            for (int y = 0; y < AT_KEYS / 32; ++y) {
+                                const int x = (y & 1) + 2 * part + 4 * (y >> 1);
+                                tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, v + x * (2048 / 16), ID_O,
+                                               j != 0 || part != 0 || y != 0);
+                            }
+                        }
+                        if (!ok) break;
                         tc_commit(&sh.ofull[q]);
                         ++nt[q];
                         if (j == 0) ++no[q];
@@ -488,10 +507,14 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         }
         __syncwarp();
     } else if (warp < W_PROD) {
-        // ================= softmax of row tile q: thread = row = TMEM lane
-        const int q = warp >> 2, row = tid & 127;
+        // ================= softmax of row tile q: two threads a row (a TMEM lane), 64 scores each
+        const int q = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, wg_tid = tid & 255;
+        const int pair = 1 + (q << 2) + (warp & 3);      // the named barrier of the two warps of these rows
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t t_o = tbase + lanes + O_COL + q * D;
+        float *swap = sh.swap[q][row];
+        AtWalk<NQ> &w = sh.walk[pair - 1];
+        const bool leads = half == 0 && lane == 0;       // moves the pair's walk
         int n = 0, n0 = 0;            // tiles of this row tile so far, and of the CTA
         uint32_t wg_phase = 0;
         bool ok = true;
@@ -499,7 +522,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             if (ok) ok = __all_sync(FULL, mbar_wait_bounded(bar, parity, p.wait_ns));
             return ok;
         };
-        // rendezvous of the four warps (a bounded wait, unlike bar.sync)
+        // rendezvous of the row tile's warps (a bounded wait, unlike bar.sync)
         auto wg_sync = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.wg[q]);
@@ -507,176 +530,197 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             wg_phase ^= 1u;
             return ok;
         };
-        for (; ok && w.seek(p); n0 += w.i1 - w.i0, w.step(p)) {
+        // whether x holds for any thread of the pair of warps.  Both warps make the same calls, whatever
+        // happens: a failed wait is told to the other warp by one of them
+        auto either = [&](bool x) {
+            uint32_t r;
+            asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %2, 0;\n\t"
+                         "barrier.cta.red.or.pred b, %1, 64, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+                         : "=r"(r)
+                         : "r"(pair), "r"((uint32_t)x)
+                         : "memory");
+            return r != 0;
+        };
+        if (leads) {
+            w.begin(p, f0, sh.start_base, sh.start_pair);
+            sh.more[pair - 1] = w.seek(p, f0, f1);
+        }
+        auto next = [&]() {
+            if (leads) {
+                w.step(p);
+                sh.more[pair - 1] = w.seek(p, f0, f1);
+            }
+        };
+        while (!either(!ok) && sh.more[pair - 1]) {
             const int live = w.live_rows(p) - q * AT_ROWS;   // of this row tile
-            if (live <= 0) continue;
+            const int tiles = w.i1 - w.i0;
+            if (live <= 0) {
+                n0 += tiles;
+                either(false);
+                next();
+                continue;
+            }
             const bool warp_live = 32 * (warp & 3) < live;
-            const int t = w.it.t0 + ((q * AT_ROWS + row) >> p.lg_g);
-            const int P = w.it.first + t;
-            const int lo = p.window > 0 ? P - p.window + 1 : 0;
-            const int kmax = w.it.first + w.it.t1;
+            const int P = w.it.first + w.it.t0 + ((q * AT_ROWS + row) >> p.lg_g);
+            const int open_hi = w.it.first + w.it.t0 - AT_KEYS, open_lo = p.window > 0 ? w.it.first + w.it.t1 - p.window : -1;
             float m = NEG_INF, l = 0.f;
-            int i = w.i0;
-            for (; i < w.i1; ++i, ++n) {
+            int left = w.it.nsink - w.i0, key = w.it.key(w.i0);
+            for (int i = 0; i < tiles; ++i, ++n) {
                 const int buf = NQ == 2 ? q : n & 1;
                 const uint32_t t_s = tbase + lanes + buf * AT_KEYS;
-                const int key = w.it.key(i);
-                const bool open = w.open(p, key);
-                if (!wait(&sh.sfull[buf], (NQ == 2 ? n : n >> 1) & 1)) break;
+                // whether all tokens of the item see all keys of the tile
+                const bool open = key < open_hi + 2 && (key > open_lo || key + AT_KEYS <= p.sinks);
+                wait(&sh.sfull[buf], (NQ == 2 ? n : n >> 1) & 1);
                 if (!open && q == 0) {
                     // values of V that are not finite become zeros
-                    const int f = 2 * (n0 + i - w.i0) + 1;
-                    if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
-                    uint8_t *v = ring + (f % NS) * SB;
-#pragma unroll 4
-                    for (int c = tid; c < SB / 16; c += 128) {
-                        uint4 x = reinterpret_cast<uint4 *>(v)[c];
-                        const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
-                        if (b0 | b1 | b2 | b3) {
-                            x.x &= ~((b0 >> 15) * 0xffffu);
-                            x.y &= ~((b1 >> 15) * 0xffffu);
-                            x.z &= ~((b2 >> 15) * 0xffffu);
-                            x.w &= ~((b3 >> 15) * 0xffffu);
-                            reinterpret_cast<uint4 *>(v)[c] = x;
-                            const int j = key + (c % (PANEL / 16)) / 8;
-                            if (j <= kmax && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
+                    const int f = 2 * (n0 + i) + 1;
+                    if (wait(&sh.full[f % NS], (f / NS) & 1)) {
+                        uint8_t *v = ring + (f % NS) * SB;
+#pragma unroll 2
+                        for (int c = wg_tid; c < SB / 16; c += 256) {
+                            uint4 x = reinterpret_cast<uint4 *>(v)[c];
+                            const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
+                            if (b0 | b1 | b2 | b3) {
+                                x.x &= ~((b0 >> 15) * 0xffffu);
+                                x.y &= ~((b1 >> 15) * 0xffffu);
+                                x.z &= ~((b2 >> 15) * 0xffffu);
+                                x.w &= ~((b3 >> 15) * 0xffffu);
+                                reinterpret_cast<uint4 *>(v)[c] = x;
+                                const int j = key + (c % (PANEL / 16)) / 8;
+                                if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
+                            }
                         }
+                        fence_proxy_async_smem();
                     }
-                    fence_proxy_async_smem();
                 }
                 if (warp_live) {
                     tc_fence_after();
-                    // the upper half of the scores stays in registers from here to its weights, the lower
-                    // half is read again: 128 of them, beside all else, would not fit 168 registers
-                    uint32_t lo_s[64], hi_s[64];
-                    tmem_ld32_start(t_s, lo_s);
-                    tmem_ld32_start(t_s + 32, lo_s + 32);
-                    tmem_ld_wait();
-                    tmem_ready<64>(lo_s);
-                    tmem_ld32_start(t_s + 64, hi_s);
-                    tmem_ld32_start(t_s + 96, hi_s + 32);
-                    const int ub = P + 1 - key, lb = lo - key, sk = p.sinks - key;
-                    auto hide = [&](uint32_t *s, int c0) {
+                    uint32_t s[64];
+                    float top = NEG_INF;
+                    if (ok) {
+                        tmem_ld32_start(t_s + 64 * half, s);
+                        tmem_ld32_start(t_s + 64 * half + 32, s + 32);
+                        tmem_ld_wait();
+                        tmem_ready<64>(s);
+                        if (!open) {
+                            const int at = key + 64 * half;
+                            const int ub = P + 1 - at, lb = (p.window > 0 ? P - p.window + 1 : 0) - at, sk = p.sinks - at;
 #pragma unroll
-                        for (int c = 0; c < 64; c += 32) {
-                            const int at = c0 + c;
-                            const uint32_t seen = at_low_bits(ub - at) & (~at_low_bits(lb - at) | at_low_bits(sk - at));
+                            for (int c = 0; c < 64; c += 32) {
+                                const uint32_t seen = at_low_bits(ub - c) & (~at_low_bits(lb - c) | at_low_bits(sk - c));
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
+                                for (int e = 0; e < 32; ++e)
+                                    if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
+                            }
                         }
-                    };
-                    float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-                    auto most = [&](const uint32_t *s) {
+                        float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
                         for (int e = 0; e < 64; e += 8)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1])));
-                    };
-                    if (!open) hide(lo_s, 0);
-                    most(lo_s);
-                    tmem_ld_wait();
-                    tmem_ready<64>(hi_s);
-                    if (!open) hide(hi_s, 64);
-                    most(hi_s);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
-                    if (__any_sync(FULL, grow)) {
+                            for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1]));
+                        top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    }
+                    bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
+                    if (either(grow || !ok)) {
+                        // both threads of a row take its larger maximum
+                        swap[half] = ok ? top : __int_as_float(0x7fffffff);
+                        either(false);
+                        const float other = swap[half ^ 1];
+                        ok = ok && __all_sync(FULL, __float_as_int(other) != 0x7fffffff);
+                        top = fmaxf(top, other);
+                        grow = (top - m) * p.k2 > AT_SLACK;
                         const float f = grow ? (m == NEG_INF ? 0.f : at_ratio(m, top, p.k2)) : 1.f;
                         if (grow) m = top;
                         l *= f;
-                        if (i > w.i0) {
-                            if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
+                        if (i > 0 && wait(&sh.ofull[q], (n - 1) & 1)) {
                             tc_fence_after();
+                            // (few columns at a time: the scores keep their registers)
+#pragma unroll 1
+                            for (uint32_t at = t_o + half * (D / 2); at < t_o + (half + 1) * (D / 2); at += 8) {
+                                uint32_t o[8];
+                                tmem_ld32<8>(at, o);
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32_start(t_o + 32 * c, o);
-                                tmem_ld_wait();
-                                tmem_ready<32>(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(t_o + 32 * c, o);
+                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st8(at, o);
                             }
                         }
+                        if (either(!ok)) ok = false;
+                        if (!ok) break;
                     }
                     const float ref = m == NEG_INF ? 0.f : m;
-                    const bool far = at_far(ref, p.k2), any_far = __any_sync(FULL, far);
-                    const float off = far ? 0.f : -(ref * p.k2), sub = far ? ref : 0.f;
+                    const bool far = at_far(ref, p.k2);
+                    const float off = far ? 0.f : -(ref * p.k2);
+                    if (__any_sync(FULL, far)) {
+                        const float sub = far ? ref : 0.f;
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
+                    }
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    auto weigh = [&](uint32_t *s, int c0) {
-                        if (any_far) {
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 x = fma2(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]), p.k2, p.k2, off, off);
+                            pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
+                            add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], bf16lo_to_f32(pk[e]), bf16hi_to_f32(pk[e]));
                         }
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float2 x = fma2(__uint_as_float(s[32 * c + 2 * e]), __uint_as_float(s[32 * c + 2 * e + 1]), p.k2,
-                                                      p.k2, off, off);
-                                pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
-                                add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], bf16lo_to_f32(pk[e]), bf16hi_to_f32(pk[e]));
-                            }
-                            tmem_st16(t_s + P_COL + (c0 + 32 * c) / 2, pk);
-                        }
-                    };
-                    weigh(hi_s, 64);
-                    tmem_ld32_start(t_s, lo_s);
-                    tmem_ld32_start(t_s + 32, lo_s + 32);
-                    tmem_st_wait();
+                        tmem_st8(t_s + P_COL + 32 * half + c / 2, pk);
+                        if (c == 0 || c == 32) continue;
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(c == 48 ? &sh.pfull[buf] : &sh.phalf[buf]);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                } else {
+                    if (!ok) break;
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.phalf[buf]);
-                    tmem_ld_wait();
-                    tmem_ready<64>(lo_s);
-                    if (!open) hide(lo_s, 0);
-                    weigh(lo_s, 0);
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_st_wait();
-                } else if (lane == 0) {
-                    mbar_arrive(&sh.phalf[buf]);
+                    if (lane == 0) {
+                        mbar_arrive(&sh.phalf[buf]);
+                        mbar_arrive(&sh.pfull[buf]);
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.pfull[buf]);
+                key += AT_KEYS;
+                if (--left == 0) key = w.it.tlo * AT_KEYS;
             }
-            if (!ok) break;
+            n0 += tiles;
             // (a parity tells only two phases apart.  The last scores follow the product of two tiles
             // before with two buffers, of the tile before with one: the phase between is waited for)
-            if (NQ == 1 && n > 1 && !wait(&sh.ofull[q], (n - 2) & 1)) break;
-            if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
+            if (NQ == 1 && n > 1) wait(&sh.ofull[q], (n - 2) & 1);
+            wait(&sh.ofull[q], (n - 1) & 1);
             tc_fence_after();
+            swap[half] = l;
+            if (either(!ok)) break;
+            l += swap[half ^ 1];   // (written again after another rendezvous)
 
             // ---- the item's (or the piece's) sums
             const bool whole = w.whole(), mine_live = row < live;
             const bool fix = *reinterpret_cast<volatile int *>(&sh.bad_v) != 0;
             const int slot = w.i0 > 0 ? 0 : 1;
-            const float inv = whole ? 1.f / l : 1.f;
-            float *piece = p.part + ((size_t)(blockIdx.x * 2 + slot) * p.piece_rows + q * AT_ROWS + row) * D;
-            uint16_t *out = p.out + (((size_t)w.b * p.T + t) * p.H_q + (w.h << p.lg_g) + ((q * AT_ROWS + row) & ((1 << p.lg_g) - 1))) * D;
+            const int R = q * AT_ROWS + row;
             if (warp_live) {
+                const float inv = whole ? 1.f / l : 1.f;
+                const size_t at_piece = (size_t)(blockIdx.x * 2 + slot) * p.piece_rows + R;
+                uint16_t *out = p.out + (((size_t)w.b * p.T + w.it.t0 + (R >> p.lg_g)) * p.H_q + (w.h << p.lg_g) + (R & ((1 << p.lg_g) - 1))) * D;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32_start(t_o + 32 * c, o);
-                    tmem_ld_wait();
-                    tmem_ready<32>(o);
+                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                    uint32_t o[16];
+                    tmem_ld32<16>(t_o + c, o);
                     if (fix && mine_live) {
                         // values that are not finite, of the keys that this row sees
                         for (int x = w.i0; x < w.i1; ++x) {
-                            const int key = w.it.key(x);
-                            if (w.open(p, key)) continue;
-                            for (int j = key; j < key + AT_KEYS && j <= P; ++j) {
-                                if (j < lo && j >= p.sinks) continue;
+                            const int first = w.it.key(x);
+                            if (w.open(p, first)) continue;
+                            for (int j = first; j < first + AT_KEYS && j <= P; ++j) {
+                                if (p.window > 0 && j <= P - p.window && j >= p.sinks) continue;
                                 const int entry = p.table[(size_t)w.b * p.cols + (j >> p.page_shift)];
                                 if ((unsigned)entry >= (unsigned)p.n_pages) continue;
                                 const uint32_t *v = reinterpret_cast<const uint32_t *>(
-                                    p.v + ((((long long)entry * p.H_kv + w.h) << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D + 32 * c);
+                                    p.v + ((((long long)entry * p.H_kv + w.h) << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D + c);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) {
+                                for (int e = 0; e < 8; ++e) {
                                     const uint32_t u = v[e], bad = at_not_finite(u);
                                     if (bad & 0x8000u) o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + bf16lo_to_f32(u));
                                     if (bad >> 31) o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + bf16hi_to_f32(u));
@@ -687,64 +731,66 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     if (!mine_live) continue;
                     if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
+                        for (int e = 0; e < 16; e += 8) {
                             uint4 x;
                             x.x = at_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
                             x.y = at_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
                             x.z = at_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
                             x.w = at_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                            *reinterpret_cast<uint4 *>(out + 32 * c + e) = x;
+                            *reinterpret_cast<uint4 *>(out + c + e) = x;
                         }
                     } else {
+                        float *piece = p.part + at_piece * D;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            __stcg(reinterpret_cast<uint4 *>(piece + 32 * c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                        for (int e = 0; e < 16; e += 4)
+                            __stcg(reinterpret_cast<uint4 *>(piece + c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                     }
                 }
+                if (!whole && mine_live && half == 0) __stcg(reinterpret_cast<float2 *>(p.part_ml + at_piece * 2), make_float2(m, l));
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.oempty[q]);
-            if (whole) continue;
 
             // ---- a piece: the last CTA of the item to arrive joins them all
-            if (mine_live)
-                __stcg(reinterpret_cast<float2 *>(p.part_ml + ((size_t)(blockIdx.x * 2 + slot) * p.piece_rows + q * AT_ROWS + row) * 2),
-                       make_float2(m, l));
-            __threadfence();
-            if (!wg_sync()) break;
-            const int c0 = owner(w.base + AT_SETUP), c1 = owner(w.base + AT_SETUP + w.it.L - 1);
-            if (row == 0) {
-                int32_t *arrivals = p.ctrl + CTRL_GROUPS + 2 * c0 + q;
-                sh.arrived[slot][q] = 1;
-                const bool last = atomicAdd(arrivals, 1) == c1 - c0;
-                if (last) *arrivals = 0;
-                sh.is_last[q] = last;
+            const int c0 = whole ? 0 : owner(w.base + AT_SETUP), c1 = whole ? 0 : owner(w.base + AT_SETUP + w.it.L - 1);
+            if (!whole) {
                 __threadfence();
-            }
-            if (!wg_sync()) break;
-            if (!sh.is_last[q]) continue;
-            __threadfence();
-            const int rows_live = min(live, AT_ROWS);
-            auto at = [&](int c, int r) { return (size_t)(c * 2 + (c == c0 ? 1 : 0)) * p.piece_rows + q * AT_ROWS + r; };
-            for (int x = row; x < rows_live * (D / 4); x += 128) {
-                const int r = x / (D / 4), e = x % (D / 4);
-                float M = NEG_INF;
-                for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + at(c, r) * 2));
-                float sl = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-#pragma unroll 4
-                for (int c = c0; c <= c1; ++c) {
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c, r) * 2));
-                    const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c, r) * D) + e);
-                    const float f = ml.x == NEG_INF ? 0.f : at_ratio(ml.x, M, p.k2);
-                    sl = fmaf(f, ml.y, sl);
-                    o0 = fmaf(f, o.x, o0), o1 = fmaf(f, o.y, o1), o2 = fmaf(f, o.z, o2), o3 = fmaf(f, o.w, o3);
+                if (wg_sync() && wg_tid == 0) {
+                    int32_t *arrivals = p.ctrl + CTRL_GROUPS + 2 * c0 + q;
+                    sh.arrived[slot][q] = 1;
+                    const bool last = atomicAdd(arrivals, 1) == c1 - c0;
+                    if (last) *arrivals = 0;
+                    sh.is_last[q] = last;
+                    __threadfence();
                 }
-                const float inv = 1.f / sl;
-                const int R = q * AT_ROWS + r;
-                uint16_t *dst = p.out + (((size_t)w.b * p.T + w.it.t0 + (R >> p.lg_g)) * p.H_q + (w.h << p.lg_g) + (R & ((1 << p.lg_g) - 1))) * D;
-                *reinterpret_cast<uint2 *>(dst + 4 * e) = make_uint2(at_bf16x2(o0 * inv, o1 * inv), at_bf16x2(o2 * inv, o3 * inv));
+                if (wg_sync() && sh.is_last[q]) {
+                    __threadfence();
+                    const int rows_live = min(live, AT_ROWS);
+                    auto at = [&](int c, int r) { return (size_t)(c * 2 + (c == c0 ? 1 : 0)) * p.piece_rows + q * AT_ROWS + r; };
+                    for (int x = wg_tid; x < rows_live * (D / 4); x += 256) {
+                        const int r = x / (D / 4), e = x % (D / 4);
+                        float M = NEG_INF;
+#pragma unroll 4
+                        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + at(c, r) * 2));
+                        float sl = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+#pragma unroll 4
+                        for (int c = c0; c <= c1; ++c) {
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c, r) * 2));
+                            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c, r) * D) + e);
+                            const float f = ml.x == NEG_INF ? 0.f : at_ratio(ml.x, M, p.k2);
+                            sl = fmaf(f, ml.y, sl);
+                            o0 = fmaf(f, o.x, o0), o1 = fmaf(f, o.y, o1), o2 = fmaf(f, o.z, o2), o3 = fmaf(f, o.w, o3);
+                        }
+                        const float inv = 1.f / sl;
+                        const int Rr = q * AT_ROWS + r;
+                        uint16_t *dst = p.out + (((size_t)w.b * p.T + w.it.t0 + (Rr >> p.lg_g)) * p.H_q + (w.h << p.lg_g) + (Rr & ((1 << p.lg_g) - 1))) * D;
+                        *reinterpret_cast<uint2 *>(dst + 4 * e) = make_uint2(at_bf16x2(o0 * inv, o1 * inv), at_bf16x2(o2 * inv, o3 * inv));
+                    }
+                }
             }
+            if (either(!ok)) break;
+            next();
         }
         if (!ok && lane == 0) failed();
         __syncwarp();
@@ -764,8 +810,8 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             if (!mbar_wait_bounded(&sh.full[f % NS], (f / NS) & 1, DRAIN_NS)) break;
         if (sh.qfills_used < sh.qfills) mbar_wait_bounded(&sh.qfull, (sh.qfills - 1) & 1, DRAIN_NS);
         AtWalk<NQ> a;
-        a.begin(p, f0, f1, sh.start_base, sh.start_pair);
-        for (; a.seek(p); a.step(p)) {
+        a.begin(p, f0, sh.start_base, sh.start_pair);
+        for (; a.seek(p, f0, f1); a.step(p)) {
             if (a.whole()) continue;
             const int c0 = owner(a.base + AT_SETUP), c1 = owner(a.base + AT_SETUP + a.it.L - 1);
             for (int q = 0; q < NQ && a.live_rows(p) > q * AT_ROWS; ++q) {
