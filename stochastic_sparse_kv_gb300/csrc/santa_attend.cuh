@@ -45,7 +45,7 @@ constexpr int AT_KEYS = 128;              // keys of a tile
 constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
 constexpr int AT_SETUP = 2;               // what an item costs beside its tiles, in tiles
 constexpr int AT_MIN_SHARE = 4;           // a share's least size, in tiles
-constexpr float AT_SLACK = 8.f;           // log2 of the largest p
+constexpr float AT_SLACK = 24.f;          // log2 of the largest p
 constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
 constexpr int AT_MISC = 3072;             // of it for barriers and the like
 constexpr int AT_STAGES_MAX = 8;
@@ -168,6 +168,28 @@ struct AtWalk {
     }
 };
 
+// mbar_wait_bounded for warps that wait long and often beside warps that work: a thread sleeps in
+// the hardware up to AT_NAP ns before it looks at the clock (polling took a third of all issue slots).
+constexpr uint32_t AT_NAP = 20000;
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(AT_NAP)
+            : "memory");
+        if (ok) return true;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit_ns) return false;
+    }
+}
+
 template <int NQ>
 struct AtSmem {
     uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
@@ -222,6 +244,29 @@ __device__ __forceinline__ float at_ratio(float m, float n, float k2)
     return ex2(x);
 }
 
+// Pairs of fp32 numbers in 64 bits, so that one that is used often is packed once.
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2_packed(float a, float b, uint64_t m, uint64_t c)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%2, %3};\n\tfma.rn.f32x2 p, p, %4, %5;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a), "f"(b), "l"(m), "l"(c));
+    return r;
+}
+// a += the low half of w, b += the high half, in fp32
+__device__ __forceinline__ void add_bf16x2(float &a, float &b, uint32_t w)
+{
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.bf16 %0, x, %0;\n\tadd.rn.f32.bf16 %1, y, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(w));
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -249,7 +294,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     constexpr int W_PROD = NQ * 8, W_MMA = W_PROD + 1;
     constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_KEYS), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
     constexpr uint32_t O_COL = 256;            // scores in columns 0-255, outputs behind them
-    constexpr uint32_t P_COL = 0;              // weights over the lower half of their scores
+    constexpr uint32_t P_COL = 32;             // weights over the scores of the middle 64 keys
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(NS >= 4, "ring");
     const float NEG_INF = __int_as_float(0xff800000);
@@ -258,7 +303,10 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     uint8_t *qs = at_shared;
     uint8_t *ring = at_shared + at_qbytes(D, NQ);
     AtSmem<NQ> &sh = *reinterpret_cast<AtSmem<NQ> *>(ring + NS * SB);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // (the same in all lanes, which the compiler sees of a shuffle: such values take no thread's registers)
+    auto uniform = [&](int x) { return __shfl_sync(FULL, x, 0); };
+    const int warp = uniform(tid >> 5);
 
     // ---- the list's size, and where this CTA's share begins
     const int tpi = (NQ * AT_ROWS) >> p.lg_g;
@@ -363,7 +411,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         bool ok = true;
         for (; ok && w.seek(p, f0, f1); w.step(p), ++items) {
             const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
-            if (items > 0 && !__all_sync(FULL, mbar_wait_bounded(&sh.qempty, (items - 1) & 1, p.wait_ns))) {
+            if (items > 0 && !__all_sync(FULL, at_wait(&sh.qempty, (items - 1) & 1, p.wait_ns))) {
                 ok = false;
                 break;
             }
@@ -394,7 +442,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (!__all_sync(FULL, mbar_wait_bounded(&sh.empty[stage], phase, p.wait_ns))) {
+                    if (!__all_sync(FULL, at_wait(&sh.empty[stage], phase, p.wait_ns))) {
                         ok = false;
                         break;
                     }
@@ -413,98 +461,115 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         if (!ok && lane == 0) failed();
         __syncwarp();
     } else if (warp == W_MMA) {
-        // ================= MMA issuer: one thread
-        if (lane == 0) {
-            AtWalk<NQ> w;
-            w.begin(p, f0, sh.start_base, sh.start_pair);
-            int n = 0, items = 0;
-            int nt[2] = {0, 0};       // tiles of each row tile so far
-            int no[2] = {0, 0};       // its items so far
-            const uint32_t qaddr = smem_u32(qs);
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (ok && !mbar_wait_bounded(bar, parity, p.wait_ns)) ok = false;
-                return ok;
-            };
-            // fill f of the ring (K of tile n: 2n, V: 2n + 1) has landed
-            auto landed = [&](int f) {
-                if (wait(&sh.full[f % NS], (f / NS) & 1) && sh.fills_used < f + 1) sh.fills_used = f + 1;
-                return ok;
-            };
-            // (descriptors are made where they are used: kept for the whole loop they fill the registers)
-            auto scores = [&](int q, int f, int buf) {
-                uint64_t k = umma_desc_sw128(smem_u32(ring + (f % NS) * SB)), a = umma_desc_sw128(qaddr + q * AT_ROWS * D * 2);
-                asm volatile("" : "+l"(k), "+l"(a));
+        // ================= MMA issuer: the whole warp waits, one lane issues
+        AtWalk<NQ> w;
+        w.begin(p, f0, sh.start_base, sh.start_pair);
+        int n = 0, items = 0;
+        int nt[2] = {0, 0};       // tiles of each row tile so far
+        int no[2] = {0, 0};       // its items so far
+        const uint32_t qaddr = smem_u32(qs), raddr = smem_u32(ring);
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns));
+            return ok;
+        };
+        int stage = 0, phase = 0, used = 0;   // of the next fill to wait for
+        int k_at = 0, v_at = 0;               // stages of the current K and V
+        // the next fill of the ring (K of tile n: 2n, V: 2n + 1) has landed
+        auto landed = [&]() {
+            const int at = stage;
+            if (wait(&sh.full[stage], phase)) {
+                if (lane == 0) sh.fills_used = ++used;
+                if (++stage == NS) stage = 0, phase ^= 1;
+            }
+            return at;
+        };
+        auto scores = [&](int q, int buf) {
+            if (elect_one()) {
+                const uint64_t k = umma_desc_sw128(raddr + k_at * SB), a = umma_desc_sw128(qaddr + q * AT_ROWS * D * 2);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
                     tc_mma_bf16(tbase + buf * AT_KEYS, a + ((x / 4) * (AT_ROWS * 128) + (x % 4) * 32) / 16,
                                 k + ((x / 4) * PANEL + (x % 4) * 32) / 16, ID_S, x != 0);
                 tc_commit(&sh.sfull[buf]);
-            };
-            for (; ok && w.seek(p, f0, f1); w.step(p), ++items) {
-                const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
-                const int L = w.i1 - w.i0;
-                if (!wait(&sh.qfull, items & 1)) break;
-                sh.qfills_used = items + 1;
-                if (!landed(2 * n)) break;
-                tc_fence_after();
-                for (int q = 0; q < nq; ++q) scores(q, 2 * n, NQ == 2 ? q : nt[0] & 1);
-                tc_commit(&sh.empty[(2 * n) % NS]);
-                if (L == 1) tc_commit(&sh.qempty);
-                for (int j = 0; ok && j < L; ++j, ++n) {
-                    const bool more = j + 1 < L;
-                    if (NQ == 1 && more) {
-                        if (!landed(2 * n + 2)) break;
-                        scores(0, 2 * n + 2, (nt[0] + 1) & 1);
-                        tc_commit(&sh.empty[(2 * n + 2) % NS]);
-                        if (j + 2 == L) tc_commit(&sh.qempty);
-                    }
-                    for (int q = 0; ok && q < nq; ++q) {
-                        const int buf = NQ == 2 ? q : nt[0] & 1;
-                        const uint32_t parity = (NQ == 2 ? nt[q] : nt[0] >> 1) & 1;
-                        if (q == 0 && !landed(2 * n + 1)) break;
-                        if (!wait(&sh.phalf[buf], parity)) break;
-                        if (j == 0 && no[q] > 0 && !wait(&sh.oempty[q], (no[q] - 1) & 1)) break;
-                        tc_fence_after();
-                        uint64_t v = umma_desc_sw128_mn(smem_u32(ring + ((2 * n + 1) % NS) * SB), PANEL);
-                        asm volatile("" : "+l"(v));
-                        // the weights come in two parts: the first 32 and the next 32 of each 64 keys
+            }
+            __syncwarp();
+        };
+        // O += P V over the keys of one part of the weights: the middle 64, then the others
+        auto values = [&](int q, int buf, int part, bool first) {
+            if (elect_one()) {
+                const uint64_t v = umma_desc_sw128_mn(raddr + v_at * SB, PANEL);
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            if (part) {
-                                if (!wait(&sh.pfull[buf], parity)) break;
-                                tc_fence_after();
-                            }
+                for (int y = 0; y < AT_KEYS / 32; ++y) {
+                    const int x = part ? (y & 1) + 6 * (y >> 1) : y + 2;
+                    tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, v + x * (2048 / 16), ID_O,
+                                   !first || part != 0 || y != 0);
+                }
+                if (part) tc_commit(&sh.ofull[q]);
+            }
+            __syncwarp();
+        };
+        auto commit = [&](uint64_t *bar) {
+            if (elect_one()) tc_commit(bar);
+            __syncwarp();
+        };
+        for (; ok && w.seek(p, f0, f1); w.step(p), ++items) {
+            const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
+            const int L = w.i1 - w.i0;
+            if (!wait(&sh.qfull, items & 1)) break;
+            if (lane == 0) sh.qfills_used = items + 1;
+            k_at = landed();
+            if (!ok) break;
+            tc_fence_after();
+            for (int q = 0; q < nq; ++q) scores(q, NQ == 2 ? q : nt[0] & 1);
+            commit(&sh.empty[k_at]);
+            if (L == 1) commit(&sh.qempty);
+            for (int j = 0; ok && j < L; ++j, ++n) {
+                const bool more = j + 1 < L;
+                v_at = landed();
+                if (!ok) break;
+                if (NQ == 1 && more) {
+                    k_at = landed();
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(0, (nt[0] + 1) & 1);
+                    commit(&sh.empty[k_at]);
+                    if (j + 2 == L) commit(&sh.qempty);
+                }
 #pragma unroll
-                            for (int y = 0; y < AT_KEYS / 32; ++y) {
-                                const int x = (y & 1) + 2 * part + 4 * (y >> 1);
-                                tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, v + x * (2048 / 16), ID_O,
-                                               j != 0 || part != 0 || y != 0);
-                            }
-                        }
+                for (int q = 0; q < NQ; ++q) {
+                    if (q >= nq) break;
+                    const int buf = NQ == 2 ? q : nt[0] & 1;
+                    const uint32_t parity = (NQ == 2 ? nt[q] : nt[0] >> 1) & 1;
+                    wait(&sh.phalf[buf], parity);
+                    if (j == 0 && no[q] > 0) wait(&sh.oempty[q], (no[q] - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(q, buf, 0, j == 0);
+                    if (!wait(&sh.pfull[buf], parity)) break;
+                    tc_fence_after();
+                    values(q, buf, 1, j == 0);
+                    ++nt[q];
+                    if (j == 0) ++no[q];
+                    if (NQ == 2 && more) {
+                        if (q == 0) k_at = landed();
                         if (!ok) break;
-                        tc_commit(&sh.ofull[q]);
-                        ++nt[q];
-                        if (j == 0) ++no[q];
+                        tc_fence_after();
+                        scores(q, q);
+                    }
+                    if (q == nq - 1) {
+                        commit(&sh.empty[v_at]);
                         if (NQ == 2 && more) {
-                            if (q == 0 && !landed(2 * n + 2)) break;
-                            tc_fence_after();
-                            scores(q, 2 * n + 2, q);
-                        }
-                        if (q == nq - 1) {
-                            tc_commit(&sh.empty[(2 * n + 1) % NS]);
-                            if (NQ == 2 && more) {
-                                tc_commit(&sh.empty[(2 * n + 2) % NS]);
-                                if (j + 2 == L) tc_commit(&sh.qempty);
-                            }
+                            commit(&sh.empty[k_at]);
+                            if (j + 2 == L) commit(&sh.qempty);
                         }
                     }
                 }
             }
-            if (!ok) failed();
-            tc_commit(&sh.drain);
-            mbar_wait_bounded(&sh.drain, 0u, DRAIN_NS);
         }
+        if (!ok && lane == 0) failed();
+        commit(&sh.drain);
+        if (lane == 0) mbar_wait_bounded(&sh.drain, 0u, DRAIN_NS);
         __syncwarp();
     } else if (warp < W_PROD) {
         // ================= softmax of row tile q: two threads a row (a TMEM lane), 64 scores each
@@ -512,14 +577,13 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         const int pair = 1 + (q << 2) + (warp & 3);      // the named barrier of the two warps of these rows
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t t_o = tbase + lanes + O_COL + q * D;
-        float *swap = sh.swap[q][row];
         AtWalk<NQ> &w = sh.walk[pair - 1];
         const bool leads = half == 0 && lane == 0;       // moves the pair's walk
         int n = 0, n0 = 0;            // tiles of this row tile so far, and of the CTA
         uint32_t wg_phase = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = __all_sync(FULL, mbar_wait_bounded(bar, parity, p.wait_ns));
+            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns));
             return ok;
         };
         // rendezvous of the row tile's warps (a bounded wait, unlike bar.sync)
@@ -552,8 +616,8 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             }
         };
         while (!either(!ok) && sh.more[pair - 1]) {
-            const int live = w.live_rows(p) - q * AT_ROWS;   // of this row tile
-            const int tiles = w.i1 - w.i0;
+            const int live = uniform(w.live_rows(p) - q * AT_ROWS);   // of this row tile
+            const int tiles = uniform(w.i1 - w.i0);
             if (live <= 0) {
                 n0 += tiles;
                 either(false);
@@ -562,14 +626,14 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             }
             const bool warp_live = 32 * (warp & 3) < live;
             const int P = w.it.first + w.it.t0 + ((q * AT_ROWS + row) >> p.lg_g);
-            const int open_hi = w.it.first + w.it.t0 - AT_KEYS, open_lo = p.window > 0 ? w.it.first + w.it.t1 - p.window : -1;
+            const int open_hi = uniform(w.it.first + w.it.t0 - AT_KEYS + 2), open_lo = uniform(p.window > 0 ? w.it.first + w.it.t1 - p.window : -1);
             float m = NEG_INF, l = 0.f;
-            int left = w.it.nsink - w.i0, key = w.it.key(w.i0);
+            int left = uniform(w.it.nsink - w.i0), key = uniform(w.it.key(w.i0));
             for (int i = 0; i < tiles; ++i, ++n) {
                 const int buf = NQ == 2 ? q : n & 1;
                 const uint32_t t_s = tbase + lanes + buf * AT_KEYS;
                 // whether all tokens of the item see all keys of the tile
-                const bool open = key < open_hi + 2 && (key > open_lo || key + AT_KEYS <= p.sinks);
+                const bool open = key < open_hi && (key > open_lo || key + AT_KEYS <= p.sinks);
                 wait(&sh.sfull[buf], (NQ == 2 ? n : n >> 1) & 1);
                 if (!open && q == 0) {
                     // values of V that are not finite become zeros
@@ -595,37 +659,38 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
                 if (warp_live) {
                     tc_fence_after();
-                    uint32_t s[64];
+                    // of its 64 scores a thread keeps 32 and reads the others again: there are 96 registers.
+                    // The weights go over those that are kept.
+                    const int near = 32 + 32 * half, again = 96 * half;
+                    uint32_t kept[32], rest[32];
+                    auto hide = [&](uint32_t (&s)[32], int at) {
+                        const int ub = P + 1 - key - at, lb = (p.window > 0 ? P - p.window + 1 : 0) - key - at, sk = p.sinks - key - at;
+                        const uint32_t seen = at_low_bits(ub) & (~at_low_bits(lb) | at_low_bits(sk));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((seen >> e) & 1u)) s[e] = 0xff800000u;
+                    };
                     float top = NEG_INF;
                     if (ok) {
-                        tmem_ld32_start(t_s + 64 * half, s);
-                        tmem_ld32_start(t_s + 64 * half + 32, s + 32);
-                        tmem_ld_wait();
-                        tmem_ready<64>(s);
+                        tmem_ld32_two(t_s + near, kept, t_s + again, rest);
                         if (!open) {
-                            const int at = key + 64 * half;
-                            const int ub = P + 1 - at, lb = (p.window > 0 ? P - p.window + 1 : 0) - at, sk = p.sinks - at;
-#pragma unroll
-                            for (int c = 0; c < 64; c += 32) {
-                                const uint32_t seen = at_low_bits(ub - c) & (~at_low_bits(lb - c) | at_low_bits(sk - c));
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
-                            }
+                            hide(kept, near);
+                            hide(rest, again);
                         }
                         float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-                        for (int e = 0; e < 64; e += 8)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1]));
+                        for (int e = 0; e < 32; e += 2) {
+                            mx[e & 2] = max3(mx[e & 2], __uint_as_float(kept[e]), __uint_as_float(kept[e + 1]));
+                            mx[(e & 2) + 1] = max3(mx[(e & 2) + 1], __uint_as_float(rest[e]), __uint_as_float(rest[e + 1]));
+                        }
                         top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                     }
                     bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
                     if (either(grow || !ok)) {
                         // both threads of a row take its larger maximum
-                        swap[half] = ok ? top : __int_as_float(0x7fffffff);
+                        sh.swap[q][row][half] = ok ? top : __int_as_float(0x7fffffff);
                         either(false);
-                        const float other = swap[half ^ 1];
+                        const float other = sh.swap[q][row][half ^ 1];
                         ok = ok && __all_sync(FULL, __float_as_int(other) != 0x7fffffff);
                         top = fmaxf(top, other);
                         grow = (top - m) * p.k2 > AT_SLACK;
@@ -650,28 +715,40 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     const float ref = m == NEG_INF ? 0.f : m;
                     const bool far = at_far(ref, p.k2);
                     const float off = far ? 0.f : -(ref * p.k2);
-                    if (__any_sync(FULL, far)) {
-                        const float sub = far ? ref : 0.f;
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
-                    }
+                    const bool any_far = __any_sync(FULL, far);
+                    const float sub = far ? ref : 0.f;
+                    const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < 64; c += 16) {
-                        uint32_t pk[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 x = fma2(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]), p.k2, p.k2, off, off);
-                            pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
-                            add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], bf16lo_to_f32(pk[e]), bf16hi_to_f32(pk[e]));
-                        }
-                        tmem_st8(t_s + P_COL + 32 * half + c / 2, pk);
-                        if (c == 0 || c == 32) continue;
+                    auto told = [&](uint64_t *bar) {
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(c == 48 ? &sh.pfull[buf] : &sh.phalf[buf]);
-                    }
+                        if (lane == 0) mbar_arrive(bar);
+                    };
+                    auto weigh = [&](uint32_t (&s)[32], int at) {
+                        if (any_far) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 32; c += 16) {
+                            uint32_t pk[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 x = fma2_packed(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]), k2k2, offoff);
+                                pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
+                                add_bf16x2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], pk[e]);
+                            }
+                            tmem_st8(t_s + P_COL + (at + c) / 2, pk);
+                        }
+                    };
+                    tmem_ld32_begin(t_s + again, rest);
+                    weigh(kept, near);
+                    told(&sh.phalf[buf]);
+                    tmem_ld32_end(rest);
+                    if (!open) hide(rest, again);
+                    weigh(rest, again);
+                    told(&sh.pfull[buf]);
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 } else {
                     if (!ok) break;
@@ -683,7 +760,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     }
                 }
                 key += AT_KEYS;
-                if (--left == 0) key = w.it.tlo * AT_KEYS;
+                if (--left == 0) key = uniform(w.it.tlo * AT_KEYS);
             }
             n0 += tiles;
             // (a parity tells only two phases apart.  The last scores follow the product of two tiles
@@ -691,9 +768,9 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             if (NQ == 1 && n > 1) wait(&sh.ofull[q], (n - 2) & 1);
             wait(&sh.ofull[q], (n - 1) & 1);
             tc_fence_after();
-            swap[half] = l;
+            sh.swap[q][row][half] = l;
             if (either(!ok)) break;
-            l += swap[half ^ 1];   // (written again after another rendezvous)
+            l += sh.swap[q][row][half ^ 1];   // (written again after another rendezvous)
 
             // ---- the item's (or the piece's) sums
             const bool whole = w.whole(), mine_live = row < live;
