@@ -42,6 +42,7 @@ namespace santa {
 
 constexpr int AT_ROWS = 128;              // rows of a tile: (token, head) pairs
 constexpr int AT_KEYS = 128;              // keys of a tile
+constexpr int AT_SUB = 64;                // keys of a part of it: the unit of scores and weights
 constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
 constexpr int AT_SETUP = 2;               // what an item costs beside its tiles, in tiles
 constexpr int AT_MIN_SHARE = 4;           // a share's least size, in tiles
@@ -50,7 +51,8 @@ constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
 constexpr int AT_MISC = 3072;             // of it for barriers and the like
 constexpr int AT_STAGES_MAX = 8;
 
-__host__ __device__ constexpr int at_threads(int NQ) { return NQ * 256 + 64; }
+// four softmax warps and an MMA warp a row tile, and the producer
+__host__ __device__ constexpr int at_threads(int NQ) { return NQ * 160 + 32; }
 __host__ __device__ constexpr int at_qbytes(int D, int NQ) { return NQ * AT_ROWS * D * 2; }
 __host__ __device__ constexpr int at_stage_bytes(int D) { return AT_KEYS * D * 2; }
 __host__ __device__ constexpr int at_stages(int D, int NQ)
@@ -78,6 +80,7 @@ struct AttendParams {
     int window, sinks, piece_rows;
     float k2;                     // scale log2 e
     uint64_t wait_ns;
+    int tries;                    // of a wait between two looks at the clock
 };
 
 // A batch row's tokens; none where pos and counts leave the cache.
@@ -160,60 +163,48 @@ struct AtWalk {
     }
     __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == it.L; }
     __device__ __forceinline__ int live_rows(const AttendParams &p) const { return (it.t1 - it.t0 + 1) << p.lg_g; }
-    // whether all tokens of the item see all keys of tile i
+    // parts of the tile at `key` that hold a key that some token sees (the last tile may end early)
+    __device__ __forceinline__ int parts(int key) const { return key + AT_SUB <= it.first + it.t1 ? 2 : 1; }
+    // whether all tokens of the item see all keys of the part at `key`
     __device__ __forceinline__ bool open(const AttendParams &p, int key) const
     {
-        return key + AT_KEYS - 1 <= it.first + it.t0 &&
-               (p.window == 0 || key > it.first + it.t1 - p.window || key + AT_KEYS <= p.sinks);
+        return key + AT_SUB - 1 <= it.first + it.t0 &&
+               (p.window == 0 || key > it.first + it.t1 - p.window || key + AT_SUB <= p.sinks);
     }
 };
 
-// mbar_wait_bounded for warps that wait long and often beside warps that work: a thread sleeps in
-// the hardware up to AT_NAP ns before it looks at the clock (polling took a third of all issue slots).
-constexpr uint32_t AT_NAP = 20000;
-__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+// mbar_wait_bounded for warps that wait long and often beside warps that work: the clock is looked at
+// after `tries` tries only (reading it at each took more issue slots than the work).
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns, int tries)
 {
     uint64_t t0 = 0;
     for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(AT_NAP)
-            : "memory");
-        if (ok) return true;
+#pragma unroll 1
+        for (int i = 0; i < tries; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t = globaltimer_ns();
         if (t0 == 0) t0 = t;
         if (t - t0 > limit_ns) return false;
     }
 }
 
-template <int NQ>
 struct AtSmem {
     uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
     uint64_t qfull, qempty;
-    uint64_t sfull[2], phalf[2], pfull[2];  // NQ = 2: of a row tile; NQ = 1: of a score buffer
-    uint64_t ofull[2], oempty[2], wg[2];
-    uint64_t drain;
-    long long total, start_base;
-    int start_pair, last;
+    uint64_t sfull[2][2], pfull[2][2];   // [row tile][score buffer]
+    uint64_t ofull[2], oempty[2], wg[2], drain[2];
+    long long sums[16];
+    long long start_base;
+    int start_pair;
     uint32_t tmem;
     int bad_v;                    // a value that is not finite was set to zero
     int timeout;
-    int fills, fills_used;        // stages filled, and their fills seen by the MMA thread
-    int qfills, qfills_used;
+    int fills, fills_used[2];     // stages filled, and their fills seen by the MMA warps
+    int qfills, qfills_used[2];
     int is_last[2];
     int arrived[2][2];            // [slot][row tile]: arrivals of this CTA's pieces
-    AtWalk<NQ> walk[NQ * 4];      // of the pairs of softmax warps: not in their registers
-    int more[NQ * 4];
-    union {
-        long long sums[20];
-        float swap[NQ][AT_ROWS][2];   // between the two threads of a row: maxima, sums
-    };
 };
-static_assert(sizeof(AtSmem<2>) <= AT_MISC && sizeof(AtSmem<1>) <= AT_MISC, "barriers and the like");
+static_assert(sizeof(AtSmem) <= AT_MISC, "barriers and the like");
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -291,10 +282,9 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     constexpr int SB = at_stage_bytes(D);
     constexpr int PANELS = D / 64;
     constexpr int PANEL = AT_KEYS * 128;       // bytes of 64 columns of a tile
-    constexpr int W_PROD = NQ * 8, W_MMA = W_PROD + 1;
-    constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_KEYS), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
-    constexpr uint32_t O_COL = 256;            // scores in columns 0-255, outputs behind them
-    constexpr uint32_t P_COL = 32;             // weights over the scores of the middle 64 keys
+    constexpr int W_MMA = NQ * 4, W_PROD = W_MMA + NQ;   // warps: softmax, MMA (one a row tile), producer
+    constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_SUB), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
+    constexpr uint32_t O_COL = 256;            // two score buffers a row tile in columns 0-255, outputs behind them
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(NS >= 4, "ring");
     const float NEG_INF = __int_as_float(0xff800000);
@@ -302,11 +292,9 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     extern __shared__ __align__(1024) uint8_t at_shared[];
     uint8_t *qs = at_shared;
     uint8_t *ring = at_shared + at_qbytes(D, NQ);
-    AtSmem<NQ> &sh = *reinterpret_cast<AtSmem<NQ> *>(ring + NS * SB);
+    AtSmem &sh = *reinterpret_cast<AtSmem *>(ring + NS * SB);
     const int tid = threadIdx.x, lane = tid & 31;
-    // (the same in all lanes, which the compiler sees of a shuffle: such values take no thread's registers)
-    auto uniform = [&](int x) { return __shfl_sync(FULL, x, 0); };
-    const int warp = uniform(tid >> 5);
+    const int warp = __shfl_sync(FULL, tid >> 5, 0);
 
     // ---- the list's size, and where this CTA's share begins
     const int tpi = (NQ * AT_ROWS) >> p.lg_g;
@@ -374,23 +362,25 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         tma_prefetch_map(&tm_v);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], 1);
+            mbar_init(&sh.empty[s], NQ);
         }
         mbar_init(&sh.qfull, 1);
-        mbar_init(&sh.qempty, 1);
+        mbar_init(&sh.qempty, NQ);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.sfull[i], 1);
-            mbar_init(&sh.phalf[i], 8);
-            mbar_init(&sh.pfull[i], 8);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&sh.sfull[i][j], 1);
+                mbar_init(&sh.pfull[i][j], 4);
+                sh.arrived[i][j] = 0;
+            }
             mbar_init(&sh.ofull[i], 1);
-            mbar_init(&sh.oempty[i], 8);
-            mbar_init(&sh.wg[i], 8);
-            for (int j = 0; j < 2; ++j) sh.arrived[i][j] = 0;
+            mbar_init(&sh.oempty[i], 4);
+            mbar_init(&sh.wg[i], 4);
+            mbar_init(&sh.drain[i], 1);
+            sh.fills_used[i] = sh.qfills_used[i] = 0;
         }
-        mbar_init(&sh.drain, 1);
         mbar_fence_init();
         sh.bad_v = sh.timeout = 0;
-        sh.fills = sh.fills_used = sh.qfills = sh.qfills_used = 0;
+        sh.fills = sh.qfills = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -411,7 +401,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         bool ok = true;
         for (; ok && w.seek(p, f0, f1); w.step(p), ++items) {
             const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
-            if (items > 0 && !__all_sync(FULL, at_wait(&sh.qempty, (items - 1) & 1, p.wait_ns))) {
+            if (items > 0 && !__all_sync(FULL, at_wait(&sh.qempty, (items - 1) & 1, p.wait_ns, p.tries))) {
                 ok = false;
                 break;
             }
@@ -442,7 +432,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (!__all_sync(FULL, at_wait(&sh.empty[stage], phase, p.wait_ns))) {
+                    if (!__all_sync(FULL, at_wait(&sh.empty[stage], phase, p.wait_ns, p.tries))) {
                         ok = false;
                         break;
                     }
@@ -460,52 +450,50 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         }
         if (!ok && lane == 0) failed();
         __syncwarp();
-    } else if (warp == W_MMA) {
-        // ================= MMA issuer: the whole warp waits, one lane issues
+    } else if (warp >= W_MMA) {
+        // ================= MMA issuer of row tile q: the whole warp waits, one lane issues
+        const int q = warp - W_MMA;
         AtWalk<NQ> w;
         w.begin(p, f0, sh.start_base, sh.start_pair);
-        int n = 0, items = 0;
-        int nt[2] = {0, 0};       // tiles of each row tile so far
-        int no[2] = {0, 0};       // its items so far
-        const uint32_t qaddr = smem_u32(qs), raddr = smem_u32(ring);
+        int items = 0;
+        int nu = 0, no = 0;                   // parts and items of this row tile so far
+        int stage = 0, phase = 0, used = 0;   // of the next fill to wait for
+        const uint32_t qaddr = smem_u32(qs) + q * AT_ROWS * D * 2, raddr = smem_u32(ring);
+        const uint32_t t_o = tbase + O_COL + q * D, t_s = tbase + q * AT_KEYS;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns));
+            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns, p.tries));
             return ok;
         };
-        int stage = 0, phase = 0, used = 0;   // of the next fill to wait for
-        int k_at = 0, v_at = 0;               // stages of the current K and V
-        // the next fill of the ring (K of tile n: 2n, V: 2n + 1) has landed
+        // the next fill of the ring (K of a tile, then its V) has landed; its stage
         auto landed = [&]() {
             const int at = stage;
             if (wait(&sh.full[stage], phase)) {
-                if (lane == 0) sh.fills_used = ++used;
+                if (lane == 0) sh.fills_used[q] = ++used;
                 if (++stage == NS) stage = 0, phase ^= 1;
             }
             return at;
         };
-        auto scores = [&](int q, int buf) {
+        // S = Q K^T over part h of the keys of a stage
+        auto scores = [&](int at, int h, int buf) {
             if (elect_one()) {
-                const uint64_t k = umma_desc_sw128(raddr + k_at * SB), a = umma_desc_sw128(qaddr + q * AT_ROWS * D * 2);
+                const uint64_t k = umma_desc_sw128(raddr + at * SB + h * (AT_SUB * 128)), a = umma_desc_sw128(qaddr);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    tc_mma_bf16(tbase + buf * AT_KEYS, a + ((x / 4) * (AT_ROWS * 128) + (x % 4) * 32) / 16,
+                    tc_mma_bf16(t_s + buf * AT_SUB, a + ((x / 4) * (AT_ROWS * 128) + (x % 4) * 32) / 16,
                                 k + ((x / 4) * PANEL + (x % 4) * 32) / 16, ID_S, x != 0);
-                tc_commit(&sh.sfull[buf]);
+                tc_commit(&sh.sfull[q][buf]);
             }
             __syncwarp();
         };
-        // O += P V over the keys of one part of the weights: the middle 64, then the others
-        auto values = [&](int q, int buf, int part, bool first) {
+        // O += P V over part h
+        auto values = [&](int at, int h, int buf, bool first) {
             if (elect_one()) {
-                const uint64_t v = umma_desc_sw128_mn(raddr + v_at * SB, PANEL);
+                const uint64_t v = umma_desc_sw128_mn(raddr + at * SB + h * (AT_SUB * 128), PANEL);
 #pragma unroll
-                for (int y = 0; y < AT_KEYS / 32; ++y) {
-                    const int x = part ? (y & 1) + 6 * (y >> 1) : y + 2;
-                    tc_mma_bf16_ta(tbase + O_COL + q * D, tbase + buf * AT_KEYS + P_COL + x * 8, v + x * (2048 / 16), ID_O,
-                                   !first || part != 0 || y != 0);
-                }
-                if (part) tc_commit(&sh.ofull[q]);
+                for (int x = 0; x < AT_SUB / 16; ++x)
+                    tc_mma_bf16_ta(t_o, t_s + buf * AT_SUB + x * 8, v + x * (2048 / 16), ID_O, !first || x != 0);
+                tc_commit(&sh.ofull[q]);
             }
             __syncwarp();
         };
@@ -514,76 +502,76 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             __syncwarp();
         };
         for (; ok && w.seek(p, f0, f1); w.step(p), ++items) {
-            const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
             const int L = w.i1 - w.i0;
             if (!wait(&sh.qfull, items & 1)) break;
-            if (lane == 0) sh.qfills_used = items + 1;
-            k_at = landed();
+            if (lane == 0) sh.qfills_used[q] = items + 1;
+            if (NQ == 2 && w.live_rows(p) <= q * AT_ROWS) {
+                // no row of this tile lives: its stages are given back as they come
+                if (lane == 0) mbar_arrive(&sh.qempty);
+                for (int f = 0; ok && f < 2 * L; ++f) {
+                    const int at = landed();
+                    if (ok && lane == 0) mbar_arrive(&sh.empty[at]);
+                }
+                continue;
+            }
+            int k_at = landed(), parts = w.parts(w.it.key(w.i0));
             if (!ok) break;
             tc_fence_after();
-            for (int q = 0; q < nq; ++q) scores(q, NQ == 2 ? q : nt[0] & 1);
-            commit(&sh.empty[k_at]);
-            if (L == 1) commit(&sh.qempty);
-            for (int j = 0; ok && j < L; ++j, ++n) {
-                const bool more = j + 1 < L;
-                v_at = landed();
-                if (!ok) break;
-                if (NQ == 1 && more) {
-                    k_at = landed();
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(0, (nt[0] + 1) & 1);
-                    commit(&sh.empty[k_at]);
-                    if (j + 2 == L) commit(&sh.qempty);
-                }
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    if (q >= nq) break;
-                    const int buf = NQ == 2 ? q : nt[0] & 1;
-                    const uint32_t parity = (NQ == 2 ? nt[q] : nt[0] >> 1) & 1;
-                    wait(&sh.phalf[buf], parity);
-                    if (j == 0 && no[q] > 0) wait(&sh.oempty[q], (no[q] - 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    values(q, buf, 0, j == 0);
-                    if (!wait(&sh.pfull[buf], parity)) break;
-                    tc_fence_after();
-                    values(q, buf, 1, j == 0);
-                    ++nt[q];
-                    if (j == 0) ++no[q];
-                    if (NQ == 2 && more) {
-                        if (q == 0) k_at = landed();
+            scores(k_at, 0, nu & 1);
+            if (parts == 1) {
+                commit(&sh.empty[k_at]);
+                if (L == 1) commit(&sh.qempty);
+            }
+            for (int j = 0; ok && j < L; ++j) {
+                int v_at = 0;
+                const int np = parts;
+                for (int h = 0; h < np; ++h, ++nu) {
+                    // the next part's scores are under way before this one's weights are waited for
+                    if (h == 0) {
+                        if (np == 2) {
+                            scores(k_at, 1, (nu + 1) & 1);
+                            commit(&sh.empty[k_at]);
+                            if (j + 1 == L) commit(&sh.qempty);
+                        }
+                        v_at = landed();
+                    }
+                    if (h == np - 1 && j + 1 < L) {
+                        k_at = landed();
                         if (!ok) break;
                         tc_fence_after();
-                        scores(q, q);
-                    }
-                    if (q == nq - 1) {
-                        commit(&sh.empty[v_at]);
-                        if (NQ == 2 && more) {
+                        parts = w.parts(w.it.key(w.i0 + j + 1));
+                        scores(k_at, 0, (nu + 1) & 1);
+                        if (parts == 1) {
                             commit(&sh.empty[k_at]);
                             if (j + 2 == L) commit(&sh.qempty);
                         }
                     }
+                    wait(&sh.pfull[q][nu & 1], (nu >> 1) & 1);
+                    if (j == 0 && h == 0 && no > 0) wait(&sh.oempty[q], (no - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(v_at, h, nu & 1, j == 0 && h == 0);
+                    if (h == np - 1) commit(&sh.empty[v_at]);
                 }
             }
+            ++no;
         }
         if (!ok && lane == 0) failed();
-        commit(&sh.drain);
-        if (lane == 0) mbar_wait_bounded(&sh.drain, 0u, DRAIN_NS);
+        commit(&sh.drain[q]);
+        if (lane == 0) mbar_wait_bounded(&sh.drain[q], 0u, DRAIN_NS);
         __syncwarp();
-    } else if (warp < W_PROD) {
-        // ================= softmax of row tile q: two threads a row (a TMEM lane), 64 scores each
-        const int q = warp >> 3, half = (warp >> 2) & 1, row = tid & 127, wg_tid = tid & 255;
-        const int pair = 1 + (q << 2) + (warp & 3);      // the named barrier of the two warps of these rows
+    } else {
+        // ================= softmax of row tile q: a thread a row, which is a lane of TMEM
+        const int q = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t t_o = tbase + lanes + O_COL + q * D;
-        AtWalk<NQ> &w = sh.walk[pair - 1];
-        const bool leads = half == 0 && lane == 0;       // moves the pair's walk
-        int n = 0, n0 = 0;            // tiles of this row tile so far, and of the CTA
+        AtWalk<NQ> w;
+        w.begin(p, f0, sh.start_base, sh.start_pair);
+        int n = 0, n0 = 0;            // parts of this row tile so far; fills of the ring before the item
         uint32_t wg_phase = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns));
+            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns, p.tries));
             return ok;
         };
         // rendezvous of the row tile's warps (a bounded wait, unlike bar.sync)
@@ -594,144 +582,94 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             wg_phase ^= 1u;
             return ok;
         };
-        // whether x holds for any thread of the pair of warps.  Both warps make the same calls, whatever
-        // happens: a failed wait is told to the other warp by one of them
-        auto either = [&](bool x) {
-            uint32_t r;
-            asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %2, 0;\n\t"
-                         "barrier.cta.red.or.pred b, %1, 64, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-                         : "=r"(r)
-                         : "r"(pair), "r"((uint32_t)x)
-                         : "memory");
-            return r != 0;
-        };
-        if (leads) {
-            w.begin(p, f0, sh.start_base, sh.start_pair);
-            sh.more[pair - 1] = w.seek(p, f0, f1);
-        }
-        auto next = [&]() {
-            if (leads) {
-                w.step(p);
-                sh.more[pair - 1] = w.seek(p, f0, f1);
-            }
-        };
-        while (!either(!ok) && sh.more[pair - 1]) {
-            const int live = uniform(w.live_rows(p) - q * AT_ROWS);   // of this row tile
-            const int tiles = uniform(w.i1 - w.i0);
-            if (live <= 0) {
-                n0 += tiles;
-                either(false);
-                next();
-                continue;
-            }
+        for (; ok && w.seek(p, f0, f1); n0 += 2 * (w.i1 - w.i0), w.step(p)) {
+            const int live = w.live_rows(p) - q * AT_ROWS;   // of this row tile
+            if (live <= 0) continue;
             const bool warp_live = 32 * (warp & 3) < live;
             const int P = w.it.first + w.it.t0 + ((q * AT_ROWS + row) >> p.lg_g);
-            const int open_hi = uniform(w.it.first + w.it.t0 - AT_KEYS + 2), open_lo = uniform(p.window > 0 ? w.it.first + w.it.t1 - p.window : -1);
             float m = NEG_INF, l = 0.f;
-            int left = uniform(w.it.nsink - w.i0), key = uniform(w.it.key(w.i0));
-            for (int i = 0; i < tiles; ++i, ++n) {
-                const int buf = NQ == 2 ? q : n & 1;
-                const uint32_t t_s = tbase + lanes + buf * AT_KEYS;
-                // whether all tokens of the item see all keys of the tile
-                const bool open = key < open_hi && (key > open_lo || key + AT_KEYS <= p.sinks);
-                wait(&sh.sfull[buf], (NQ == 2 ? n : n >> 1) & 1);
-                if (!open && q == 0) {
-                    // values of V that are not finite become zeros
-                    const int f = 2 * (n0 + i) + 1;
-                    if (wait(&sh.full[f % NS], (f / NS) & 1)) {
-                        uint8_t *v = ring + (f % NS) * SB;
-#pragma unroll 2
-                        for (int c = wg_tid; c < SB / 16; c += 256) {
-                            uint4 x = reinterpret_cast<uint4 *>(v)[c];
+            bool begun = false;       // O holds sums
+            for (int i = w.i0; ok && i < w.i1; ++i) {
+                const int tile = w.it.key(i), parts = w.parts(tile);
+                for (int h = 0; h < parts; ++h, ++n) {
+                    const int key = tile + h * AT_SUB, buf = n & 1;
+                    const uint32_t t_s = tbase + lanes + q * AT_KEYS + buf * AT_SUB;
+                    const bool open = w.open(p, key);
+                    if (!wait(&sh.sfull[q][buf], (n >> 1) & 1)) break;
+                    if (!open) {
+                        // values of V that are not finite become zeros (both row tiles' warps look at all of
+                        // them: what the other has set to zero is zero, or becomes it twice)
+                        const int f = n0 + 2 * (i - w.i0) + 1;
+                        if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
+                        uint8_t *v = ring + (f % NS) * SB + h * (AT_SUB * 128);
+#pragma unroll 4
+                        for (int c = row; c < AT_SUB * D / 8; c += 128) {
+                            uint4 &at = *reinterpret_cast<uint4 *>(v + (c / (AT_SUB * 8)) * PANEL + (c % (AT_SUB * 8)) * 16);
+                            uint4 x = at;
                             const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
                             if (b0 | b1 | b2 | b3) {
                                 x.x &= ~((b0 >> 15) * 0xffffu);
                                 x.y &= ~((b1 >> 15) * 0xffffu);
                                 x.z &= ~((b2 >> 15) * 0xffffu);
                                 x.w &= ~((b3 >> 15) * 0xffffu);
-                                reinterpret_cast<uint4 *>(v)[c] = x;
-                                const int j = key + (c % (PANEL / 16)) / 8;
+                                at = x;
+                                const int j = key + (c % (AT_SUB * 8)) / 8;
                                 if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
                             }
                         }
                         fence_proxy_async_smem();
                     }
-                }
-                if (warp_live) {
-                    tc_fence_after();
-                    // of its 64 scores a thread keeps 32 and reads the others again: there are 96 registers.
-                    // The weights go over those that are kept.
-                    const int near = 32 + 32 * half, again = 96 * half;
-                    uint32_t kept[32], rest[32];
-                    auto hide = [&](uint32_t (&s)[32], int at) {
-                        const int ub = P + 1 - key - at, lb = (p.window > 0 ? P - p.window + 1 : 0) - key - at, sk = p.sinks - key - at;
-                        const uint32_t seen = at_low_bits(ub) & (~at_low_bits(lb) | at_low_bits(sk));
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((seen >> e) & 1u)) s[e] = 0xff800000u;
-                    };
-                    float top = NEG_INF;
-                    if (ok) {
-                        tmem_ld32_two(t_s + near, kept, t_s + again, rest);
+                    if (warp_live) {
+                        tc_fence_after();
+                        uint32_t s[AT_SUB];
+                        tmem_ld32<AT_SUB>(t_s, s);
                         if (!open) {
-                            hide(kept, near);
-                            hide(rest, again);
+                            const int ub = P + 1 - key, lb = (p.window > 0 ? P - p.window + 1 : 0) - key, sk = p.sinks - key;
+#pragma unroll
+                            for (int c = 0; c < AT_SUB; c += 32) {
+                                const uint32_t seen = at_low_bits(ub - c) & (~at_low_bits(lb - c) | at_low_bits(sk - c));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
+                            }
                         }
                         float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            mx[e & 2] = max3(mx[e & 2], __uint_as_float(kept[e]), __uint_as_float(kept[e + 1]));
-                            mx[(e & 2) + 1] = max3(mx[(e & 2) + 1], __uint_as_float(rest[e]), __uint_as_float(rest[e + 1]));
-                        }
-                        top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                    }
-                    bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
-                    if (either(grow || !ok)) {
-                        // both threads of a row take its larger maximum
-                        sh.swap[q][row][half] = ok ? top : __int_as_float(0x7fffffff);
-                        either(false);
-                        const float other = sh.swap[q][row][half ^ 1];
-                        ok = ok && __all_sync(FULL, __float_as_int(other) != 0x7fffffff);
-                        top = fmaxf(top, other);
-                        grow = (top - m) * p.k2 > AT_SLACK;
-                        const float f = grow ? (m == NEG_INF ? 0.f : at_ratio(m, top, p.k2)) : 1.f;
-                        if (grow) m = top;
-                        l *= f;
-                        if (i > 0 && wait(&sh.ofull[q], (n - 1) & 1)) {
-                            tc_fence_after();
-                            // (few columns at a time: the scores keep their registers)
-#pragma unroll 1
-                            for (uint32_t at = t_o + half * (D / 2); at < t_o + (half + 1) * (D / 2); at += 8) {
-                                uint32_t o[8];
-                                tmem_ld32<8>(at, o);
+                        for (int e = 0; e < AT_SUB; e += 8)
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st8(at, o);
+                            for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1]));
+                        const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                        const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
+                        if (__any_sync(FULL, grow)) {
+                            const float f = grow ? (m == NEG_INF ? 0.f : at_ratio(m, top, p.k2)) : 1.f;
+                            if (grow) m = top;
+                            l *= f;
+                            if (begun) {
+                                if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (uint32_t at = t_o; at < t_o + D; at += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld32<16>(at, o);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st8(at, o);
+                                    tmem_st8(at + 8, o + 8);
+                                }
                             }
                         }
-                        if (either(!ok)) ok = false;
-                        if (!ok) break;
-                    }
-                    const float ref = m == NEG_INF ? 0.f : m;
-                    const bool far = at_far(ref, p.k2);
-                    const float off = far ? 0.f : -(ref * p.k2);
-                    const bool any_far = __any_sync(FULL, far);
-                    const float sub = far ? ref : 0.f;
-                    const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    auto told = [&](uint64_t *bar) {
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar);
-                    };
-                    auto weigh = [&](uint32_t (&s)[32], int at) {
-                        if (any_far) {
+                        const float ref = m == NEG_INF ? 0.f : m;
+                        const bool far = at_far(ref, p.k2);
+                        const float off = far ? 0.f : -(ref * p.k2);
+                        if (__any_sync(FULL, far)) {
+                            const float sub = far ? ref : 0.f;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
+                            for (int e = 0; e < AT_SUB; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
                         }
+                        const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int c = 0; c < 32; c += 16) {
+                        for (int c = 0; c < AT_SUB; c += 16) {
                             uint32_t pk[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
@@ -739,38 +677,22 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                                 pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
                                 add_bf16x2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], pk[e]);
                             }
-                            tmem_st8(t_s + P_COL + (at + c) / 2, pk);
+                            tmem_st8(t_s + c / 2, pk);
                         }
-                    };
-                    tmem_ld32_begin(t_s + again, rest);
-                    weigh(kept, near);
-                    told(&sh.phalf[buf]);
-                    tmem_ld32_end(rest);
-                    if (!open) hide(rest, again);
-                    weigh(rest, again);
-                    told(&sh.pfull[buf]);
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                } else {
-                    if (!ok) break;
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tmem_st_wait();
+                    }
+                    begun = true;
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sh.phalf[buf]);
-                        mbar_arrive(&sh.pfull[buf]);
-                    }
+                    if (lane == 0) mbar_arrive(&sh.pfull[q][buf]);
                 }
-                key += AT_KEYS;
-                if (--left == 0) key = uniform(w.it.tlo * AT_KEYS);
             }
-            n0 += tiles;
-            // (a parity tells only two phases apart.  The last scores follow the product of two tiles
-            // before with two buffers, of the tile before with one: the phase between is waited for)
-            if (NQ == 1 && n > 1) wait(&sh.ofull[q], (n - 2) & 1);
-            wait(&sh.ofull[q], (n - 1) & 1);
+            // (a parity tells only two phases apart, and the last scores follow the product of two parts
+            // before: the phase between is waited for)
+            if (n > 1) wait(&sh.ofull[q], (n - 2) & 1);
+            if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
             tc_fence_after();
-            sh.swap[q][row][half] = l;
-            if (either(!ok)) break;
-            l += sh.swap[q][row][half ^ 1];   // (written again after another rendezvous)
 
             // ---- the item's (or the piece's) sums
             const bool whole = w.whole(), mine_live = row < live;
@@ -782,15 +704,15 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 const size_t at_piece = (size_t)(blockIdx.x * 2 + slot) * p.piece_rows + R;
                 uint16_t *out = p.out + (((size_t)w.b * p.T + w.it.t0 + (R >> p.lg_g)) * p.H_q + (w.h << p.lg_g) + (R & ((1 << p.lg_g) - 1))) * D;
 #pragma unroll 1
-                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                for (int c = 0; c < D; c += 16) {
                     uint32_t o[16];
                     tmem_ld32<16>(t_o + c, o);
                     if (fix && mine_live) {
                         // values that are not finite, of the keys that this row sees
-                        for (int x = w.i0; x < w.i1; ++x) {
-                            const int first = w.it.key(x);
+                        for (int x = 2 * w.i0; x < 2 * w.i1; ++x) {
+                            const int first = w.it.key(x / 2) + (x & 1) * AT_SUB;
                             if (w.open(p, first)) continue;
-                            for (int j = first; j < first + AT_KEYS && j <= P; ++j) {
+                            for (int j = first; j < first + AT_SUB && j <= P; ++j) {
                                 if (p.window > 0 && j <= P - p.window && j >= p.sinks) continue;
                                 const int entry = p.table[(size_t)w.b * p.cols + (j >> p.page_shift)];
                                 if ((unsigned)entry >= (unsigned)p.n_pages) continue;
@@ -823,17 +745,17 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                             __stcg(reinterpret_cast<uint4 *>(piece + c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                     }
                 }
-                if (!whole && mine_live && half == 0) __stcg(reinterpret_cast<float2 *>(p.part_ml + at_piece * 2), make_float2(m, l));
+                if (!whole && mine_live) __stcg(reinterpret_cast<float2 *>(p.part_ml + at_piece * 2), make_float2(m, l));
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.oempty[q]);
 
             // ---- a piece: the last CTA of the item to arrive joins them all
-            const int c0 = whole ? 0 : owner(w.base + AT_SETUP), c1 = whole ? 0 : owner(w.base + AT_SETUP + w.it.L - 1);
             if (!whole) {
+                const int c0 = owner(w.base + AT_SETUP), c1 = owner(w.base + AT_SETUP + w.it.L - 1);
                 __threadfence();
-                if (wg_sync() && wg_tid == 0) {
+                if (wg_sync() && row == 0) {
                     int32_t *arrivals = p.ctrl + CTRL_GROUPS + 2 * c0 + q;
                     sh.arrived[slot][q] = 1;
                     const bool last = atomicAdd(arrivals, 1) == c1 - c0;
@@ -845,7 +767,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     __threadfence();
                     const int rows_live = min(live, AT_ROWS);
                     auto at = [&](int c, int r) { return (size_t)(c * 2 + (c == c0 ? 1 : 0)) * p.piece_rows + q * AT_ROWS + r; };
-                    for (int x = wg_tid; x < rows_live * (D / 4); x += 256) {
+                    for (int x = row; x < rows_live * (D / 4); x += 128) {
                         const int r = x / (D / 4), e = x % (D / 4);
                         float M = NEG_INF;
 #pragma unroll 4
@@ -866,8 +788,6 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     }
                 }
             }
-            if (either(!ok)) break;
-            next();
         }
         if (!ok && lane == 0) failed();
         __syncwarp();
@@ -883,9 +803,10 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         tmem_dealloc(tbase, 512);
     }
     if (warp == W_PROD && lane == 0 && sh.timeout) {
-        for (int f = sh.fills_used; f < sh.fills; ++f)
+        for (int f = NQ == 2 ? min(sh.fills_used[0], sh.fills_used[1]) : sh.fills_used[0]; f < sh.fills; ++f)
             if (!mbar_wait_bounded(&sh.full[f % NS], (f / NS) & 1, DRAIN_NS)) break;
-        if (sh.qfills_used < sh.qfills) mbar_wait_bounded(&sh.qfull, (sh.qfills - 1) & 1, DRAIN_NS);
+        if (sh.qfills_used[0] < sh.qfills || (NQ == 2 && sh.qfills_used[1] < sh.qfills))
+            mbar_wait_bounded(&sh.qfull, (sh.qfills - 1) & 1, DRAIN_NS);
         AtWalk<NQ> a;
         a.begin(p, f0, sh.start_base, sh.start_pair);
         for (; a.seek(p, f0, f1); a.step(p)) {
