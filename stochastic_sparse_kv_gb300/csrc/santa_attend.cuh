@@ -42,7 +42,7 @@ namespace santa {
 
 constexpr int AT_ROWS = 128;              // rows of a tile: (token, head) pairs
 constexpr int AT_KEYS = 128;              // keys of a tile
-constexpr int AT_SUB = 64;                // keys of a part of it: the unit of scores and weights
+constexpr int AT_SUB = 64;                // keys of one of its halves
 constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
 constexpr int AT_SETUP = 2;               // what an item costs beside its tiles, in tiles
 constexpr int AT_MIN_SHARE = 4;           // a share's least size, in tiles
@@ -163,13 +163,15 @@ struct AtWalk {
     }
     __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == it.L; }
     __device__ __forceinline__ int live_rows(const AttendParams &p) const { return (it.t1 - it.t0 + 1) << p.lg_g; }
-    // parts of the tile at `key` that hold a key that some token sees (the last tile may end early)
-    __device__ __forceinline__ int parts(int key) const { return key + AT_SUB <= it.first + it.t1 ? 2 : 1; }
-    // whether all tokens of the item see all keys of the part at `key`
+    // whether all tokens of the item see key j; all keys of the tile at `key`
+    __device__ __forceinline__ bool all_see(const AttendParams &p, int j) const
+    {
+        return j <= it.first + it.t0 && (p.window == 0 || j > it.first + it.t1 - p.window || j < p.sinks);
+    }
     __device__ __forceinline__ bool open(const AttendParams &p, int key) const
     {
-        return key + AT_SUB - 1 <= it.first + it.t0 &&
-               (p.window == 0 || key > it.first + it.t1 - p.window || key + AT_SUB <= p.sinks);
+        return key + AT_KEYS - 1 <= it.first + it.t0 &&
+               (p.window == 0 || key > it.first + it.t1 - p.window || key + AT_KEYS <= p.sinks);
     }
 };
 
@@ -191,8 +193,9 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t
 struct AtSmem {
     uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
     uint64_t qfull, qempty;
-    uint64_t sfull[2][2], pfull[2][2];   // [row tile][score buffer]
+    uint64_t sfull[2], phalf[2], pfull[2];   // of a score buffer (NQ = 2: one a row tile)
     uint64_t ofull[2], oempty[2], wg[2], drain[2];
+    uint64_t turn;                // NQ = 2, an item with two row tiles: the second one may begin
     long long sums[16];
     long long start_base;
     int start_pair;
@@ -271,6 +274,27 @@ __device__ __forceinline__ uint32_t at_not_finite(uint32_t w) { return ((w & 0x7
 // bits 0 .. x-1
 __device__ __forceinline__ uint32_t at_low_bits(int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1u; }
 
+__device__ __forceinline__ uint32_t at_scaled(uint32_t a, uint32_t b, float f)
+{
+    return at_bf16x2(__uint_as_float(a) * f, __uint_as_float(b) * f);
+}
+
+// Element of `out` where row R (token by token, head by head) of an item begins.
+template <int D>
+__device__ __forceinline__ size_t out_at(const AttendParams &p, int b, int t0, int h, int R)
+{
+    return (((size_t)b * p.T + t0 + (R >> p.lg_g)) * p.H_q + (h << p.lg_g) + (R & ((1 << p.lg_g) - 1))) * D;
+}
+
+// Float of a piece where columns 4 c .. 4 c + 3 of row r are: row by row where rows are few and the threads
+// of a join take columns, else the rows of a column group side by side (a warp's accesses are 512 bytes).
+constexpr int AT_FEW = 32;
+template <int D>
+__device__ __forceinline__ size_t at_piece(int rows, int r, int c)
+{
+    return rows > AT_FEW ? ((size_t)c * rows + r) * 4 : (size_t)r * D + 4 * c;
+}
+
 template <int D, int NQ>
 __global__ void __launch_bounds__(at_threads(NQ), 1)
     santa_attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -283,8 +307,9 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     constexpr int PANELS = D / 64;
     constexpr int PANEL = AT_KEYS * 128;       // bytes of 64 columns of a tile
     constexpr int W_MMA = NQ * 4, W_PROD = W_MMA + NQ;   // warps: softmax, MMA (one a row tile), producer
-    constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_SUB), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
-    constexpr uint32_t O_COL = 256;            // two score buffers a row tile in columns 0-255, outputs behind them
+    constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_KEYS), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
+    constexpr uint32_t O_COL = 256;            // score buffers in columns 0-255, outputs behind them
+    constexpr uint32_t P_COL = 64;             // weights over the upper half of their scores
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(NS >= 4, "ring");
     const float NEG_INF = __int_as_float(0xff800000);
@@ -366,12 +391,12 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         }
         mbar_init(&sh.qfull, 1);
         mbar_init(&sh.qempty, NQ);
+        mbar_init(&sh.turn, 1);
         for (int i = 0; i < 2; ++i) {
-            for (int j = 0; j < 2; ++j) {
-                mbar_init(&sh.sfull[i][j], 1);
-                mbar_init(&sh.pfull[i][j], 4);
-                sh.arrived[i][j] = 0;
-            }
+            mbar_init(&sh.sfull[i], 1);
+            mbar_init(&sh.phalf[i], 4);
+            mbar_init(&sh.pfull[i], 4);
+            sh.arrived[i][0] = sh.arrived[i][1] = 0;
             mbar_init(&sh.ofull[i], 1);
             mbar_init(&sh.oempty[i], 4);
             mbar_init(&sh.wg[i], 4);
@@ -456,10 +481,11 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         AtWalk<NQ> w;
         w.begin(p, f0, sh.start_base, sh.start_pair);
         int items = 0;
-        int nu = 0, no = 0;                   // parts and items of this row tile so far
+        int n = 0, no = 0;                    // tiles and items of this row tile so far
+        int twos = 0;                         // items with two row tiles so far
         int stage = 0, phase = 0, used = 0;   // of the next fill to wait for
         const uint32_t qaddr = smem_u32(qs) + q * AT_ROWS * D * 2, raddr = smem_u32(ring);
-        const uint32_t t_o = tbase + O_COL + q * D, t_s = tbase + q * AT_KEYS;
+        const uint32_t t_o = tbase + O_COL + q * D;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns, p.tries));
@@ -474,26 +500,32 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             }
             return at;
         };
-        // S = Q K^T over part h of the keys of a stage
-        auto scores = [&](int at, int h, int buf) {
+        // S = Q K^T
+        auto scores = [&](int at, int buf) {
             if (elect_one()) {
-                const uint64_t k = umma_desc_sw128(raddr + at * SB + h * (AT_SUB * 128)), a = umma_desc_sw128(qaddr);
+                const uint64_t k = umma_desc_sw128(raddr + at * SB), a = umma_desc_sw128(qaddr);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    tc_mma_bf16(t_s + buf * AT_SUB, a + ((x / 4) * (AT_ROWS * 128) + (x % 4) * 32) / 16,
+                    tc_mma_bf16(tbase + buf * AT_KEYS, a + ((x / 4) * (AT_ROWS * 128) + (x % 4) * 32) / 16,
                                 k + ((x / 4) * PANEL + (x % 4) * 32) / 16, ID_S, x != 0);
-                tc_commit(&sh.sfull[q][buf]);
+                tc_commit(&sh.sfull[buf]);
+                tc_commit(&sh.empty[at]);
             }
             __syncwarp();
         };
-        // O += P V over part h
-        auto values = [&](int at, int h, int buf, bool first) {
+        // O += P V over the upper (part 0) or the lower half of the keys
+        auto values = [&](int at, int buf, int part, bool first) {
             if (elect_one()) {
-                const uint64_t v = umma_desc_sw128_mn(raddr + at * SB + h * (AT_SUB * 128), PANEL);
+                const uint64_t v = umma_desc_sw128_mn(raddr + at * SB, PANEL);
 #pragma unroll
-                for (int x = 0; x < AT_SUB / 16; ++x)
-                    tc_mma_bf16_ta(t_o, t_s + buf * AT_SUB + x * 8, v + x * (2048 / 16), ID_O, !first || x != 0);
-                tc_commit(&sh.ofull[q]);
+                for (int y = 0; y < AT_SUB / 16; ++y) {
+                    const int x = y + (part ? 0 : AT_SUB / 16);
+                    tc_mma_bf16_ta(t_o, tbase + buf * AT_KEYS + P_COL + x * 8, v + x * (2048 / 16), ID_O, !first || part != 0 || y != 0);
+                }
+                if (part) {
+                    tc_commit(&sh.ofull[q]);
+                    tc_commit(&sh.empty[at]);
+                }
             }
             __syncwarp();
         };
@@ -514,47 +546,43 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
                 continue;
             }
-            int k_at = landed(), parts = w.parts(w.it.key(w.i0));
+            int k_at = landed();
+            // the second row tile begins when the first has half of its weights, so that one is in the
+            // tensor cores while the other is in its softmax: nothing brings them together again
+            const bool two = NQ == 2 && w.live_rows(p) > AT_ROWS;
+            if (two && q == 1) wait(&sh.turn, twos & 1);
             if (!ok) break;
             tc_fence_after();
-            scores(k_at, 0, nu & 1);
-            if (parts == 1) {
-                commit(&sh.empty[k_at]);
-                if (L == 1) commit(&sh.qempty);
-            }
-            for (int j = 0; ok && j < L; ++j) {
-                int v_at = 0;
-                const int np = parts;
-                for (int h = 0; h < np; ++h, ++nu) {
-                    // the next part's scores are under way before this one's weights are waited for
-                    if (h == 0) {
-                        if (np == 2) {
-                            scores(k_at, 1, (nu + 1) & 1);
-                            commit(&sh.empty[k_at]);
-                            if (j + 1 == L) commit(&sh.qempty);
-                        }
-                        v_at = landed();
-                    }
-                    if (h == np - 1 && j + 1 < L) {
-                        k_at = landed();
-                        if (!ok) break;
-                        tc_fence_after();
-                        parts = w.parts(w.it.key(w.i0 + j + 1));
-                        scores(k_at, 0, (nu + 1) & 1);
-                        if (parts == 1) {
-                            commit(&sh.empty[k_at]);
-                            if (j + 2 == L) commit(&sh.qempty);
-                        }
-                    }
-                    wait(&sh.pfull[q][nu & 1], (nu >> 1) & 1);
-                    if (j == 0 && h == 0 && no > 0) wait(&sh.oempty[q], (no - 1) & 1);
-                    if (!ok) break;
+            scores(k_at, NQ == 2 ? q : n & 1);
+            if (L == 1) commit(&sh.qempty);
+            for (int j = 0; ok && j < L; ++j, ++n) {
+                const bool more = j + 1 < L;
+                const int buf = NQ == 2 ? q : n & 1;
+                const uint32_t parity = (NQ == 2 ? n : n >> 1) & 1;
+                const int v_at = landed();
+                if (more) k_at = landed();   // (here by the time that the weights are)
+                if (!ok) break;
+                if (NQ == 1 && more) {       // two buffers: the next scores are under way before
                     tc_fence_after();
-                    values(v_at, h, nu & 1, j == 0 && h == 0);
-                    if (h == np - 1) commit(&sh.empty[v_at]);
+                    scores(k_at, (n + 1) & 1);
+                    if (j + 2 == L) commit(&sh.qempty);
+                }
+                wait(&sh.phalf[buf], parity);
+                if (two && q == 0 && j == 0 && lane == 0) mbar_arrive(&sh.turn);
+                if (j == 0 && no > 0) wait(&sh.oempty[q], (no - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                values(v_at, buf, 0, j == 0);
+                if (!wait(&sh.pfull[buf], parity)) break;
+                tc_fence_after();
+                values(v_at, buf, 1, j == 0);
+                if (NQ == 2 && more) {
+                    scores(k_at, buf);
+                    if (j + 2 == L) commit(&sh.qempty);
                 }
             }
             ++no;
+            twos += two;
         }
         if (!ok && lane == 0) failed();
         commit(&sh.drain[q]);
@@ -567,7 +595,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         const uint32_t t_o = tbase + lanes + O_COL + q * D;
         AtWalk<NQ> w;
         w.begin(p, f0, sh.start_base, sh.start_pair);
-        int n = 0, n0 = 0;            // parts of this row tile so far; fills of the ring before the item
+        int n = 0, n0 = 0;            // tiles of this row tile so far; tiles of the CTA before the item
         uint32_t wg_phase = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -582,92 +610,103 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             wg_phase ^= 1u;
             return ok;
         };
-        for (; ok && w.seek(p, f0, f1); n0 += 2 * (w.i1 - w.i0), w.step(p)) {
+        for (; ok && w.seek(p, f0, f1); n0 += w.i1 - w.i0, w.step(p)) {
             const int live = w.live_rows(p) - q * AT_ROWS;   // of this row tile
             if (live <= 0) continue;
             const bool warp_live = 32 * (warp & 3) < live;
             const int P = w.it.first + w.it.t0 + ((q * AT_ROWS + row) >> p.lg_g);
-            float m = NEG_INF, l = 0.f;
-            bool begun = false;       // O holds sums
-            for (int i = w.i0; ok && i < w.i1; ++i) {
-                const int tile = w.it.key(i), parts = w.parts(tile);
-                for (int h = 0; h < parts; ++h, ++n) {
-                    const int key = tile + h * AT_SUB, buf = n & 1;
-                    const uint32_t t_s = tbase + lanes + q * AT_KEYS + buf * AT_SUB;
-                    const bool open = w.open(p, key);
-                    if (!wait(&sh.sfull[q][buf], (n >> 1) & 1)) break;
-                    if (!open) {
-                        // values of V that are not finite become zeros (both row tiles' warps look at all of
-                        // them: what the other has set to zero is zero, or becomes it twice)
-                        const int f = n0 + 2 * (i - w.i0) + 1;
-                        if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
-                        uint8_t *v = ring + (f % NS) * SB + h * (AT_SUB * 128);
+            const int seen_lo = p.window > 0 ? P - p.window + 1 : 0;
+            // m: the reference of the row's weights (a score so far); off, sub: how they are taken with it
+            float m = NEG_INF, l = 0.f, off = 0.f, sub = 0.f;
+            bool any_far = false;
+            for (int i = w.i0; i < w.i1; ++i, ++n) {
+                const int buf = NQ == 2 ? q : n & 1;
+                const uint32_t t_s = tbase + lanes + buf * AT_KEYS;
+                const int key = w.it.key(i);
+                const bool open = w.open(p, key);
+                if (!wait(&sh.sfull[buf], (NQ == 2 ? n : n >> 1) & 1)) break;
+                if (!open) {
+                    // values of V that are not finite become zeros (both row tiles' warps look at all of
+                    // them: what the other has set to zero is zero, or becomes it twice)
+                    const int f = 2 * (n0 + i - w.i0) + 1;
+                    if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
+                    uint8_t *v = ring + (f % NS) * SB;
 #pragma unroll 4
-                        for (int c = row; c < AT_SUB * D / 8; c += 128) {
-                            uint4 &at = *reinterpret_cast<uint4 *>(v + (c / (AT_SUB * 8)) * PANEL + (c % (AT_SUB * 8)) * 16);
-                            uint4 x = at;
-                            const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
-                            if (b0 | b1 | b2 | b3) {
-                                x.x &= ~((b0 >> 15) * 0xffffu);
-                                x.y &= ~((b1 >> 15) * 0xffffu);
-                                x.z &= ~((b2 >> 15) * 0xffffu);
-                                x.w &= ~((b3 >> 15) * 0xffffu);
-                                at = x;
-                                const int j = key + (c % (AT_SUB * 8)) / 8;
-                                if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
-                            }
+                    for (int c = row; c < SB / 16; c += 128) {
+                        const int j = key + (c % (PANEL / 16)) / 8;
+                        if (w.all_see(p, j)) continue;
+                        uint4 x = reinterpret_cast<uint4 *>(v)[c];
+                        const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
+                        if (b0 | b1 | b2 | b3) {
+                            x.x &= ~((b0 >> 15) * 0xffffu);
+                            x.y &= ~((b1 >> 15) * 0xffffu);
+                            x.z &= ~((b2 >> 15) * 0xffffu);
+                            x.w &= ~((b3 >> 15) * 0xffffu);
+                            reinterpret_cast<uint4 *>(v)[c] = x;
+                            if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
                         }
-                        fence_proxy_async_smem();
                     }
-                    if (warp_live) {
-                        tc_fence_after();
-                        uint32_t s[AT_SUB];
-                        tmem_ld32<AT_SUB>(t_s, s);
-                        if (!open) {
-                            const int ub = P + 1 - key, lb = (p.window > 0 ? P - p.window + 1 : 0) - key, sk = p.sinks - key;
+                    fence_proxy_async_smem();
+                }
+                if (warp_live) {
+                    tc_fence_after();
+                    // the upper half of the scores stays in registers, the lower half is read again
+                    uint32_t lower[AT_SUB], upper[AT_SUB];
+                    auto hide = [&](uint32_t (&s)[AT_SUB], int at) {
 #pragma unroll
-                            for (int c = 0; c < AT_SUB; c += 32) {
-                                const uint32_t seen = at_low_bits(ub - c) & (~at_low_bits(lb - c) | at_low_bits(sk - c));
+                        for (int c = 0; c < AT_SUB; c += 32) {
+                            const int k0 = key + at + c;
+                            const uint32_t seen = at_low_bits(P + 1 - k0) & (~at_low_bits(seen_lo - k0) | at_low_bits(p.sinks - k0));
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
                         }
-                        float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+                    };
+                    float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+                    auto most = [&](const uint32_t (&s)[AT_SUB]) {
 #pragma unroll
                         for (int e = 0; e < AT_SUB; e += 8)
 #pragma unroll
                             for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1]));
-                        const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                        const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
-                        if (__any_sync(FULL, grow)) {
-                            const float f = grow ? (m == NEG_INF ? 0.f : at_ratio(m, top, p.k2)) : 1.f;
-                            if (grow) m = top;
-                            l *= f;
-                            if (begun) {
-                                if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
-                                tc_fence_after();
+                    };
+                    tmem_ld32_two(t_s, lower, t_s + AT_SUB, upper);
+                    if (!open) {
+                        hide(lower, 0);
+                        hide(upper, AT_SUB);
+                    }
+                    most(lower);
+                    most(upper);
+                    const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
+                    if (__any_sync(FULL, grow)) {
+                        const float f = grow ? (m == NEG_INF ? 0.f : at_ratio(m, top, p.k2)) : 1.f;
+                        if (grow) m = top;
+                        l *= f;
+                        const bool far = at_far(m == NEG_INF ? 0.f : m, p.k2);
+                        sub = far ? m : 0.f;
+                        off = far || m == NEG_INF ? 0.f : -(m * p.k2);
+                        any_far = __any_sync(FULL, far);
+                        if (i > w.i0) {
+                            if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
+                            tc_fence_after();
 #pragma unroll 1
-                                for (uint32_t at = t_o; at < t_o + D; at += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld32<16>(at, o);
+                            for (uint32_t at = t_o; at < t_o + D; at += 16) {
+                                uint32_t o[16];
+                                tmem_ld32<16>(at, o);
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st8(at, o);
-                                    tmem_st8(at + 8, o + 8);
-                                }
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st8(at, o);
+                                tmem_st8(at + 8, o + 8);
                             }
                         }
-                        const float ref = m == NEG_INF ? 0.f : m;
-                        const bool far = at_far(ref, p.k2);
-                        const float off = far ? 0.f : -(ref * p.k2);
-                        if (__any_sync(FULL, far)) {
-                            const float sub = far ? ref : 0.f;
+                    }
+                    const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    auto weigh = [&](uint32_t (&s)[AT_SUB], int at) {
+                        if (any_far) {
 #pragma unroll
                             for (int e = 0; e < AT_SUB; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
                         }
-                        const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int c = 0; c < AT_SUB; c += 16) {
                             uint32_t pk[8];
@@ -677,20 +716,35 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                                 pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
                                 add_bf16x2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], pk[e]);
                             }
-                            tmem_st8(t_s + c / 2, pk);
+                            tmem_st8(t_s + P_COL + (at + c) / 2, pk);
                         }
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    };
+                    auto told = [&](uint64_t *bar) {
                         tmem_st_wait();
-                    }
-                    begun = true;
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar);
+                    };
+                    weigh(upper, AT_SUB);
+                    told(&sh.phalf[buf]);
+                    tmem_ld32<AT_SUB>(t_s, lower);
+                    if (!open) hide(lower, 0);
+                    weigh(lower, 0);
+                    told(&sh.pfull[buf]);
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                } else {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.pfull[q][buf]);
+                    if (lane == 0) {
+                        mbar_arrive(&sh.phalf[buf]);
+                        mbar_arrive(&sh.pfull[buf]);
+                    }
                 }
             }
-            // (a parity tells only two phases apart, and the last scores follow the product of two parts
-            // before: the phase between is waited for)
-            if (n > 1) wait(&sh.ofull[q], (n - 2) & 1);
+            if (!ok) break;
+            // (a parity tells only two phases apart.  The last scores follow the product of two tiles
+            // before with two buffers, of the tile before with one: the phase between is waited for)
+            if (NQ == 1 && n > 1) wait(&sh.ofull[q], (n - 2) & 1);
             if (!wait(&sh.ofull[q], (n - 1) & 1)) break;
             tc_fence_after();
 
@@ -701,25 +755,24 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             const int R = q * AT_ROWS + row;
             if (warp_live) {
                 const float inv = whole ? 1.f / l : 1.f;
-                const size_t at_piece = (size_t)(blockIdx.x * 2 + slot) * p.piece_rows + R;
-                uint16_t *out = p.out + (((size_t)w.b * p.T + w.it.t0 + (R >> p.lg_g)) * p.H_q + (w.h << p.lg_g) + (R & ((1 << p.lg_g) - 1))) * D;
+                const size_t slot_at = (size_t)(blockIdx.x * 2 + slot) * p.piece_rows;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld32<16>(t_o + c, o);
+                for (int c = 0; c < D; c += 64) {
+                    uint32_t o[64];
+                    tmem_ld32<64>(t_o + c, o);
                     if (fix && mine_live) {
                         // values that are not finite, of the keys that this row sees
-                        for (int x = 2 * w.i0; x < 2 * w.i1; ++x) {
-                            const int first = w.it.key(x / 2) + (x & 1) * AT_SUB;
+                        for (int x = w.i0; x < w.i1; ++x) {
+                            const int first = w.it.key(x);
                             if (w.open(p, first)) continue;
-                            for (int j = first; j < first + AT_SUB && j <= P; ++j) {
-                                if (p.window > 0 && j <= P - p.window && j >= p.sinks) continue;
+                            for (int j = first; j < first + AT_KEYS && j <= P; ++j) {
+                                if (w.all_see(p, j) || (p.window > 0 && j <= P - p.window && j >= p.sinks)) continue;
                                 const int entry = p.table[(size_t)w.b * p.cols + (j >> p.page_shift)];
                                 if ((unsigned)entry >= (unsigned)p.n_pages) continue;
                                 const uint32_t *v = reinterpret_cast<const uint32_t *>(
                                     p.v + ((((long long)entry * p.H_kv + w.h) << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D + c);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
+                                for (int e = 0; e < 32; ++e) {
                                     const uint32_t u = v[e], bad = at_not_finite(u);
                                     if (bad & 0x8000u) o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + bf16lo_to_f32(u));
                                     if (bad >> 31) o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + bf16hi_to_f32(u));
@@ -729,23 +782,21 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     }
                     if (!mine_live) continue;
                     if (whole) {
+                        uint16_t *out = p.out + out_at<D>(p, w.b, w.it.t0, w.h, R) + c;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8) {
-                            uint4 x;
-                            x.x = at_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                            x.y = at_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                            x.z = at_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                            x.w = at_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                            *reinterpret_cast<uint4 *>(out + c + e) = x;
-                        }
+                        for (int e = 0; e < 64; e += 8)
+                            *reinterpret_cast<uint4 *>(out + e) =
+                                make_uint4(at_scaled(o[e], o[e + 1], inv), at_scaled(o[e + 2], o[e + 3], inv),
+                                           at_scaled(o[e + 4], o[e + 5], inv), at_scaled(o[e + 6], o[e + 7], inv));
                     } else {
-                        float *piece = p.part + at_piece * D;
+                        float *piece = p.part + slot_at * D;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            __stcg(reinterpret_cast<uint4 *>(piece + c + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                        for (int e = 0; e < 64; e += 4)
+                            __stcg(reinterpret_cast<uint4 *>(piece + at_piece<D>(p.piece_rows, R, (c + e) / 4)),
+                                   make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                     }
                 }
-                if (!whole && mine_live) __stcg(reinterpret_cast<float2 *>(p.part_ml + at_piece * 2), make_float2(m, l));
+                if (!whole && mine_live) __stcg(reinterpret_cast<float2 *>(p.part_ml + (slot_at + R) * 2), make_float2(m, l));
             }
             tc_fence_before();
             __syncwarp();
@@ -766,25 +817,63 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 if (wg_sync() && sh.is_last[q]) {
                     __threadfence();
                     const int rows_live = min(live, AT_ROWS);
-                    auto at = [&](int c, int r) { return (size_t)(c * 2 + (c == c0 ? 1 : 0)) * p.piece_rows + q * AT_ROWS + r; };
-                    for (int x = row; x < rows_live * (D / 4); x += 128) {
-                        const int r = x / (D / 4), e = x % (D / 4);
-                        float M = NEG_INF;
+                    auto at = [&](int c) { return (size_t)(c * 2 + (c == c0 ? 1 : 0)) * p.piece_rows; };
+                    if (p.piece_rows > AT_FEW) {
+                        // a thread a row, 64 columns at a time: a row's pieces lie side by side for the lanes
+                        if (mine_live) {
+                            float M = NEG_INF, sl = 0.f;
 #pragma unroll 4
-                        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + at(c, r) * 2));
-                        float sl = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-#pragma unroll 4
-                        for (int c = c0; c <= c1; ++c) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c, r) * 2));
-                            const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c, r) * D) + e);
-                            const float f = ml.x == NEG_INF ? 0.f : at_ratio(ml.x, M, p.k2);
-                            sl = fmaf(f, ml.y, sl);
-                            o0 = fmaf(f, o.x, o0), o1 = fmaf(f, o.y, o1), o2 = fmaf(f, o.z, o2), o3 = fmaf(f, o.w, o3);
+                            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + (at(c) + R) * 2));
+#pragma unroll 1
+                            for (int x = 0; x < D / 4; x += 16) {
+                                float4 o[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                sl = 0.f;
+#pragma unroll 1
+                                for (int c = c0; c <= c1; ++c) {
+                                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (at(c) + R) * 2));
+                                    float4 v[16];
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        v[e] = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c) * D + at_piece<D>(p.piece_rows, R, x + e)));
+                                    const float f = ml.x == NEG_INF ? 0.f : at_ratio(ml.x, M, p.k2);
+                                    sl = fmaf(f, ml.y, sl);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        o[e].x = fmaf(f, v[e].x, o[e].x), o[e].y = fmaf(f, v[e].y, o[e].y);
+                                        o[e].z = fmaf(f, v[e].z, o[e].z), o[e].w = fmaf(f, v[e].w, o[e].w);
+                                    }
+                                }
+                                const float inv = 1.f / sl;
+                                uint16_t *out = p.out + out_at<D>(p, w.b, w.it.t0, w.h, R) + 4 * x;
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2)
+                                    *reinterpret_cast<uint4 *>(out + 4 * e) =
+                                        make_uint4(at_bf16x2(o[e].x * inv, o[e].y * inv), at_bf16x2(o[e].z * inv, o[e].w * inv),
+                                                   at_bf16x2(o[e + 1].x * inv, o[e + 1].y * inv), at_bf16x2(o[e + 1].z * inv, o[e + 1].w * inv));
+                            }
                         }
-                        const float inv = 1.f / sl;
-                        const int Rr = q * AT_ROWS + r;
-                        uint16_t *dst = p.out + (((size_t)w.b * p.T + w.it.t0 + (Rr >> p.lg_g)) * p.H_q + (w.h << p.lg_g) + (Rr & ((1 << p.lg_g) - 1))) * D;
-                        *reinterpret_cast<uint2 *>(dst + 4 * e) = make_uint2(at_bf16x2(o0 * inv, o1 * inv), at_bf16x2(o2 * inv, o3 * inv));
+                    } else {
+                        // few rows, many pieces: a thread four columns of a row
+                        for (int x = row; x < rows_live * (D / 4); x += 128) {
+                            const int r = x / (D / 4), e = x % (D / 4);
+                            float M = NEG_INF;
+#pragma unroll 8
+                            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + (at(c) + r) * 2));
+                            float sl = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+#pragma unroll 8
+                            for (int c = c0; c <= c1; ++c) {
+                                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (at(c) + r) * 2));
+                                const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c) * D + at_piece<D>(p.piece_rows, r, e)));
+                                const float f = ml.x == NEG_INF ? 0.f : at_ratio(ml.x, M, p.k2);
+                                sl = fmaf(f, ml.y, sl);
+                                o0 = fmaf(f, o.x, o0), o1 = fmaf(f, o.y, o1), o2 = fmaf(f, o.z, o2), o3 = fmaf(f, o.w, o3);
+                            }
+                            const float inv = 1.f / sl;
+                            *reinterpret_cast<uint2 *>(p.out + out_at<D>(p, w.b, w.it.t0, w.h, r) + 4 * e) =
+                                make_uint2(at_bf16x2(o0 * inv, o1 * inv), at_bf16x2(o2 * inv, o3 * inv));
+                        }
                     }
                 }
             }
