@@ -42,12 +42,10 @@ namespace santa {
 
 constexpr int AT_ROWS = 128;              // rows of a tile: (token, head) pairs
 constexpr int AT_KEYS = 128;              // keys of a tile
-// Keys of a part of a tile, the unit of scores and weights: two score buffers of a part each fit TMEM beside
-// the outputs, of all 128 keys with one row tile, of 64 with two.
-__host__ __device__ constexpr int at_part(int NQ) { return NQ == 2 ? 64 : 128; }
+constexpr int AT_SUB = 64;                // keys of one of its halves
 constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
-constexpr int AT_SETUP = 2;               // what an item costs beside its tiles, in tiles
-constexpr int AT_MIN_SHARE = 4;           // a share's least size, in tiles
+constexpr int AT_SETUP = 4;               // what an item costs beside its tiles, in tiles
+constexpr int AT_MIN_SHARE = 2;           // a share's least size, in tiles
 constexpr float AT_SLACK = 24.f;          // log2 of the largest p
 constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
 constexpr int AT_MISC = 3072;             // of it for barriers and the like
@@ -165,18 +163,16 @@ struct AtWalk {
     }
     __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == it.L; }
     __device__ __forceinline__ int live_rows(const AttendParams &p) const { return (it.t1 - it.t0 + 1) << p.lg_g; }
-    // whether all tokens of the item see key j; all keys of the part at `key`
+    // whether all tokens of the item see key j; all keys of the tile at `key`
     __device__ __forceinline__ bool all_see(const AttendParams &p, int j) const
     {
         return j <= it.first + it.t0 && (p.window == 0 || j > it.first + it.t1 - p.window || j < p.sinks);
     }
     __device__ __forceinline__ bool open(const AttendParams &p, int key) const
     {
-        return key + at_part(NQ) - 1 <= it.first + it.t0 &&
-               (p.window == 0 || key > it.first + it.t1 - p.window || key + at_part(NQ) <= p.sinks);
+        return key + AT_KEYS - 1 <= it.first + it.t0 &&
+               (p.window == 0 || key > it.first + it.t1 - p.window || key + AT_KEYS <= p.sinks);
     }
-    // parts of the tile at `key` that hold a key that some token sees (the last tile may end early)
-    __device__ __forceinline__ int parts(int key) const { return NQ == 2 && key + at_part(NQ) <= it.first + it.t1 ? 2 : 1; }
 };
 
 // mbar_wait_bounded for warps that wait long and often beside warps that work: the clock is looked at
@@ -197,9 +193,10 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t
 struct AtSmem {
     uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
     uint64_t qfull, qempty;
-    uint64_t sfull[2][2], pfull[2][2];   // [row tile][score buffer]
-    uint64_t ofull[2][2];                // [row tile][part % 2]
+    uint64_t sfull[2], phalf[2], pfull[2];   // of a score buffer (NQ = 2: one a row tile)
+    uint64_t ofull[2][2];         // [row tile][tile % 2]
     uint64_t oempty[2], wg[2], drain[2];
+    uint64_t turn[2];             // NQ = 2, items with two row tiles: whose products come next
     long long sums[16];
     long long start_base;
     int start_pair;
@@ -308,12 +305,12 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     constexpr int NW = NT_ / 32;
     constexpr int NS = at_stages(D, NQ);
     constexpr int SB = at_stage_bytes(D);
-    constexpr int PART = at_part(NQ);
     constexpr int PANELS = D / 64;
     constexpr int PANEL = AT_KEYS * 128;       // bytes of 64 columns of a tile
     constexpr int W_MMA = NQ * 4, W_PROD = W_MMA + NQ;   // warps: softmax, MMA (one a row tile), producer
-    constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, PART), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
+    constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_KEYS), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
     constexpr uint32_t O_COL = 256;            // score buffers in columns 0-255, outputs behind them
+    constexpr uint32_t P_COL = 64;             // weights over the upper half of their scores
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(NS >= 4, "ring");
     const float NEG_INF = __int_as_float(0xff800000);
@@ -396,12 +393,13 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         mbar_init(&sh.qfull, 1);
         mbar_init(&sh.qempty, NQ);
         for (int i = 0; i < 2; ++i) {
-            for (int j = 0; j < 2; ++j) {
-                mbar_init(&sh.sfull[i][j], 1);
-                mbar_init(&sh.pfull[i][j], 4);
-                mbar_init(&sh.ofull[i][j], 1);
-                sh.arrived[i][j] = 0;
-            }
+            mbar_init(&sh.sfull[i], 1);
+            mbar_init(&sh.phalf[i], 4);
+            mbar_init(&sh.pfull[i], 4);
+            sh.arrived[i][0] = sh.arrived[i][1] = 0;
+            mbar_init(&sh.ofull[i][0], 1);
+            mbar_init(&sh.ofull[i][1], 1);
+            mbar_init(&sh.turn[i], 1);
             mbar_init(&sh.oempty[i], 4);
             mbar_init(&sh.wg[i], 4);
             mbar_init(&sh.drain[i], 1);
@@ -485,10 +483,12 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         AtWalk<NQ> w;
         w.begin(p, f0, sh.start_base, sh.start_pair);
         int items = 0;
-        int n = 0, no = 0;                    // parts and items of this row tile so far
+        int n = 0, no = 0;                    // tiles and items of this row tile so far
+        int turns = 0;                        // turns taken
+        bool first_two = true;
         int stage = 0, phase = 0, used = 0;   // of the next fill to wait for
         const uint32_t qaddr = smem_u32(qs) + q * AT_ROWS * D * 2, raddr = smem_u32(ring);
-        const uint32_t t_o = tbase + O_COL + q * D, t_s = tbase + q * 2 * PART;
+        const uint32_t t_o = tbase + O_COL + q * D;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns, p.tries));
@@ -503,28 +503,32 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             }
             return at;
         };
-        // S = Q K^T over part h of the keys of a stage, which is given back after the last
-        auto scores = [&](int at, int h, int buf, bool last) {
+        // S = Q K^T
+        auto scores = [&](int at, int buf) {
             if (elect_one()) {
-                const uint64_t k = umma_desc_sw128(raddr + at * SB + h * (PART * 128)), a = umma_desc_sw128(qaddr);
+                const uint64_t k = umma_desc_sw128(raddr + at * SB), a = umma_desc_sw128(qaddr);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    tc_mma_bf16(t_s + buf * PART, a + ((x / 4) * (AT_ROWS * 128) + (x % 4) * 32) / 16,
+                    tc_mma_bf16(tbase + buf * AT_KEYS, a + ((x / 4) * (AT_ROWS * 128) + (x % 4) * 32) / 16,
                                 k + ((x / 4) * PANEL + (x % 4) * 32) / 16, ID_S, x != 0);
-                tc_commit(&sh.sfull[q][buf]);
-                if (last) tc_commit(&sh.empty[at]);
+                tc_commit(&sh.sfull[buf]);
+                tc_commit(&sh.empty[at]);
             }
             __syncwarp();
         };
-        // O += P V over part h
-        auto values = [&](int at, int h, int buf, bool first, bool last) {
+        // O += P V over the upper (part 0) or the lower half of the keys
+        auto values = [&](int at, int buf, int part, bool first) {
             if (elect_one()) {
-                const uint64_t v = umma_desc_sw128_mn(raddr + at * SB + h * (PART * 128), PANEL);
+                const uint64_t v = umma_desc_sw128_mn(raddr + at * SB, PANEL);
 #pragma unroll
-                for (int x = 0; x < PART / 16; ++x)
-                    tc_mma_bf16_ta(t_o, t_s + buf * PART + x * 8, v + x * (2048 / 16), ID_O, !first || x != 0);
-                tc_commit(&sh.ofull[q][buf]);
-                if (last) tc_commit(&sh.empty[at]);
+                for (int y = 0; y < AT_SUB / 16; ++y) {
+                    const int x = y + (part ? 0 : AT_SUB / 16);
+                    tc_mma_bf16_ta(t_o, tbase + buf * AT_KEYS + P_COL + x * 8, v + x * (2048 / 16), ID_O, !first || part != 0 || y != 0);
+                }
+                if (part) {
+                    tc_commit(&sh.ofull[q][n & 1]);
+                    tc_commit(&sh.empty[at]);
+                }
             }
             __syncwarp();
         };
@@ -545,37 +549,49 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
                 continue;
             }
-            int k_at = landed(), parts = w.parts(w.it.key(w.i0));
+            int k_at = landed();
+            // two row tiles take turns in the tensor cores, so that one is in its softmax meanwhile: side by
+            // side, both would be in the tensor cores and then both in their softmax
+            const bool two = NQ == 2 && w.live_rows(p) > AT_ROWS;
+            auto my_turn = [&]() {
+                if (two) wait(&sh.turn[q], turns++ & 1);
+            };
+            auto your_turn = [&]() {
+                if (two && lane == 0) mbar_arrive(&sh.turn[q ^ 1]);
+            };
+            if (q == 1 || !first_two) my_turn();
+            if (two) first_two = false;
             if (!ok) break;
             tc_fence_after();
-            scores(k_at, 0, n & 1, parts == 1);
-            if (L == 1 && parts == 1) commit(&sh.qempty);
-            for (int j = 0; ok && j < L; ++j) {
-                int v_at = 0;
-                const int np = parts;
-                for (int h = 0; h < np; ++h, ++n) {
-                    // the next part's scores are under way before this one's weights are waited for
-                    if (h == 0) {
-                        if (np == 2) {
-                            scores(k_at, 1, (n + 1) & 1, true);
-                            if (j + 1 == L) commit(&sh.qempty);
-                        }
-                        v_at = landed();
-                    }
-                    if (h == np - 1 && j + 1 < L) {
-                        k_at = landed();
-                        if (!ok) break;
-                        tc_fence_after();
-                        parts = w.parts(w.it.key(w.i0 + j + 1));
-                        scores(k_at, 0, (n + 1) & 1, parts == 1);
-                        if (parts == 1 && j + 2 == L) commit(&sh.qempty);
-                    }
-                    wait(&sh.pfull[q][n & 1], (n >> 1) & 1);
-                    if (j == 0 && h == 0 && no > 0) wait(&sh.oempty[q], (no - 1) & 1);
-                    if (!ok) break;
+            scores(k_at, NQ == 2 ? q : n & 1);
+            your_turn();
+            if (L == 1) commit(&sh.qempty);
+            for (int j = 0; ok && j < L; ++j, ++n) {
+                const bool more = j + 1 < L;
+                const int buf = NQ == 2 ? q : n & 1;
+                const uint32_t parity = (NQ == 2 ? n : n >> 1) & 1;
+                const int v_at = landed();
+                if (more) k_at = landed();   // (here by the time that the weights are)
+                if (!ok) break;
+                if (NQ == 1 && more) {       // two buffers: the next scores are under way before
                     tc_fence_after();
-                    values(v_at, h, n & 1, j == 0 && h == 0, h == np - 1);
+                    scores(k_at, (n + 1) & 1);
+                    if (j + 2 == L) commit(&sh.qempty);
                 }
+                wait(&sh.phalf[buf], parity);
+                my_turn();
+                if (j == 0 && no > 0) wait(&sh.oempty[q], (no - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                values(v_at, buf, 0, j == 0);
+                if (!wait(&sh.pfull[buf], parity)) break;
+                tc_fence_after();
+                values(v_at, buf, 1, j == 0);
+                if (NQ == 2 && more) {
+                    scores(k_at, buf);
+                    if (j + 2 == L) commit(&sh.qempty);
+                }
+                your_turn();
             }
             ++no;
         }
@@ -590,7 +606,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         const uint32_t t_o = tbase + lanes + O_COL + q * D;
         AtWalk<NQ> w;
         w.begin(p, f0, sh.start_base, sh.start_pair);
-        int n = 0, n0 = 0;            // parts of this row tile so far; tiles of the CTA before the item
+        int n = 0, n0 = 0;            // tiles of this row tile so far; tiles of the CTA before the item
         uint32_t wg_phase = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -614,92 +630,96 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             // m: the reference of the row's weights (a score so far); off, sub: how they are taken with it
             float m = NEG_INF, l = 0.f, off = 0.f, sub = 0.f;
             bool any_far = false;
-            bool begun = false;       // O holds sums
-            for (int i = w.i0; ok && i < w.i1; ++i) {
-                const int tile = w.it.key(i), parts = w.parts(tile);
-                for (int h = 0; h < parts; ++h, ++n) {
-                    const int key = tile + h * PART, buf = n & 1;
-                    const uint32_t t_s = tbase + lanes + (2 * q + buf) * PART;
-                    const bool open = w.open(p, key);
-                    if (!wait(&sh.sfull[q][buf], (n >> 1) & 1)) break;
-                    if (!open) {
-                        // values of V that are not finite become zeros where some token does not see them (both row
-                        // tiles' warps look at all of them: what the other has set to zero is zero, or becomes it twice)
-                        const int f = 2 * (n0 + i - w.i0) + 1;
-                        if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
-                        uint8_t *v = ring + (f % NS) * SB + h * (PART * 128);
+            for (int i = w.i0; i < w.i1; ++i, ++n) {
+                const int buf = NQ == 2 ? q : n & 1;
+                const uint32_t t_s = tbase + lanes + buf * AT_KEYS;
+                const int key = w.it.key(i);
+                const bool open = w.open(p, key);
+                if (!wait(&sh.sfull[buf], (NQ == 2 ? n : n >> 1) & 1)) break;
+                if (!open) {
+                    // values of V that are not finite become zeros (both row tiles' warps look at all of
+                    // them: what the other has set to zero is zero, or becomes it twice)
+                    const int f = 2 * (n0 + i - w.i0) + 1;
+                    if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
+                    uint8_t *v = ring + (f % NS) * SB;
 #pragma unroll 4
-                        for (int c = row; c < PART * D / 8; c += 128) {
-                            const int j = key + (c % (PART * 8)) / 8;
-                            if (w.all_see(p, j)) continue;
-                            uint4 &at = *reinterpret_cast<uint4 *>(v + (c / (PART * 8)) * PANEL + (c % (PART * 8)) * 16);
-                            uint4 x = at;
-                            const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
-                            if (b0 | b1 | b2 | b3) {
-                                x.x &= ~((b0 >> 15) * 0xffffu);
-                                x.y &= ~((b1 >> 15) * 0xffffu);
-                                x.z &= ~((b2 >> 15) * 0xffffu);
-                                x.w &= ~((b3 >> 15) * 0xffffu);
-                                at = x;
-                                if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
-                            }
+                    for (int c = row; c < SB / 16; c += 128) {
+                        const int j = key + (c % (PANEL / 16)) / 8;
+                        if (w.all_see(p, j)) continue;
+                        uint4 x = reinterpret_cast<uint4 *>(v)[c];
+                        const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
+                        if (b0 | b1 | b2 | b3) {
+                            x.x &= ~((b0 >> 15) * 0xffffu);
+                            x.y &= ~((b1 >> 15) * 0xffffu);
+                            x.z &= ~((b2 >> 15) * 0xffffu);
+                            x.w &= ~((b3 >> 15) * 0xffffu);
+                            reinterpret_cast<uint4 *>(v)[c] = x;
+                            if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
                         }
-                        fence_proxy_async_smem();
                     }
-                    if (warp_live) {
-                        tc_fence_after();
-                        uint32_t s[PART];
-                        if constexpr (PART == 128)
-                            tmem_ld32_two(t_s, *reinterpret_cast<uint32_t (*)[64]>(s), t_s + 64, *reinterpret_cast<uint32_t (*)[64]>(s + 64));
-                        else
-                            tmem_ld32<PART>(t_s, s);
-                        if (!open) {
+                    fence_proxy_async_smem();
+                }
+                if (warp_live) {
+                    tc_fence_after();
+                    // the upper half of the scores stays in registers, the lower half is read again
+                    uint32_t lower[AT_SUB], upper[AT_SUB];
+                    auto hide = [&](uint32_t (&s)[AT_SUB], int at) {
 #pragma unroll
-                            for (int c = 0; c < PART; c += 32) {
-                                const int k0 = key + c;
-                                const uint32_t seen = at_low_bits(P + 1 - k0) & (~at_low_bits(seen_lo - k0) | at_low_bits(p.sinks - k0));
+                        for (int c = 0; c < AT_SUB; c += 32) {
+                            const int k0 = key + at + c;
+                            const uint32_t seen = at_low_bits(P + 1 - k0) & (~at_low_bits(seen_lo - k0) | at_low_bits(p.sinks - k0));
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
                         }
-                        float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+                    };
+                    float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+                    auto most = [&](const uint32_t (&s)[AT_SUB]) {
 #pragma unroll
-                        for (int e = 0; e < PART; e += 8)
+                        for (int e = 0; e < AT_SUB; e += 8)
 #pragma unroll
                             for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1]));
-                        const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                        const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
-                        if (__any_sync(FULL, grow)) {
-                            const float f = grow ? (m == NEG_INF ? 0.f : at_ratio(m, top, p.k2)) : 1.f;
-                            if (grow) m = top;
-                            l *= f;
-                            const bool far = at_far(m == NEG_INF ? 0.f : m, p.k2);
-                            sub = far ? m : 0.f;
-                            off = far || m == NEG_INF ? 0.f : -(m * p.k2);
-                            any_far = __any_sync(FULL, far);
-                            if (begun) {
-                                if (!wait(&sh.ofull[q][(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
-                                tc_fence_after();
+                    };
+                    tmem_ld32_two(t_s, lower, t_s + AT_SUB, upper);
+                    if (!open) {
+                        hide(lower, 0);
+                        hide(upper, AT_SUB);
+                    }
+                    most(lower);
+                    most(upper);
+                    const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
+                    if (__any_sync(FULL, grow)) {
+                        const float f = grow ? (m == NEG_INF ? 0.f : at_ratio(m, top, p.k2)) : 1.f;
+                        if (grow) m = top;
+                        l *= f;
+                        const bool far = at_far(m == NEG_INF ? 0.f : m, p.k2);
+                        sub = far ? m : 0.f;
+                        off = far || m == NEG_INF ? 0.f : -(m * p.k2);
+                        any_far = __any_sync(FULL, far);
+                        if (i > w.i0) {
+                            if (!wait(&sh.ofull[q][(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
+                            tc_fence_after();
 #pragma unroll 1
-                                for (uint32_t at = t_o; at < t_o + D; at += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld32<16>(at, o);
+                            for (uint32_t at = t_o; at < t_o + D; at += 16) {
+                                uint32_t o[16];
+                                tmem_ld32<16>(at, o);
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st8(at, o);
-                                    tmem_st8(at + 8, o + 8);
-                                }
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st8(at, o);
+                                tmem_st8(at + 8, o + 8);
                             }
                         }
+                    }
+                    const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    auto weigh = [&](uint32_t (&s)[AT_SUB], int at) {
                         if (any_far) {
 #pragma unroll
-                            for (int e = 0; e < PART; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
+                            for (int e = 0; e < AT_SUB; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
                         }
-                        const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int c = 0; c < PART; c += 16) {
+                        for (int c = 0; c < AT_SUB; c += 16) {
                             uint32_t pk[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
@@ -707,20 +727,34 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                                 pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
                                 add_bf16x2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], pk[e]);
                             }
-                            tmem_st8(t_s + c / 2, pk);
+                            tmem_st8(t_s + P_COL + (at + c) / 2, pk);
                         }
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    };
+                    auto told = [&](uint64_t *bar) {
                         tmem_st_wait();
-                    }
-                    begun = true;
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar);
+                    };
+                    weigh(upper, AT_SUB);
+                    told(&sh.phalf[buf]);
+                    tmem_ld32<AT_SUB>(t_s, lower);
+                    if (!open) hide(lower, 0);
+                    weigh(lower, 0);
+                    told(&sh.pfull[buf]);
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                } else {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.pfull[q][buf]);
+                    if (lane == 0) {
+                        mbar_arrive(&sh.phalf[buf]);
+                        mbar_arrive(&sh.pfull[buf]);
+                    }
                 }
             }
             if (!ok) break;
-            // (a parity tells only a phase from the next.  When the scores of part n are here, the product of
-            // part n - 2 is done and that of n - 1 may be: one barrier would be one or two phases on)
+            // (a parity tells only a phase from the next.  When scores are here, the product of two tiles before
+            // is done and that of the tile before may be: one barrier would be one or two phases on)
             if (!wait(&sh.ofull[q][(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
             tc_fence_after();
 
@@ -740,6 +774,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                         // values that are not finite, of the keys that this row sees
                         for (int x = w.i0; x < w.i1; ++x) {
                             const int first = w.it.key(x);
+                            if (w.open(p, first)) continue;
                             for (int j = first; j < first + AT_KEYS && j <= P; ++j) {
                                 if (w.all_see(p, j) || (p.window > 0 && j <= P - p.window && j >= p.sinks)) continue;
                                 const int entry = p.table[(size_t)w.b * p.cols + (j >> p.page_shift)];
