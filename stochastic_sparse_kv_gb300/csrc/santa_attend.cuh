@@ -81,6 +81,7 @@ struct AttendParams {
     float k2;                     // scale log2 e
     uint64_t wait_ns;
     int tries;                    // of a wait between two looks at the clock
+    int wide;                     // out begins at a multiple of 32 bytes
 };
 
 // A batch row's tokens; none where pos and counts leave the cache.
@@ -290,6 +291,7 @@ __device__ __forceinline__ size_t out_at(const AttendParams &p, int b, int t0, i
 // Float of a piece where columns 4 c .. 4 c + 3 of row r are: row by row where rows are few and the threads
 // of a join take columns, else the rows of a column group side by side (a warp's accesses are 512 bytes).
 constexpr int AT_FEW = 32;
+constexpr int AT_BATCH = 10;
 template <int D>
 __device__ __forceinline__ size_t at_piece(int rows, int r, int c)
 {
@@ -642,21 +644,29 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     const int f = 2 * (n0 + i - w.i0) + 1;
                     if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
                     uint8_t *v = ring + (f % NS) * SB;
+                    auto clear = [&](int r0, int r1) {   // in rows r0 .. r1 - 1
+#pragma unroll
+                        for (int h = 0; h < PANELS; ++h)
 #pragma unroll 4
-                    for (int c = row; c < SB / 16; c += 128) {
-                        const int j = key + (c % (PANEL / 16)) / 8;
-                        if (w.all_see(p, j)) continue;
-                        uint4 x = reinterpret_cast<uint4 *>(v)[c];
-                        const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
-                        if (b0 | b1 | b2 | b3) {
-                            x.x &= ~((b0 >> 15) * 0xffffu);
-                            x.y &= ~((b1 >> 15) * 0xffffu);
-                            x.z &= ~((b2 >> 15) * 0xffffu);
-                            x.w &= ~((b3 >> 15) * 0xffffu);
-                            reinterpret_cast<uint4 *>(v)[c] = x;
-                            if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
-                        }
-                    }
+                            for (int c = 8 * r0 + row; c < 8 * r1; c += 128) {
+                                uint4 &at = *reinterpret_cast<uint4 *>(v + h * PANEL + c * 16);
+                                uint4 x = at;
+                                const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
+                                if (b0 | b1 | b2 | b3) {
+                                    x.x &= ~((b0 >> 15) * 0xffffu);
+                                    x.y &= ~((b1 >> 15) * 0xffffu);
+                                    x.z &= ~((b2 >> 15) * 0xffffu);
+                                    x.w &= ~((b3 >> 15) * 0xffffu);
+                                    at = x;
+                                    const int j = key + c / 8;
+                                    if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
+                                }
+                            }
+                    };
+                    // keys beyond the first token, and keys before the last one's window
+                    const int beyond = min(AT_KEYS, max(0, w.it.first + w.it.t0 + 1 - key));
+                    clear(beyond, AT_KEYS);
+                    if (p.window > 0) clear(max(0, p.sinks - key), min(beyond, w.it.first + w.it.t1 - p.window + 1 - key));
                     fence_proxy_async_smem();
                 }
                 if (warp_live) {
@@ -684,6 +694,8 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     if (!open) {
                         hide(lower, 0);
                         hide(upper, AT_SUB);
+#pragma unroll
+                        for (int c = 0; c < AT_SUB; c += 8) tmem_st8(t_s + c, lower + c);   // (as it is read again)
                     }
                     most(lower);
                     most(upper);
@@ -739,7 +751,6 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     weigh(upper, AT_SUB);
                     told(&sh.phalf[buf]);
                     tmem_ld32<AT_SUB>(t_s, lower);
-                    if (!open) hide(lower, 0);
                     weigh(lower, 0);
                     told(&sh.pfull[buf]);
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -794,10 +805,19 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     if (whole) {
                         uint16_t *out = p.out + out_at<D>(p, w.b, w.it.t0, w.h, R) + c;
 #pragma unroll
-                        for (int e = 0; e < 64; e += 8)
-                            *reinterpret_cast<uint4 *>(out + e) =
-                                make_uint4(at_scaled(o[e], o[e + 1], inv), at_scaled(o[e + 2], o[e + 3], inv),
-                                           at_scaled(o[e + 4], o[e + 5], inv), at_scaled(o[e + 6], o[e + 7], inv));
+                        for (int e = 0; e < 32; ++e) o[e] = at_scaled(o[2 * e], o[2 * e + 1], inv);
+                        if (p.wide) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(o[e]), "r"(o[e + 1]),
+                                             "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7]),
+                                             "l"(__cvta_generic_to_global(out + 2 * e))
+                                             : "memory");
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4 *>(out + 2 * e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
                     } else {
                         float *piece = p.part + slot_at * D;
 #pragma unroll
@@ -868,17 +888,32 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                         // few rows, many pieces: a thread four columns of a row
                         for (int x = row; x < rows_live * (D / 4); x += 128) {
                             const int r = x / (D / 4), e = x % (D / 4);
-                            float M = NEG_INF;
-#pragma unroll 8
-                            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_ml + (at(c) + r) * 2));
-                            float sl = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-#pragma unroll 8
-                            for (int c = c0; c <= c1; ++c) {
-                                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (at(c) + r) * 2));
-                                const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c) * D + at_piece<D>(p.piece_rows, r, e)));
-                                const float f = ml.x == NEG_INF ? 0.f : at_ratio(ml.x, M, p.k2);
-                                sl = fmaf(f, ml.y, sl);
-                                o0 = fmaf(f, o.x, o0), o1 = fmaf(f, o.y, o1), o2 = fmaf(f, o.z, o2), o3 = fmaf(f, o.w, o3);
+                            // AT_BATCH pieces are on their way at a time
+                            float M = NEG_INF, sl = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+                            for (int c = c0; c <= c1; c += AT_BATCH) {
+                                float2 ml[AT_BATCH];
+                                float4 o[AT_BATCH];
+#pragma unroll
+                                for (int y = 0; y < AT_BATCH; ++y) {
+                                    ml[y] = make_float2(NEG_INF, 0.f);
+                                    o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                    if (c + y <= c1) {
+                                        ml[y] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (at(c + y) + r) * 2));
+                                        o[y] = __ldcg(reinterpret_cast<const float4 *>(p.part + at(c + y) * D + at_piece<D>(p.piece_rows, r, e)));
+                                    }
+                                }
+                                float N = M;
+#pragma unroll
+                                for (int y = 0; y < AT_BATCH; ++y) N = fmaxf(N, ml[y].x);
+                                const float g = M == NEG_INF ? 0.f : at_ratio(M, N, p.k2);
+                                M = N;
+                                sl *= g, o0 *= g, o1 *= g, o2 *= g, o3 *= g;
+#pragma unroll
+                                for (int y = 0; y < AT_BATCH; ++y) {
+                                    const float f = ml[y].x == NEG_INF ? 0.f : at_ratio(ml[y].x, M, p.k2);
+                                    sl = fmaf(f, ml[y].y, sl);
+                                    o0 = fmaf(f, o[y].x, o0), o1 = fmaf(f, o[y].y, o1), o2 = fmaf(f, o[y].z, o2), o3 = fmaf(f, o[y].w, o3);
+                                }
                             }
                             const float inv = 1.f / sl;
                             *reinterpret_cast<uint2 *>(p.out + out_at<D>(p, w.b, w.it.t0, w.h, r) + 4 * e) =
