@@ -46,7 +46,7 @@ constexpr int AT_SUB = 64;                // keys of one of its halves
 constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
 constexpr int AT_SETUP = 4;               // what an item costs beside its tiles, in tiles
 constexpr int AT_MIN_SHARE = 2;           // a share's least size, in tiles
-constexpr float AT_SLACK = 24.f;          // log2 of the largest p
+constexpr float AT_SLACK = 14.f;          // log2 of the largest p
 constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
 constexpr int AT_MISC = 3072;             // of it for barriers and the like
 constexpr int AT_STAGES_MAX = 8;
@@ -176,6 +176,19 @@ struct AtWalk {
     }
 };
 
+__device__ __forceinline__ bool at_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // mbar_wait_bounded for warps that wait long and often beside warps that work: the clock is looked at
 // after `tries` tries only (reading it at each took more issue slots than the work).
 __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns, int tries)
@@ -185,6 +198,8 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t
 #pragma unroll 1
         for (int i = 0; i < tries; ++i)
             if (mbar_try_wait(bar, parity)) return true;
+        // (a limit shorter than such a try may last)
+        if (tries == 0 && at_test(bar, parity)) return true;
         const uint64_t t = globaltimer_ns();
         if (t0 == 0) t0 = t;
         if (t - t0 > limit_ns) return false;
@@ -456,7 +471,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                         row = ((entry * p.H_kv + w.h) << p.page_shift) + (j & (page - 1));
                     } else {
                         row = rows_all;
-                        set_dev_error(p.ctrl, DEV_BAD_PAGE);
+                        if (j + box > w.it.lo || j < p.sinks) set_dev_error(p.ctrl, DEV_BAD_PAGE);   // (else no token sees it)
                     }
                 }
 #pragma unroll

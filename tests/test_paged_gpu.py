@@ -224,7 +224,7 @@ def check(got, want, spread, counts, before=None):
         assert np.array_equal(np.isnan(g), np.isnan(w)), f"row {b}: NaN in other places"
         fine = np.isfinite(w)
         assert np.array_equal(g[~fine & ~np.isnan(w)], w[~fine & ~np.isnan(w)])
-        err = np.abs(g - w)[fine]
+        err = np.abs(g[fine] - w[fine])
         tol = pu.tolerance(w[fine], spread[b, :n][fine])
         assert (err <= tol).all(), f"row {b}: {(err - tol).max()} beyond, {(err / np.maximum(tol, 1e-30)).max()} of it"
         if before is not None:
@@ -383,6 +383,70 @@ def test_a_page_outside_the_pool_counts_as_zeros():
     got = attend(q[2:], k, v, torch.cat((table[2:], table[:1]), 1)[:, :19], pos[2:], workspace=ws)
     assert santa.device_status(ws) == 0
     check(got, want[2:], spread[2:], [6])
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("T", [1, 70])
+def test_pages_before_the_window_may_be_gone(page, T):
+    """A cache that gives back the pages behind the window: their entries name no page, and no error is
+    reported; one page fewer, and it is."""
+    g = gen(page + T)
+    n, window, sinks = 1300, 200, 5
+    q, k, v, table, pos = problem(g, 2, T, 2, 4, 64, page, [n, n - 100], [T, T])
+    want, spread = pu.attention(q, k, v, table, pos, None, window, sinks)
+    ws = santa.new_workspace(64 << 20, DEV)
+    lowest = [pos[b] - window + 1 for b in range(2)]
+    for b in range(2):
+        table[b, -(-sinks // page):lowest[b] // page] = -1
+    check(attend(q, k, v, table, pos, None, window, sinks, workspace=ws), want, spread, [T, T])
+    assert santa.device_status(ws) == 0
+    table[1, lowest[1] // page] = k.shape[0]
+    attend(q, k, v, table, pos, None, window, sinks, workspace=ws)
+    assert santa.device_status(ws) == santa.DEV_BAD_PAGE
+
+
+@pytest.mark.parametrize("B,T,H_kv,G,d,page,lengths,window", [
+    (1, 1, 8, 4, 128, 64, [100003], 0), (3, 1, 8, 4, 128, 128, [30011, 1, 9000], 0), (1, 7, 4, 8, 64, 16, [50001], 0),
+    (1, 33, 2, 4, 128, 32, [20000], 0), (2, 300, 4, 4, 128, 64, [5000, 300], 0), (4, 100, 2, 8, 64, 16, [3000, 100, 101, 1777], 333),
+    (1, 600, 1, 2, 128, 256, [4096], 0), (7, 65, 2, 4, 128, 16, [65, 70, 1000, 129, 128, 257, 4000], 0),
+])
+def test_the_same_bits_every_time(B, T, H_kv, G, d, page, lengths, window):
+    """Forty calls each, cold and warm caches in turn, on one workspace: no wait runs out, no piece is
+    missed, no bit differs."""
+    g = gen(B + T)
+    q, k, v, table = big(g, B, T, H_kv, G, d, page, lengths, T + d)
+    pos = ints([n - min(T, n) for n in lengths])
+    counts = ints([min(T, n) for n in lengths])
+    cache = santa.PagedCache(k, v, table.to(DEV))
+    ws = santa.new_workspace(64 << 20, DEV)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    first = None
+    for i in range(40):
+        if i % 2:
+            flush.fill_(i)
+        out = torch.full_like(q, 3.0)
+        santa.attend_paged(q, cache, pos, counts, window, 4, out=out, workspace=ws)
+        if first is None:
+            first = out
+            assert torch.isfinite(out).all()
+        assert torch.equal(out, first)
+    assert santa.device_status(ws) == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls without a workspace of their own, on two streams, each many times over."""
+    g = gen(20)
+    q, k, v, table = big(g, 2, 40, 2, 4, 128, 64, [3000, 2000], 5)
+    cache, pos = santa.PagedCache(k, v, table.to(DEV)), ints([2960, 1960])
+    want = santa.attend_paged(q, cache, pos)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            outs[i].append(santa.attend_paged(q, cache, pos, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for row in outs for o in row)
 
 
 def test_positions_out_of_range_skip_the_row():
