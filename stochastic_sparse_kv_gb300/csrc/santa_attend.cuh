@@ -46,7 +46,7 @@ constexpr int AT_SUB = 64;                // keys of one of its halves
 constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
 constexpr int AT_SETUP = 4;               // what an item costs beside its tiles, in tiles
 constexpr int AT_MIN_SHARE = 2;           // a share's least size, in tiles
-constexpr float AT_SLACK = 14.f;          // log2 of the largest p
+constexpr float AT_SLACK = 24.f;          // log2 of the largest p (sums of values below 2^80 stay in range)
 constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
 constexpr int AT_MISC = 3072;             // of it for barriers and the like
 constexpr int AT_STAGES_MAX = 8;
@@ -81,6 +81,7 @@ struct AttendParams {
     float k2;                     // scale log2 e
     uint64_t wait_ns;
     int tries;                    // of a wait between two looks at the clock
+    uint32_t nap;                 // ns that one may sleep
     int wide;                     // out begins at a multiple of 32 bytes
 };
 
@@ -176,30 +177,25 @@ struct AtWalk {
     }
 };
 
-__device__ __forceinline__ bool at_test(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // mbar_wait_bounded for warps that wait long and often beside warps that work: the clock is looked at
-// after `tries` tries only (reading it at each took more issue slots than the work).
-__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns, int tries)
+// after `tries` tries only, each of which may sleep `nap` ns in the hardware (a line more in this loop, which
+// every wait has, cost 6% of a long chunk's time).  No tries: the wait is given up.
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns, int tries, uint32_t nap)
 {
     uint64_t t0 = 0;
     for (;;) {
 #pragma unroll 1
-        for (int i = 0; i < tries; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        // (a limit shorter than such a try may last)
-        if (tries == 0 && at_test(bar, parity)) return true;
+        for (int i = 0; i < tries; ++i) {
+            uint32_t ok;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity), "r"(nap)
+                : "memory");
+            if (ok) return true;
+        }
         const uint64_t t = globaltimer_ns();
         if (t0 == 0) t0 = t;
         if (t - t0 > limit_ns) return false;
@@ -445,7 +441,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         bool ok = true;
         for (; ok && w.seek(p, f0, f1); w.step(p), ++items) {
             const int nq = NQ == 2 && w.live_rows(p) > AT_ROWS ? 2 : 1;
-            if (items > 0 && !__all_sync(FULL, at_wait(&sh.qempty, (items - 1) & 1, p.wait_ns, p.tries))) {
+            if (items > 0 && !__all_sync(FULL, at_wait(&sh.qempty, (items - 1) & 1, p.wait_ns, p.tries, p.nap))) {
                 ok = false;
                 break;
             }
@@ -476,7 +472,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (!__all_sync(FULL, at_wait(&sh.empty[stage], phase, p.wait_ns, p.tries))) {
+                    if (!__all_sync(FULL, at_wait(&sh.empty[stage], phase, p.wait_ns, p.tries, p.nap))) {
                         ok = false;
                         break;
                     }
@@ -508,7 +504,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         const uint32_t t_o = tbase + O_COL + q * D;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns, p.tries));
+            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns, p.tries, p.nap));
             return ok;
         };
         // the next fill of the ring (K of a tile, then its V) has landed; its stage
@@ -627,7 +623,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         uint32_t wg_phase = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns, p.tries));
+            if (ok) ok = __all_sync(FULL, at_wait(bar, parity, p.wait_ns, p.tries, p.nap));
             return ok;
         };
         // rendezvous of the row tile's warps (a bounded wait, unlike bar.sync)
