@@ -323,7 +323,6 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     constexpr int W_MMA = NQ * 4, W_PROD = W_MMA + NQ;   // warps: softmax, MMA (one a row tile), producer
     constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_KEYS), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
     constexpr uint32_t O_COL = 256;            // score buffers in columns 0-255, outputs behind them
-    constexpr uint32_t P_COL = 64;             // weights over the upper half of their scores
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(NS >= 4, "ring");
     const float NEG_INF = __int_as_float(0xff800000);
@@ -529,14 +528,14 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             }
             __syncwarp();
         };
-        // O += P V over the upper (part 0) or the lower half of the keys
+        // O += P V over the lower (part 0) or the upper half of the keys
         auto values = [&](int at, int buf, int part, bool first) {
             if (elect_one()) {
                 const uint64_t v = umma_desc_sw128_mn(raddr + at * SB, PANEL);
 #pragma unroll
                 for (int y = 0; y < AT_SUB / 16; ++y) {
-                    const int x = y + (part ? 0 : AT_SUB / 16);
-                    tc_mma_bf16_ta(t_o, tbase + buf * AT_KEYS + P_COL + x * 8, v + x * (2048 / 16), ID_O, !first || part != 0 || y != 0);
+                    const int x = y + part * (AT_SUB / 16);
+                    tc_mma_bf16_ta(t_o, tbase + buf * AT_KEYS + x * 8, v + x * (2048 / 16), ID_O, !first || part != 0 || y != 0);
                 }
                 if (part) {
                     tc_commit(&sh.ofull[q][n & 1]);
@@ -682,34 +681,30 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
                 if (warp_live) {
                     tc_fence_after();
-                    // the upper half of the scores stays in registers, the lower half is read again
-                    uint32_t lower[AT_SUB], upper[AT_SUB];
-                    auto hide = [&](uint32_t (&s)[AT_SUB], int at) {
+                    // the scores are read twice: for their maximum, and half by half for the weights, which
+                    // go over what has been read.  (One loop for both halves: the less code, the
+                    // fewer waits for instructions)
+                    uint32_t s[2][AT_SUB];
+                    tmem_ld32_two(t_s, s[0], t_s + AT_SUB, s[1]);
+                    if (!open) {
 #pragma unroll
-                        for (int c = 0; c < AT_SUB; c += 32) {
-                            const int k0 = key + at + c;
+                        for (int c = 0; c < AT_KEYS; c += 32) {
+                            const int k0 = key + c;
                             const uint32_t seen = at_low_bits(P + 1 - k0) & (~at_low_bits(seen_lo - k0) | at_low_bits(p.sinks - k0));
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
+                            for (int e = c % AT_SUB; e < c % AT_SUB + 32; ++e)
+                                if (!((seen >> (e % 32)) & 1u)) s[c / AT_SUB][e] = 0xff800000u;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) tmem_st8(t_s + c + e, s[c / AT_SUB] + c % AT_SUB + e);
                         }
-                    };
-                    float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-                    auto most = [&](const uint32_t (&s)[AT_SUB]) {
-#pragma unroll
-                        for (int e = 0; e < AT_SUB; e += 8)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1]));
-                    };
-                    tmem_ld32_two(t_s, lower, t_s + AT_SUB, upper);
-                    if (!open) {
-                        hide(lower, 0);
-                        hide(upper, AT_SUB);
-#pragma unroll
-                        for (int c = 0; c < AT_SUB; c += 8) tmem_st8(t_s + c, lower + c);   // (as it is read again)
+                        tmem_st_wait();
                     }
-                    most(lower);
-                    most(upper);
+                    float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+                    for (int e = 0; e < AT_KEYS; e += 8)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            mx[c] = max3(mx[c], __uint_as_float(s[e / AT_SUB][e % AT_SUB + 2 * c]), __uint_as_float(s[e / AT_SUB][e % AT_SUB + 2 * c + 1]));
                     const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                     const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
                     if (__any_sync(FULL, grow)) {
@@ -736,34 +731,30 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     }
                     const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    auto weigh = [&](uint32_t (&s)[AT_SUB], int at) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[AT_SUB];
+                        tmem_ld32<AT_SUB>(t_s + h * AT_SUB, x);
                         if (any_far) {
 #pragma unroll
-                            for (int e = 0; e < AT_SUB; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - sub);
+                            for (int e = 0; e < AT_SUB; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - sub);
                         }
 #pragma unroll
                         for (int c = 0; c < AT_SUB; c += 16) {
                             uint32_t pk[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                const float2 x = fma2_packed(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]), k2k2, offoff);
-                                pk[e] = at_bf16x2(ex2(x.x), ex2(x.y));
+                                const float2 y = fma2_packed(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]), k2k2, offoff);
+                                pk[e] = at_bf16x2(ex2(y.x), ex2(y.y));
                                 add_bf16x2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], pk[e]);
                             }
-                            tmem_st8(t_s + P_COL + (at + c) / 2, pk);
+                            tmem_st8(t_s + (h * AT_SUB + c) / 2, pk);
                         }
-                    };
-                    auto told = [&](uint64_t *bar) {
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar);
-                    };
-                    weigh(upper, AT_SUB);
-                    told(&sh.phalf[buf]);
-                    tmem_ld32<AT_SUB>(t_s, lower);
-                    weigh(lower, 0);
-                    told(&sh.pfull[buf]);
+                        if (lane == 0) mbar_arrive(h ? &sh.pfull[buf] : &sh.phalf[buf]);
+                    }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 } else {
                     tc_fence_before();
