@@ -479,7 +479,7 @@ int santa_attend_workspace_size(const santa_shape *shape, int32_t T, size_t *byt
  * A batch row with pos < 0, counts outside [0, T] or pos + counts > n_max is skipped
  * (SANTA_DEV_BAD_POSITION).  Keys of a page outside [0, n_pages) count as zeros, K and V
  * (SANTA_DEV_BAD_PAGE).  Scores and sums in fp32, weights rounded to bf16 (and summed as
- * rounded), the result rounded once.  One launch; it can be captured.  Results do not depend on timing:
+ * rounded), the result rounded once; sums of values below 2^80 stay in range.  One launch; it can be captured.  Results do not depend on timing:
  * the same call on the same device gives the same bits.
  */
 int santa_attend_paged(const santa_shape *shape, const void *q, const int64_t q_stride[3], const santa_paged *cache,

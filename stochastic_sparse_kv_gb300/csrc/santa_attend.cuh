@@ -7,32 +7,56 @@
 //
 // Rows and items.  The G query heads of a KV head and consecutive tokens share K and V: they are
 // the rows of one product, token by token, 128 to a tile (a row of the MMA, a lane of TMEM).  An
-// item is NQ tiles (NQ = 1 where the whole chunk is one) of one sequence and KV head, with the
-// tiles of 128 keys that any of its tokens sees.
+// item is NQ tiles of one sequence and KV head with the tiles of 128 keys that any of its tokens sees.
+// NQ = 1 where the whole chunk is one tile (decode steps, drafted tokens): HBM bounds it, and all
+// other shared memory is ring.  NQ = 2 else: K and V in shared memory serve 256 rows.
 //
 // Shares.  The list of all items' key tiles, over sequences, row tiles and KV heads, is cut into
 // equal contiguous shares, one a CTA, one CTA an SM: any mix of prompts, decode steps, lengths and
-// windows fills the GPU, without a queue.  An item that spans CTAs leaves pieces (the running
-// maximum and sum, and the sum over V, of each row) in the workspace; the last CTA to arrive joins
-// them in the order of the list, so results do not depend on timing.
+// windows fills the GPU, without a queue.  An item counts AT_SETUP tiles more than it has (prompts
+// of 2 x 8k tokens: 2 1024 us, 3 901, 4 844, 6 846, 8 859).  One that spans CTAs leaves pieces (the reference
+// and the sum of the weights, and the sum over V, of each row) in the workspace; the last CTA to arrive
+// joins them in the order of the list, so results do not depend on timing.
 //
 // Warps of a CTA:
-//  * a producer warp: the item's q rows by one tiled TMA copy (strides of any projection's slice),
-//    then K and V of each tile, page by page, a lane a page, into a ring of stages;
-//  * an MMA warp, one thread of which issues S = Q K^T (both from shared memory) and O += P V, P
-//    read from TMEM and V from shared memory as it lies (keys as rows: MN-major);
-//  * eight softmax warps a row tile, two threads a row: scores from TMEM to registers, their maximum,
-//    p = 2^(k2 (s - m)), rounded to bf16 and written to TMEM over the scores; the sum l of the
-//    rounded values, so that a rounding moves numerator and denominator alike.  m is a score so
-//    far and moves only when one exceeds it by 2^AT_SLACK, so that O in TMEM is seldom rescaled.
-// With two row tiles one is in the tensor cores while the other is in its softmax; with one, the
-// next tile's scores are (two score buffers).
+//  * a producer: the item's q rows by one tiled TMA copy a column block (strides of any projection's
+//    slice), then K and V of each tile, page by page, a lane a page, into a ring of 32 KB stages (five,
+//    or six with one row tile; d = 64: eight of 16 KB);
+//  * an MMA warp a row tile, an elected lane of which issues S = Q K^T (both from shared memory) and
+//    O += P V, P read from TMEM, V from shared memory as it lies (keys as rows: MN-major);
+//  * four softmax warps a row tile, a thread a row: the scores' maximum; p = 2^(k2 s - r), rounded to bf16
+//    and written to TMEM over the scores, in two halves, so that P V begins with the first; the sum of the
+//    rounded values, so that a rounding moves numerator and denominator alike.  r belongs to a score
+//    so far and moves only when one exceeds it by 2^AT_SLACK, so that O in TMEM is seldom
+//    rescaled.
+// TMEM has room for one score buffer a row tile beside two outputs of 128 columns, so the chain scores,
+// softmax, product, scores of a row tile cannot overlap itself.  The two row tiles overlap one
+// another: their MMA warps take turns, and while one row tile is in the tensor cores the other is in
+// its softmax (without turns both came to do the same at the same time: 2048 tokens on 30k 895 us
+// against 786).  One row tile has two score buffers.
 //
 // Masks.  A tile that all the item's tokens see whole takes no mask.  In the others the scores of
 // hidden keys become minus infinity.  p is 0 there, but 0 times a NaN or an infinity in V is not:
-// in those tiles such values are set to zero in shared memory, and when one belongs to a key that
-// some token sees, the rows that see it get it added at the end.  That also covers what a page
+// in those tiles such values of hidden keys are set to zero in shared memory, and when one belongs to a key
+// that some token sees, the rows that see it get it added at the end.  That also covers what a page
 // holds behind the last key.
+//
+// Precision.  Scores, references, sums of weights and outputs are fp32 (a score is a chain of d / 16 MMA
+// steps, an output one of a step for every 16 keys of the share).  P is bf16, as V is: one rounding of each
+// weight, 2^-8 at most, of which the common part cancels.  Error against 64 bits (root mean square,
+// relative) 1.9e-3 to 2.1e-3; the rounding of the result alone is 1.7e-3.
+//
+// What bounds it.  Long chunks: the chain of a row tile, about 3500 clocks a tile of 128 keys, of which
+// 2 x 1024 are MMAs (the tensor pipe is active 60% of the time, issue slots 48%, the exponential
+// unit 30%).  2048 tokens on 30k keys, 32 heads: 1.07 TFLOP in 786 us, 1.36 PFLOP/s, 0.70 of the measured
+// dense rate; 2 prompts of 8192 tokens 846 us, 0.67.  Of an item's ends, the tiles with masks take 5000
+// clocks and the results 2500.  One token on 16 sequences of 32k keys: 312 us, 6.9 TB/s, above the measured
+// copy rate; on one sequence of 32k keys 34 us, of which 6 are the first copies' way and 6 the
+// joins.  Steps that led here, by 2048 tokens on 30k: 1069 us with one MMA warp whose lane was picked by
+// its number (operands then move to uniform registers one at a time: 95 clocks an MMA instead of 64);
+// 883 with two threads a row (same exponentials, one more rendezvous a tile); 918 with parts of 64
+// keys and two score buffers a row tile (an MMA of 64 columns takes as long as one of 128); 895 with an MMA
+// warp a row tile; 786 with turns.
 #pragma once
 
 #include "santa_kv4.cuh"
