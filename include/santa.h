@@ -442,7 +442,8 @@ typedef struct {
  *            with pos < 0, counts outside [0, T] or pos + counts > n_max is skipped
  *            (SANTA_DEV_BAD_POSITION); a token whose table entry is outside [0, n_pages) is not
  *            written, but its query is rotated (SANTA_DEV_BAD_PAGE)
- * No two live tokens may go to the same row of the same page (not checked).  B * T * (H_q +
+ * No two live tokens may go to the same row of the same page, and what is written (the pools, q_out)
+ * may not share memory with itself or with `rows` (not checked, but for one pool given as both).  B * T * (H_q +
  * 2 H_kv) * d / 16 below 2^31.  One launch; it can be captured, the table, positions and counts are read
  * when it runs.
  */
@@ -474,7 +475,8 @@ int santa_attend_workspace_size(const santa_shape *shape, int32_t T, size_t *byt
  *  pos       device int32 [B]: tokens in the cache before the chunk
  *  counts    device int32 [B] or NULL: how many of the T tokens are live
  *  window    >= 0; sinks >= 0 (ignored when window = 0); shape->scale >= 0
- *  out       device bf16 [B, T, H_q, d], contiguous; rows t >= counts[b] stay as they were
+ *  out       device bf16 [B, T, H_q, d], contiguous; rows t >= counts[b] stay as they were; may be
+ *            q itself
  *  workspace of santa_attend_workspace_size bytes, 256-byte aligned, initialised once
  * A batch row with pos < 0, counts outside [0, T] or pos + counts > n_max is skipped
  * (SANTA_DEV_BAD_POSITION).  Keys of a page outside [0, n_pages) count as zeros, K and V

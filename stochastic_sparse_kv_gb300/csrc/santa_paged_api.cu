@@ -174,6 +174,7 @@ int santa_paged_append(const santa_shape *shape, const santa_paged *cache, const
     int rc = check_paged(shape, cache);
     if (rc) return rc;
     if (!rows || !rows->k || !rows->v || !pos || T < 0 || !q != !q_out) return SANTA_ERR_INVALID_ARG;
+    if (cache->k == cache->v) return SANTA_ERR_INVALID_ARG;  // (K and V would be written to the same rows)
     if (q && (!q_stride || !q_out_stride || !rotation)) return SANTA_ERR_INVALID_ARG;
     if (!aligned(rows->k, 16) || !aligned(rows->v, 16) || !aligned(pos, 4) || (counts && !aligned(counts, 4)) ||
         (q && (!aligned(q, 16) || !aligned(q_out, 16))) || (workspace && !aligned(workspace, 256)))

@@ -614,14 +614,27 @@ def _rotation_arg(table: RopeTable, dev):
 
 
 _strides = ctypes.c_int64 * 3
+_stride_args: dict = {}   # strides of a [B, T, H, d] tensor -> those of (batch, token, head) as a C argument
+_append_shapes: dict = {}
+
+
+def _kept(cache: dict, key, make):
+    """cache[key], made on first use; these are C arguments of plain numbers."""
+    got = cache.get(key)
+    if got is None:
+        if len(cache) >= 1024:
+            cache.clear()
+        got = cache[key] = make(key)
+    return got
 
 
 def _row_tensor(t: torch.Tensor, name: str, shape, dev):
-    if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 4 or t.stride(3) != 1:
+    st = t.stride()
+    if t.dtype is not torch.bfloat16 or t.device != dev or len(st) != 4 or st[3] != 1:
         raise ValueError(f"{name} must be a bf16 tensor [B, T, H, d] on the inputs' device, contiguous in d")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    return t.data_ptr(), _strides(*t.stride()[:3])
+    return t.data_ptr(), _kept(_stride_args, st, lambda x: _strides(*x[:3]))
 
 
 def _on_stream(stream, dev, call, made):
@@ -661,7 +674,7 @@ def rope(x: torch.Tensor, table: RopeTable, pos: torch.Tensor, counts: torch.Ten
     if T == 0:
         return out
     with _on_device(dev):
-        rc = load().santa_rope(B, T, H, d, x_ptr, x_st, o_ptr, o_st, rotation, pos.data_ptr(),
+        rc = (_lib or load()).santa_rope(B, T, H, d, x_ptr, x_st, o_ptr, o_st, rotation, pos.data_ptr(),
                                counts.data_ptr() if counts is not None else None,
                                workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
     if rc:
@@ -672,16 +685,16 @@ def rope(x: torch.Tensor, table: RopeTable, pos: torch.Tensor, counts: torch.Ten
 def _paged_dims(cache: PagedCache):
     """(B, H_kv, n_max, d, page, device) of a checked cache."""
     k, v, table = cache
-    dev = k.device
-    if k.dim() != 4 or v.shape != k.shape or not k.is_cuda:
+    dev, size, columns = k.device, k.shape, table.shape
+    if len(size) != 4 or v.shape != size or not k.is_cuda:
         raise ValueError("a paged cache holds CUDA tensors k and v [n_pages, H_kv, page, d]")
-    for t in (k, v):
-        if t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
-            raise ValueError("a paged cache holds contiguous bf16 tensors on one CUDA device")
-    if table.dtype != torch.int32 or table.device != dev or table.dim() != 2 or not table.is_contiguous():
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or v.device != dev or not k.is_contiguous() or \
+            not v.is_contiguous():
+        raise ValueError("a paged cache holds contiguous bf16 tensors on one CUDA device")
+    if table.dtype is not torch.int32 or table.device != dev or len(columns) != 2 or not table.is_contiguous():
         raise ValueError("a paged cache's table is a contiguous int32 tensor [B, columns] on its device")
-    _, H_kv, page, d = k.shape
-    return table.shape[0], H_kv, table.shape[1] * page, d, page, dev
+    _, H_kv, page, d = size
+    return columns[0], H_kv, columns[1] * page, d, page, dev
 
 
 def _paged_arg(cache: PagedCache):
@@ -722,9 +735,9 @@ def paged_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, po
     rotation = _rotation_arg(rope, dev) if rope is not None else None
     if T == 0:
         return q_out
-    shape = make_shape(B, H_q, H_kv, d, n_max)
+    shape = _kept(_append_shapes, (B, H_q, H_kv, d, n_max), lambda x: ctypes.byref(make_shape(*x)))
     with _on_device(dev):
-        rc = load().santa_paged_append(ctypes.byref(shape), _paged_arg(cache), ctypes.byref(_Rows(k_ptr, v_ptr, k_st, v_st)), T,
+        rc = (_lib or load()).santa_paged_append(shape, _paged_arg(cache), ctypes.byref(_Rows(k_ptr, v_ptr, k_st, v_st)), T,
                                        pos.data_ptr(), counts.data_ptr() if counts is not None else None, rotation, *q_arg,
                                        workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
     if rc:
@@ -737,15 +750,9 @@ _attend_shapes: dict = {}
 
 def _attend_shape_of(key):
     """(the shape as a C argument, the workspace bytes of attend_paged), kept per shape and T."""
-    got = _attend_shapes.get(key)
-    if got is None:
-        shape, n = make_shape(*key[:-1]), ctypes.c_size_t(0)
-        _check(load().santa_attend_workspace_size(ctypes.byref(shape), key[-1], ctypes.byref(n)),
-               "santa_attend_workspace_size")
-        if len(_attend_shapes) >= 1024:
-            _attend_shapes.clear()
-        got = _attend_shapes[key] = (ctypes.byref(shape), int(n.value))
-    return got
+    shape, n = make_shape(*key[:-1]), ctypes.c_size_t(0)
+    _check(load().santa_attend_workspace_size(ctypes.byref(shape), key[-1], ctypes.byref(n)), "santa_attend_workspace_size")
+    return ctypes.byref(shape), int(n.value)
 
 
 def attend_paged(q: torch.Tensor, cache: PagedCache, pos: torch.Tensor, counts: torch.Tensor | None = None, window: int = 0,
@@ -765,23 +772,24 @@ def attend_paged(q: torch.Tensor, cache: PagedCache, pos: torch.Tensor, counts: 
         return _on_stream(stream, dev, lambda: attend_paged(q, cache, pos, counts, window, sinks, scale, out, workspace),
                           out is None)
     q_ptr, q_st = _row_tensor(q, "q", None, dev)
-    if q.shape[0] != B or q.shape[3] != d:
+    size = q.shape
+    if size[0] != B or size[3] != d:
         raise ValueError("q [B, T, H_q, d] and the cache's shape disagree")
     _int_vector(pos, "pos", B, dev)
     if counts is not None:
         _int_vector(counts, "counts", B, dev)
-    T = q.shape[1]
-    shape, nbytes = _attend_shape_of((B, q.shape[2], H_kv, d, n_max, scale, T))
+    T = size[1]
+    shape, nbytes = _kept(_attend_shapes, (B, size[2], H_kv, d, n_max, scale, T), _attend_shape_of)
     if out is None:
         out = _out_rows(q, counts)
-    elif out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != q.shape or out.device != dev:
+    elif out.dtype is not torch.bfloat16 or not out.is_contiguous() or out.shape != size or out.device != dev:
         raise ValueError("out must be a contiguous bf16 tensor [B, T, H_q, d] on q's device")
     if T == 0:
         return out
     with _on_device(dev):
         raw = _raw_stream(None, dev)
         ws = workspace if workspace is not None else _own_workspace("attend", nbytes, dev, raw)
-        rc = load().santa_attend_paged(shape, q_ptr, q_st, _paged_arg(cache), T, pos.data_ptr(),
+        rc = (_lib or load()).santa_attend_paged(shape, q_ptr, q_st, _paged_arg(cache), T, pos.data_ptr(),
                                        counts.data_ptr() if counts is not None else None, window, sinks, out.data_ptr(),
                                        ws.data_ptr(), ws.numel(), raw)
     if rc:

@@ -26,7 +26,7 @@ def shape(B=2, H_q=8, H_kv=2, d=128, n_max=256, scale=0.0):
     return ctypes.byref(santa.make_shape(B, H_q, H_kv, d, n_max, scale))
 
 
-def pool(k=A, v=A, table=A, n_pages=40, page=16):
+def pool(k=A, v=2 * A, table=A, n_pages=40, page=16):
     return ctypes.byref(santa._Paged(k, v, table, n_pages, page))
 
 
@@ -69,7 +69,7 @@ def test_append_refusals(lib):
     assert call(T=0) == 0 and call(T=0, ro=rot(), q=A, qs=st, qo=A, qos=st) == 0
     assert call(T=-1) == -1 and call(pos=None) == -1 and call(r=rows(k=None)) == -1 and call(r=rows(v=None)) == -1
     assert call(c=pool(k=None)) == -1 and call(c=pool(v=None)) == -1 and call(c=pool(table=None)) == -1
-    assert call(c=pool(n_pages=0)) == -1
+    assert call(c=pool(n_pages=0)) == -1 and call(c=pool(v=A)) == -1                 # one pool for K and V
     for page in (0, 8, 24, 48, 512, -16):
         assert call(c=pool(page=page)) == -4
     assert call(sh=shape(n_max=100)) == -4 and call(sh=shape(n_max=524288 + 16)) == -4 and call(sh=shape(n_max=0)) == -1

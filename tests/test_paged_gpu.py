@@ -197,6 +197,21 @@ def test_append_skips_what_has_no_place():
         assert (pool[2] == 9).all() and (pool[7] == 9).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_as_many_tokens_as_there_may_be(d):
+    """2^31 - 1 groups of features, or the most below, of which few tokens are live (one row stands for
+    them all: token stride 0)."""
+    T = ((1 << 31) - 1) // (2 * (d // 16))
+    row = rand(gen(d), 1, 1, 1, d).to(DEV)
+    cache = santa.PagedCache(*(torch.zeros(4, 1, 16, d, dtype=bf16, device=DEV) for _ in range(2)), ints([[2, 0, 3]]))
+    santa.paged_append(cache, row.expand(1, T, 1, d), row.expand(1, T, 1, d), ints([14]), ints([3]))
+    for pool in (cache.k, cache.v):
+        assert torch.equal(pool[2, 0, 14:], row[0, 0].expand(2, d)) and torch.equal(pool[0, 0, 0], row[0, 0, 0])
+        assert not pool[2, 0, :14].any() and not pool[0, 0, 1:].any() and not pool[1].any() and not pool[3].any()
+    with pytest.raises(santa.SantaError):
+        santa.paged_append(cache, row.expand(1, T + 1, 1, d), row.expand(1, T + 1, 1, d), ints([14]), ints([3]))
+
+
 # ------------------------------------------------------------------ attend
 
 def problem(g, B, T, H_kv, G, d, page, lengths, counts, std=3.0, extra=0):
@@ -505,6 +520,10 @@ def big(g, B, T, H_kv, G, d, page, lengths, seed):
     (2, 1500, 2, 8, 128, 16, [1500, 6001], 1000, 100),
     (1, 4099, 1, 1, 64, 32, [20000], 0, 0),
     (64, 9, 2, 4, 64, 64, [100 + 97 * i for i in range(64)], 0, 0),
+    (1, 1, 1, 8, 64, 256, [524288], 0, 0),                                    # the longest cache
+    (1024, 1, 1, 4, 64, 16, [1 + (i * 7) % 53 for i in range(1024)], 0, 0),   # the most rows
+    (1000, 40, 1, 4, 64, 16, [(i * 7) % 41 for i in range(1000)], 0, 0),      # padded, rows of no length among them
+    (2, 4096, 1, 4, 64, 64, [5, 4100], 0, 0),                                 # padded: few tokens of a long chunk
 ])
 def test_attend_at_length(B, T, H_kv, G, d, page, lengths, window, sinks):
     """Work that spans many CTAs: tokens of every sequence against 64 bits on the GPU; the same call
@@ -520,9 +539,23 @@ def test_attend_at_length(B, T, H_kv, G, d, page, lengths, window, sinks):
     assert torch.equal(out, santa.attend_paged(q, cache, ints(pos), ints(counts), window, sinks, workspace=ws))
     for b in list(range(B))[:: max(1, B // 8)]:
         c = counts[b]
+        if c == 0:
+            continue
         rows = sorted({0, c - 1, c // 2, c // 3, min(c - 1, 63), min(c - 1, 64), min(c - 1, 257)})
         want, spread = reference_on_gpu(q, k, v, table, pos, window, sinks, b, rows)
         check(out[b, rows][None], want[None], spread[None], [len(rows)])
+
+
+def test_the_result_may_go_over_the_queries():
+    """out = q: every row of a tile is read before the tile's results are written."""
+    g = gen(21)
+    q, k, v, table = big(g, 2, 300, 2, 4, 128, 64, [5000, 300], 9)
+    cache, pos = santa.PagedCache(k, v, table.to(DEV)), ints([4700, 0])
+    want = santa.attend_paged(q, cache, pos)
+    for _ in range(5):
+        x = q.clone()
+        assert santa.attend_paged(x, cache, pos, out=x) is x
+        assert torch.equal(x, want)
 
 
 def test_pool_rows_beyond_32_bits():
