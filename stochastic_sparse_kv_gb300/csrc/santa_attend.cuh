@@ -226,6 +226,8 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t
     }
 }
 
+constexpr int AT_WALK = 96;
+static_assert(sizeof(AtWalk<1>) <= AT_WALK && sizeof(AtWalk<2>) <= AT_WALK, "room for a walk");
 struct AtSmem {
     uint64_t full[AT_STAGES_MAX], empty[AT_STAGES_MAX];
     uint64_t qfull, qempty;
@@ -243,6 +245,7 @@ struct AtSmem {
     int qfills, qfills_used[2];
     int is_last[2];
     int arrived[2][2];            // [slot][row tile]: arrivals of this CTA's pieces
+    alignas(16) uint8_t walk[8][AT_WALK];   // the softmax warps' walks: not in their registers
 };
 static_assert(sizeof(AtSmem) <= AT_MISC, "barriers and the like");
 
@@ -640,8 +643,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         const int q = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t t_o = tbase + lanes + O_COL + q * D;
-        AtWalk<NQ> w;
-        w.begin(p, f0, sh.start_base, sh.start_pair);
+        AtWalk<NQ> &w = *reinterpret_cast<AtWalk<NQ> *>(sh.walk[warp]);   // (lane 0 moves it)
         int n = 0, n0 = 0;            // tiles of this row tile so far; tiles of the CTA before the item
         uint32_t wg_phase = 0;
         bool ok = true;
@@ -657,25 +659,44 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             wg_phase ^= 1u;
             return ok;
         };
-        for (; ok && w.seek(p, f0, f1); n0 += w.i1 - w.i0, w.step(p)) {
+        int more = 0;
+        if (lane == 0) {
+            w.begin(p, f0, sh.start_base, sh.start_pair);
+            more = w.seek(p, f0, f1);
+        }
+        auto next = [&]() {
+            __syncwarp();
+            if (lane == 0) {
+                w.step(p);
+                more = w.seek(p, f0, f1);
+            }
+        };
+        for (; ok && __shfl_sync(FULL, more, 0); next()) {
+            __syncwarp();
             const int live = w.live_rows(p) - q * AT_ROWS;   // of this row tile
-            if (live <= 0) continue;
+            const int tiles = w.i1 - w.i0;
+            if (live <= 0) {
+                n0 += tiles;
+                continue;
+            }
             const bool warp_live = 32 * (warp & 3) < live;
             const int P = w.it.first + w.it.t0 + ((q * AT_ROWS + row) >> p.lg_g);
             const int seen_lo = p.window > 0 ? P - p.window + 1 : 0;
+            // a tile that begins before the one and after the other all tokens see whole
+            const int open_hi = w.it.first + w.it.t0 - AT_KEYS + 2, open_lo = p.window > 0 ? w.it.first + w.it.t1 - p.window : -1;
+            int key = w.it.key(w.i0), left = w.it.nsink - w.i0;
             // m: the reference of the row's weights (a score so far); off, sub: how they are taken with it
             float m = NEG_INF, l = 0.f, off = 0.f, sub = 0.f;
             bool any_far = false;
-            for (int i = w.i0; i < w.i1; ++i, ++n) {
+            for (int i = 0; i < tiles; ++i, ++n) {
                 const int buf = NQ == 2 ? q : n & 1;
                 const uint32_t t_s = tbase + lanes + buf * AT_KEYS;
-                const int key = w.it.key(i);
-                const bool open = w.open(p, key);
+                const bool open = key < open_hi && (key > open_lo || key + AT_KEYS <= p.sinks);
                 if (!wait(&sh.sfull[buf], (NQ == 2 ? n : n >> 1) & 1)) break;
                 if (!open) {
                     // values of V that are not finite become zeros (both row tiles' warps look at all of
                     // them: what the other has set to zero is zero, or becomes it twice)
-                    const int f = 2 * (n0 + i - w.i0) + 1;
+                    const int f = 2 * (n0 + i) + 1;
                     if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
                     uint8_t *v = ring + (f % NS) * SB;
                     auto clear = [&](int r0, int r1) {   // in rows r0 .. r1 - 1
@@ -705,9 +726,6 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
                 if (warp_live) {
                     tc_fence_after();
-                    // the scores are read twice: for their maximum, and half by half for the weights, which
-                    // go over what has been read.  (One loop for both halves: the less code, the
-                    // fewer waits for instructions)
                     uint32_t s[2][AT_SUB];
                     tmem_ld32_two(t_s, s[0], t_s + AT_SUB, s[1]);
                     if (!open) {
@@ -718,10 +736,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
 #pragma unroll
                             for (int e = c % AT_SUB; e < c % AT_SUB + 32; ++e)
                                 if (!((seen >> (e % 32)) & 1u)) s[c / AT_SUB][e] = 0xff800000u;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8) tmem_st8(t_s + c + e, s[c / AT_SUB] + c % AT_SUB + e);
                         }
-                        tmem_st_wait();
                     }
                     float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
@@ -739,7 +754,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                         sub = far ? m : 0.f;
                         off = far || m == NEG_INF ? 0.f : -(m * p.k2);
                         any_far = __any_sync(FULL, far);
-                        if (i > w.i0) {
+                        if (i > 0) {
                             if (!wait(&sh.ofull[q][(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
                             tc_fence_after();
 #pragma unroll 1
@@ -755,10 +770,9 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     }
                     const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
+#pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t x[AT_SUB];
-                        tmem_ld32<AT_SUB>(t_s + h * AT_SUB, x);
+                        uint32_t (&x)[AT_SUB] = s[h];
                         if (any_far) {
 #pragma unroll
                             for (int e = 0; e < AT_SUB; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - sub);
@@ -788,7 +802,10 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                         mbar_arrive(&sh.pfull[buf]);
                     }
                 }
+                key += AT_KEYS;
+                if (--left == 0) key = w.it.tlo * AT_KEYS;
             }
+            n0 += tiles;
             if (!ok) break;
             // (a parity tells only a phase from the next.  When scores are here, the product of two tiles before
             // is done and that of the tile before may be: one barrier would be one or two phases on)
