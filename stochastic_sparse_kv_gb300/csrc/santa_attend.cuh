@@ -49,7 +49,7 @@
 // What bounds it.  Long chunks: the chain of a row tile, about 3500 clocks a tile of 128 keys, of which
 // 2 x 1024 are MMAs (the tensor pipe is active 60% of the time, issue slots 48%, the exponential
 // unit 30%).  2048 tokens on 30k keys, 32 heads: 1.07 TFLOP in 786 us, 1.36 PFLOP/s, 0.70 of the measured
-// dense rate; 2 prompts of 8192 tokens 846 us, 0.67.  Of an item's ends, the tiles with masks take 5000
+// dense rate; 2 prompts of 8192 tokens 834 us, 0.68.  Of an item's ends, the tiles with masks take 5000
 // clocks and the results 2500.  One token on 16 sequences of 32k keys: 312 us, 6.9 TB/s, above the measured
 // copy rate; on one sequence of 32k keys 34 us, of which 6 are the first copies' way and 6 the
 // joins.  Steps that led here, by 2048 tokens on 30k: 1069 us with one MMA warp whose lane was picked by
@@ -700,22 +700,28 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     if (!wait(&sh.full[f % NS], (f / NS) & 1)) break;
                     uint8_t *v = ring + (f % NS) * SB;
                     auto clear = [&](int r0, int r1) {   // in rows r0 .. r1 - 1
+                        uint32_t bad = 0;
 #pragma unroll
                         for (int h = 0; h < PANELS; ++h)
-#pragma unroll 4
+#pragma unroll 8
+                            for (int c = 8 * r0 + row; c < 8 * r1; c += 128) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(v + h * PANEL + c * 16);
+                                bad |= at_not_finite(x.x) | at_not_finite(x.y) | at_not_finite(x.z) | at_not_finite(x.w);
+                            }
+                        if (bad == 0) return;   // (nearly always)
+                        for (int h = 0; h < PANELS; ++h)
                             for (int c = 8 * r0 + row; c < 8 * r1; c += 128) {
                                 uint4 &at = *reinterpret_cast<uint4 *>(v + h * PANEL + c * 16);
-                                uint4 x = at;
-                                const uint32_t b0 = at_not_finite(x.x), b1 = at_not_finite(x.y), b2 = at_not_finite(x.z), b3 = at_not_finite(x.w);
-                                if (b0 | b1 | b2 | b3) {
-                                    x.x &= ~((b0 >> 15) * 0xffffu);
-                                    x.y &= ~((b1 >> 15) * 0xffffu);
-                                    x.z &= ~((b2 >> 15) * 0xffffu);
-                                    x.w &= ~((b3 >> 15) * 0xffffu);
-                                    at = x;
-                                    const int j = key + c / 8;
-                                    if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) sh.bad_v = 1;
-                                }
+                                const uint4 x = at;
+                                const uint4 y = make_uint4(x.x & ~((at_not_finite(x.x) >> 15) * 0xffffu), x.y & ~((at_not_finite(x.y) >> 15) * 0xffffu),
+                                                           x.z & ~((at_not_finite(x.z) >> 15) * 0xffffu), x.w & ~((at_not_finite(x.w) >> 15) * 0xffffu));
+                                if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
+                                const int j = key + c / 8;
+                                if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) *(volatile int *)&sh.bad_v = 1;
+                                *(volatile uint32_t *)&at.x = y.x;   // (in this order: who finds zeros finds the flag)
+                                *(volatile uint32_t *)&at.y = y.y;
+                                *(volatile uint32_t *)&at.z = y.z;
+                                *(volatile uint32_t *)&at.w = y.w;
                             }
                     };
                     // keys beyond the first token, and keys before the last one's window
