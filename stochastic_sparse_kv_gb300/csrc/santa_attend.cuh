@@ -59,7 +59,6 @@
 // warp a row tile; 786 with turns.
 #pragma once
 
-#include "santa_kv4.cuh"
 #include "santa_tcgen05.cuh"
 
 namespace santa {
@@ -72,7 +71,7 @@ constexpr int AT_SETUP = 4;               // what an item costs beside its tiles
 constexpr int AT_MIN_SHARE = 2;           // a share's least size, in tiles
 constexpr float AT_SLACK = 24.f;          // log2 of the largest p (sums of values below 2^80 stay in range)
 constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
-constexpr int AT_MISC = 3072;             // of it for barriers and the like
+constexpr int AT_MISC = 2048;             // of it for barriers and the like
 constexpr int AT_STAGES_MAX = 8;
 
 // four softmax warps and an MMA warp a row tile, and the producer
@@ -89,7 +88,10 @@ __host__ __device__ constexpr int at_smem(int D, int NQ)
     return at_qbytes(D, NQ) + at_stages(D, NQ) * at_stage_bytes(D) + AT_MISC;
 }
 
-// Row tiles of an item, and rows that a piece holds, by the rows T * G of a sequence and KV head.
+// Row tiles of an item, and rows that a piece holds, by the rows T * G of a sequence and KV head.  One tile
+// against two: 2048 tokens on 30k keys (8192 rows) 1069 and 817 us, prompts of 8192 tokens 1141 and 847,
+// the mixed batch of up to 2040 rows 309 and 240; one token (4 rows) on 32k keys 35 and 55, on 16 x 32k 317 and
+// 334, 5 tokens (20 rows) 105 and 113.
 __host__ __device__ constexpr int at_nq(long long rows) { return rows > AT_ROWS ? 2 : 1; }
 __host__ __device__ constexpr int at_piece_rows(long long rows) { return rows > AT_ROWS ? 2 * AT_ROWS : (int)rows; }
 
@@ -256,13 +258,6 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
-__device__ __forceinline__ uint32_t at_bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Weights are 2^(k2 s - r), r = k2 m rounded to fp32: its rounding moves all weights of a row alike.  Where
 // that could be by more than 2^0.5 (scores of a size that no model has), they are 2^(k2 (s - m))
 // instead, r = k2 m exactly.
@@ -316,7 +311,7 @@ __device__ __forceinline__ uint32_t at_low_bits(int x) { return x <= 0 ? 0u : x 
 
 __device__ __forceinline__ uint32_t at_scaled(uint32_t a, uint32_t b, float f)
 {
-    return at_bf16x2(__uint_as_float(a) * f, __uint_as_float(b) * f);
+    return bf16x2(__uint_as_float(a) * f, __uint_as_float(b) * f);
 }
 
 // Element of `out` where row R (token by token, head by head) of an item begins.
@@ -327,8 +322,10 @@ __device__ __forceinline__ size_t out_at(const AttendParams &p, int b, int t0, i
 }
 
 // Float of a piece where columns 4 c .. 4 c + 3 of row r are: row by row where rows are few and the threads
-// of a join take columns, else the rows of a column group side by side (a warp's accesses are 512 bytes).
-constexpr int AT_FEW = 32;
+// of a join take columns, else the rows of a column group side by side (a warp's accesses are 512 bytes), a
+// thread a row.  The first way against the second: 4 rows and 20 pieces 35 and 51 us (one token on 32k keys), 20
+// rows 105 and 102, 256 rows 838 and 799 (2048 tokens on 30k), 277 and 240 (mixed batch).
+constexpr int AT_FEW = 16;
 constexpr int AT_BATCH = 10;
 template <int D>
 __device__ __forceinline__ size_t at_piece(int rows, int r, int c)
@@ -350,6 +347,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     constexpr int W_MMA = NQ * 4, W_PROD = W_MMA + NQ;   // warps: softmax, MMA (one a row tile), producer
     constexpr uint32_t ID_S = idesc_bf16_f32(AT_ROWS, AT_KEYS), ID_O = idesc_bf16_f32(AT_ROWS, D) | IDESC_B_MN;
     constexpr uint32_t O_COL = 256;            // score buffers in columns 0-255, outputs behind them
+    constexpr uint32_t P_COL = 64;             // weights over the upper half of their scores
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(NS >= 4, "ring");
     const float NEG_INF = __int_as_float(0xff800000);
@@ -555,14 +553,14 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             }
             __syncwarp();
         };
-        // O += P V over the lower (part 0) or the upper half of the keys
+        // O += P V over the upper (part 0) or the lower half of the keys
         auto values = [&](int at, int buf, int part, bool first) {
             if (elect_one()) {
                 const uint64_t v = umma_desc_sw128_mn(raddr + at * SB, PANEL);
 #pragma unroll
                 for (int y = 0; y < AT_SUB / 16; ++y) {
-                    const int x = y + part * (AT_SUB / 16);
-                    tc_mma_bf16_ta(t_o, tbase + buf * AT_KEYS + x * 8, v + x * (2048 / 16), ID_O, !first || part != 0 || y != 0);
+                    const int x = y + (part ? 0 : AT_SUB / 16);
+                    tc_mma_bf16_ta(t_o, tbase + buf * AT_KEYS + P_COL + x * 8, v + x * (2048 / 16), ID_O, !first || part != 0 || y != 0);
                 }
                 if (part) {
                     tc_commit(&sh.ofull[q][n & 1]);
@@ -732,24 +730,35 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
                 if (warp_live) {
                     tc_fence_after();
-                    uint32_t s[2][AT_SUB];
-                    tmem_ld32_two(t_s, s[0], t_s + AT_SUB, s[1]);
-                    if (!open) {
+                    // the upper half of the scores stays in registers, the lower half is read again (all kept,
+                    // or both halves read again: 2048 tokens on 30k keys 811 and 807 us against 788)
+                    uint32_t lower[AT_SUB], upper[AT_SUB];
+                    auto hide = [&](uint32_t (&s)[AT_SUB], int at) {
 #pragma unroll
-                        for (int c = 0; c < AT_KEYS; c += 32) {
-                            const int k0 = key + c;
+                        for (int c = 0; c < AT_SUB; c += 32) {
+                            const int k0 = key + at + c;
                             const uint32_t seen = at_low_bits(P + 1 - k0) & (~at_low_bits(seen_lo - k0) | at_low_bits(p.sinks - k0));
 #pragma unroll
-                            for (int e = c % AT_SUB; e < c % AT_SUB + 32; ++e)
-                                if (!((seen >> (e % 32)) & 1u)) s[c / AT_SUB][e] = 0xff800000u;
+                            for (int e = 0; e < 32; ++e)
+                                if (!((seen >> e) & 1u)) s[c + e] = 0xff800000u;
                         }
-                    }
+                    };
                     float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+                    auto most = [&](const uint32_t (&s)[AT_SUB]) {
 #pragma unroll
-                    for (int e = 0; e < AT_KEYS; e += 8)
+                        for (int e = 0; e < AT_SUB; e += 8)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            mx[c] = max3(mx[c], __uint_as_float(s[e / AT_SUB][e % AT_SUB + 2 * c]), __uint_as_float(s[e / AT_SUB][e % AT_SUB + 2 * c + 1]));
+                            for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(s[e + 2 * c]), __uint_as_float(s[e + 2 * c + 1]));
+                    };
+                    tmem_ld32_two(t_s, lower, t_s + AT_SUB, upper);
+                    if (!open) {
+                        hide(lower, 0);
+                        hide(upper, AT_SUB);
+#pragma unroll
+                        for (int c = 0; c < AT_SUB; c += 8) tmem_st8(t_s + c, lower + c);   // (as it is read again)
+                    }
+                    most(lower);
+                    most(upper);
                     const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                     const bool grow = (top - m) * p.k2 > AT_SLACK;   // (a first one: infinity)
                     if (__any_sync(FULL, grow)) {
@@ -776,9 +785,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                     }
                     const uint64_t k2k2 = pack2(p.k2, p.k2), offoff = pack2(off, off);
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t (&x)[AT_SUB] = s[h];
+                    auto weigh = [&](uint32_t (&x)[AT_SUB], int at) {
                         if (any_far) {
 #pragma unroll
                             for (int e = 0; e < AT_SUB; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - sub);
@@ -789,16 +796,23 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const float2 y = fma2_packed(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]), k2k2, offoff);
-                                pk[e] = at_bf16x2(ex2(y.x), ex2(y.y));
+                                pk[e] = bf16x2(ex2(y.x), ex2(y.y));
                                 add_bf16x2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], pk[e]);
                             }
-                            tmem_st8(t_s + (h * AT_SUB + c) / 2, pk);
+                            tmem_st8(t_s + P_COL + (at + c) / 2, pk);
                         }
+                    };
+                    auto told = [&](uint64_t *bar) {
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(h ? &sh.pfull[buf] : &sh.phalf[buf]);
-                    }
+                        if (lane == 0) mbar_arrive(bar);
+                    };
+                    weigh(upper, AT_SUB);
+                    told(&sh.phalf[buf]);
+                    tmem_ld32<AT_SUB>(t_s, lower);
+                    weigh(lower, 0);
+                    told(&sh.pfull[buf]);
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 } else {
                     tc_fence_before();
@@ -929,8 +943,8 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
 #pragma unroll
                                 for (int e = 0; e < 16; e += 2)
                                     *reinterpret_cast<uint4 *>(out + 4 * e) =
-                                        make_uint4(at_bf16x2(o[e].x * inv, o[e].y * inv), at_bf16x2(o[e].z * inv, o[e].w * inv),
-                                                   at_bf16x2(o[e + 1].x * inv, o[e + 1].y * inv), at_bf16x2(o[e + 1].z * inv, o[e + 1].w * inv));
+                                        make_uint4(bf16x2(o[e].x * inv, o[e].y * inv), bf16x2(o[e].z * inv, o[e].w * inv),
+                                                   bf16x2(o[e + 1].x * inv, o[e + 1].y * inv), bf16x2(o[e + 1].z * inv, o[e + 1].w * inv));
                             }
                         }
                     } else {
@@ -966,7 +980,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                             }
                             const float inv = 1.f / sl;
                             *reinterpret_cast<uint2 *>(p.out + out_at<D>(p, w.b, w.it.t0, w.h, r) + 4 * e) =
-                                make_uint2(at_bf16x2(o0 * inv, o1 * inv), at_bf16x2(o2 * inv, o3 * inv));
+                                make_uint2(bf16x2(o0 * inv, o1 * inv), bf16x2(o2 * inv, o3 * inv));
                         }
                     }
                 }

@@ -234,6 +234,14 @@ __device__ __forceinline__ void prefetch_l2(const void *p)
 __device__ __forceinline__ float bf16lo_to_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi_to_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Two bf16 in a word, each rounded to the nearest (ties to even).
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Error-free transformations (Knuth's TwoSum, Dekker's Fast2Sum, FMA-based TwoProd):
 // s + e == a + b exactly.  The _rn intrinsics keep the compiler from contracting or
 // reassociating them.

@@ -51,13 +51,6 @@ struct RopeParams {
     int32_t *ctrl;                        // device error word (or NULL)
 };
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // A thread's 16 features as two 16-byte accesses, and what it does with them.
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(RP_NT, 4) santa_rope_kernel(const RopeParams p)
