@@ -340,6 +340,12 @@ int santa_decode_kv4(const santa_shape *shape, const void *q, const santa_kv4 *c
                      int32_t window, int32_t sinks, int32_t flags, float *out, void *workspace,
                      size_t workspace_bytes, void *stream);
 
+/* Flag, or-ed into T of santa_rope, santa_paged_append and santa_attend_paged: rows of the result (out,
+ * q_out) that no live token writes become zeros instead of staying as they were, the tokens from
+ * counts[b] on and all of a batch row that is skipped.  For a result in memory that holds anything.
+ * (T itself stays below 2^30 in every call.) */
+#define SANTA_CLEAR_REST 0x40000000
+
 /* ------------------------------------------------------------------ rotary positions
  *
  * A head at position p is rotated pair by pair: features (x, y) of pair i become

@@ -109,6 +109,7 @@ struct AttendParams {
     int tries;                    // of a wait between two looks at the clock
     uint32_t nap;                 // ns that one may sleep
     int wide;                     // out begins at a multiple of 32 bytes
+    int clear;                    // rows of out that no live token writes become zeros
 };
 
 // A batch row's tokens; none where pos and counts leave the cache.
@@ -333,6 +334,28 @@ __device__ __forceinline__ size_t at_piece(int rows, int r, int c)
     return rows > AT_FEW ? ((size_t)c * rows + r) * 4 : (size_t)r * D + 4 * c;
 }
 
+// Rows of `out` behind the live tokens of every batch row, all of them where the row is skipped, become
+// zeros: equal shares of each to the CTAs of the grid, of a few rows to other CTAs for every batch row.  Half of
+// 134 MB (32 x 255 tokens of 64 heads, d = 128): 13 us in the call, a fill of the whole before it 37.
+template <int D>
+__device__ __noinline__ void at_clear(const AttendParams &p)
+{
+    const long long row = (long long)p.H_q * (D / 8);   // of a token, in 16 bytes
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int mine = b0 + (threadIdx.x & 31);
+        int first, cnt = p.T;
+        if (mine < p.B) at_row(p, mine, first, cnt);
+        for (uint32_t some = __ballot_sync(0xffffffffu, cnt < p.T); some; some &= some - 1) {
+            const int at = __ffs(some) - 1, b = b0 + at, live = __shfl_sync(0xffffffffu, cnt, at);
+            uint4 *out = reinterpret_cast<uint4 *>(p.out) + ((long long)b * p.T + live) * row;
+            const long long n = (p.T - live) * row, step = (long long)gridDim.x * blockDim.x;
+            const unsigned cta = n < step ? (blockIdx.x + b) % gridDim.x : blockIdx.x;
+            for (long long i = (long long)cta * blockDim.x + threadIdx.x; i < n; i += step)
+                out[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 template <int D, int NQ>
 __global__ void __launch_bounds__(at_threads(NQ), 1)
     santa_attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -366,11 +389,13 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     const long long per = (pairs + NT_ - 1) / NT_;
     const long long x0 = min(pairs, per * tid), x1 = min(pairs, x0 + per);
     long long mine = 0;
+    bool dead = false;   // some token is not live
     {
         int b_at = -1, first = 0, cnt = 0;
         for (long long x = x0; x < x1; ++x) {
             const int b = (int)(x / qts), qt = (int)(x % qts);
             if (b != b_at) at_row(p, b_at = b, first, cnt);
+            dead |= cnt < p.T;
             AtItem it;
             const int L = at_item<NQ>(p, first, cnt, qt, it);
             if (L) mine += (long long)p.H_kv * (AT_SETUP + L);
@@ -383,7 +408,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         if (lane >= o) incl += up;
     }
     if (lane == 31) sh.sums[warp] = incl;
-    __syncthreads();
+    if (__syncthreads_or(p.clear && dead)) at_clear<D>(p);
     long long total = 0, before = incl - mine;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {

@@ -62,6 +62,14 @@ int check_paged(const santa_shape *sh, const santa_paged *c)
     return SANTA_OK;
 }
 
+// T of a call is the number of tokens and a flag.
+bool take_clear(int32_t &T)
+{
+    const bool clear = T > 0 && (T & SANTA_CLEAR_REST);
+    if (clear) T &= ~SANTA_CLEAR_REST;
+    return clear;
+}
+
 int log2_of(int x)
 {
     int s = 0;
@@ -147,6 +155,7 @@ int santa_rope(int32_t B, int32_t T, int32_t H, int32_t d, const void *x, const 
                const int64_t out_stride[3], const santa_rotation *rotation, const int32_t *pos, const int32_t *counts,
                void *workspace, void *stream)
 {
+    const bool clear = take_clear(T);
     if (B < 1 || T < 0 || H < 1 || d < 1 || !x || !x_stride || !out || !out_stride || !rotation || !pos)
         return SANTA_ERR_INVALID_ARG;
     if (B > BMAX || H > 1024 || (d != 64 && d != 128)) return SANTA_ERR_UNSUPPORTED;
@@ -160,6 +169,7 @@ int santa_rope(int32_t B, int32_t T, int32_t H, int32_t d, const void *x, const 
     RopeParams p{};
     p.q = rope_rows(x, x_stride, out, out_stride);
     p.B = B, p.T = T, p.H_q = H;
+    p.clear = clear;
     p.pos = pos, p.counts = counts;
     p.last = 0x7fffffff;
     p.ctrl = static_cast<int32_t *>(workspace);
@@ -171,6 +181,7 @@ int santa_paged_append(const santa_shape *shape, const santa_paged *cache, const
                        const int64_t q_stride[3], void *q_out, const int64_t q_out_stride[3], void *workspace,
                        void *stream)
 {
+    const bool clear = take_clear(T);
     int rc = check_paged(shape, cache);
     if (rc) return rc;
     if (!rows || !rows->k || !rows->v || !pos || T < 0 || !q != !q_out) return SANTA_ERR_INVALID_ARG;
@@ -191,6 +202,7 @@ int santa_paged_append(const santa_shape *shape, const santa_paged *cache, const
     p.k = rope_rows(rows->k, rows->k_stride, cache->k, nullptr);
     p.v = rope_rows(rows->v, rows->v_stride, cache->v, nullptr);
     p.B = B, p.T = T;
+    p.clear = clear;
     p.H_q = q ? shape->H_q : 0;
     p.H_kv = shape->H_kv;
     p.pos = pos, p.counts = counts;
@@ -222,6 +234,7 @@ int santa_attend_paged(const santa_shape *shape, const void *q, const int64_t q_
                        int32_t T, const int32_t *pos, const int32_t *counts, int32_t window, int32_t sinks, void *out,
                        void *workspace, size_t workspace_bytes, void *stream)
 {
+    const bool clear = take_clear(T);
     int rc = check_paged(shape, cache);
     if (rc) return rc;
     if (!q || !q_stride || !pos || !out || T < 0 || window < 0 || sinks < 0 || shape->scale < 0.f) return SANTA_ERR_INVALID_ARG;
@@ -256,6 +269,7 @@ int santa_attend_paged(const santa_shape *shape, const void *q, const int64_t q_
     p.k2 = (float)k2;
     p.wait_ns = wait_limit_ns();
     p.wide = aligned(out, 32);
+    p.clear = clear;
     // (the hardware may sleep longer than a limit below a millisecond; with one below a microsecond, which
     // only makes the waits run out, none is tried)
     p.tries = p.wait_ns < 1000 ? 0 : p.wait_ns < 1000000 ? 1 : 64;

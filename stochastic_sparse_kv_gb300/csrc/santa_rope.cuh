@@ -41,6 +41,7 @@ struct RopeParams {
     RopeRows q, k, v;
     int H_q, H_kv;                        // heads of q, of K and of V (H_kv = 0: q alone)
     int T, B, rot;                        // rot = 0: nothing is rotated
+    int clear;                            // rows of q that no live token writes become zeros
     int groups;                           // threads that share a token's heads: each takes every groups-th
     const uint64_t *turns;
     float amplitude;
@@ -61,11 +62,16 @@ __global__ void __launch_bounds__(RP_NT, 4) santa_rope_kernel(const RopeParams p
     const int c = idx % NU, slot = idx / NU;
     const int g = slot % p.groups, t = slot / p.groups;
     const int first = p.pos[b], cnt = p.counts ? p.counts[b] : p.T;
-    if (first < 0 || cnt < 0 || cnt > p.T || first > p.last - cnt) {
-        if (p.ctrl && idx == 0) set_dev_error(p.ctrl, DEV_BAD_POSITION);
+    const bool skip = first < 0 || cnt < 0 || cnt > p.T || first > p.last - cnt;
+    if (skip && p.ctrl && idx == 0) set_dev_error(p.ctrl, DEV_BAD_POSITION);
+    if (skip || t >= cnt) {
+        if (!p.clear || t >= p.T) return;
+        for (int h = g; h < p.H_q; h += p.groups) {
+            uint16_t *dst = p.q.dst + (b * p.q.db + t * p.q.dt + h * p.q.dh) + RP_VALUES * c;
+            *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(0, 0, 0, 0);
+        }
         return;
     }
-    if (t >= cnt) return;
     const int at = first + t;
     const bool turn = RP_VALUES * c < p.rot;
     // where the two halves of this thread's features begin

@@ -23,6 +23,7 @@ GROUP_DEDUP = 0x100  # or-ed into a sampling mode: V rows loaded once per KV-hea
 OUT_BF16 = 0x200     # or-ed into any mode: out is bf16 (the fp32 result rounded once)
 BERNOULLI_QK = 0x400  # or-ed into any mode: score with each head's ternary query draw
 TWO_PASS = 0x800      # or-ed into a sampling mode: never the single-pass cluster kernel
+CLEAR_REST = 1 << 30  # or-ed into T: rows of the result that no live token writes become zeros
 DEV_BAD_SEQLEN, DEV_TIMEOUT, DEV_BAD_POSITION, DEV_BAD_PAGE = 1, 2, 4, 8
 ROPE_LAYOUTS = {"halves": 0, "pairs": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
@@ -647,16 +648,18 @@ def _on_stream(stream, dev, call, made):
     return got
 
 
-def _out_rows(x: torch.Tensor, counts) -> torch.Tensor:
-    """Rows for a result: those that no live token writes are zeros."""
-    return (torch.empty if counts is None else torch.zeros)(x.shape, dtype=torch.bfloat16, device=x.device)
+def _out_rows(x: torch.Tensor) -> torch.Tensor:
+    """Rows for a result; the call gets CLEAR_REST, so that those that no live token writes are zeros."""
+    return torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
 
 
 def rope(x: torch.Tensor, table: RopeTable, pos: torch.Tensor, counts: torch.Tensor | None = None,
          out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rows x [B, T, H, d] (bf16, any strides that are multiples of 8) rotated to the positions
     pos[b] + t (int32 [B]), for t < counts[b] (default T).  Into `out` (x itself: in place), whose
-    other rows stay as they were; without it into new rows, the others zero."""
+    other rows stay as they were; without it into new rows, the others zero.  Batch rows with a position or
+    a count out of range are skipped (in new rows: zeros); give a `workspace` to have that reported by
+    device_status (DEV_BAD_POSITION)."""
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
     dev = x.device
@@ -669,12 +672,14 @@ def rope(x: torch.Tensor, table: RopeTable, pos: torch.Tensor, counts: torch.Ten
         _int_vector(counts, "counts", B, dev)
     rotation = _rotation_arg(table, dev)
     if out is None:
-        out = _out_rows(x, counts)
+        out, clear = _out_rows(x), CLEAR_REST
+    else:
+        clear = 0
     o_ptr, o_st = _row_tensor(out, "out", x.shape, dev)
     if T == 0:
         return out
     with _on_device(dev):
-        rc = (_lib or load()).santa_rope(B, T, H, d, x_ptr, x_st, o_ptr, o_st, rotation, pos.data_ptr(),
+        rc = (_lib or load()).santa_rope(B, T | clear, H, d, x_ptr, x_st, o_ptr, o_st, rotation, pos.data_ptr(),
                                counts.data_ptr() if counts is not None else None,
                                workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
     if rc:
@@ -708,8 +713,8 @@ def paged_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, po
     """Write new rows [B, T, H_kv, d] (bf16, any strides that are multiples of 8) to positions
     pos[b] + t of a paged cache, for t < counts[b] (default T), K rotated by `rope` if one is given.
     With it, the same tokens' queries q [B, T, H_q, d] can be rotated in the same launch: into
-    q_out (q itself: in place) or into new rows, which are returned.  Batch rows that would leave
-    the table, and tokens without a page, are not written; give a `workspace` to have that reported
+    q_out (q itself: in place) or into new rows, which are returned (as for rope).  Batch rows that would
+    leave the table, and tokens without a page, are not written; give a `workspace` to have that reported
     by device_status (DEV_BAD_POSITION, DEV_BAD_PAGE)."""
     B, H_kv, n_max, d, _, dev = _paged_dims(cache)
     if q is None and q_out is not None:
@@ -725,19 +730,19 @@ def paged_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, po
     _int_vector(pos, "pos", B, dev)
     if counts is not None:
         _int_vector(counts, "counts", B, dev)
-    H_q, q_arg = H_kv, (None,) * 4
+    H_q, q_arg, clear = H_kv, (None,) * 4, 0
     if q is not None:
         H_q = q.shape[2] if q.dim() == 4 else 0
         q_args = _row_tensor(q, "q", (B, T, H_q, d), dev)
         if q_out is None:
-            q_out = _out_rows(q, counts)
+            q_out, clear = _out_rows(q), CLEAR_REST
         q_arg = (*q_args, *_row_tensor(q_out, "q_out", q.shape, dev))
     rotation = _rotation_arg(rope, dev) if rope is not None else None
     if T == 0:
         return q_out
     shape = _kept(_append_shapes, (B, H_q, H_kv, d, n_max), lambda x: ctypes.byref(make_shape(*x)))
     with _on_device(dev):
-        rc = (_lib or load()).santa_paged_append(shape, _paged_arg(cache), ctypes.byref(_Rows(k_ptr, v_ptr, k_st, v_st)), T,
+        rc = (_lib or load()).santa_paged_append(shape, _paged_arg(cache), ctypes.byref(_Rows(k_ptr, v_ptr, k_st, v_st)), T | clear,
                                        pos.data_ptr(), counts.data_ptr() if counts is not None else None, rotation, *q_arg,
                                        workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
     if rc:
@@ -762,7 +767,9 @@ def attend_paged(q: torch.Tensor, cache: PagedCache, pos: torch.Tensor, counts: 
     their K and V already.  q [B, T, H_q, d] (bf16, any strides that are multiples of 8); token t < counts[b]
     (default T) sits at pos[b] + t (int32 [B]) and sees the keys up to its own, with window > 0 the
     last `window` of them and the first `sinks`.  Returns bf16 [B, T, H_q, d]: `out`, whose other rows
-    stay as they were, or new rows, the others zero.  On an explicit `stream`, the call and all that it
+    stay as they were, or new rows, the others zero.  Batch rows with a position or a count out of range are
+    skipped (in new rows: zeros), and a key without a page counts as zeros; give a `workspace` to have that
+    reported by device_status (DEV_BAD_POSITION, DEV_BAD_PAGE).  On an explicit `stream`, the call and all that it
     allocates are that stream's: order its inputs and its result with the current stream as for any
     work on another one."""
     B, H_kv, n_max, d, _, dev = _paged_dims(cache)
@@ -780,8 +787,9 @@ def attend_paged(q: torch.Tensor, cache: PagedCache, pos: torch.Tensor, counts: 
         _int_vector(counts, "counts", B, dev)
     T = size[1]
     shape, nbytes = _kept(_attend_shapes, (B, size[2], H_kv, d, n_max, scale, T), _attend_shape_of)
+    clear = 0
     if out is None:
-        out = _out_rows(q, counts)
+        out, clear = _out_rows(q), CLEAR_REST
     elif out.dtype is not torch.bfloat16 or not out.is_contiguous() or out.shape != size or out.device != dev:
         raise ValueError("out must be a contiguous bf16 tensor [B, T, H_q, d] on q's device")
     if T == 0:
@@ -789,7 +797,7 @@ def attend_paged(q: torch.Tensor, cache: PagedCache, pos: torch.Tensor, counts: 
     with _on_device(dev):
         raw = _raw_stream(None, dev)
         ws = workspace if workspace is not None else _own_workspace("attend", nbytes, dev, raw)
-        rc = (_lib or load()).santa_attend_paged(shape, q_ptr, q_st, _paged_arg(cache), T, pos.data_ptr(),
+        rc = (_lib or load()).santa_attend_paged(shape, q_ptr, q_st, _paged_arg(cache), T | clear, pos.data_ptr(),
                                        counts.data_ptr() if counts is not None else None, window, sinks, out.data_ptr(),
                                        ws.data_ptr(), ws.numel(), raw)
     if rc:
