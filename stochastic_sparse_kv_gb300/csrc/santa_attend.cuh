@@ -1013,9 +1013,10 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         }
         if (!ok && lane == 0) failed();
         __syncwarp();
+        tmem_st_wait();   // (after a wait that ran out, stores to TMEM may be under way)
     }
 
-    // ---- teardown: every MMA has completed (drained above); release TMEM.  After a timeout, copies
+    // ---- teardown: every MMA and every store to TMEM has completed (waited for above); release TMEM.  After a timeout, copies
     // that were not waited for get a bounded wait to land, and pieces that did not arrive do, so that
     // the counters are zero again after the last CTA.
     tc_fence_before();
