@@ -172,6 +172,8 @@ int santa_call_info(const santa_shape *shape, int32_t S, int32_t mode, int32_t *
  * exits, leaving the context usable.  Applies to calls made after it, process-wide.
  * limit_ns = 0 restores the default of 2 s.  A diagnostic: a short limit makes the
  * timeout path run (the library's tests do that), normal use never needs it.
+ * (santa_attend_paged: one look at a barrier may last some microseconds, which a wait can go beyond its limit;
+ * with a limit below a microsecond no barrier is looked at and every wait gives up.)
  * Returns SANTA_OK.
  */
 int santa_set_wait_limit(uint64_t limit_ns);

@@ -270,10 +270,10 @@ int santa_attend_paged(const santa_shape *shape, const void *q, const int64_t q_
     p.wait_ns = wait_limit_ns();
     p.wide = aligned(out, 32);
     p.clear = clear;
-    // (the hardware may sleep longer than a limit below a millisecond; with one below a microsecond, which
-    // only makes the waits run out, none is tried)
+    // (a try that may sleep would outlast a limit below a millisecond; one that may not still takes some
+    // microseconds, so with limits below a microsecond, which only make the waits run out, none is tried)
     p.tries = p.wait_ns < 1000 ? 0 : p.wait_ns < 1000000 ? 1 : 64;
-    p.nap = p.wait_ns < 1000000 ? 1 : 10000000;
+    p.nap = p.wait_ns < 1000000 ? 0 : 10000000;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.ctrl = reinterpret_cast<int32_t *>(ws);
     p.part = reinterpret_cast<float *>(ws + CTRL_BYTES);
