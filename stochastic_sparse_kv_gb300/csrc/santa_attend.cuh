@@ -304,6 +304,12 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+// A store to shared memory that whoever reads it finds this thread's earlier ones behind.
+__device__ __forceinline__ void st_release(uint32_t *at, uint32_t x)
+{
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(at)), "r"(x) : "memory");
+}
+
 // Whether one of the bf16 halves of w is not finite; bit 15 and bit 31 say which.
 __device__ __forceinline__ uint32_t at_not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
@@ -741,10 +747,10 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                                 if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
                                 const int j = key + c / 8;
                                 if (j <= w.it.first + w.it.t1 && (j >= w.it.lo || j < p.sinks)) *(volatile int *)&sh.bad_v = 1;
-                                *(volatile uint32_t *)&at.x = y.x;   // (in this order: who finds zeros finds the flag)
-                                *(volatile uint32_t *)&at.y = y.y;
-                                *(volatile uint32_t *)&at.z = y.z;
-                                *(volatile uint32_t *)&at.w = y.w;
+                                st_release(&at.x, y.x);   // (who finds zeros finds the flag)
+                                st_release(&at.y, y.y);
+                                st_release(&at.z, y.z);
+                                st_release(&at.w, y.w);
                             }
                     };
                     // keys beyond the first token, and keys before the last one's window
