@@ -475,7 +475,9 @@ int santa_attend_workspace_size(const santa_shape *shape, int32_t T, size_t *byt
  * (with T = 1, what santa_decode_window sees with seq_lens = pos + 1).  Keys that a token does not
  * see are not read into its result, whatever they hold (NaN too).  A visible key with a score of minus
  * infinity weighs nothing; a token all of whose visible scores are has a NaN result, as with a
- * score that is NaN or plus infinity.
+ * score that is NaN or plus infinity.  A value of V that is not finite makes that feature not finite for every token
+ * that sees the key, the infinity itself or a NaN; where the key's weight is 0 or too small for fp32 (a score of minus
+ * infinity), which of the two depends on where the key lies.
  *
  *  q         device bf16 [B, T, H_q, d], 16-byte aligned; q_stride in elements for (batch, token,
  *            head): multiples of 8, not negative, those of dimensions of size 1 are not read
