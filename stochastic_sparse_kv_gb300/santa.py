@@ -35,6 +35,7 @@ EXPORTS = ("santa_workspace_size", "santa_workspace_init", "santa_decode", "sant
            "santa_kv4_append", "santa_kv4_read", "santa_decode_kv4", "santa_decode_window",
            "santa_window_workspace_size", "santa_rope_turns", "santa_rope", "santa_paged_append",
            "santa_attend_workspace_size", "santa_attend_paged")
+ERR_UNSUPPORTED = -4
 ERR_DEVICE = -6
 ERR_SCRATCH = -7
 STATIC_SCRATCH_BYTES = (16 << 20) + 65536
@@ -584,8 +585,10 @@ def rope_table(rot: int, base: float = 10000.0, layout: str = "halves", scaling:
     context).  rot: a multiple of 16 up to the head dimension."""
     if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
         raise ValueError(f"layout is one of {list(ROPE_LAYOUTS)}, scaling one of {list(ROPE_SCALINGS)}")
+    if not (-1 << 31 <= original < 1 << 31 and -1 << 31 <= rot < 1 << 31):
+        raise ValueError("rot and original are 32-bit numbers")
     spec = _RopeSpec(base, ROPE_SCALINGS[scaling], factor, low, high, original)
-    turns, amplitude = (ctypes.c_uint64 * max(int(rot) // 2, 1))(), ctypes.c_float(0)
+    turns, amplitude = (ctypes.c_uint64 * max(min(int(rot), 65536) // 2, 1))(), ctypes.c_float(0)
     _check(load().santa_rope_turns(ctypes.byref(spec), int(rot), turns, ctypes.byref(amplitude)), "santa_rope_turns")
     bits = torch.tensor([x - (1 << 64) if x >> 63 else x for x in turns], dtype=torch.int64)
     return RopeTable(bits.to(device), int(rot), layout, float(amplitude.value))
@@ -629,6 +632,19 @@ def _kept(cache: dict, key, make):
     return got
 
 
+def _checked_shape(key):
+    """make_shape of sizes that C's 32 bits hold."""
+    if max(key[:5]) >= 1 << 31:
+        raise SantaError(ERR_UNSUPPORTED, f"sizes {key[:5]}")
+    return make_shape(*key)
+
+
+def _check_tokens(T: int):
+    """T is a number of tokens below CLEAR_REST, which goes into the same C argument."""
+    if T >= CLEAR_REST:
+        raise SantaError(ERR_UNSUPPORTED, f"{T} tokens")
+
+
 def _row_tensor(t: torch.Tensor, name: str, shape, dev):
     st = t.stride()
     if t.dtype is not torch.bfloat16 or t.device != dev or len(st) != 4 or st[3] != 1:
@@ -667,6 +683,9 @@ def rope(x: torch.Tensor, table: RopeTable, pos: torch.Tensor, counts: torch.Ten
         return _on_stream(stream, dev, lambda: rope(x, table, pos, counts, out, workspace), out is None)
     x_ptr, x_st = _row_tensor(x, "x", None, dev)
     B, T, H, d = x.shape
+    _check_tokens(T)
+    if B | H >= 1 << 31:
+        raise SantaError(ERR_UNSUPPORTED, f"{B} batch rows, {H} heads")
     _int_vector(pos, "pos", B, dev)
     if counts is not None:
         _int_vector(counts, "counts", B, dev)
@@ -725,6 +744,7 @@ def paged_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, po
         return _on_stream(stream, dev, lambda: paged_append(cache, k_new, v_new, pos, counts, rope, q, q_out, workspace),
                           q_out is None)
     T = k_new.shape[1] if k_new.dim() == 4 else -1
+    _check_tokens(T)
     k_ptr, k_st = _row_tensor(k_new, "K rows", (B, T, H_kv, d), dev)
     v_ptr, v_st = _row_tensor(v_new, "V rows", (B, T, H_kv, d), dev)
     _int_vector(pos, "pos", B, dev)
@@ -740,10 +760,10 @@ def paged_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, po
     rotation = _rotation_arg(rope, dev) if rope is not None else None
     if T == 0:
         return q_out
-    shape = _kept(_append_shapes, (B, H_q, H_kv, d, n_max), lambda x: ctypes.byref(make_shape(*x)))
+    shape = _kept(_append_shapes, (B, H_q, H_kv, d, n_max), lambda x: ctypes.byref(_checked_shape(x)))
     with _on_device(dev):
-        rc = (_lib or load()).santa_paged_append(shape, _paged_arg(cache), ctypes.byref(_Rows(k_ptr, v_ptr, k_st, v_st)), T | clear,
-                                       pos.data_ptr(), counts.data_ptr() if counts is not None else None, rotation, *q_arg,
+        rc = (_lib or load()).santa_paged_append(shape, _paged_arg(cache), ctypes.byref(_Rows(k_ptr, v_ptr, k_st, v_st)),
+                                       T | clear, pos.data_ptr(), counts.data_ptr() if counts is not None else None, rotation, *q_arg,
                                        workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
     if rc:
         _check(rc, "santa_paged_append")
@@ -755,7 +775,8 @@ _attend_shapes: dict = {}
 
 def _attend_shape_of(key):
     """(the shape as a C argument, the workspace bytes of attend_paged), kept per shape and T."""
-    shape, n = make_shape(*key[:-1]), ctypes.c_size_t(0)
+    shape, n = _checked_shape(key[:-1]), ctypes.c_size_t(0)
+    _check_tokens(key[-1])
     _check(load().santa_attend_workspace_size(ctypes.byref(shape), key[-1], ctypes.byref(n)), "santa_attend_workspace_size")
     return ctypes.byref(shape), int(n.value)
 

@@ -24,3 +24,14 @@ def test_the_flag_in_T_changes_no_check(lib):  # noqa: F811
     for T in (-1, -(1 << 31)):
         assert lib.santa_rope(2, T, 2, 128, A, i64(*st), A, i64(*st), rot(), A, None, None, STREAM) == -1
         assert lib.santa_attend_paged(shape(), A, i64(*st), pool(), T, A, None, 0, 0, A, A, n.value, STREAM) == -1
+
+
+def test_numbers_past_32_bits_of_a_rope_table(lib):  # noqa: F811
+    """(a C argument takes the low 32 bits: 2^32 + 8192 positions were 8192)"""
+    for bad in (dict(original=(1 << 32) + 8192), dict(original=1 << 31), dict(rot=(1 << 32) + 64)):
+        with pytest.raises(ValueError, match="32-bit"):
+            santa.rope_table(**{"rot": 64, "scaling": "bands", "factor": 2.0, "device": "cpu", **bad})
+    for rot in (65538, (1 << 31) - 2, -2, 0):
+        with pytest.raises(santa.SantaError):
+            santa.rope_table(rot, device="cpu")
+    assert santa.rope_table(64, scaling="bands", factor=2.0, original=(1 << 31) - 1, device="cpu").rot == 64
