@@ -645,6 +645,15 @@ def _check_tokens(T: int):
         raise SantaError(ERR_UNSUPPORTED, f"{T} tokens")
 
 
+def _workspace_ptr(workspace: torch.Tensor | None, dev):
+    """The address of a workspace that was given, which the kernels write to."""
+    if workspace is None:
+        return None
+    if workspace.device != dev:
+        raise ValueError("the workspace is not on the inputs' device")
+    return workspace.data_ptr()
+
+
 def _row_tensor(t: torch.Tensor, name: str, shape, dev):
     st = t.stride()
     if t.dtype is not torch.bfloat16 or t.device != dev or len(st) != 4 or st[3] != 1:
@@ -700,7 +709,7 @@ def rope(x: torch.Tensor, table: RopeTable, pos: torch.Tensor, counts: torch.Ten
     with _on_device(dev):
         rc = (_lib or load()).santa_rope(B, T | clear, H, d, x_ptr, x_st, o_ptr, o_st, rotation, pos.data_ptr(),
                                counts.data_ptr() if counts is not None else None,
-                               workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
+                               _workspace_ptr(workspace, dev), _raw_stream(None, dev))
     if rc:
         _check(rc, "santa_rope")
     return out
@@ -764,7 +773,7 @@ def paged_append(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, po
     with _on_device(dev):
         rc = (_lib or load()).santa_paged_append(shape, _paged_arg(cache), ctypes.byref(_Rows(k_ptr, v_ptr, k_st, v_st)),
                                        T | clear, pos.data_ptr(), counts.data_ptr() if counts is not None else None, rotation, *q_arg,
-                                       workspace.data_ptr() if workspace is not None else None, _raw_stream(None, dev))
+                                       _workspace_ptr(workspace, dev), _raw_stream(None, dev))
     if rc:
         _check(rc, "santa_paged_append")
     return q_out
@@ -815,6 +824,7 @@ def attend_paged(q: torch.Tensor, cache: PagedCache, pos: torch.Tensor, counts: 
         raise ValueError("out must be a contiguous bf16 tensor [B, T, H_q, d] on q's device")
     if T == 0:
         return out
+    _workspace_ptr(workspace, dev)
     with _on_device(dev):
         raw = _raw_stream(None, dev)
         ws = workspace if workspace is not None else _own_workspace("attend", nbytes, dev, raw)

@@ -54,3 +54,17 @@ def test_columns():
             call()
         assert e.value.status == santa.ERR_UNSUPPORTED
     assert not cache.k.any() and not cache.v.any()
+
+
+def test_a_workspace_of_another_device():
+    """(the kernels would write to its address)"""
+    cache, new, table = small(), torch.ones(1, 1, 2, 64, dtype=bf16, device=DEV), santa.rope_table(64)
+    for ws in (torch.zeros(64 << 20, dtype=torch.uint8), torch.empty(64 << 20, dtype=torch.uint8, device="meta")):
+        for call in (lambda: santa.rope(new, table, ints([0]), workspace=ws), lambda: santa.attend_paged(new, cache, ints([0]), workspace=ws),
+                     lambda: santa.paged_append(cache, new, new, ints([0]), workspace=ws)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
+    assert not cache.k.any() and not cache.v.any()
+    # an empty one is too small, not none
+    with pytest.raises(santa.SantaError):
+        santa.attend_paged(new, cache, ints([0]), workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
