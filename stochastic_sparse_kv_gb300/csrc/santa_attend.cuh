@@ -41,8 +41,11 @@
 // that some token sees, the rows that see it get it added at the end.  That also covers what a page
 // holds behind the last key.
 //
-// Precision.  Scores, references, sums of weights and outputs are fp32 (a score is a chain of d / 16 MMA
-// steps, an output one of a step for every 16 keys of the share).  P is bf16, as V is: one rounding of each
+// Precision.  Scores, references, sums of weights and outputs are fp32.  A score is a chain of d / 16 MMA
+// steps, an output one of a step for every 16 keys of AT_CHAIN tiles at most.  A step cuts off what is below 2^-25 of the
+// sum's power of 2 in each product and below 2^-23 in the sum (measured), 2.5 2^-23 on average: where all values have
+// one sign, 3e-4 of a chain of 2048 steps (measured 2.3e-4), but 2.1e-3 of 300000 keys in one chain.  So a longer
+// share's chains are added up in fp32, rounded to the nearest, in the CTA's piece.  P is bf16, as V is: one rounding of each
 // weight, 2^-8 at most, of which the common part cancels.  Error against 64 bits (root mean square,
 // relative) 1.9e-3 to 2.1e-3; the rounding of the result alone is 1.7e-3.
 //
@@ -69,6 +72,7 @@ constexpr int AT_SUB = 64;                // keys of one of its halves
 constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
 constexpr int AT_SETUP = 4;               // what an item costs beside its tiles, in tiles
 constexpr int AT_MIN_SHARE = 2;           // a share's least size, in tiles
+constexpr int AT_CHAIN = 256;             // tiles that the tensor cores add up (a power of 2)
 constexpr float AT_SLACK = 24.f;          // log2 of the largest p (sums of values below 2^80 stay in range)
 constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
 constexpr int AT_MISC = 2048;             // of it for barriers and the like
@@ -362,7 +366,9 @@ __device__ __noinline__ void at_clear(const AttendParams &p)
     }
 }
 
-template <int D, int NQ>
+// CHAINS: a share may have more than AT_CHAIN tiles of an item.  Against the kernel without chains: one token on 16 x
+// 64k keys 625 and 620 us, d = 64 on 32 x 128k 1807 and 1780, 2048 tokens on 64k 1493 and 1449, d = 64 1327 and 1367.
+template <int D, int NQ, bool CHAINS>
 __global__ void __launch_bounds__(at_threads(NQ), 1)
     santa_attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v)
@@ -551,7 +557,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         AtWalk<NQ> w;
         w.begin(p, f0, sh.start_base, sh.start_pair);
         int items = 0;
-        int n = 0, no = 0;                    // tiles and items of this row tile so far
+        int n = 0, no = 0;                    // tiles and chains of this row tile so far
         int turns = 0;                        // turns taken
         bool first_two = true;
         int stage = 0, phase = 0, used = 0;   // of the next fill to wait for
@@ -648,20 +654,20 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 }
                 wait(&sh.phalf[buf], parity);
                 my_turn();
-                if (j == 0 && no > 0) wait(&sh.oempty[q], (no - 1) & 1);
+                const bool fresh = CHAINS ? j % AT_CHAIN == 0 : j == 0;
+                if (fresh && no++ > 0) wait(&sh.oempty[q], no & 1);
                 if (!ok) break;
                 tc_fence_after();
-                values(v_at, buf, 0, j == 0);
+                values(v_at, buf, 0, fresh);
                 if (!wait(&sh.pfull[buf], parity)) break;
                 tc_fence_after();
-                values(v_at, buf, 1, j == 0);
+                values(v_at, buf, 1, fresh);
                 if (NQ == 2 && more) {
                     scores(k_at, buf);
                     if (j + 2 == L) commit(&sh.qempty);
                 }
                 your_turn();
             }
-            ++no;
         }
         if (!ok && lane == 0) failed();
         commit(&sh.drain[q]);
@@ -717,7 +723,51 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             // m: the reference of the row's weights (a score so far); off, sub: how they are taken with it
             float m = NEG_INF, l = 0.f, off = 0.f, sub = 0.f;
             bool any_far = false;
+            // The output of a chain of AT_CHAIN tiles is added to that of the chains before it, which is kept in this
+            // CTA's piece; `last`: the other way round, for the item's end.  `i` tiles are done.
+            auto chain = [&](int i, bool last) {
+                const int R = q * AT_ROWS + row;
+                const bool mine_live = row < live, some = last || i > AT_CHAIN;
+                const size_t at = (size_t)(blockIdx.x * 2 + (w.i0 > 0 ? 0 : 1)) * p.piece_rows;
+                float f = 0.f;
+                if (some && mine_live) {
+                    const float was = __ldcg(p.part_ml + (at + R) * 2);
+                    f = was == NEG_INF ? 0.f : at_ratio(was, m, p.k2);
+                }
+#pragma unroll 1
+                for (int c = 0; c < D; c += 8) {
+                    uint32_t o[8];
+                    __syncwarp();
+                    tmem_ld32<8>(t_o + c, o);
+                    if (mine_live) {
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            float4 *sum = reinterpret_cast<float4 *>(p.part + at * D + at_piece<D>(p.piece_rows, R, (c + e) / 4));
+                            const float4 x = some ? __ldcg(sum) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            o[e] = __float_as_uint(fmaf(f, x.x, __uint_as_float(o[e])));
+                            o[e + 1] = __float_as_uint(fmaf(f, x.y, __uint_as_float(o[e + 1])));
+                            o[e + 2] = __float_as_uint(fmaf(f, x.z, __uint_as_float(o[e + 2])));
+                            o[e + 3] = __float_as_uint(fmaf(f, x.w, __uint_as_float(o[e + 3])));
+                            if (!last) __stcg(reinterpret_cast<uint4 *>(sum), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                        }
+                    }
+                    __syncwarp();
+                    if (last) tmem_st8(t_o + c, o);
+                }
+                if (last)
+                    tmem_st_wait();
+                else if (mine_live)
+                    __stcg(p.part_ml + (at + R) * 2, m);
+            };
             for (int i = 0; i < tiles; ++i, ++n) {
+                if (CHAINS && i > 0 && i % AT_CHAIN == 0) {
+                    if (!wait(&sh.ofull[q][(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
+                    tc_fence_after();
+                    if (warp_live) chain(i, false);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.oempty[q]);
+                }
                 const int buf = NQ == 2 ? q : n & 1;
                 const uint32_t t_s = tbase + lanes + buf * AT_KEYS;
                 const bool open = key < open_hi && (key > open_lo || key + AT_KEYS <= p.sinks);
@@ -862,6 +912,8 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
             // is done and that of the tile before may be: one barrier would be one or two phases on)
             if (!wait(&sh.ofull[q][(n - 1) & 1], ((n - 1) >> 1) & 1)) break;
             tc_fence_after();
+
+            if (CHAINS && tiles > AT_CHAIN && warp_live) chain(tiles, true);
 
             // ---- the item's (or the piece's) sums
             const bool whole = w.whole(), mine_live = row < live;

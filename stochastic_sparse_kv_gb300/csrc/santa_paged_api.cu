@@ -70,6 +70,13 @@ bool take_clear(int32_t &T)
     return clear;
 }
 
+template <int D>
+const void *attend_kernel(int NQ, bool chains)
+{
+    if (NQ == 2) return chains ? (const void *)santa_attend_kernel<D, 2, true> : (const void *)santa_attend_kernel<D, 2, false>;
+    return chains ? (const void *)santa_attend_kernel<D, 1, true> : (const void *)santa_attend_kernel<D, 1, false>;
+}
+
 int log2_of(int x)
 {
     int s = 0;
@@ -281,17 +288,19 @@ int santa_attend_paged(const santa_shape *shape, const void *q, const int64_t q_
 
     int dev, sms, optin, occ = 0;
     if ((rc = device_info(&dev, &sms, &optin))) return rc;
-    const void *fn = D == 128 ? (NQ == 2 ? (const void *)santa_attend_kernel<128, 2> : (const void *)santa_attend_kernel<128, 1>)
-                              : (NQ == 2 ? (const void *)santa_attend_kernel<64, 2> : (const void *)santa_attend_kernel<64, 1>);
-    const int smem = at_smem(D, NQ);
-    if (smem > optin) return SANTA_ERR_UNSUPPORTED;
-    if ((rc = prepare_fn(fn, dev, smem, at_threads(NQ), &occ))) return rc;
     // no more shares than the longest sequences would give
     const long long qts = ((long long)T * G + NQ * AT_ROWS - 1) / (NQ * AT_ROWS);
     const long long most = p.window > 0 ? std::min<long long>(p.n_max, (long long)p.window + p.sinks + (NQ * AT_ROWS) / G) : p.n_max;
     const long long units = (most + AT_KEYS - 1) / AT_KEYS + 2 + AT_SETUP;
-    const long long want = (units * shape->B * shape->H_kv * qts + AT_MIN_SHARE - 1) / AT_MIN_SHARE;
-    const long long grid = std::min<long long>(std::min(sms, AT_MAX_CTAS), want);
+    const long long all = units * shape->B * shape->H_kv * qts;
+    const long long grid = std::min<long long>(std::min(sms, AT_MAX_CTAS), (all + AT_MIN_SHARE - 1) / AT_MIN_SHARE);
+    // tiles of an item in a share, at the most (a window may begin and end inside one)
+    const long long tiles = (most + AT_KEYS - 1) / AT_KEYS + (p.window > 0 ? 2 : 0);
+    const bool chains = std::min(tiles, all / grid + 1) > AT_CHAIN;
+    const void *fn = D == 128 ? attend_kernel<128>(NQ, chains) : attend_kernel<64>(NQ, chains);
+    const int smem = at_smem(D, NQ);
+    if (smem > optin) return SANTA_ERR_UNSUPPORTED;
+    if ((rc = prepare_fn(fn, dev, smem, at_threads(NQ), &occ))) return rc;
     CUtensorMap tm_q, tm_k, tm_v;
     const long long rows = (long long)cache->n_pages * shape->H_kv * cache->page;
     const int box = std::min<int>(cache->page, AT_KEYS);
