@@ -46,8 +46,11 @@
 // sum's power of 2 in each product and below 2^-23 in the sum (measured), 2.5 2^-23 on average: where all values have
 // one sign, 3e-4 of a chain of 2048 steps (measured 2.3e-4), but 2.1e-3 of 300000 keys in one chain.  So a longer
 // share's chains are added up in fp32, rounded to the nearest, in the CTA's piece.  P is bf16, as V is: one rounding of each
-// weight, 2^-8 at most, of which the common part cancels.  Error against 64 bits (root mean square,
-// relative) 1.9e-3 to 2.1e-3; the rounding of the result alone is 1.7e-3.
+// weight, 2^-8 at most, of which the common part cancels.  Error against 64 bits (root mean square, relative) 1.8e-3 (a
+// few keys lead) to 2.4e-3 (scores nearly alike); the rounding of the result alone is 1.7e-3.  With two terms a weight
+// that is all that is left, but with one row tile, whose four warps have no time to spare, one token on 16 x 32k keys
+// takes 368 us instead of 317 and 32 ragged sequences of 5 tokens 136 instead of 103, and with two the tensor cores
+// would have half as much again to do.  Decode steps in fp32: santa_decode_window, over a contiguous cache.
 //
 // What bounds it.  Long chunks: the chain of a row tile, about 3500 clocks a tile of 128 keys, of which
 // 2 x 1024 are MMAs (the tensor pipe is active 60% of the time, issue slots 48%, the exponential

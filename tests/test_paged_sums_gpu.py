@@ -121,3 +121,38 @@ def test_scores_that_rise_or_fall_from_chain_to_chain(T, d, G, rise):
         want = (a * float(v[0, 0, 0, 0]) + w * b * float(v[1, 0, 0, 0])) / (a + w * b)
         # (the scale is rounded to 2^-25 of it: a weight of 2^60 by 60 2^-25)
         assert float((got[:, t].double() / want - 1).abs().max()) <= 2.0 ** -8 + CUT + 2.0 ** -18
+
+
+@pytest.mark.parametrize("B,T,H_kv,G,d,n,window", [(8, 1, 4, 4, 128, 4096, 0), (2, 1, 4, 8, 64, 20000, 0), (4, 5, 2, 4, 128, 9000, 4096),
+                                                   (2, 300, 2, 4, 128, 5000, 0), (2, 130, 2, 8, 64, 1500, 600), (1, 64, 8, 1, 128, 400, 0)])
+@pytest.mark.parametrize("std", [0.5, 3.0])
+def test_root_mean_square_error(B, T, H_kv, G, d, n, window, std):
+    """Values of both signs: the result's rounding, and one rounding of each weight, e_j, in the sums of weights and of
+    values alike: sum p_j e_j (v_j - o).  The relative error of a bf16 rounding has the root mean square 2^-7 / sqrt(12) of
+    the number's power of 2, and E[2^-2x] = 0.541 of mantissas 2^x whose logarithms are even; errors of keys are independent."""
+    g = torch.Generator(device=DEV).manual_seed(n + d)
+    cols = -(-n // 64)
+    k, v = (torch.randn(B * cols, H_kv, 64, d, generator=g, device=DEV).to(bf16) for _ in range(2))
+    table = torch.arange(B * cols, device=DEV, dtype=torch.int32).view(B, cols)
+    x = torch.randn(B, T, H_kv * G, d, generator=g, device=DEV)
+    q = (std * math.sqrt(d) * x / x.norm(dim=-1, keepdim=True)).to(bf16)
+    got = santa.attend_paged(q, santa.PagedCache(k, v, table), torch.full((B,), n - T, dtype=torch.int32, device=DEV), window=window)
+    u = 2.0 ** -7 * math.sqrt(0.541 / 12)
+    error, expected, size, count = 0.0, 0.0, 0.0, 0
+    for b in range(B):
+        for t in sorted({0, T // 2, T - 1}):
+            P = n - T + t
+            lo = max(0, P - window + 1) if window else 0
+            kb, vb = (x[table[b].long()].transpose(1, 2).flatten(0, 1)[lo:P + 1].double() for x in (k, v))   # [keys, H_kv, d]
+            s = torch.einsum("hgd,nhd->hgn", q[b, t].double().view(H_kv, G, d), kb) / math.sqrt(d)
+            p = torch.softmax(s, -1)
+            o = torch.einsum("hgn,nhd->hgd", p, vb)
+            moved = torch.einsum("hgn,nhd->hgd", p.pow(2), vb.pow(2)) - 2 * o * torch.einsum("hgn,nhd->hgd", p.pow(2), vb) + \
+                o.pow(2) * p.pow(2).sum(-1, keepdim=True)
+            error += float((got[b, t].double().view_as(o) - o).pow(2).sum())
+            expected += float((o.to(bf16).double() - o).pow(2).sum() + u * u * moved.sum())
+            size += float(o.pow(2).sum())
+            count += o.numel()
+    print("rms", math.sqrt(error / size), "of", math.sqrt(expected / size))
+    # (thousands of results: chance leaves a few hundredths)
+    assert count >= 2000 and error <= 1.1 ** 2 * expected
