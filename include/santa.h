@@ -91,7 +91,7 @@ extern "C" {
 
 /* Device error bits (santa_device_status). */
 #define SANTA_DEV_BAD_SEQLEN 1      /* some seq_lens[b] outside [0, n_max]; treated as 0 */
-#define SANTA_DEV_TIMEOUT 2         /* a bounded wait on a shared-memory barrier gave up */
+#define SANTA_DEV_TIMEOUT 2         /* a bounded wait on a shared-memory barrier gave up: the call's results are not complete */
 #define SANTA_DEV_BAD_POSITION 4    /* a row's pos / counts outside the cache; the row is skipped */
 #define SANTA_DEV_BAD_PAGE 8        /* a needed entry of a page table names no page */
 

@@ -13,8 +13,7 @@
 //
 // Shares.  The list of all items' key tiles, over sequences, row tiles and KV heads, is cut into
 // equal contiguous shares, one a CTA, one CTA an SM: any mix of prompts, decode steps, lengths and
-// windows fills the GPU, without a queue.  An item counts AT_SETUP tiles more than it has (prompts
-// of 2 x 8k tokens: 2 1024 us, 3 901, 4 844, 6 846, 8 859).  One that spans CTAs leaves pieces (the reference
+// windows fills the GPU, without a queue.  An item counts AT_SETUP tiles more than it has, for its ends.  One that spans CTAs leaves pieces (the reference
 // and the sum of the weights, and the sum over V, of each row) in the workspace; the last CTA to arrive
 // joins them in the order of the list, so results do not depend on timing.
 //
@@ -32,8 +31,8 @@
 // TMEM has room for one score buffer a row tile beside two outputs of 128 columns, so the chain scores,
 // softmax, product, scores of a row tile cannot overlap itself.  The two row tiles overlap one
 // another: their MMA warps take turns, and while one row tile is in the tensor cores the other is in
-// its softmax (without turns both came to do the same at the same time: 2048 tokens on 30k 895 us
-// against 786).  One row tile has two score buffers.
+// its softmax (without turns both come to do the same at the same time: 2048 tokens on 30k keys 850 us
+// against 772, d = 64 631 against 595).  One row tile has two score buffers.
 //
 // Masks.  A tile that all the item's tokens see whole takes no mask.  In the others the scores of
 // hidden keys become minus infinity.  p is 0 there, but 0 times a NaN or an infinity in V is not:
@@ -54,15 +53,13 @@
 //
 // What bounds it.  Long chunks: the chain of a row tile, about 3500 clocks a tile of 128 keys, of which
 // 2 x 1024 are MMAs (the tensor pipe is active 60% of the time, issue slots 48%, the exponential
-// unit 30%).  2048 tokens on 30k keys, 32 heads: 1.07 TFLOP in 786 us, 1.36 PFLOP/s, 0.70 of the measured
-// dense rate; 2 prompts of 8192 tokens 834 us, 0.68.  Of an item's ends, the tiles with masks take 5000
-// clocks and the results 2500.  One token on 16 sequences of 32k keys: 312 us, 6.9 TB/s, above the measured
-// copy rate; on one sequence of 32k keys 34 us, of which 6 are the first copies' way and 6 the
-// joins.  Steps that led here, by 2048 tokens on 30k: 1069 us with one MMA warp whose lane was picked by
-// its number (operands then move to uniform registers one at a time: 95 clocks an MMA instead of 64);
-// 883 with two threads a row (same exponentials, one more rendezvous a tile); 918 with parts of 64
-// keys and two score buffers a row tile (an MMA of 64 columns takes as long as one of 128); 895 with an MMA
-// warp a row tile; 786 with turns.
+// unit 30%).  2048 tokens on 30k keys, 32 heads: 1.07 TFLOP in 772 to 805 us (boxes differ), 0.69 to 0.72 of the
+// measured dense rate; 2 prompts of 8192 tokens 795 to 848 us, 0.67 to 0.72; at d = 64 595 and 671 us, 0.46 and 0.44, as
+// the softmax is as long as at d = 128 and an MMA of 64 columns takes as long as one of 128.  Of an item's ends, the
+// tiles with masks take 5000 clocks and the results 2500.  One token on 16 sequences of 32k keys: 312 to 318 us, 6.8 TB/s,
+// above the measured copy rate; on one sequence of 32k keys 34.5 us, of which 6 are the first copies' way and 6
+// the joins.  (MMAs whose lane is picked by its number have their operands moved to uniform registers one at a time:
+// 95 clocks an MMA instead of 64.)
 #pragma once
 
 #include "santa_tcgen05.cuh"
@@ -73,8 +70,13 @@ constexpr int AT_ROWS = 128;              // rows of a tile: (token, head) pairs
 constexpr int AT_KEYS = 128;              // keys of a tile
 constexpr int AT_SUB = 64;                // keys of one of its halves
 constexpr int AT_MAX_CTAS = 160;          // shares that the workspace has pieces for
-constexpr int AT_SETUP = 4;               // what an item costs beside its tiles, in tiles
-constexpr int AT_MIN_SHARE = 2;           // a share's least size, in tiles
+// What an item costs beside its tiles, in tiles.  2, 3, 4, 6 and 8: prompts of 2 x 8k tokens 879, 798, 795, 815 and 818 us,
+// d = 64 692, 664, 671, 691 and 703; 64 prompts of 200 tokens 129, 135, 129, 131 and 130, d = 64 108, 111, 112, 109 and 109;
+// the mixed ragged batch 243, 244, 242, 244 and 243; 32 ragged sequences of 5 tokens 104, 103, 101, 104 and 106.
+constexpr int AT_SETUP = 4;
+// A share's least size, in tiles.  1, 2, 4 and 8: one token on 777 keys, 4 KV heads, d = 64 11.9, 12.4, 14.5 and 20.6 us, d = 128
+// 14.1, 14.4, 16.5 and 22.5; four sequences, d = 64 14.4, 14.4, 14.4 and 18.3; eight, d = 128 16.5, 16.5, 17.0 and 20.6.
+constexpr int AT_MIN_SHARE = 2;
 constexpr int AT_CHAIN = 256;             // tiles that the tensor cores add up (a power of 2)
 constexpr float AT_SLACK = 24.f;          // log2 of the largest p (sums of values below 2^80 stay in range)
 constexpr int AT_SMEM = 232448;           // shared memory a CTA may have
@@ -96,9 +98,10 @@ __host__ __device__ constexpr int at_smem(int D, int NQ)
 }
 
 // Row tiles of an item, and rows that a piece holds, by the rows T * G of a sequence and KV head.  One tile
-// against two: 2048 tokens on 30k keys (8192 rows) 1069 and 817 us, prompts of 8192 tokens 1141 and 847,
-// the mixed batch of up to 2040 rows 309 and 240; one token (4 rows) on 32k keys 35 and 55, on 16 x 32k 317 and
-// 334, 5 tokens (20 rows) 105 and 113.
+// against two: 2048 tokens on 30k keys (8192 rows) 1016 and 771 us, d = 64 877 and 596, the mixed batch of up to 2040
+// rows 303 and 243, 16 x 64 tokens on 4k (256 rows) 100 and 77, 16 x 40 (160 rows) 99 and 72; 16 x 32 (128 rows) 63 and 67,
+// 16 x 5 (20 rows) 58 and 60, one token (4 rows) on 32k keys 34.5 and 36.9, on 16 x 32k 316 and 321, on 777 keys, d = 64 12.5
+// and 14.4.
 __host__ __device__ constexpr int at_nq(long long rows) { return rows > AT_ROWS ? 2 : 1; }
 __host__ __device__ constexpr int at_piece_rows(long long rows) { return rows > AT_ROWS ? 2 * AT_ROWS : (int)rows; }
 
@@ -213,7 +216,7 @@ struct AtWalk {
 
 // mbar_wait_bounded for warps that wait long and often beside warps that work: the clock is looked at
 // after `tries` tries only, each of which may sleep `nap` ns in the hardware (a line more in this loop, which
-// every wait has, cost 6% of a long chunk's time).  No tries: the wait is given up.
+// every wait has, cost 3 to 6% of a long chunk's time).  No tries: the wait is given up.
 __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns, int tries, uint32_t nap)
 {
     uint64_t t0 = 0;
@@ -337,8 +340,9 @@ __device__ __forceinline__ size_t out_at(const AttendParams &p, int b, int t0, i
 
 // Float of a piece where columns 4 c .. 4 c + 3 of row r are: row by row where rows are few and the threads
 // of a join take columns, else the rows of a column group side by side (a warp's accesses are 512 bytes), a
-// thread a row.  The first way against the second: 4 rows and 20 pieces 35 and 51 us (one token on 32k keys), 20
-// rows 105 and 102, 256 rows 838 and 799 (2048 tokens on 30k), 277 and 240 (mixed batch).
+// thread a row.  The first way against the second: 4 rows and 20 pieces 34.5 and 52.1 us (one token on 32k keys), 2 rows
+// and few pieces 12.4 and 14.5 (777 keys), 20 rows 59.6 and 57.3 (16 x 5 tokens on 4k keys) and 104 and 101 (32 ragged
+// sequences of 5), 40 rows 65.9 and 58.0, 128 rows 95.8 and 62.4.
 constexpr int AT_FEW = 16;
 constexpr int AT_BATCH = 10;
 template <int D>
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
                 if (warp_live) {
                     tc_fence_after();
                     // the upper half of the scores stays in registers, the lower half is read again (all kept,
-                    // or both halves read again: 2048 tokens on 30k keys 811 and 807 us against 788)
+                    // or both halves read again: 2 to 3% more of a long chunk's time)
                     uint32_t lower[AT_SUB], upper[AT_SUB];
                     auto hide = [&](uint32_t (&s)[AT_SUB], int at) {
 #pragma unroll
