@@ -352,22 +352,26 @@ __device__ __forceinline__ size_t at_piece(int rows, int r, int c)
 }
 
 // Rows of `out` behind the live tokens of every batch row, all of them where the row is skipped, become
-// zeros: equal shares of each to the CTAs of the grid, of a few rows to other CTAs for every batch row.  Half of
-// 134 MB (32 x 255 tokens of 64 heads, d = 128): 13 us in the call, a fill of the whole before it 37.
+// zeros: equal shares of each to the CTAs of the grid, of a few rows to other CTAs for every batch row.  One warp of a
+// CTA calls it, the producer behind its last copy.  Half of 134 MB (32 x 255 tokens of 64 heads, d = 128): 16 us more
+// for the call; by all warps before their work 14, but then a call with nothing to clear took 2 more; a fill of the whole
+// before the call 40.
 template <int D>
 __device__ __noinline__ void at_clear(const AttendParams &p)
 {
+    const int lane = threadIdx.x & 31;
     const long long row = (long long)p.H_q * (D / 8);   // of a token, in 16 bytes
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int mine = b0 + (threadIdx.x & 31);
+        const int mine = b0 + lane;
         int first, cnt = p.T;
         if (mine < p.B) at_row(p, mine, first, cnt);
         for (uint32_t some = __ballot_sync(0xffffffffu, cnt < p.T); some; some &= some - 1) {
             const int at = __ffs(some) - 1, b = b0 + at, live = __shfl_sync(0xffffffffu, cnt, at);
             uint4 *out = reinterpret_cast<uint4 *>(p.out) + ((long long)b * p.T + live) * row;
-            const long long n = (p.T - live) * row, step = (long long)gridDim.x * blockDim.x;
+            const long long n = (p.T - live) * row, step = (long long)gridDim.x * 32;
             const unsigned cta = n < step ? (blockIdx.x + b) % gridDim.x : blockIdx.x;
-            for (long long i = (long long)cta * blockDim.x + threadIdx.x; i < n; i += step)
+#pragma unroll 8
+            for (long long i = (long long)cta * 32 + lane; i < n; i += step)
                 out[i] = make_uint4(0, 0, 0, 0);
         }
     }
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         if (lane >= o) incl += up;
     }
     if (lane == 31) sh.sums[warp] = incl;
-    if (__syncthreads_or(p.clear && dead)) at_clear<D>(p);
+    const bool clear = __syncthreads_or(p.clear && dead);
     long long total = 0, before = incl - mine;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
@@ -437,7 +441,10 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
     }
     const long long ctas = max(1ll, min((long long)gridDim.x, total / AT_MIN_SHARE));
     const long long cta = blockIdx.x;
-    if (total == 0 || cta >= ctas) return;
+    if (total == 0 || cta >= ctas) {
+        if (clear && warp == 0) at_clear<D>(p);
+        return;
+    }
     const long long f0 = total * cta / ctas, f1 = total * (cta + 1) / ctas;
     if (before <= f0 && f0 < before + mine) {
         int b_at = -1, first = 0, cnt = 0;
@@ -558,6 +565,7 @@ __global__ void __launch_bounds__(at_threads(NQ), 1)
         }
         if (!ok && lane == 0) failed();
         __syncwarp();
+        if (clear) at_clear<D>(p);
     } else if (warp >= W_MMA) {
         // ================= MMA issuer of row tile q: the whole warp waits, one lane issues
         const int q = warp - W_MMA;
