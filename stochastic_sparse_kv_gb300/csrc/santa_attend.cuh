@@ -53,7 +53,7 @@
 //
 // What bounds it.  Long chunks: the chain of a row tile, about 3500 clocks a tile of 128 keys, of which
 // 2 x 1024 are MMAs (the tensor pipe is active 60% of the time, issue slots 48%, the exponential
-// unit 30%).  2048 tokens on 30k keys, 32 heads: 1.07 TFLOP in 772 to 805 us (boxes differ), 0.69 to 0.72 of the
+// unit 30%).  2048 tokens on 30k keys, 32 heads: 1.07 TFLOP in 772 to 805 us (machines differ), 0.69 to 0.72 of the
 // measured dense rate; 2 prompts of 8192 tokens 795 to 848 us, 0.67 to 0.72; at d = 64 595 and 671 us, 0.46 and 0.44, as
 // the softmax is as long as at d = 128 and an MMA of 64 columns takes as long as one of 128.  Of an item's ends, the
 // tiles with masks take 5000 clocks and the results 2500.  One token on 16 sequences of 32k keys: 312 to 318 us, 6.8 TB/s,

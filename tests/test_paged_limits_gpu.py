@@ -68,3 +68,25 @@ def test_a_workspace_of_another_device():
     # an empty one is too small, not none
     with pytest.raises(santa.SantaError):
         santa.attend_paged(new, cache, ints([0]), workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("T", [1, 20, 150])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [150, 5000])
+def test_a_result_at_16_bytes(T, d, n):
+    """(rows of a result at a multiple of 32 bytes are stored 32 bytes at a time)"""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    cols = -(-n // 16)
+    k, v = (torch.randn(2 * cols, 2, 16, d, generator=g, device=DEV).to(bf16) for _ in range(2))
+    cache = santa.PagedCache(k, v, torch.arange(2 * cols, device=DEV, dtype=torch.int32).view(2, cols))
+    q = torch.randn(2, T, 8, d, generator=g, device=DEV).to(bf16)
+    pos, counts = ints([n - T, 0]), ints([T, T - T // 3])
+    want = santa.attend_paged(q, cache, pos, counts)
+    room = torch.full((q.numel() + 16,), 7.0, dtype=bf16, device=DEV)
+    out = room[8:-8].view_as(q)
+    assert out.data_ptr() % 32 == 16
+    santa.attend_paged(q, cache, pos, counts, out=out)
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1, :T - T // 3], want[1, :T - T // 3])
+    assert (out[1, T - T // 3:] == 7).all() and (room[:8] == 7).all() and (room[-8:] == 7).all()
+    with pytest.raises(santa.SantaError):
+        santa.attend_paged(q, cache, pos, counts, out=room[4:-12].view_as(q))
